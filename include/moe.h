@@ -407,6 +407,126 @@ int32_t moe_layer_workspace_offsets(int32_t T, int32_t E_tot, int32_t k, int32_t
                                     int32_t H, int32_t I, int32_t s, uint32_t flags,
                                     size_t* offsets13);
 
+/* ---- 16-bit grouped products ------------------------------------------------ */
+/*
+ * The expert products of a training step in 16-bit types, next to the MX
+ * grouped GEMMs above: ragged groups of rows given by the device offsets that
+ * moe_permute writes, no host sync, fp32 accumulation, one rounding.
+ *
+ *   moe_grouped_mm     y[r][n] = sum_k x[s(r)][k] * W_g[n][k]      W [G, N, K]
+ *                      (MOE_MM_W_KN: W_g[k][n], W [G, K, N]: with the weights
+ *                      of the forward product, the gradient of its rows)
+ *   moe_grouped_wgrad  dW_g[n][k] = sum_{r in g} dy[t(r)][n] * x[s(r)][k]
+ *
+ * for every row r in [offsets[g], offsets[g+1]) (offsets are held inside
+ * [0, R_max]). s(r) = row_src[r] (or x_src), t(r) = dy_src[r], each r itself
+ * when NULL, so token-order arrays are read through moe_permute's row_src
+ * without a gathered copy. Rows of y that belong to no group are left as they
+ * were. A group without rows has dW_g = 0 (unchanged with
+ * MOE_WGRAD_ACCUMULATE, which adds to what dW holds).
+ *
+ * dtype: MOE_T_BF16 or MOE_T_F16, of x, w, dy and y. dW is of the same type,
+ * or fp32 with MOE_WGRAD_F32. Leading dimensions are in elements; rows start
+ * at multiples of 16 bytes (8 bytes for y). N % 8 == 0, K % 8 == 0, both at
+ * most MOE_MM_MAX_DIM; G <= 2049. With a source array (row_src, x_src,
+ * dy_src) the indexed array must stay below 4 GiB; sources outside it read as
+ * zero rows.
+ *
+ * x as an 8-bit checkpoint (moe_grouped_wgrad, xs non-NULL): x holds E4M3
+ * codes and xs [x_rows, ceil(K/128)] the scales moe_quantize_block wrote;
+ * the decoded values are rounded to BF16 (exact for its power-of-two scales).
+ * dtype MOE_T_BF16 only; ldx % 8 == 0 and rows at multiples of 8 bytes.
+ *
+ * ws: workspace of the matching size function (may be 0).
+ */
+#define MOE_T_BF16 0
+#define MOE_T_F16  1
+#define MOE_T_F32  2
+#define MOE_MM_MAX_DIM (1 << 20)
+#define MOE_MM_W_KN           (1u << 16)
+#define MOE_WGRAD_ACCUMULATE  (1u << 17)
+#define MOE_WGRAD_F32         (1u << 18)
+
+size_t  moe_grouped_mm_workspace_size(int32_t R_max, int32_t G, int32_t N, int32_t K);
+int32_t moe_grouped_mm(const void* x, int32_t x_rows, int32_t ldx, const int32_t* row_src,
+                       const void* w, int32_t dtype, const int32_t* offsets, int32_t R_max,
+                       int32_t N, int32_t K, int32_t G, uint32_t flags, void* y, int32_t ldy,
+                       void* ws, size_t ws_bytes, hipStream_t stream);
+
+size_t  moe_grouped_wgrad_workspace_size(int32_t R_max, int32_t G, int32_t N, int32_t K);
+int32_t moe_grouped_wgrad(const void* dy, int32_t dy_rows, int32_t ld_dy, const int32_t* dy_src,
+                          const void* x, int32_t x_rows, int32_t ldx, const int32_t* x_src,
+                          const float* xs, int32_t dtype, const int32_t* offsets, int32_t R_max,
+                          int32_t N, int32_t K, int32_t G, uint32_t flags, void* dw, void* ws,
+                          size_t ws_bytes, hipStream_t stream);
+
+/* ---- FP8 with a scale for each block of 128 ----------------------------------- */
+/*
+ * moe_quantize_block: rows of x (dtype MOE_T_*, [rows, K], leading dimension
+ * ld) to E4M3 codes q [rows, K] and fp32 scales s [rows, ceil(K/128)]. The
+ * scale of a block is the smallest power of two, at least 2^-126, that brings
+ * its largest finite |value| to at most 448 (1 for a block of zeros); codes
+ * are value / scale rounded to nearest even, so decoding loses nothing but
+ * that rounding. NaN and infinite values get the NaN code (0x7F with the
+ * value's sign) and do not count for the scale. n_rows: NULL, or a device
+ * count: rows from *n_rows on are left as they were. K % 8 == 0; rows start at
+ * multiples of 16 bytes.
+ *
+ * moe_quantize_block_weights: w [G, N, K] densely packed to q [G, N, K] and
+ * s [G, ceil(N/128), ceil(K/128)], one scale per 128 x 128 block, same rule.
+ */
+int32_t moe_quantize_block(const void* x, int32_t dtype, int32_t rows, int32_t K, int32_t ld,
+                           const int32_t* n_rows, uint8_t* q, float* s, hipStream_t stream);
+int32_t moe_quantize_block_weights(const void* w, int32_t dtype, int32_t G, int32_t N, int32_t K,
+                                   uint8_t* q, float* s, hipStream_t stream);
+
+/*
+ * The grouped product of block-scaled operands (any finite fp32 scales, so
+ * weights quantised elsewhere can be used as they are):
+ *   y[r][n] = sum_b xs[s(r)][b] * ws_g[n / 128][b] * sum_{k in block b} xq[s(r)][k] * wq_g[n][k]
+ * blocks of 128 along K, the inner sums on the FP8 matrix instructions, the
+ * outer one in fp32, one rounding to dtype (MOE_T_BF16 or MOE_T_F16).
+ * xq [x_rows, K], xs [x_rows, ceil(K/128)], wq [G, N, K],
+ * wscale [G, ceil(N/128), ceil(K/128)], y [R_max, N] with leading dimension
+ * ldy. Groups, row_src and untouched rows as in moe_grouped_mm; G = 1 with
+ * offsets {0, R} is a dense product. K % 16 == 0, N % 8 == 0.
+ */
+size_t  moe_grouped_mm_fp8_workspace_size(int32_t R_max, int32_t G, int32_t N, int32_t K);
+int32_t moe_grouped_mm_fp8(const uint8_t* xq, const float* xs, int32_t x_rows, const int32_t* row_src,
+                           const uint8_t* wq, const float* wscale, const int32_t* offsets,
+                           int32_t R_max, int32_t N, int32_t K, int32_t G, int32_t dtype, void* y,
+                           int32_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---- the gated activation with its input kept in 8 bits -------------------------- */
+/*
+ * moe_glu_checkpoint: pre = [g | u] rows of 2I (dtype MOE_T_BF16 or MOE_T_F16,
+ * leading dimension ld) to
+ *   h[r][i] = a(clamp(g)) * clamp(u) * row_w[r]          [rows, I], dtype
+ * with the activation, beta and limit of epi (as moe_epilogue; NULL: SwiGLU,
+ * beta = 1; bias and save_pre must be NULL), and pre itself as E4M3 codes
+ * q [rows, 2I] and scales s [rows, 2, ceil(I/128)], blocks of 128 counted
+ * from the start of each half, by the rule of moe_quantize_block. The 16-bit
+ * pre need not be kept for the backward pass. q and s may both be NULL (h
+ * only). row_w NULL: 1.
+ *
+ * moe_glu_checkpoint_backward: from the decoded (g, u) and dh [rows, I]
+ * (leading dimension ld_dh):
+ *   dpre[r] = [dg | du]   dg = dh * w * clamp(u) * a'(clamp(g)) * [|g| <= limit]
+ *                         du = dh * w * a(clamp(g)) * [|u| <= limit]    [rows, 2I], dtype
+ *   h[r]    as the forward forms it, from the decoded values (NULL: not written);
+ *           the input of the second product's weight gradient
+ *   dw[r]   = sum_i dh * a(clamp(g)) * clamp(u)  (fp32, NULL: not written)
+ * n_rows: NULL, or a device count: rows from *n_rows on are left as they were.
+ * I % 8 == 0.
+ */
+int32_t moe_glu_checkpoint(const void* pre, int32_t dtype, int32_t rows, int32_t I, int32_t ld,
+                           const float* row_w, const int32_t* n_rows, const moe_epilogue* epi, void* h,
+                           uint8_t* q, float* s, hipStream_t stream);
+int32_t moe_glu_checkpoint_backward(const uint8_t* q, const float* s, const void* dh, int32_t dtype,
+                                    int32_t rows, int32_t I, int32_t ld_dh, const float* row_w,
+                                    const int32_t* n_rows, const moe_epilogue* epi, void* dpre, void* h,
+                                    float* dw, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

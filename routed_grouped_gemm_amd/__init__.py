@@ -17,8 +17,9 @@ from . import _lib
 from ._lib import (MOE_ACT_GEGLU, MOE_ACT_SRELU, MOE_ACT_SWIGLU, MOE_FMT_MXFP4,  # noqa: F401
                    MOE_FMT_MXFP8, MOE_GEMM_PASS, MOE_GEMM_STREAMED, MOE_GEMM_TILED,
                    MOE_LAYER_SEPARATE_KERNELS,
-                   MOE_LAYER_TOKEN_RING, MOE_ROUTE_RENORM,
-                   MOE_SCALE_RULE_CEIL, MOE_W1_WRITE_TRANSPOSE, MOE_WEIGHT_AT_COMBINE,
+                   MOE_LAYER_TOKEN_RING, MOE_MM_W_KN, MOE_ROUTE_RENORM,
+                   MOE_SCALE_RULE_CEIL, MOE_T_BF16, MOE_T_F16, MOE_T_F32, MOE_W1_WRITE_TRANSPOSE,
+                   MOE_WEIGHT_AT_COMBINE, MOE_WGRAD_ACCUMULATE, MOE_WGRAD_F32,
                    moe_epilogue, moe_layer_args, moe_weights)
 
 lib = _lib.load()
@@ -425,3 +426,245 @@ def layer(xq, xs, logits, w1: PackedWeights, w2: PackedWeights, k: int, e0: int 
     """moe_layer with the argument order of the activation-first call form
     (x codes, x scales, router logits, weights, top-k)."""
     return moe_layer(logits, xq, xs, w1, w2, k, e0, n_local, shared, flags, out=out, **kw)
+
+
+# ------------------------------------------- 16-bit and block-FP8 products
+_T16 = {torch.bfloat16: MOE_T_BF16, torch.float16: MOE_T_F16}
+_T_ANY = {**_T16, torch.float32: MOE_T_F32}
+
+
+def _mat(t: torch.Tensor, types, name: str, device=None) -> torch.Tensor:
+    """A 2-D device tensor whose rows are dense (its row stride may be larger)."""
+    if t.device.type != "cuda":
+        raise MoeError(f"{name} must be a device tensor")
+    if device is not None and t.device != device:
+        raise MoeError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in types:
+        raise MoeError(f"{name} must be one of {[str(d) for d in types]}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise MoeError(f"{name} must be 2-D with dense rows")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Leading dimension: the row stride (a single row's is not defined by its data)."""
+    if t.shape[0] > 1:
+        if t.stride(0) < t.shape[1]:
+            raise MoeError("rows overlap")
+        return t.stride(0)
+    return t.shape[1]
+
+
+def _dense(t, shape, dtype, name: str, device) -> None:
+    """Check an optional dense device tensor of a known shape and type."""
+    if t is None:
+        return
+    if t.device != device:
+        raise MoeError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise MoeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise MoeError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+@contextlib.contextmanager
+def _at(device, stream):
+    """The operands' device made current, and `stream` (or that device's
+    current stream) the one that allocates and launches."""
+    if stream is not None and stream.device != device:
+        raise MoeError(f"stream is on {stream.device}, expected {device}")
+    with torch.cuda.device(device), _on(stream):
+        yield
+
+
+def _ws(nbytes: int, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _offsets(offsets, G: int, device) -> None:
+    _dense(offsets, (G + 1,), torch.int32, "offsets", device)
+
+
+def moe_grouped_mm(x, w, offsets, w_kn: bool = False, row_src=None, out=None, stream=None):
+    """y[r] = x[r] . W_g^T for the rows r of group g (offsets, int32 [G + 1] on
+    the device): w [G, N, K], or [G, K, N] with w_kn. x [R, K], or [T, K] read
+    through row_src (int32 [R]). bf16 or fp16; returns [R, N] of that type,
+    rows of no group unwritten."""
+    _mat(x, _T16, "x")
+    dev, (T, K) = x.device, x.shape
+    if w.dim() != 3 or w.shape[1 if w_kn else 2] != K:
+        raise MoeError(f"w {tuple(w.shape)} does not fit rows of {K}")
+    _dense(w, w.shape, x.dtype, "w", dev)
+    G, N = w.shape[0], w.shape[2 if w_kn else 1]
+    _offsets(offsets, G, dev)
+    R = T if row_src is None else row_src.shape[0]
+    _dense(row_src, (R,), torch.int32, "row_src", dev)
+    with _at(dev, stream):
+        if out is None:
+            out = torch.empty((R, N), dtype=x.dtype, device=dev)
+        elif tuple(_mat(out, (x.dtype,), "out", dev).shape) != (R, N):
+            raise MoeError(f"out must be [{R}, {N}], got {tuple(out.shape)}")
+        nws = int(lib.moe_grouped_mm_workspace_size(R, G, N, K))
+        ws = _ws(nws, dev)
+        _check(lib.moe_grouped_mm(_p(x), T, _ld(x), _p(row_src), _p(w), _T16[x.dtype], _p(offsets), R, N, K, G,
+                                  MOE_MM_W_KN if w_kn else 0, _p(out), _ld(out), _p(ws), nws, _stream()),
+               "moe_grouped_mm")
+    return out
+
+
+def moe_grouped_wgrad(dy, x, offsets, dy_src=None, x_src=None, x_scales=None, out=None, accumulate: bool = False,
+                      out_dtype=torch.float32, stream=None):
+    """dW_g = dy^T x over the rows of each group: [G, N, K] in out_dtype
+    (float32, or dy's type). dy [R, N] and x [R, K], or token-order arrays
+    read through dy_src / x_src (int32 [R]). With x_scales, x is an 8-bit
+    checkpoint (codes and scales of moe_quantize_block). accumulate adds to
+    `out`, which must then be given."""
+    _mat(dy, _T16, "dy")
+    dev, N = dy.device, dy.shape[1]
+    _mat(x, (torch.uint8,) if x_scales is not None else (dy.dtype,), "x", dev)
+    K = x.shape[1]
+    _dense(x_scales, (x.shape[0], -(-K // 128)), torch.float32, "x_scales", dev)
+    G = offsets.shape[0] - 1
+    _offsets(offsets, G, dev)
+    n = {t.shape[0] for t in (dy if dy_src is None else dy_src, x if x_src is None else x_src)}
+    if len(n) != 1:
+        raise MoeError(f"dy and x give different numbers of rows: {sorted(n)}")
+    R = n.pop()
+    _dense(dy_src, (R,), torch.int32, "dy_src", dev)
+    _dense(x_src, (R,), torch.int32, "x_src", dev)
+    if out_dtype not in (torch.float32, dy.dtype):
+        raise MoeError(f"out_dtype must be float32 or {dy.dtype}, got {out_dtype}")
+    if accumulate and out is None:
+        raise MoeError("accumulate needs out")
+    flags = (MOE_WGRAD_ACCUMULATE if accumulate else 0) | (MOE_WGRAD_F32 if out_dtype == torch.float32 else 0)
+    with _at(dev, stream):
+        if out is None:
+            out = torch.empty((G, N, K), dtype=out_dtype, device=dev)
+        _dense(out, (G, N, K), out_dtype, "out", dev)
+        nws = int(lib.moe_grouped_wgrad_workspace_size(R, G, N, K))
+        ws = _ws(nws, dev)
+        _check(lib.moe_grouped_wgrad(_p(dy), dy.shape[0], _ld(dy), _p(dy_src), _p(x), x.shape[0], _ld(x), _p(x_src),
+                                     _p(x_scales), _T16[dy.dtype], _p(offsets), R, N, K, G, flags, _p(out), _p(ws),
+                                     nws, _stream()), "moe_grouped_wgrad")
+    return out
+
+
+def moe_quantize_block(x, n_rows=None, codes=None, scales=None, stream=None):
+    """Rows of x (bf16, fp16 or fp32 [R, K]) to E4M3 codes uint8 [R, K] and
+    power-of-two scales f32 [R, ceil(K/128)]. n_rows: an int32 device tensor
+    of one element; rows from it on are left unwritten."""
+    _mat(x, _T_ANY, "x")
+    dev, (R, K) = x.device, x.shape
+    _dense(n_rows, () if n_rows is not None and n_rows.dim() == 0 else (1,), torch.int32, "n_rows", dev)
+    with _at(dev, stream):
+        if codes is None:
+            codes = torch.empty((R, K), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty((R, -(-K // 128)), dtype=torch.float32, device=dev)
+        _dense(codes, (R, K), torch.uint8, "codes", dev)
+        _dense(scales, (R, -(-K // 128)), torch.float32, "scales", dev)
+        _check(lib.moe_quantize_block(_p(x), _T_ANY[x.dtype], R, K, _ld(x), _p(n_rows), _p(codes), _p(scales),
+                                      _stream()), "moe_quantize_block")
+    return codes, scales
+
+
+def moe_quantize_block_weights(w, codes=None, scales=None, stream=None):
+    """w [G, N, K] (bf16, fp16 or fp32) to E4M3 codes uint8 [G, N, K] and
+    power-of-two scales f32 [G, ceil(N/128), ceil(K/128)]."""
+    if w.device.type != "cuda" or w.dtype not in _T_ANY or w.dim() != 3 or not w.is_contiguous():
+        raise MoeError("w must be a contiguous 3-D device tensor of bf16, fp16 or fp32")
+    dev, (G, N, K) = w.device, w.shape
+    shp = (G, -(-N // 128), -(-K // 128))
+    with _at(dev, stream):
+        if codes is None:
+            codes = torch.empty((G, N, K), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty(shp, dtype=torch.float32, device=dev)
+        _dense(codes, (G, N, K), torch.uint8, "codes", dev)
+        _dense(scales, shp, torch.float32, "scales", dev)
+        _check(lib.moe_quantize_block_weights(_p(w), _T_ANY[w.dtype], G, N, K, _p(codes), _p(scales), _stream()),
+               "moe_quantize_block_weights")
+    return codes, scales
+
+
+def moe_grouped_mm_fp8(xq, xs, wq, ws, offsets, row_src=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """Grouped product of block-scaled FP8 operands: xq uint8 [R, K] (or [T, K]
+    read through row_src) with xs f32 [.., ceil(K/128)], wq uint8 [G, N, K]
+    with ws f32 [G, ceil(N/128), ceil(K/128)]. Returns [R, N] bf16 or fp16."""
+    if xq.device.type != "cuda" or xq.dim() != 2 or wq.dim() != 3 or wq.shape[2] != xq.shape[1]:
+        raise MoeError("xq must be a 2-D device tensor and wq [G, N, K] of the same K")
+    dev, (T, K) = xq.device, xq.shape
+    G, N = wq.shape[0], wq.shape[1]
+    kb = -(-K // 128)
+    _dense(xq, (T, K), torch.uint8, "xq", dev)
+    _dense(xs, (T, kb), torch.float32, "xs", dev)
+    _dense(wq, (G, N, K), torch.uint8, "wq", dev)
+    _dense(ws, (G, -(-N // 128), kb), torch.float32, "ws", dev)
+    _offsets(offsets, G, dev)
+    R = T if row_src is None else row_src.shape[0]
+    _dense(row_src, (R,), torch.int32, "row_src", dev)
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _T16:
+        raise MoeError(f"out_dtype must be bf16 or fp16, got {out_dtype}")
+    with _at(dev, stream):
+        if out is None:
+            out = torch.empty((R, N), dtype=out_dtype, device=dev)
+        elif tuple(_mat(out, _T16, "out", dev).shape) != (R, N):
+            raise MoeError(f"out must be [{R}, {N}], got {tuple(out.shape)}")
+        nws = int(lib.moe_grouped_mm_fp8_workspace_size(R, G, N, K))
+        wsp = _ws(nws, dev)
+        _check(lib.moe_grouped_mm_fp8(_p(xq), _p(xs), T, _p(row_src), _p(wq), _p(ws), _p(offsets), R, N, K, G,
+                                      _T16[out_dtype], _p(out), _ld(out), _p(wsp), nws, _stream()),
+               "moe_grouped_mm_fp8")
+    return out
+
+
+def moe_glu_checkpoint(pre, row_w=None, n_rows=None, epi: Epilogue | None = None, keep: bool = True, h=None,
+                       codes=None, scales=None, stream=None):
+    """pre = [gate | up] rows [R, 2I] (bf16 or fp16) to h = act(gate) * up * w
+    [R, I] and, with keep, pre in 8 bits: codes uint8 [R, 2I], scales f32
+    [R, 2, ceil(I/128)]. Returns (h, codes, scales)."""
+    _mat(pre, _T16, "pre")
+    dev, R, I = pre.device, pre.shape[0], pre.shape[1] // 2
+    if pre.shape[1] % 2:
+        raise MoeError("pre must have an even number of columns")
+    if not keep and (codes is not None or scales is not None):
+        raise MoeError("codes and scales are written only with keep")
+    shp = (R, 2, -(-I // 128))
+    _dense(row_w, (R,), torch.float32, "row_w", dev)
+    _dense(n_rows, () if n_rows is not None and n_rows.dim() == 0 else (1,), torch.int32, "n_rows", dev)
+    with _at(dev, stream):
+        if h is None:
+            h = torch.empty((R, I), dtype=pre.dtype, device=dev)
+        if keep and codes is None:
+            codes = torch.empty((R, 2 * I), dtype=torch.uint8, device=dev)
+        if keep and scales is None:
+            scales = torch.empty(shp, dtype=torch.float32, device=dev)
+        _dense(h, (R, I), pre.dtype, "h", dev)
+        _dense(codes, (R, 2 * I), torch.uint8, "codes", dev)
+        _dense(scales, shp, torch.float32, "scales", dev)
+        _check(lib.moe_glu_checkpoint(_p(pre), _T16[pre.dtype], R, I, _ld(pre), _p(row_w), _p(n_rows), _eref(epi),
+                                      _p(h), _p(codes), _p(scales), _stream()), "moe_glu_checkpoint")
+    return h, codes, scales
+
+
+def moe_glu_checkpoint_backward(codes, scales, dh, row_w=None, n_rows=None, epi: Epilogue | None = None,
+                                want_h: bool = True, want_dw: bool = True, stream=None):
+    """The backward of moe_glu_checkpoint from its 8-bit codes and scales and
+    dh [R, I] (bf16 or fp16). Returns a dict: dpre [R, 2I], h [R, I] (the
+    forward's product, recomputed) and dw f32 [R] (None where not wanted)."""
+    _mat(dh, _T16, "dh")
+    dev, (R, I) = dh.device, dh.shape
+    _dense(codes, (R, 2 * I), torch.uint8, "codes", dev)
+    _dense(scales, (R, 2, -(-I // 128)), torch.float32, "scales", dev)
+    _dense(row_w, (R,), torch.float32, "row_w", dev)
+    _dense(n_rows, () if n_rows is not None and n_rows.dim() == 0 else (1,), torch.int32, "n_rows", dev)
+    with _at(dev, stream):
+        out = dict(dpre=torch.empty((R, 2 * I), dtype=dh.dtype, device=dev),
+                   h=torch.empty((R, I), dtype=dh.dtype, device=dev) if want_h else None,
+                   dw=torch.empty(R, dtype=torch.float32, device=dev) if want_dw else None)
+        _check(lib.moe_glu_checkpoint_backward(_p(codes), _p(scales), _p(dh), _T16[dh.dtype], R, I, _ld(dh),
+                                               _p(row_w), _p(n_rows), _eref(epi), _p(out["dpre"]), _p(out["h"]),
+                                               _p(out["dw"]), _stream()), "moe_glu_checkpoint_backward")
+    return out

@@ -19,6 +19,11 @@ MOE_GEMM_PASS = 1 << 12
 MOE_LAYER_SEPARATE_KERNELS = 1 << 10
 MOE_LAYER_TOKEN_RING = 1 << 11
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
+MOE_T_BF16, MOE_T_F16, MOE_T_F32 = 0, 1, 2
+MOE_MM_MAX_DIM = 1 << 20
+MOE_MM_W_KN = 1 << 16
+MOE_WGRAD_ACCUMULATE = 1 << 17
+MOE_WGRAD_F32 = 1 << 18
 
 
 class moe_weights(C.Structure):
@@ -73,6 +78,17 @@ SIGNATURES = {
     "moe_layer": (I32, [C.POINTER(moe_layer_args), P, SZ, P]),
     "moe_layer_noalloc": (I32, [C.POINTER(moe_layer_args), P]),
     "moe_layer_workspace_offsets": (I32, [I32, I32, I32, I32, I32, I32, I32, U32, C.POINTER(SZ)]),
+    "moe_grouped_mm_workspace_size": (SZ, [I32, I32, I32, I32]),
+    "moe_grouped_mm": (I32, [P, I32, I32, P, P, I32, P, I32, I32, I32, I32, U32, P, I32, P, SZ, P]),
+    "moe_grouped_wgrad_workspace_size": (SZ, [I32, I32, I32, I32]),
+    "moe_grouped_wgrad": (I32, [P, I32, I32, P, P, I32, I32, P, P, I32, P, I32, I32, I32, I32, U32, P, P,
+                                SZ, P]),
+    "moe_quantize_block": (I32, [P, I32, I32, I32, I32, P, P, P, P]),
+    "moe_quantize_block_weights": (I32, [P, I32, I32, I32, I32, P, P, P]),
+    "moe_grouped_mm_fp8_workspace_size": (SZ, [I32, I32, I32, I32]),
+    "moe_grouped_mm_fp8": (I32, [P, P, I32, P, P, P, P, I32, I32, I32, I32, I32, P, I32, P, SZ, P]),
+    "moe_glu_checkpoint": (I32, [P, I32, I32, I32, I32, P, P, EP, P, P, P, P]),
+    "moe_glu_checkpoint_backward": (I32, [P, P, P, I32, I32, I32, I32, P, P, EP, P, P, P, P]),
 }
 
 _lib = None

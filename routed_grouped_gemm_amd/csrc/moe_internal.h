@@ -124,3 +124,38 @@ int moe_launch_quantize(const float* src, int rows, int K, int fmt, uint32_t fla
                         uint8_t* q, uint8_t* s, hipStream_t stream);
 int moe_launch_prepack(const uint8_t* q, const uint8_t* sc, int G, int N, int K, int fmt,
                        int is_w1, uint8_t* dst, hipStream_t stream);
+
+// Grouped products (grouped_mm.hip): operands as the C ABI has them, checked
+// by the caller. kind: see MmCall.
+struct MmCall {
+    int kind;                        // 0: W [N, K]; 1: W [K, N]; 2: weight gradient
+    int dtype;                       // MOE_T_BF16 / MOE_T_F16: operands (fp8: y only)
+    bool fp8;                        // E4M3 operands with block scales (kind 0)
+    const void* x; int x_rows, ldx; const int32_t* x_src; const float* xs;   // xs with kind 2: 8-bit x
+    const void* w; const float* wscale;
+    const void* dy; int dy_rows, ld_dy; const int32_t* dy_src;
+    const int32_t* offsets;
+    int R_max, N, K, G;
+    bool out_f32, accumulate;
+    void* out; int ldy;
+    void* ws; size_t ws_bytes;
+};
+size_t moe_mm_workspace_bytes(int kind, bool fp8, int R_max, int G, int N, int K);
+int moe_launch_mm(const MmCall& c, hipStream_t stream);
+
+// Block-128 quantisation and the checkpointed activation (block_quant.hip)
+int moe_launch_quantize_block(const void* x, int dtype, int rows, int K, int ld, const int32_t* n_rows,
+                              uint8_t* q, float* s, hipStream_t stream);
+int moe_launch_quantize_block_weights(const void* w, int dtype, int G, int N, int K, uint8_t* q, float* s,
+                                      hipStream_t stream);
+struct GluCall {
+    int dtype, rows, I, ld;          // ld: of pre (forward) or dh (backward)
+    const float* row_w; const int32_t* n_rows;
+    int act; float beta, limit;
+    const void* in;                  // pre or dh
+    const uint8_t* q_in; const float* s_in;     // backward
+    void* h; uint8_t* q; float* s;              // forward (backward: h)
+    void* dpre; float* dw;                      // backward
+};
+int moe_launch_glu_forward(const GluCall& c, hipStream_t stream);
+int moe_launch_glu_backward(const GluCall& c, hipStream_t stream);
