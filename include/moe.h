@@ -429,8 +429,8 @@ int32_t moe_layer_workspace_offsets(int32_t T, int32_t E_tot, int32_t k, int32_t
  * or fp32 with MOE_WGRAD_F32. Leading dimensions are in elements; rows start
  * at multiples of 16 bytes (8 bytes for y). N % 8 == 0, K % 8 == 0, both at
  * most MOE_MM_MAX_DIM; G <= 2049. With a source array (row_src, x_src,
- * dy_src) the indexed array must stay below 4 GiB; sources outside it read as
- * zero rows.
+ * dy_src) the indexed array must stay below 2^32 - 2^22 bytes; sources outside
+ * it read as zero rows.
  *
  * x as an 8-bit checkpoint (moe_grouped_wgrad, xs non-NULL): x holds E4M3
  * codes and xs [x_rows, ceil(K/128)] the scales moe_quantize_block wrote;

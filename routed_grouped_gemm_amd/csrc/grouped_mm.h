@@ -18,13 +18,16 @@ enum { kElBf16 = 0, kElF16 = 1, kElFp8 = 2 };           // operand element kinds
 
 // Byte offset that no bounded resource contains (their sizes stay below it).
 constexpr uint32_t kMmInvalid = 0xFFFFFFF0u;
+// Row offset past every gathered array (they stay below it, see the size
+// checks) that remains one after adding an offset inside a row (< 2^22).
+constexpr uint32_t kMmNoRow = 0xFFC00000u;
 
 // One grouped product. mm: x rows times weights; wgrad: dy^T x per group.
 struct MmP {
     const uint8_t* w; size_t w_group; uint32_t w_ld;     // weights: bytes per group, per row
-    const uint8_t* x; uint32_t x_ld, x_bytes;            // x rows: bytes per row, and of the array (bound)
+    const uint8_t* x; uint32_t x_ld, x_bytes, x_rows;    // x rows: bytes per row; bytes and rows of the array (bounds)
     const int32_t* x_src;                                // null: row r of a group is row r of x
-    const uint8_t* dy; uint32_t dy_ld, dy_bytes;         // wgrad
+    const uint8_t* dy; uint32_t dy_ld, dy_bytes, dy_rows;   // wgrad
     const int32_t* dy_src;
     const int32_t* offsets;
     int G, N, K, R_max;

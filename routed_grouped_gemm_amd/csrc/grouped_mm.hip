@@ -65,6 +65,14 @@ MOE_DEV int tr_swz(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
 
 struct MmItem { int g, a0, b0, r0, nrows, nk; };
 
+// the item's fields as scalars again (control flow that merely looks divergent
+// would otherwise turn every descriptor load into a loop over lanes)
+MOE_DEV MmItem mm_scalar(const MmItem& c) {
+    return MmItem{__builtin_amdgcn_readfirstlane(c.g), __builtin_amdgcn_readfirstlane(c.a0),
+                  __builtin_amdgcn_readfirstlane(c.b0), __builtin_amdgcn_readfirstlane(c.r0),
+                  __builtin_amdgcn_readfirstlane(c.nrows), __builtin_amdgcn_readfirstlane(c.nk)};
+}
+
 // Where a workgroup is: its items and this lane.
 struct MmWhere { int n_items, at, grid, lane, w; };
 
@@ -75,7 +83,7 @@ MOE_DEV MmItem mm_decode(const MmP& p, const int* pass_off, int at, int item) {
     int lo, hi, bt, l;
     if constexpr (is_wgrad(MODE)) {
         bt = (p.N + BT - 1) / BT;
-        c.g = item / (at * bt);
+        c.g = __builtin_amdgcn_readfirstlane(item / (at * bt));
         l = item - c.g * (at * bt);
     } else {
         int glo = 0, ghi = p.G;                              // largest g with pass_off[g] * at <= item
@@ -91,8 +99,10 @@ MOE_DEV MmItem mm_decode(const MmP& p, const int* pass_off, int at, int item) {
     // bands of four b tiles, b fastest: the items that run together on one
     // XCD share operands in its L2
     const int band = l / (4 * at), h = min(4, bt - 4 * band), l2 = l - band * 4 * at;
-    c.a0 = (l2 / h) * kATile;
-    c.b0 = (4 * band + l2 % h) * BT;
+    // (scalar registers: a descriptor built from them must not look divergent)
+    const int ai = __builtin_amdgcn_readfirstlane(l2 / h);
+    c.a0 = ai * kATile;
+    c.b0 = (4 * __builtin_amdgcn_readfirstlane(band) + __builtin_amdgcn_readfirstlane(l2 - ai * h)) * BT;
     group_rows(p, c.g, lo, hi);
     c.r0 = __builtin_amdgcn_readfirstlane(lo);
     c.nrows = __builtin_amdgcn_readfirstlane(hi) - c.r0;
@@ -121,9 +131,12 @@ struct MmReq {
 template <int MODE, int NB>
 MOE_DEV void mm_open_src(const MmP& p, const MmWhere& wh, MmReq<NB>& R) {
     if constexpr (is_wgrad(MODE)) {
-        const int k = R.kt * 64 + 16 * wh.w + (wh.lane & 15);
-        if (MODE == kWgrad && p.x_src) R.psrc = k < R.c.nrows ? p.x_src[R.c.r0 + k] : -1;
-        if (p.dy_src) R.qsrc = k < R.c.nrows ? p.dy_src[R.c.r0 + k] : -1;
+        const int k = R.kt * 64 + 16 * wh.w + (wh.lane & 15);    // rows past the group: 0, never used
+        if constexpr (MODE == kWgrad)
+            R.psrc = __builtin_amdgcn_raw_buffer_load_b32(
+                make_rsrc(p.x_src + R.c.r0, p.x_src ? (uint32_t)(R.c.nrows * 4) : 0u), k * 4, 0, 0);
+        R.qsrc = __builtin_amdgcn_raw_buffer_load_b32(
+            make_rsrc(p.dy_src + R.c.r0, p.dy_src ? (uint32_t)(R.c.nrows * 4) : 0u), k * 4, 0, 0);
     }
 }
 
@@ -131,39 +144,55 @@ MOE_DEV void mm_open_src(const MmP& p, const MmWhere& wh, MmReq<NB>& R) {
 template <int EL, int MODE, int NB>
 MOE_DEV void mm_open_item(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NB>& R) {
     constexpr int BT = 32 * NB;
-    R.live = false;
-    for (; R.item < wh.n_items && !R.live; R.item += wh.grid) {
-        R.c = mm_decode<EL, MODE, NB>(p, pass_off, wh.at, R.item);
-        R.live = R.c.nk > 0;
+    int item = R.item;
+    bool live = false;
+    while (item < wh.n_items && !live) {
+        R.c = mm_decode<EL, MODE, NB>(p, pass_off, wh.at, item);
+        live = R.c.nk > 0;
+        item += wh.grid;
     }
-    R.kt = 0;
-    if (!R.live) return;
+    R.item = item;
+    R.live = live;
+    if (!live) return;
+    R.c = mm_scalar(R.c);
     if constexpr (!is_wgrad(MODE)) {
+        // source rows without a branch: past the item (and without a source
+        // array, whose resource is then empty) the loads return 0
+        const rsrc_t rm = make_rsrc(p.x_src + R.c.r0, p.x_src ? (uint32_t)(R.c.nrows * 4) : 0u);
         #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const int row = (BT / 4) * wh.w + 8 * i + (wh.lane >> 3);
-            const bool ok = row < R.c.nrows;
-            const uint32_t s = p.x_src ? (ok ? (uint32_t)p.x_src[R.c.r0 + row] : 0u) : (uint32_t)row;
-            R.row[i] = ok ? s * p.x_ld : kMmInvalid;
+            const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, row * 4, 0, 0);
+            R.row[i] = row < R.c.nrows && s < p.x_rows ? (p.x_src ? s : (uint32_t)row) * p.x_ld : kMmNoRow;
         }
         if constexpr (EL == kElFp8) {
             const int row = (BT / 4) * wh.w + wh.lane;
-            const bool ok = wh.lane < BT / 4 && row < R.c.nrows;
-            const uint32_t s = p.x_src ? (ok ? (uint32_t)p.x_src[R.c.r0 + row] : 0u) : (uint32_t)row;
-            R.srow = ok ? s * (uint32_t)(p.kb * 4) : kMmInvalid;
+            const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, row * 4, 0, 0);
+            R.srow = wh.lane < BT / 4 && row < R.c.nrows && s < p.x_rows ? (p.x_src ? s : (uint32_t)row) * (uint32_t)(p.kb * 4)
+                                                                          : kMmNoRow;
         }
     }
-    mm_open_src<MODE>(p, wh, R);
+}
+
+// The lane number as a value the compiler cannot relate to the last K-tile's:
+// offsets formed from it are recomputed (one or two instructions each) instead
+// of being kept in registers across the products.
+MOE_DEV int mm_fresh(int lane) {
+    asm volatile("" : "+v"(lane));
+    return lane;
 }
 
 // Slow form: K-tile rows [16 w, 16 w + 16) of an operand into dst. With a map
 // the row of k is src (one per lane % 16) from the array's start, else row
 // first + k. krem: rows left; columns [c0, c0 + 256) of ncols.
-MOE_DEV void mm_stage_slow(uint8_t* dst, const uint8_t* base, uint32_t ld, uint32_t bytes, bool mapped, int src,
-                           int first, int krem, int c0, int ncols, int w, int lane) {
-    const rsrc_t r = mapped ? make_rsrc(base, bytes)
-                            : make_rsrc(base + (size_t)first * ld + (size_t)c0 * 2,
-                                        (uint32_t)(min(krem, 64) - 1) * ld + (uint32_t)(min(ncols - c0, 256) * 2));
+MOE_DEV void mm_stage_slow(uint8_t* dst, const uint8_t* base, uint32_t ld, uint32_t bytes, uint32_t rows, bool mapped,
+                           int src, int first, int krem, int c0, int ncols, int w, int lane) {
+    if (!mapped) {
+        base += (size_t)first * ld + (size_t)c0 * 2;
+        bytes = (uint32_t)(min(krem, 64) - 1) * ld + (uint32_t)(min(ncols - c0, 256) * 2);
+    }
+    const rsrc_t r = make_rsrc(base, bytes);
+    lane = mm_fresh(lane);
     #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int k = 16 * w + 2 * i + (lane >> 5);
@@ -173,7 +202,7 @@ MOE_DEV void mm_stage_slow(uint8_t* dst, const uint8_t* base, uint32_t ld, uint3
         if (mapped) {
             const int s0 = __builtin_amdgcn_readlane(src, 2 * i), s1 = __builtin_amdgcn_readlane(src, 2 * i + 1);
             const int s = lane < 32 ? s0 : s1;
-            ok = ok && s >= 0;
+            ok = ok && (uint32_t)s < rows;
             o = (uint32_t)s * ld + (uint32_t)((c0 + col) * 2);
         }
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void_t*)(dst + (16 * w + 2 * i) * 512), 16,
@@ -186,7 +215,7 @@ template <int EL, int MODE, int NB>
 MOE_DEV void mm_request(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NB>& R, uint8_t* smem) {
     using Geo = MmGeom<EL, NB>;
     constexpr int EB = EL == kElFp8 ? 1 : 2, BT = 32 * NB;
-    const int lane = wh.lane, w = wh.w;
+    const int lane = mm_fresh(wh.lane), w = wh.w;
     const MmItem& c = R.c;
     uint8_t* st = smem + (R.step % Geo::NST) * Geo::Stage;
     const int kbyte = R.kt * 128;
@@ -195,48 +224,50 @@ MOE_DEV void mm_request(const MmP& p, const int* pass_off, const MmWhere& wh, Mm
         const rsrc_t rw = make_rsrc(p.w + (size_t)c.g * p.w_group + (size_t)c.a0 * p.w_ld, (uint32_t)rows * p.w_ld);
         #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int row = 64 * w + 8 * i + (lane >> 3);
-            const int kb = kbyte + 16 * ((lane & 7) ^ kc_swz(row));
+            // the swizzle of row 64 w + 8 i + lane / 8 depends on i's parity alone
+            const int kb = kbyte + 16 * ((lane & 7) ^ ((lane >> 4) | (4 * (i & 1))));
+            const uint32_t o = (uint32_t)(64 * w + (lane >> 3)) * p.w_ld + (uint32_t)kb;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rw, (mm_lds_void_t*)(st + (64 * w + 8 * i) * 128), 16,
-                kb < p.K * EB ? (uint32_t)row * p.w_ld + (uint32_t)kb : kMmInvalid, 0, 0, 0);
+                kb < p.K * EB ? o + (uint32_t)(8 * i) * p.w_ld : kMmInvalid, 0, 0, 0);
         }
     } else if constexpr (MODE == kMmKN) {
-        mm_stage_slow(st, p.w + (size_t)c.g * p.w_group, p.w_ld, 0, false, 0, R.kt * 64, p.K - R.kt * 64, c.a0, p.N,
+        mm_stage_slow(st, p.w + (size_t)c.g * p.w_group, p.w_ld, 0, 0, false, 0, R.kt * 64, p.K - R.kt * 64, c.a0, p.N,
                       w, lane);
     } else {
         if constexpr (MODE == kWgrad)
-            mm_stage_slow(st, p.x, p.x_ld, p.x_bytes, p.x_src != nullptr, R.psrc, c.r0 + R.kt * 64, c.nrows - R.kt * 64,
+            mm_stage_slow(st, p.x, p.x_ld, p.x_bytes, p.x_rows, p.x_src != nullptr, R.psrc, c.r0 + R.kt * 64, c.nrows - R.kt * 64,
                           c.a0, p.K, w, lane);
-        mm_stage_slow(st + Geo::QOff, p.dy, p.dy_ld, p.dy_bytes, p.dy_src != nullptr, R.qsrc, c.r0 + R.kt * 64,
+        mm_stage_slow(st + Geo::QOff, p.dy, p.dy_ld, p.dy_bytes, p.dy_rows, p.dy_src != nullptr, R.qsrc, c.r0 + R.kt * 64,
                       c.nrows - R.kt * 64, c.b0, p.N, w, lane);
     }
     if constexpr (!is_wgrad(MODE)) {
         // gathered rows are addressed from the array's start, a group's own rows from the tile's first
-        const rsrc_t rx = p.x_src ? make_rsrc(p.x, p.x_bytes)
-                                  : make_rsrc(p.x + (size_t)c.r0 * p.x_ld,
-                                              (uint32_t)(c.nrows - 1) * p.x_ld + (uint32_t)(p.K * EB));
+        const rsrc_t rx = make_rsrc(p.x_src ? p.x : p.x + (size_t)c.r0 * p.x_ld,
+                                    p.x_src ? p.x_bytes : (uint32_t)(c.nrows - 1) * p.x_ld + (uint32_t)(p.K * EB));
         #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const int row = (BT / 4) * w + 8 * i + (lane >> 3);
             const int kb = kbyte + 16 * ((lane & 7) ^ kc_swz(row));
-            const bool ok = kb < p.K * EB && R.row[i] != kMmInvalid;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rx, (mm_lds_void_t*)(st + Geo::QOff + ((BT / 4) * w + 8 * i) * 128), 16,
-                ok ? R.row[i] + (uint32_t)kb : kMmInvalid, 0, 0, 0);
+                kb < p.K * EB ? R.row[i] + (uint32_t)kb : kMmInvalid, 0, 0, 0);
         }
         if constexpr (EL == kElFp8) {
-            const rsrc_t rs = p.x_src ? make_rsrc(p.xs, p.xs_bytes)
-                                      : make_rsrc(p.xs + (size_t)c.r0 * p.kb, (uint32_t)(c.nrows * p.kb * 4));
+            const rsrc_t rs = make_rsrc(p.x_src ? p.xs : p.xs + (size_t)c.r0 * p.kb,
+                                        p.x_src ? p.xs_bytes : (uint32_t)(c.nrows * p.kb * 4));
             if (lane < BT / 4)          // only these lanes' 4 bytes are written
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     rs, (mm_lds_void_t*)(st + Geo::SOff + (BT / 4) * w * 4), 4,
-                    R.srow != kMmInvalid ? R.srow + (uint32_t)(R.kt * 4) : kMmInvalid, 0, 0, 0);
+                    R.srow + (uint32_t)(R.kt * 4), 0, 0, 0);
         }
     }
     ++R.step;
-    if (++R.kt == c.nk) mm_open_item<EL, MODE, NB>(p, pass_off, wh, R);
-    else mm_open_src<MODE>(p, wh, R);
+    const int kt = R.kt + 1;
+    const bool last = kt == c.nk;
+    R.kt = last ? 0 : kt;
+    if (last) mm_open_item<EL, MODE, NB>(p, pass_off, wh, R);
+    if (R.live) mm_open_src<MODE>(p, wh, R);
 }
 
 // wgrad from 8-bit rows: the a operand passes through registers. Every wave
@@ -254,25 +285,30 @@ struct MmKept {
 
 template <int NB>
 MOE_DEV void kept_open(const MmP& p, const MmWhere& wh, MmKept& X) {
-    X.live = false;
-    for (; X.item < wh.n_items && !X.live; X.item += wh.grid) {
-        X.c = mm_decode<kElBf16, kWgrad8, NB>(p, nullptr, wh.at, X.item);
-        X.live = X.c.nk > 0;
+    int item = X.item;
+    bool live = false;
+    while (item < wh.n_items && !live) {
+        X.c = mm_decode<kElBf16, kWgrad8, NB>(p, nullptr, wh.at, item);
+        live = X.c.nk > 0;
+        item += wh.grid;
     }
-    X.kt = 0;
+    X.item = item;
+    X.live = live;
+    X.c = mm_scalar(X.c);
 }
 MOE_DEV void kept_src(const MmP& p, const MmWhere& wh, MmKept& X) {
     const int k = X.kt * 64 + 8 * wh.w + (wh.lane & 7);
-    if (p.x_src && X.live) X.src = k < X.c.nrows ? p.x_src[X.c.r0 + k] : -1;
+    X.src = __builtin_amdgcn_raw_buffer_load_b32(
+        make_rsrc(p.x_src + X.c.r0, p.x_src ? (uint32_t)(X.c.nrows * 4) : 0u), k * 4, 0, 0);
 }
 template <int NB>
 MOE_DEV void kept_load(const MmP& p, const MmWhere& wh, MmKept& X) {
     const int k0 = X.kt * 64, krem = X.c.nrows - k0, first = X.c.r0 + k0, rows = min(krem, 64);
     const bool mapped = p.x_src != nullptr;
-    const rsrc_t rx = mapped ? make_rsrc(p.x, p.x_bytes)
-                             : make_rsrc(p.x + (size_t)first * p.x_ld, (uint32_t)(rows - 1) * p.x_ld + (uint32_t)p.K);
-    const rsrc_t rs = mapped ? make_rsrc(p.xs, p.xs_bytes)
-                             : make_rsrc(p.xs + (size_t)first * p.kb, (uint32_t)(rows * p.kb * 4));
+    const rsrc_t rx = make_rsrc(mapped ? p.x : p.x + (size_t)first * p.x_ld,
+                                mapped ? p.x_bytes : (uint32_t)(rows - 1) * p.x_ld + (uint32_t)p.K);
+    const rsrc_t rs = make_rsrc(mapped ? p.xs : p.xs + (size_t)first * p.kb,
+                                mapped ? p.xs_bytes : (uint32_t)(rows * p.kb * 4));
     const int col = X.c.a0 + (wh.lane & 31) * 8;
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -282,15 +318,18 @@ MOE_DEV void kept_load(const MmP& p, const MmWhere& wh, MmKept& X) {
             const int s0 = __builtin_amdgcn_readlane(X.src, 2 * i), s1 = __builtin_amdgcn_readlane(X.src, 2 * i + 1);
             row = wh.lane < 32 ? s0 : s1;
         }
-        const bool ok = k < krem && col < p.K && row >= 0;
+        const bool ok = k < krem && col < p.K && (!mapped || (uint32_t)row < p.x_rows);
         X.q[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
             rx, ok ? (uint32_t)row * p.x_ld + (uint32_t)col : kMmInvalid, 0, 0));
         X.s[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
             rs, ok ? ((uint32_t)row * (uint32_t)p.kb + (uint32_t)(col >> 7)) * 4u : kMmInvalid, 0, 0));
     }
     X.held = true;
-    if (++X.kt == X.c.nk) kept_open<NB>(p, wh, X);
-    kept_src(p, wh, X);
+    const int kt = X.kt + 1;
+    const bool last = kt == X.c.nk;
+    X.kt = last ? 0 : kt;
+    if (last) kept_open<NB>(p, wh, X);
+    if (X.live) kept_src(p, wh, X);
 }
 MOE_DEV void kept_write(const MmWhere& wh, MmKept& X, uint8_t* st) {
     #pragma unroll
@@ -406,15 +445,41 @@ void grouped_mm_kernel(MmP p) {
     auto multiply = [&](auto half) __attribute__((always_inline)) {
         constexpr int h = decltype(half)::value;
         if constexpr (EL == kElFp8) {
+            // the K-tile is one block of 128: its products go to cleared
+            // registers and are added with the two scales' product, one b tile
+            // behind: 4 additions in the shadow of each matrix instruction. The
+            // empty asm statements order the two (b tile u's products before
+            // and b tile u - 1's additions before u's); left alone the compiler
+            // starts every product first and spills the accumulators.
+            f32x4 d[2][4];
+            float sc = 0.f;
             #pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                const float sc = fs[u] * fw;
-                #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const f32x4 d = mfma_fp8(fp[0][t], fp[1][t], fq[0][u], fq[1][u], f32x4{0.f, 0.f, 0.f, 0.f});
+            for (int u = 0; u <= NU; ++u) {
+                if (u < NU)
                     #pragma unroll
-                    for (int v = 0; v < 4; ++v) acc[h * NU + u][t][v] = fmaf(d[v], sc, acc[h * NU + u][t][v]);
+                    for (int t = 0; t < 4; ++t)
+                        d[u & 1][t] = mfma_fp8(fp[0][t], fp[1][t], fq[0][u], fq[1][u], f32x4{0.f, 0.f, 0.f, 0.f});
+                if (u > 0) {
+                    f32x4* a = acc[h * NU + u - 1];
+                    #pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        #pragma unroll
+                        for (int v = 0; v < 4; ++v) a[t][v] = fmaf(d[(u - 1) & 1][t][v], sc, a[t][v]);
+                    if (u < NU) {
+                        #pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                        }
+                    }
+                    asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
                 }
+                if (u < NU) {
+                    sc = fs[u] * fw;
+                    const f32x4* e = d[u & 1];
+                    asm volatile("" : "+v"(sc) : "v"(e[0]), "v"(e[1]), "v"(e[2]), "v"(e[3]));
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
         } else {
             #pragma unroll
@@ -431,7 +496,8 @@ void grouped_mm_kernel(MmP p) {
             for (int t = 0; t < 4; ++t) acc[u][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     };
     // sums stay in 32 bits until here: the one rounding to the output's type
-    auto store = [&](const MmItem& c) __attribute__((always_inline)) {
+    auto store = [&](const MmItem& c, auto f16_) __attribute__((always_inline)) {
+        constexpr int f16 = decltype(f16_)::value;
         #pragma unroll
         for (int u = 0; u < NB; ++u) {
             const int b = 16 * NB * ti + 16 * u + j;
@@ -450,16 +516,16 @@ void grouped_mm_kernel(MmP p) {
                             u32x2_t* d = (u32x2_t*)((uint16_t*)p.out + o);
                             if (p.accumulate) {
                                 const u32x2_t e = *d;
-                                v[0] += lo16(e.x, p.out_f16); v[1] += hi16(e.x, p.out_f16);
-                                v[2] += lo16(e.y, p.out_f16); v[3] += hi16(e.y, p.out_f16);
+                                v[0] += lo16(e.x, f16); v[1] += hi16(e.x, f16);
+                                v[2] += lo16(e.y, f16); v[3] += hi16(e.y, f16);
                             }
-                            *d = u32x2_t{pack16(v[0], v[1], p.out_f16), pack16(v[2], v[3], p.out_f16)};
+                            *d = u32x2_t{pack16(v[0], v[1], f16), pack16(v[2], v[3], f16)};
                         }
                     }
                 } else {
                     if (b < c.nrows && a < p.N)
                         *(u32x2_t*)((uint16_t*)p.out + (size_t)(c.r0 + b) * p.out_ld + a) =
-                            u32x2_t{pack16(v[0], v[1], p.out_f16), pack16(v[2], v[3], p.out_f16)};
+                            u32x2_t{pack16(v[0], v[1], f16), pack16(v[2], v[3], f16)};
                 }
             }
         }
@@ -469,17 +535,18 @@ void grouped_mm_kernel(MmP p) {
     MmKept kept;
     if constexpr (MODE == kWgrad8) {
         kept.item = slot;
-        kept.step = 0;
+        kept.step = kept.kt = 0;
         kept.held = false;
         kept_open<NB>(p, wh, kept);
-        kept_src(p, wh, kept);
+        if (kept.live) kept_src(p, wh, kept);
         if (kept.live) kept_load<NB>(p, wh, kept);
         if (kept.held) kept_write(wh, kept, smem);
         if (kept.live) kept_load<NB>(p, wh, kept);
     }
     if (lead) {
-        rq.step = 0;
+        rq.step = rq.kt = 0;
         mm_open_item<EL, MODE, NB>(p, pass_off, wh, rq);
+        if (rq.live) mm_open_src<MODE>(p, wh, rq);
         #pragma unroll 1
         for (int i = 0; i < NST - 1; ++i)
             if (rq.live) mm_request<EL, MODE, NB>(p, pass_off, wh, rq, smem);
@@ -512,7 +579,14 @@ void grouped_mm_kernel(MmP p) {
                 bare_barrier();
             });
         }
-        if (!is_wgrad(MODE) || c.nk > 0 || !p.accumulate) store(c);
+        if (!is_wgrad(MODE) || c.nk > 0 || !p.accumulate) {
+            if constexpr (EL == kElFp8) {
+                if (p.out_f16) store(c, std::integral_constant<int, 1>{});
+                else store(c, std::integral_constant<int, 0>{});
+            } else {
+                store(c, std::integral_constant<int, EL == kElF16>{});
+            }
+        }
     }
     if (lead) bare_barrier();
 }
@@ -561,6 +635,7 @@ int moe_launch_mm(const MmCall& c, hipStream_t stream) {
     const int eb = c.fp8 ? 1 : 2;
     MmP p{};
     p.x = (const uint8_t*)c.x; p.x_ld = (uint32_t)(c.ldx * eb); p.x_src = c.x_src;
+    p.x_rows = (uint32_t)c.x_rows;
     if (c.x_src) p.x_bytes = (uint32_t)((int64_t)(c.x_rows - 1) * c.ldx * eb + (int64_t)c.K * eb);
     p.offsets = c.offsets;
     p.G = c.G; p.N = c.N; p.K = c.K; p.R_max = c.R_max;
@@ -577,6 +652,7 @@ int moe_launch_mm(const MmCall& c, hipStream_t stream) {
             }
         }
         p.dy = (const uint8_t*)c.dy; p.dy_ld = (uint32_t)(c.ld_dy * 2); p.dy_src = c.dy_src;
+        p.dy_rows = (uint32_t)c.dy_rows;
         if (c.dy_src) p.dy_bytes = (uint32_t)((int64_t)(c.dy_rows - 1) * c.ld_dy * 2 + (int64_t)c.N * 2);
         const int64_t tiles = (int64_t)c.G * ((c.N + 255) / 256) * ((c.K + 255) / 256);
         const int items = (int)std::min<int64_t>(tiles, 1 << 30);

@@ -14,8 +14,9 @@ inline int32_t hip_status(int e) { return e == 0 ? MOE_OK : MOE_ERR_HIP; }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// the largest array that gathered rows are read from: 32-bit byte offsets
-constexpr int64_t kGatherBytes = (1ll << 32) - 256;
+// bound on an array that gathered rows are read from: 32-bit byte offsets, the
+// last 4 MiB of which mark rows that are not there
+constexpr int64_t kGatherBytes = (1ll << 32) - (1ll << 22);
 
 int32_t check_dims(int32_t R_max, int32_t N, int32_t K, int32_t G, int kmult) {
     if (R_max < 0 || G < 1 || G > MOE_MAX_EXPERTS + 1) return MOE_ERR_SHAPE;
