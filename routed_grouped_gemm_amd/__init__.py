@@ -457,24 +457,48 @@ def _ld(t: torch.Tensor) -> int:
 
 def _dense(t, shape, dtype, name: str, device) -> None:
     """Check an optional dense device tensor of a known shape and type."""
-    if t is None:
+    if t is None or (t.device == device and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
         return
     if t.device != device:
         raise MoeError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise MoeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise MoeError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise MoeError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+class _Here:
+    """The context of a call on the current device and stream: nothing to switch."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
 
 
 @contextlib.contextmanager
-def _at(device, stream):
-    """The operands' device made current, and `stream` (or that device's
-    current stream) the one that allocates and launches."""
+def _elsewhere(device, stream):
     if stream is not None and stream.device != device:
         raise MoeError(f"stream is on {stream.device}, expected {device}")
     with torch.cuda.device(device), _on(stream):
         yield
+
+
+def _at(device, stream):
+    """The operands' device made current, and `stream` (or that device's
+    current stream) the one that allocates and launches. The usual case, both
+    already current, costs no switch: a small call's time is host time."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE
+    return _elsewhere(device, stream)
+
+
+def _raw_stream(device) -> int:
+    """Handle of the device's current stream, without building a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _ws(nbytes: int, device):
@@ -502,12 +526,12 @@ def moe_grouped_mm(x, w, offsets, w_kn: bool = False, row_src=None, out=None, st
     with _at(dev, stream):
         if out is None:
             out = torch.empty((R, N), dtype=x.dtype, device=dev)
-        elif tuple(_mat(out, (x.dtype,), "out", dev).shape) != (R, N):
+        elif _mat(out, (x.dtype,), "out", dev).shape != (R, N):
             raise MoeError(f"out must be [{R}, {N}], got {tuple(out.shape)}")
         nws = int(lib.moe_grouped_mm_workspace_size(R, G, N, K))
         ws = _ws(nws, dev)
         _check(lib.moe_grouped_mm(_p(x), T, _ld(x), _p(row_src), _p(w), _T16[x.dtype], _p(offsets), R, N, K, G,
-                                  MOE_MM_W_KN if w_kn else 0, _p(out), _ld(out), _p(ws), nws, _stream()),
+                                  MOE_MM_W_KN if w_kn else 0, _p(out), _ld(out), _p(ws), nws, _raw_stream(dev)),
                "moe_grouped_mm")
     return out
 
@@ -545,7 +569,7 @@ def moe_grouped_wgrad(dy, x, offsets, dy_src=None, x_src=None, x_scales=None, ou
         ws = _ws(nws, dev)
         _check(lib.moe_grouped_wgrad(_p(dy), dy.shape[0], _ld(dy), _p(dy_src), _p(x), x.shape[0], _ld(x), _p(x_src),
                                      _p(x_scales), _T16[dy.dtype], _p(offsets), R, N, K, G, flags, _p(out), _p(ws),
-                                     nws, _stream()), "moe_grouped_wgrad")
+                                     nws, _raw_stream(dev)), "moe_grouped_wgrad")
     return out
 
 
@@ -564,7 +588,7 @@ def moe_quantize_block(x, n_rows=None, codes=None, scales=None, stream=None):
         _dense(codes, (R, K), torch.uint8, "codes", dev)
         _dense(scales, (R, -(-K // 128)), torch.float32, "scales", dev)
         _check(lib.moe_quantize_block(_p(x), _T_ANY[x.dtype], R, K, _ld(x), _p(n_rows), _p(codes), _p(scales),
-                                      _stream()), "moe_quantize_block")
+                                      _raw_stream(dev)), "moe_quantize_block")
     return codes, scales
 
 
@@ -582,7 +606,7 @@ def moe_quantize_block_weights(w, codes=None, scales=None, stream=None):
             scales = torch.empty(shp, dtype=torch.float32, device=dev)
         _dense(codes, (G, N, K), torch.uint8, "codes", dev)
         _dense(scales, shp, torch.float32, "scales", dev)
-        _check(lib.moe_quantize_block_weights(_p(w), _T_ANY[w.dtype], G, N, K, _p(codes), _p(scales), _stream()),
+        _check(lib.moe_quantize_block_weights(_p(w), _T_ANY[w.dtype], G, N, K, _p(codes), _p(scales), _raw_stream(dev)),
                "moe_quantize_block_weights")
     return codes, scales
 
@@ -610,12 +634,12 @@ def moe_grouped_mm_fp8(xq, xs, wq, ws, offsets, row_src=None, out=None, out_dtyp
     with _at(dev, stream):
         if out is None:
             out = torch.empty((R, N), dtype=out_dtype, device=dev)
-        elif tuple(_mat(out, _T16, "out", dev).shape) != (R, N):
+        elif _mat(out, _T16, "out", dev).shape != (R, N):
             raise MoeError(f"out must be [{R}, {N}], got {tuple(out.shape)}")
         nws = int(lib.moe_grouped_mm_fp8_workspace_size(R, G, N, K))
         wsp = _ws(nws, dev)
         _check(lib.moe_grouped_mm_fp8(_p(xq), _p(xs), T, _p(row_src), _p(wq), _p(ws), _p(offsets), R, N, K, G,
-                                      _T16[out_dtype], _p(out), _ld(out), _p(wsp), nws, _stream()),
+                                      _T16[out_dtype], _p(out), _ld(out), _p(wsp), nws, _raw_stream(dev)),
                "moe_grouped_mm_fp8")
     return out
 
@@ -645,7 +669,7 @@ def moe_glu_checkpoint(pre, row_w=None, n_rows=None, epi: Epilogue | None = None
         _dense(codes, (R, 2 * I), torch.uint8, "codes", dev)
         _dense(scales, shp, torch.float32, "scales", dev)
         _check(lib.moe_glu_checkpoint(_p(pre), _T16[pre.dtype], R, I, _ld(pre), _p(row_w), _p(n_rows), _eref(epi),
-                                      _p(h), _p(codes), _p(scales), _stream()), "moe_glu_checkpoint")
+                                      _p(h), _p(codes), _p(scales), _raw_stream(dev)), "moe_glu_checkpoint")
     return h, codes, scales
 
 
@@ -666,5 +690,5 @@ def moe_glu_checkpoint_backward(codes, scales, dh, row_w=None, n_rows=None, epi:
                    dw=torch.empty(R, dtype=torch.float32, device=dev) if want_dw else None)
         _check(lib.moe_glu_checkpoint_backward(_p(codes), _p(scales), _p(dh), _T16[dh.dtype], R, I, _ld(dh),
                                                _p(row_w), _p(n_rows), _eref(epi), _p(out["dpre"]), _p(out["h"]),
-                                               _p(out["dw"]), _stream()), "moe_glu_checkpoint_backward")
+                                               _p(out["dw"]), _raw_stream(dev)), "moe_glu_checkpoint_backward")
     return out

@@ -90,4 +90,105 @@ MOE_DEV void bare_barrier() {
     asm volatile("" ::: "memory");
 }
 
+enum { kMmNK = 0, kMmKN = 1, kWgrad = 2, kWgrad8 = 3 };     // kWgrad8: x rows in E4M3 with block scales
+constexpr bool is_wgrad(int mode) { return mode >= kWgrad; }
+
+constexpr int kMmThreads = 512;
+constexpr int kMmLds = 163840;              // LDS of a compute unit
+constexpr int kATile = 256;
+constexpr int kPBytes = kATile * 128;       // one K-tile of the a operand
+
+// chunk swizzle of a row in the contiguous form, and of a k in the slow form
+MOE_DEV int kc_swz(int row) { return (row >> 1) & 7; }
+MOE_DEV int tr_swz(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
+MOE_DEV int tr_swz_half(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+
+struct MmItem { int g, a0, b0, r0, nrows, nk; };
+
+// the item's fields as scalars again (control flow that merely looks divergent
+// would otherwise turn every descriptor load into a loop over lanes)
+MOE_DEV MmItem mm_scalar(const MmItem& c) {
+    return MmItem{__builtin_amdgcn_readfirstlane(c.g), __builtin_amdgcn_readfirstlane(c.a0),
+                  __builtin_amdgcn_readfirstlane(c.b0), __builtin_amdgcn_readfirstlane(c.r0),
+                  __builtin_amdgcn_readfirstlane(c.nrows), __builtin_amdgcn_readfirstlane(c.nk)};
+}
+
+// pass_off[g] = passes of `bt` rows before group g, pass_off[G] their number,
+// in LDS; one wave writes them (a barrier must follow)
+MOE_DEV void mm_passes(const MmP& p, int bt, int lane, int* pass_off) {
+    int run = 0;
+    for (int g0 = 0; g0 < p.G; g0 += 64) {
+        int lo = 0, hi = 0;
+        if (g0 + lane < p.G) group_rows(p, g0 + lane, lo, hi);
+        const int n = (hi - lo + bt - 1) / bt;
+        const int inc = wave_incl_scan(n);
+        if (g0 + lane < p.G) pass_off[g0 + lane] = run + inc - n;
+        run += __builtin_amdgcn_readlane(inc, 63);
+    }
+    if (lane == 0) pass_off[p.G] = run;
+}
+
+// Where a workgroup is: its items and this lane.
+struct MmWhere { int n_items, at, grid, lane, w; };
+
+// work item number `item`: tiles of AT values of the a axis, BT of the b axis
+template <int EL, int MODE, int BT, int AT = kATile>
+MOE_DEV MmItem mm_decode(const MmP& p, const int* pass_off, int at, int item) {
+    constexpr int KT = EL == kElFp8 ? 128 : 64;
+    MmItem c;
+    int lo, hi, bt, l;
+    if constexpr (is_wgrad(MODE)) {
+        bt = (p.N + BT - 1) / BT;
+        c.g = __builtin_amdgcn_readfirstlane(item / (at * bt));
+        l = item - c.g * (at * bt);
+    } else {
+        int glo = 0, ghi = p.G;                              // largest g with pass_off[g] * at <= item
+        while (ghi - glo > 1) {
+            const int mid = (glo + ghi) >> 1;
+            if (pass_off[mid] * at <= item) glo = mid; else ghi = mid;
+        }
+        c.g = __builtin_amdgcn_readfirstlane(glo);
+        const int first = __builtin_amdgcn_readfirstlane(pass_off[c.g]);
+        bt = __builtin_amdgcn_readfirstlane(pass_off[c.g + 1]) - first;
+        l = item - first * at;
+    }
+    // bands of four b tiles, b fastest: the items that run together on one
+    // XCD share operands in its L2
+    const int band = l / (4 * at), h = min(4, bt - 4 * band), l2 = l - band * 4 * at;
+    // (scalar registers: a descriptor built from them must not look divergent)
+    const int ai = __builtin_amdgcn_readfirstlane(l2 / h);
+    c.a0 = ai * AT;
+    c.b0 = (4 * __builtin_amdgcn_readfirstlane(band) + __builtin_amdgcn_readfirstlane(l2 - ai * h)) * BT;
+    group_rows(p, c.g, lo, hi);
+    c.r0 = __builtin_amdgcn_readfirstlane(lo);
+    c.nrows = __builtin_amdgcn_readfirstlane(hi) - c.r0;
+    if constexpr (is_wgrad(MODE)) {
+        c.nk = (c.nrows + KT - 1) / KT;
+    } else {
+        c.r0 += c.b0;
+        c.nrows = min(BT, c.nrows - c.b0);
+        c.nk = (p.K + KT - 1) / KT;
+    }
+    return c;
+}
+
+// The lane number as a value the compiler cannot relate to the last K-tile's:
+// offsets formed from it are recomputed (one or two instructions each) instead
+// of being kept in registers across the products.
+MOE_DEV int mm_fresh(int lane) {
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+// an upper bound on the work items of a product with tiles of bt rows
+inline int mm_items(const MmP& p, int bt, int atile = kATile) {
+    const int64_t passes = (int64_t)p.R_max / bt + (p.G < p.R_max ? p.G : p.R_max);
+    const int64_t n = passes * ((p.N + atile - 1) / atile);
+    return (int)(n < (1 << 30) ? n : (1 << 30));
+}
+
 }  // namespace
+
+// Products of few rows per group (grouped_mm_rows.hip); p is an MmP, el its
+// element kind, kind 0 for W [N, K] and 1 for W [K, N].
+int moe_launch_mm_rows(const void* p, int el, int kind, hipStream_t stream);

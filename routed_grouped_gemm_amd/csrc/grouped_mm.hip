@@ -6,11 +6,11 @@
 //   fp8            y[r][n]  = sum_b xs[r][b] ws_g[n/128][b] sum_{k in block b} xq[r][k] wq_g[n][k]
 //
 // One kernel body: a workgroup of 8 waves computes D[a][b] over tiles of 256
-// values of the contiguous output axis a (n, or k for wgrad) and BT of the
-// other axis b (rows, or n for wgrad). Wave w owns a-quarter w % 4 and b-half
-// w / 4: 4 x NB tiles of the 16x16 matrix instruction. The a side is the
-// instruction's A operand, so a lane ends up with 4 consecutive a values of
-// one b: its stores are 8 or 16 bytes.
+// values of the contiguous output axis a (n, or k for wgrad) and BT = 256 or
+// 128 of the other axis b (rows, or n for wgrad). Wave w owns a-quarter w % 4
+// and b-half w / 4: 4 x NB tiles of the 16x16 matrix instruction. The a side
+// is the instruction's A operand, so a lane ends up with 4 consecutive a
+// values of one b. (Groups of few rows: grouped_mm_rows.hip.)
 //
 // Each operand is staged in LDS by buffer loads that write LDS directly, in
 // K-tiles of 64 16-bit or 128 FP8 elements (128 bytes), in one of two forms:
@@ -18,20 +18,25 @@
 //    XOR-swizzled by row so that the operand reads (16 rows, one chunk each)
 //    hit distinct banks;
 //  - reduction axis slow in memory (W [K, N]; both operands of wgrad):
-//    [k][256 values], read through the transposing LDS load (16 lanes read
-//    4 k x 16 values and receive 4 k of one value each), 32-byte chunks
-//    XOR-swizzled by k so that a half wave's 8 rows hit distinct banks.
+//    [k][256 or 128 values], read through the transposing LDS load (16 lanes
+//    read 4 k x 16 values and receive 4 k of one value each), 32-byte chunks
+//    XOR-swizzled by k so that the 4 rows hit distinct banks.
 // Elements past an edge (rows past the group, the K tail, values past N) are
 // zero: their offsets fall outside the resource.
 //
 // Two waves share a SIMD. They run half a step apart: while waves 4-7
-// multiply, waves 0-3 read their fragments of the next K-tile from LDS, and
-// the other way round, so the matrix cores and the LDS are both busy. One
-// step of a wave is [requests for a later K-tile (waves 0-3), fragment reads]
-// barrier [products] barrier; waves 4-7 start one barrier later. A K-tile's
-// stage is rewritten only after the barrier behind which waves 4-7 have read
-// it; waves 0-3 wait for their requests before the barrier that opens the
-// step using them.
+// multiply, waves 0-3 read fragments from LDS, and the other way round, so the
+// matrix cores and the LDS are both busy. A K-tile is two such turns: turn 0
+// reads the wave's a fragments and the first half of its b fragments, turn 1
+// the other half of the b fragments. So a stage's a operand and first b half
+// are free for the K-tile NST later after turn 0, and a request is in flight
+// for about a K-tile's products although LDS holds only two stages of the
+// largest tile.
+// Requests are issued between matrix instructions: the address unit takes 16
+// cycles for each, and a wave that issues them in its reading turn delays the
+// reads behind them and with them the other waves' products.
+// A wave waits for its own requests (vmcnt, leaving the newer ones in flight)
+// before the barrier that opens the turn reading them.
 //
 // Persistent grid; the requests run ahead across items, so the next item's
 // first K-tiles are in flight during an item's epilogue.
@@ -41,113 +46,46 @@
 
 namespace {
 
-enum { kMmNK = 0, kMmKN = 1, kWgrad = 2, kWgrad8 = 3 };     // kWgrad8: x rows in E4M3 with block scales
-constexpr bool is_wgrad(int mode) { return mode >= kWgrad; }
-
-constexpr int kMmThreads = 512;
-constexpr int kATile = 256;
-constexpr int kPBytes = kATile * 128;       // one K-tile of the a operand
-
 template <int EL, int NB>
 struct MmGeom {
     static constexpr int BT = 32 * NB;                       // b values per workgroup tile
+    static constexpr int NU = NB / 2;                        // b tiles of a wave per turn
+    static constexpr int NQ = NB / 4;                        // requests of a wave per half of the b operand
+    static constexpr int HRows = 2 * NB;                     // rows of a wave per half of the b operand
     static constexpr int QOff = kPBytes;
-    static constexpr int SOff = kPBytes + BT * 128;          // fp8: row scales
-    static constexpr int Stage = SOff + (EL == kElFp8 ? BT * 4 : 0);
-    static constexpr int NST = Stage * 4 + 8320 <= 163840 ? 4 : (Stage * 3 + 8320 <= 163840 ? 3 : 2);
-    static constexpr int Loads = 8 + NB + (EL == kElFp8 ? 1 : 0);   // per wave 0-3 and K-tile
+    static constexpr int SOff = kPBytes + BT * 128;          // fp8: row scales, 256 bytes per wave and half
+    static constexpr int Stage = SOff + (EL == kElFp8 ? 4096 : 0);
+    static constexpr int NST = Stage * 3 + 8320 <= kMmLds ? 3 : 2;
     static constexpr int Lds(int G) { return Stage * NST + (G + 1) * 4; }
 };
 
-// chunk swizzle of a row in the contiguous form, and of a k in the slow form
-MOE_DEV int kc_swz(int row) { return (row >> 1) & 7; }
-MOE_DEV int tr_swz(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
-
-struct MmItem { int g, a0, b0, r0, nrows, nk; };
-
-// the item's fields as scalars again (control flow that merely looks divergent
-// would otherwise turn every descriptor load into a loop over lanes)
-MOE_DEV MmItem mm_scalar(const MmItem& c) {
-    return MmItem{__builtin_amdgcn_readfirstlane(c.g), __builtin_amdgcn_readfirstlane(c.a0),
-                  __builtin_amdgcn_readfirstlane(c.b0), __builtin_amdgcn_readfirstlane(c.r0),
-                  __builtin_amdgcn_readfirstlane(c.nrows), __builtin_amdgcn_readfirstlane(c.nk)};
-}
-
-// Where a workgroup is: its items and this lane.
-struct MmWhere { int n_items, at, grid, lane, w; };
-
-template <int EL, int MODE, int NB>
-MOE_DEV MmItem mm_decode(const MmP& p, const int* pass_off, int at, int item) {
-    constexpr int BT = 32 * NB, KT = EL == kElFp8 ? 128 : 64;
-    MmItem c;
-    int lo, hi, bt, l;
-    if constexpr (is_wgrad(MODE)) {
-        bt = (p.N + BT - 1) / BT;
-        c.g = __builtin_amdgcn_readfirstlane(item / (at * bt));
-        l = item - c.g * (at * bt);
-    } else {
-        int glo = 0, ghi = p.G;                              // largest g with pass_off[g] * at <= item
-        while (ghi - glo > 1) {
-            const int mid = (glo + ghi) >> 1;
-            if (pass_off[mid] * at <= item) glo = mid; else ghi = mid;
-        }
-        c.g = __builtin_amdgcn_readfirstlane(glo);
-        const int first = __builtin_amdgcn_readfirstlane(pass_off[c.g]);
-        bt = __builtin_amdgcn_readfirstlane(pass_off[c.g + 1]) - first;
-        l = item - first * at;
-    }
-    // bands of four b tiles, b fastest: the items that run together on one
-    // XCD share operands in its L2
-    const int band = l / (4 * at), h = min(4, bt - 4 * band), l2 = l - band * 4 * at;
-    // (scalar registers: a descriptor built from them must not look divergent)
-    const int ai = __builtin_amdgcn_readfirstlane(l2 / h);
-    c.a0 = ai * kATile;
-    c.b0 = (4 * __builtin_amdgcn_readfirstlane(band) + __builtin_amdgcn_readfirstlane(l2 - ai * h)) * BT;
-    group_rows(p, c.g, lo, hi);
-    c.r0 = __builtin_amdgcn_readfirstlane(lo);
-    c.nrows = __builtin_amdgcn_readfirstlane(hi) - c.r0;
-    if constexpr (is_wgrad(MODE)) {
-        c.nk = (c.nrows + KT - 1) / KT;
-    } else {
-        c.r0 += c.b0;
-        c.nrows = min(BT, c.nrows - c.b0);
-        c.nk = (p.K + KT - 1) / KT;
-    }
-    return c;
-}
-
-// The request side of a workgroup (waves 0-3): the K-tile to request next.
-template <int NB>
+// A stream of requests: the a operand with the first half of the b operand, or
+// the second half, one K-tile after another through all items. A wave takes an
+// eighth of each: 32 rows (contiguous form) or 8 k (slow form).
+template <int NQ>
 struct MmReq {
     int item, kt, step;                 // item: the one to open after this
     bool live;
     MmItem c;
-    uint32_t row[NB];                   // contiguous form: byte offsets of this lane's rows of the b operand
+    uint32_t row[NQ];                   // contiguous b operand: byte offsets of this lane's rows
     uint32_t srow;                      // fp8: byte offset of this lane's row of scales
-    int psrc, qsrc;                     // wgrad: source rows of this wave's 16 k, one per lane % 16
+    uint32_t psrc, qsrc;                // wgrad: byte offsets of the source rows of k, one k per lane % 8
+    uint32_t po[4], qo[NQ];             // the next request's byte offsets,
+    const uint8_t *pb, *qb;             // what they count from
+    uint32_t pn, qn;                    // and the bytes that may be read there
 };
 
-// wgrad: sources of the K-tile about to be requested
-template <int MODE, int NB>
-MOE_DEV void mm_open_src(const MmP& p, const MmWhere& wh, MmReq<NB>& R) {
-    if constexpr (is_wgrad(MODE)) {
-        const int k = R.kt * 64 + 16 * wh.w + (wh.lane & 15);    // rows past the group: 0, never used
-        if constexpr (MODE == kWgrad)
-            R.psrc = __builtin_amdgcn_raw_buffer_load_b32(
-                make_rsrc(p.x_src + R.c.r0, p.x_src ? (uint32_t)(R.c.nrows * 4) : 0u), k * 4, 0, 0);
-        R.qsrc = __builtin_amdgcn_raw_buffer_load_b32(
-            make_rsrc(p.dy_src + R.c.r0, p.dy_src ? (uint32_t)(R.c.nrows * 4) : 0u), k * 4, 0, 0);
-    }
-}
+// first of the rows that wave w takes of half `half` of the b tile
+template <int NB>
+MOE_DEV int q_first(int w, int half) { return (w >> 2) * (16 * NB) + half * (8 * NB) + (w & 3) * (2 * NB); }
 
 // the next item with K-tiles, or none
-template <int EL, int MODE, int NB>
-MOE_DEV void mm_open_item(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NB>& R) {
-    constexpr int BT = 32 * NB;
+template <int EL, int MODE, int NB, int NQ>
+MOE_DEV void mm_open_item(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half) {
     int item = R.item;
     bool live = false;
     while (item < wh.n_items && !live) {
-        R.c = mm_decode<EL, MODE, NB>(p, pass_off, wh.at, item);
+        R.c = mm_decode<EL, MODE, 32 * NB>(p, pass_off, wh.at, item);
         live = R.c.nk > 0;
         item += wh.grid;
     }
@@ -159,115 +97,198 @@ MOE_DEV void mm_open_item(const MmP& p, const int* pass_off, const MmWhere& wh, 
         // source rows without a branch: past the item (and without a source
         // array, whose resource is then empty) the loads return 0
         const rsrc_t rm = make_rsrc(p.x_src + R.c.r0, p.x_src ? (uint32_t)(R.c.nrows * 4) : 0u);
+        const int first = q_first<NB>(wh.w, half);
         #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int row = (BT / 4) * wh.w + 8 * i + (wh.lane >> 3);
+        for (int i = 0; i < NQ; ++i) {
+            const int row = first + 8 * i + (wh.lane >> 3);
             const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, row * 4, 0, 0);
             R.row[i] = row < R.c.nrows && s < p.x_rows ? (p.x_src ? s : (uint32_t)row) * p.x_ld : kMmNoRow;
         }
         if constexpr (EL == kElFp8) {
-            const int row = (BT / 4) * wh.w + wh.lane;
+            const int row = first + wh.lane;
             const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, row * 4, 0, 0);
-            R.srow = wh.lane < BT / 4 && row < R.c.nrows && s < p.x_rows ? (p.x_src ? s : (uint32_t)row) * (uint32_t)(p.kb * 4)
-                                                                          : kMmNoRow;
+            R.srow = wh.lane < 2 * NB && row < R.c.nrows && s < p.x_rows
+                         ? (p.x_src ? s : (uint32_t)row) * (uint32_t)(p.kb * 4) : kMmNoRow;
         }
     }
 }
 
-// The lane number as a value the compiler cannot relate to the last K-tile's:
-// offsets formed from it are recomputed (one or two instructions each) instead
-// of being kept in registers across the products.
-MOE_DEV int mm_fresh(int lane) {
-    asm volatile("" : "+v"(lane));
-    return lane;
+// wgrad: source rows of this wave's 8 k of the K-tile it requests next
+template <int MODE, int NQ>
+MOE_DEV void mm_open_src(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, bool with_p) {
+    const int k = R.kt * 64 + 8 * wh.w + (wh.lane & 7);      // past the group: row 0, never used
+    if constexpr (MODE == kWgrad) {
+        if (with_p) {
+            const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+                make_rsrc(p.x_src + R.c.r0, p.x_src ? (uint32_t)(R.c.nrows * 4) : 0u), k * 4, 0, 0);
+            R.psrc = s < p.x_rows ? s * p.x_ld : kMmNoRow;
+        }
+    }
+    const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+        make_rsrc(p.dy_src + R.c.r0, p.dy_src ? (uint32_t)(R.c.nrows * 4) : 0u), k * 4, 0, 0);
+    R.qsrc = s < p.dy_rows ? s * p.dy_ld : kMmNoRow;
 }
 
-// Slow form: K-tile rows [16 w, 16 w + 16) of an operand into dst. With a map
-// the row of k is src (one per lane % 16) from the array's start, else row
-// first + k. krem: rows left; columns [c0, c0 + 256) of ncols.
-MOE_DEV void mm_stage_slow(uint8_t* dst, const uint8_t* base, uint32_t ld, uint32_t bytes, uint32_t rows, bool mapped,
-                           int src, int first, int krem, int c0, int ncols, int w, int lane) {
+template <int EL, int MODE, int NB, int NQ>
+MOE_DEV void mm_start(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half, int slot) {
+    R.item = slot;
+    R.step = R.kt = 0;
+    mm_open_item<EL, MODE, NB>(p, pass_off, wh, R, half);
+    if constexpr (is_wgrad(MODE)) {
+        if (R.live) mm_open_src<MODE>(p, wh, R, half == 0);
+    }
+}
+
+// step past the K-tile just requested
+template <int EL, int MODE, int NB, int NQ>
+MOE_DEV void mm_advance(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half) {
+    ++R.step;
+    if (!R.live) return;
+    const int kt = R.kt + 1;
+    const bool last = kt == R.c.nk;
+    R.kt = last ? 0 : kt;
+    if (last) mm_open_item<EL, MODE, NB>(p, pass_off, wh, R, half);
+    if constexpr (is_wgrad(MODE)) {
+        if (R.live) mm_open_src<MODE>(p, wh, R, half == 0);
+    }
+}
+
+// bounds a request to 64 rows of the slow form, or to a whole gathered array
+MOE_DEV void mm_slow_bounds(const uint8_t*& base, uint32_t& bytes, uint32_t ld, bool mapped, int first, int krem, int c0,
+                            int ncols) {
     if (!mapped) {
         base += (size_t)first * ld + (size_t)c0 * 2;
-        bytes = (uint32_t)(min(krem, 64) - 1) * ld + (uint32_t)(min(ncols - c0, 256) * 2);
-    }
-    const rsrc_t r = make_rsrc(base, bytes);
-    lane = mm_fresh(lane);
-    #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int k = 16 * w + 2 * i + (lane >> 5);
-        const int col = (((lane & 31) >> 1) ^ tr_swz(k)) * 16 + (lane & 1) * 8;
-        bool ok = k < krem && c0 + col < ncols;
-        uint32_t o = (uint32_t)k * ld + (uint32_t)(col * 2);
-        if (mapped) {
-            const int s0 = __builtin_amdgcn_readlane(src, 2 * i), s1 = __builtin_amdgcn_readlane(src, 2 * i + 1);
-            const int s = lane < 32 ? s0 : s1;
-            ok = ok && (uint32_t)s < rows;
-            o = (uint32_t)s * ld + (uint32_t)((c0 + col) * 2);
-        }
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void_t*)(dst + (16 * w + 2 * i) * 512), 16,
-                                                 ok ? o : kMmInvalid, 0, 0, 0);
+        bytes = (uint32_t)(max(min(krem, 64), 1) - 1) * ld + (uint32_t)(min(ncols - c0, 256) * 2);
     }
 }
 
-// request one K-tile into its stage, then move on
-template <int EL, int MODE, int NB>
-MOE_DEV void mm_request(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NB>& R, uint8_t* smem) {
-    using Geo = MmGeom<EL, NB>;
-    constexpr int EB = EL == kElFp8 ? 1 : 2, BT = 32 * NB;
+// Offsets of the next request (all past the resource once the items have
+// ended: such a request reads nothing and clears a stage nothing reads).
+// Slow form, RPI rows of LPR lanes each per request: k = 8 w + RPI i + lane / LPR.
+template <int COLS, int N>
+MOE_DEV void mm_slow_offsets(uint32_t (&o)[N], bool live, bool mapped, uint32_t src, uint32_t ld, int krem, int c0,
+                             int ncols, int half, int w, int lane) {
+    constexpr int RPI = 512 / COLS, LPR = 64 / RPI;
+    const int kl = lane / LPR, p32 = (lane % LPR) >> 1;
+    #pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int k = 8 * w + RPI * i + kl;
+        int col;
+        if constexpr (COLS == 256) {
+            col = (p32 ^ tr_swz(k)) * 16 + (lane & 1) * 8;
+        } else {
+            const int ch = p32 ^ tr_swz_half(k);
+            col = (ch >> 2) * 128 + half * 64 + (ch & 3) * 16 + (lane & 1) * 8;
+        }
+        const bool ok = live && k < krem && c0 + col < ncols;
+        uint32_t v = (uint32_t)k * ld + (uint32_t)(col * 2);
+        if (mapped) v = (uint32_t)__builtin_amdgcn_ds_bpermute((RPI * i + kl) * 4, (int)src) + (uint32_t)((c0 + col) * 2);
+        o[i] = ok ? v : kMmInvalid;
+    }
+}
+template <int EL, int MODE, int NB, int NQ>
+MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, int half) {
+    constexpr int EB = EL == kElFp8 ? 1 : 2;
     const int lane = mm_fresh(wh.lane), w = wh.w;
     const MmItem& c = R.c;
-    uint8_t* st = smem + (R.step % Geo::NST) * Geo::Stage;
-    const int kbyte = R.kt * 128;
-    if constexpr (MODE == kMmNK) {
-        const int rows = min(kATile, p.N - c.a0);
-        const rsrc_t rw = make_rsrc(p.w + (size_t)c.g * p.w_group + (size_t)c.a0 * p.w_ld, (uint32_t)rows * p.w_ld);
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // the swizzle of row 64 w + 8 i + lane / 8 depends on i's parity alone
-            const int kb = kbyte + 16 * ((lane & 7) ^ ((lane >> 4) | (4 * (i & 1))));
-            const uint32_t o = (uint32_t)(64 * w + (lane >> 3)) * p.w_ld + (uint32_t)kb;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rw, (mm_lds_void_t*)(st + (64 * w + 8 * i) * 128), 16,
-                kb < p.K * EB ? o + (uint32_t)(8 * i) * p.w_ld : kMmInvalid, 0, 0, 0);
+    if (half == 0) {
+        if constexpr (MODE == kMmNK) {
+            R.pb = p.w + (size_t)c.g * p.w_group + (size_t)c.a0 * p.w_ld;
+            R.pn = (uint32_t)min(kATile, p.N - c.a0) * p.w_ld;
+            // requests i and i + 2 differ by 16 rows (added when issued); the
+            // swizzle of row 32 w + 8 i + lane / 8 depends on i's parity alone
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int kb = R.kt * 128 + 16 * ((lane & 7) ^ ((lane >> 4) | (4 * h)));
+                R.po[h] = R.live && kb < p.K * EB ? (uint32_t)(32 * w + 8 * h + (lane >> 3)) * p.w_ld + (uint32_t)kb : 0x80000000u;
+            }
+        } else if constexpr (MODE == kMmKN) {
+            R.pb = p.w + (size_t)c.g * p.w_group;
+            mm_slow_bounds(R.pb, R.pn, p.w_ld, false, R.kt * 64, p.K - R.kt * 64, c.a0, p.N);
+            mm_slow_offsets<256>(R.po, R.live, false, 0, p.w_ld, p.K - R.kt * 64, c.a0, p.N, 0, w, lane);
+        } else if constexpr (MODE == kWgrad) {
+            R.pb = p.x;
+            R.pn = p.x_bytes;
+            mm_slow_bounds(R.pb, R.pn, p.x_ld, p.x_src != nullptr, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.a0, p.K);
+            mm_slow_offsets<256>(R.po, R.live, p.x_src != nullptr, R.psrc, p.x_ld, c.nrows - R.kt * 64, c.a0, p.K, 0, w, lane);
         }
-    } else if constexpr (MODE == kMmKN) {
-        mm_stage_slow(st, p.w + (size_t)c.g * p.w_group, p.w_ld, 0, 0, false, 0, R.kt * 64, p.K - R.kt * 64, c.a0, p.N,
-                      w, lane);
+    }
+    if constexpr (is_wgrad(MODE)) {
+        R.qb = p.dy;
+        R.qn = p.dy_bytes;
+        mm_slow_bounds(R.qb, R.qn, p.dy_ld, p.dy_src != nullptr, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.b0, p.N);
+        mm_slow_offsets<128>(R.qo, R.live, p.dy_src != nullptr, R.qsrc, p.dy_ld, c.nrows - R.kt * 64, c.b0, p.N, half, w, lane);
     } else {
-        if constexpr (MODE == kWgrad)
-            mm_stage_slow(st, p.x, p.x_ld, p.x_bytes, p.x_rows, p.x_src != nullptr, R.psrc, c.r0 + R.kt * 64, c.nrows - R.kt * 64,
-                          c.a0, p.K, w, lane);
-        mm_stage_slow(st + Geo::QOff, p.dy, p.dy_ld, p.dy_bytes, p.dy_rows, p.dy_src != nullptr, R.qsrc, c.r0 + R.kt * 64,
-                      c.nrows - R.kt * 64, c.b0, p.N, w, lane);
-    }
-    if constexpr (!is_wgrad(MODE)) {
         // gathered rows are addressed from the array's start, a group's own rows from the tile's first
-        const rsrc_t rx = make_rsrc(p.x_src ? p.x : p.x + (size_t)c.r0 * p.x_ld,
-                                    p.x_src ? p.x_bytes : (uint32_t)(c.nrows - 1) * p.x_ld + (uint32_t)(p.K * EB));
+        R.qb = p.x_src ? p.x : p.x + (size_t)c.r0 * p.x_ld;
+        R.qn = p.x_src ? p.x_bytes : (uint32_t)(c.nrows - 1) * p.x_ld + (uint32_t)(p.K * EB);
+        const int first = q_first<NB>(w, half);
         #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int row = (BT / 4) * w + 8 * i + (lane >> 3);
-            const int kb = kbyte + 16 * ((lane & 7) ^ kc_swz(row));
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rx, (mm_lds_void_t*)(st + Geo::QOff + ((BT / 4) * w + 8 * i) * 128), 16,
-                kb < p.K * EB ? R.row[i] + (uint32_t)kb : kMmInvalid, 0, 0, 0);
-        }
-        if constexpr (EL == kElFp8) {
-            const rsrc_t rs = make_rsrc(p.x_src ? p.xs : p.xs + (size_t)c.r0 * p.kb,
-                                        p.x_src ? p.xs_bytes : (uint32_t)(c.nrows * p.kb * 4));
-            if (lane < BT / 4)          // only these lanes' 4 bytes are written
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rs, (mm_lds_void_t*)(st + Geo::SOff + (BT / 4) * w * 4), 4,
-                    R.srow + (uint32_t)(R.kt * 4), 0, 0, 0);
+        for (int i = 0; i < NQ; ++i) {
+            const int kb = R.kt * 128 + 16 * ((lane & 7) ^ ((lane >> 4) | (4 * (((first >> 3) + i) & 1))));
+            R.qo[i] = R.live && kb < p.K * EB ? R.row[i] + (uint32_t)kb : kMmInvalid;
         }
     }
-    ++R.step;
-    const int kt = R.kt + 1;
-    const bool last = kt == c.nk;
-    R.kt = last ? 0 : kt;
-    if (last) mm_open_item<EL, MODE, NB>(p, pass_off, wh, R);
-    if (R.live) mm_open_src<MODE>(p, wh, R);
+}
+
+// Request number I of the 4 of the a operand.
+template <int EL, int MODE, int NB, int I>
+MOE_DEV void mm_request_p(const MmP& p, const MmWhere& wh, const MmReq<NB / 4>& R, uint8_t* smem) {
+#if defined(__HIP_DEVICE_COMPILE__)          // the host pass has no buffer resources
+    using Geo = MmGeom<EL, NB>;
+    uint8_t* st = smem + (R.step % Geo::NST) * Geo::Stage;
+    const rsrc_t r = make_rsrc(R.pb, R.pn);
+    if constexpr (MODE == kMmNK)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void_t*)(st + (32 * wh.w + 8 * I) * 128), 16,
+                                                 R.po[I & 1] + (uint32_t)(8 * (I & 2)) * p.w_ld, 0, 0, 0);
+    else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void_t*)(st + (8 * wh.w + 2 * I) * 512), 16, R.po[I], 0, 0, 0);
+#endif
+}
+// Request number I of the NQ of one half of the b operand.
+template <int EL, int MODE, int NB, int I>
+MOE_DEV void mm_request_q(const MmP& p, const MmWhere& wh, const MmReq<NB / 4>& R, int half, uint8_t* smem) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    using Geo = MmGeom<EL, NB>;
+    uint8_t* st = smem + (R.step % Geo::NST) * Geo::Stage + Geo::QOff;
+    const rsrc_t r = make_rsrc(R.qb, R.qn);
+    if constexpr (is_wgrad(MODE))
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            r, (mm_lds_void_t*)(st + half * (kPBytes / 2) + (8 * wh.w + 4 * I) * 256), 16, R.qo[I], 0, 0, 0);
+    else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void_t*)(st + (q_first<NB>(wh.w, half) + 8 * I) * 128), 16,
+                                                 R.qo[I], 0, 0, 0);
+#endif
+}
+// fp8: the scales of this wave's rows of one half (the first 2 NB lanes; the
+// others clear the rest of the wave's 256 bytes)
+template <int EL, int NB, int NQ>
+MOE_DEV void mm_request_s(const MmP& p, const MmWhere& wh, const MmReq<NQ>& R, int half, uint8_t* smem) {
+#if defined(__HIP_DEVICE_COMPILE__)          // the host pass has no buffer resources
+    using Geo = MmGeom<EL, NB>;
+    const MmItem& c = R.c;
+    uint8_t* st = smem + (R.step % Geo::NST) * Geo::Stage;
+    const rsrc_t r = make_rsrc(p.x_src ? p.xs : p.xs + (size_t)c.r0 * p.kb,
+                               p.x_src ? p.xs_bytes : (uint32_t)(c.nrows * p.kb * 4));
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void_t*)(st + Geo::SOff + half * 2048 + wh.w * 256), 4,
+                                             R.live ? R.srow + (uint32_t)(R.kt * 4) : kMmInvalid, 0, 0, 0);
+#endif
+}
+// Requests of turn H: the a operand (turn 1), half 1 - H of the b operand, its scales.
+constexpr int mm_turn_p(int mode, int turn) { return turn == 1 && mode != kWgrad8 ? 4 : 0; }
+constexpr int mm_turn_requests(int el, int mode, int nb, int turn) {
+    return mm_turn_p(mode, turn) + nb / 4 + (el == kElFp8 ? 1 : 0);
+}
+// numbers [I0, I1) of them
+template <int EL, int MODE, int NB, int H, int I0, int I1, int NQ>
+MOE_DEV void mm_requests(const MmP& p, const MmWhere& wh, const MmReq<NQ>& R, uint8_t* smem) {
+    if constexpr (I0 < I1) {
+        constexpr int NP = mm_turn_p(MODE, H);
+        if constexpr (I0 < NP) mm_request_p<EL, MODE, NB, I0>(p, wh, R, smem);
+        else if constexpr (I0 < NP + NQ) mm_request_q<EL, MODE, NB, I0 - NP>(p, wh, R, 1 - H, smem);
+        else mm_request_s<EL, NB>(p, wh, R, 1 - H, smem);
+        mm_requests<EL, MODE, NB, H, I0 + 1, I1>(p, wh, R, smem);
+    }
 }
 
 // wgrad from 8-bit rows: the a operand passes through registers. Every wave
@@ -288,7 +309,7 @@ MOE_DEV void kept_open(const MmP& p, const MmWhere& wh, MmKept& X) {
     int item = X.item;
     bool live = false;
     while (item < wh.n_items && !live) {
-        X.c = mm_decode<kElBf16, kWgrad8, NB>(p, nullptr, wh.at, item);
+        X.c = mm_decode<kElBf16, kWgrad8, 32 * NB>(p, nullptr, wh.at, item);
         live = X.c.nk > 0;
         item += wh.grid;
     }
@@ -373,18 +394,7 @@ void grouped_mm_kernel(MmP p) {
     if constexpr (is_wgrad(MODE)) {
         n_items = p.G * at * ((p.N + BT - 1) / BT);
     } else {
-        if (w == 0) {
-            int run = 0;
-            for (int g0 = 0; g0 < p.G; g0 += 64) {
-                int lo = 0, hi = 0;
-                if (g0 + lane < p.G) group_rows(p, g0 + lane, lo, hi);
-                const int n = (hi - lo + BT - 1) / BT;
-                const int inc = wave_incl_scan(n);
-                if (g0 + lane < p.G) pass_off[g0 + lane] = run + inc - n;
-                run += __builtin_amdgcn_readlane(inc, 63);
-            }
-            if (lane == 0) pass_off[p.G] = run;
-        }
+        if (w == 0) mm_passes(p, BT, lane, pass_off);
         __syncthreads();
         n_items = __builtin_amdgcn_readfirstlane(pass_off[p.G]) * at;
     }
@@ -393,57 +403,62 @@ void grouped_mm_kernel(MmP p) {
     if (slot >= n_items) return;
 
     const MmWhere wh{n_items, at, grid, lane, w};
-    MmReq<NB> rq;                                            // waves 0-3
-    rq.item = slot;
 
     // ---------------------------------------------------------- fragments
-    // 16-bit: half h of a step is the K-tile's k-half; FP8 (whose instruction
-    // takes the whole K-tile): half h is the wave's b tiles [h NB/2, (h+1) NB/2)
-    constexpr int NS = EL == kElFp8 ? 2 : 1;                 // 16-byte pieces per fragment
-    constexpr int NU = EL == kElFp8 && NB > 1 ? NB / 2 : NB; // b tiles per half
-    constexpr int HALVES = EL == kElFp8 && NB == 1 ? 1 : 2;
-    i32x4 fp[NS][4], fq[NS][NU];
+    constexpr int NU = Geo::NU, NQ = Geo::NQ;
+    i32x4 fp[2][4], fq[2][NU];
     float fs[NU], fw = 0.f;
-    auto read_slow = [&](const uint8_t* st, int s, int c) __attribute__((always_inline)) {
+    // 8 k of one value (k = 32 s + 8 q ..) from rows of `rb` bytes: at o + k's row
+    auto read_slow = [&](const uint8_t* st, int o, int rb) __attribute__((always_inline)) {
         i32x4 v;
-        const int o = (32 * s + 8 * q + (j >> 2)) * 512 + ((c ^ ((j >> 2) | (q << 2))) * 32) + (j & 3) * 8;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_s16x4*)(st + o));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_s16x4*)(st + o + 4 * 512));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_s16x4*)(st + o + 4 * rb));
         const u32x2_t l = __builtin_bit_cast(u32x2_t, lo), h = __builtin_bit_cast(u32x2_t, hi);
         v[0] = (int)l.x; v[1] = (int)l.y; v[2] = (int)h.x; v[3] = (int)h.y;
         return v;
     };
-    auto read_frags = [&](int step, int h, const MmItem& c, int kt) __attribute__((always_inline)) {
+    auto read_frags = [&](int step, int turn, const MmItem& c, int kt) __attribute__((always_inline)) {
         const uint8_t* st = smem + (step % NST) * Geo::Stage;
         #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            const int ks = EL == kElFp8 ? s : h;
-            const int ch = ((4 * ks + q) ^ ((j >> 1) & 7)) * 16;
-            if (EL != kElFp8 || h == 0) {
+        for (int s = 0; s < 2; ++s) {
+            const int ch = ((4 * s + q) ^ ((j >> 1) & 7)) * 16;
+            const int k = 32 * s + 8 * q + (j >> 2);
+            if (turn == 0) {
                 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    if constexpr (P_TR) fp[s][t] = read_slow(st, ks, 4 * wi + t);
-                    else fp[s][t] = *(const i32x4*)(st + (64 * wi + 16 * t + j) * 128 + ch);
+                    if constexpr (P_TR)
+                        fp[s][t] = read_slow(st, k * 512 + ((4 * wi + t) ^ ((j >> 2) | (q << 2))) * 32 + (j & 3) * 8, 512);
+                    else
+                        fp[s][t] = *(const i32x4*)(st + (64 * wi + 16 * t + j) * 128 + ch);
                 }
             }
             #pragma unroll
             for (int u = 0; u < NU; ++u) {
-                const int uu = EL == kElFp8 ? h * NU + u : u;
-                if constexpr (Q_TR) fq[s][u] = read_slow(st + Geo::QOff, ks, NB * ti + uu);
-                else fq[s][u] = *(const i32x4*)(st + Geo::QOff + (16 * NB * ti + 16 * uu + j) * 128 + ch);
+                if constexpr (Q_TR)
+                    fq[s][u] = read_slow(st + Geo::QOff + turn * (kPBytes / 2),
+                                         k * 256 + ((4 * ti + u) ^ ((j >> 2) | ((q & 1) << 2))) * 32 + (j & 3) * 8, 256);
+                else
+                    fq[s][u] = *(const i32x4*)(st + Geo::QOff + (16 * NB * ti + 16 * (turn * NU + u) + j) * 128 + ch);
             }
         }
         if constexpr (EL == kElFp8) {
             #pragma unroll
             for (int u = 0; u < NU; ++u)
-                fs[u] = *(const float*)(st + Geo::SOff + (16 * NB * ti + 16 * (h * NU + u) + j) * 4);
-            if (h == 0) fw = p.ws[((size_t)c.g * p.nb + min((c.a0 + 64 * wi) >> 7, p.nb - 1)) * p.kb + kt];
+                fs[u] = *(const float*)(st + Geo::SOff + turn * 2048 +
+                                        (ti * 4 + (16 * u + j) / Geo::HRows) * 256 + ((16 * u + j) % Geo::HRows) * 4);
+            if (turn == 0) fw = p.ws[((size_t)c.g * p.nb + min((c.a0 + 64 * wi) >> 7, p.nb - 1)) * p.kb + kt];
         }
     };
 
     f32x4 acc[NB][4];
-    auto multiply = [&](auto half) __attribute__((always_inline)) {
-        constexpr int h = decltype(half)::value;
+    // ra: the a operand and the first half of the b operand; rb: the second half
+    MmReq<NQ> ra, rb;
+
+    // the products of one turn, with the turn's requests between them
+    auto multiply = [&](auto turn) __attribute__((always_inline)) {
+        constexpr int h = decltype(turn)::value;
+        constexpr int NR = mm_turn_requests(EL, MODE, NB, h);
+        MmReq<NQ>& R = h == 1 ? ra : rb;
         if constexpr (EL == kElFp8) {
             // the K-tile is one block of 128: its products go to cleared
             // registers and are added with the two scales' product, one b tile
@@ -453,19 +468,21 @@ void grouped_mm_kernel(MmP p) {
             // starts every product first and spills the accumulators.
             f32x4 d[2][4];
             float sc = 0.f;
-            #pragma unroll
-            for (int u = 0; u <= NU; ++u) {
-                if (u < NU)
+            static_for<NU + 1>([&](auto uu) __attribute__((always_inline)) {
+                constexpr int u = decltype(uu)::value;
+                if constexpr (u < NU) {
                     #pragma unroll
                     for (int t = 0; t < 4; ++t)
                         d[u & 1][t] = mfma_fp8(fp[0][t], fp[1][t], fq[0][u], fq[1][u], f32x4{0.f, 0.f, 0.f, 0.f});
-                if (u > 0) {
+                    mm_requests<EL, MODE, NB, h, (NR * u) / NU, (NR * (u + 1)) / NU>(p, wh, R, smem);
+                }
+                if constexpr (u > 0) {
                     f32x4* a = acc[h * NU + u - 1];
                     #pragma unroll
                     for (int t = 0; t < 4; ++t)
                         #pragma unroll
                         for (int v = 0; v < 4; ++v) a[t][v] = fmaf(d[(u - 1) & 1][t][v], sc, a[t][v]);
-                    if (u < NU) {
+                    if constexpr (u < NU) {
                         #pragma unroll
                         for (int t = 0; t < 4; ++t) {
                             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
@@ -474,18 +491,27 @@ void grouped_mm_kernel(MmP p) {
                     }
                     asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
                 }
-                if (u < NU) {
+                if constexpr (u < NU) {
                     sc = fs[u] * fw;
                     const f32x4* e = d[u & 1];
                     asm volatile("" : "+v"(sc) : "v"(e[0]), "v"(e[1]), "v"(e[2]), "v"(e[3]));
                 }
                 __builtin_amdgcn_sched_barrier(0);
-            }
+            });
         } else {
+            mm_requests<EL, MODE, NB, h, 0, NR>(p, wh, R, smem);
             #pragma unroll
-            for (int u = 0; u < NB; ++u)
+            for (int s = 0; s < 2; ++s)
                 #pragma unroll
-                for (int t = 0; t < 4; ++t) acc[u][t] = mfma16x16x32<EL>(fp[0][t], fq[0][u], acc[u][t]);
+                for (int u = 0; u < NU; ++u)
+                    #pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        acc[h * NU + u][t] = mfma16x16x32<EL>(fp[s][t], fq[s][u], acc[h * NU + u][t]);
+            #pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 8 * NU / (NR + 1), 0);
+                __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+            }
         }
     };
 
@@ -543,39 +569,65 @@ void grouped_mm_kernel(MmP p) {
         if (kept.held) kept_write(wh, kept, smem);
         if (kept.live) kept_load<NB>(p, wh, kept);
     }
-    if (lead) {
-        rq.step = rq.kt = 0;
-        mm_open_item<EL, MODE, NB>(p, pass_off, wh, rq);
-        if (rq.live) mm_open_src<MODE>(p, wh, rq);
-        #pragma unroll 1
-        for (int i = 0; i < NST - 1; ++i)
-            if (rq.live) mm_request<EL, MODE, NB>(p, pass_off, wh, rq, smem);
+    mm_start<EL, MODE, NB>(p, pass_off, wh, ra, 0, slot);
+    mm_start<EL, MODE, NB>(p, pass_off, wh, rb, 1, slot);
+    #pragma unroll 1
+    for (int i = 0; i < NST; ++i) {
+        mm_offsets<EL, MODE, NB>(p, wh, ra, 0);
+        mm_requests<EL, MODE, NB, 1, 0, mm_turn_requests(EL, MODE, NB, 1)>(p, wh, ra, smem);
+        if (i < NST - 1) mm_advance<EL, MODE, NB>(p, pass_off, wh, ra, 0);
+    }
+    #pragma unroll 1
+    for (int i = 0; i < NST - 1; ++i) {
+        mm_offsets<EL, MODE, NB>(p, wh, rb, 1);
+        mm_requests<EL, MODE, NB, 0, 0, mm_turn_requests(EL, MODE, NB, 0)>(p, wh, rb, smem);
+        if (i < NST - 2) mm_advance<EL, MODE, NB>(p, pass_off, wh, rb, 1);
     }
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
     bare_barrier();
     if (!lead) bare_barrier();
+
+    // Turn 1 requests ra's K-tile NST ahead, turn 0 rb's NST - 1 ahead, both
+    // between the products. Waits: the newer requests left in flight when the
+    // ones that the next turn reads have landed. Waves 0-3 wait after their
+    // products, waves 4-7 (half a turn later, before this turn's requests) after
+    // their reads. Requests not counted (row sources, stores) only make a wait
+    // longer; once a stream has ended its requests still count.
+    constexpr int KEPT = MODE == kWgrad8 ? 8 : 0;            // requests of the 8-bit rows, one K-tile's in flight
+    constexpr int L1 = mm_turn_requests(EL, MODE, NB, 1), L2 = mm_turn_requests(EL, MODE, NB, 0);
+    auto wait_for = [&](auto n) __attribute__((always_inline)) {
+        constexpr int N = decltype(n)::value;
+        static_assert(N + KEPT < 64, "vmcnt");
+        if (MODE == kWgrad8 && !kept.live) __builtin_amdgcn_s_waitcnt(waitcnt_imm(N, 15));
+        else __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + KEPT, 15));
+    };
     int step = 0;
     for (int item = slot; item < n_items; item += grid) {
-        const MmItem c = mm_decode<EL, MODE, NB>(p, pass_off, at, item);
+        const MmItem c = mm_decode<EL, MODE, 32 * NB>(p, pass_off, at, item);
         clear();
         #pragma unroll 1
         for (int kt = 0; kt < c.nk; ++kt, ++step) {
-            if constexpr (MODE == kWgrad8) {
-                if (kept.held) kept_write(wh, kept, smem + (kept.step % NST) * Geo::Stage);
-                if (kept.live) kept_load<NB>(p, wh, kept);
-            }
-            if (lead && rq.live) mm_request<EL, MODE, NB>(p, pass_off, wh, rq, smem);
-            static_for<HALVES>([&](auto half) __attribute__((always_inline)) {
-                read_frags(step, decltype(half)::value, c, kt);
+            static_for<2>([&](auto turn) __attribute__((always_inline)) {
+                constexpr int h = decltype(turn)::value;
+                read_frags(step, h, c, kt);
+                if constexpr (MODE == kWgrad8 && h == 1) {
+                    if (kept.held) kept_write(wh, kept, smem + (kept.step % NST) * Geo::Stage);
+                    if (kept.live) kept_load<NB>(p, wh, kept);
+                }
+                if constexpr (h == 1) {
+                    mm_advance<EL, MODE, NB>(p, pass_off, wh, ra, 0);
+                    mm_offsets<EL, MODE, NB>(p, wh, ra, 0);
+                } else {
+                    mm_advance<EL, MODE, NB>(p, pass_off, wh, rb, 1);
+                    mm_offsets<EL, MODE, NB>(p, wh, rb, 1);
+                }
                 __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+                if (!lead) wait_for(std::integral_constant<int, h ? (NST - 2) * L1 + (NST - 1) * L2 : (NST - 1) * L1 + (NST - 2) * L2>{});
                 bare_barrier();
                 __builtin_amdgcn_s_setprio(1);
-                multiply(half);
+                multiply(turn);
                 __builtin_amdgcn_s_setprio(0);
-                if (lead && decltype(half)::value == HALVES - 1) {      // the next step's K-tile has landed
-                    if (rq.live) __builtin_amdgcn_s_waitcnt(waitcnt_imm(Geo::Loads * (NST - 2), 15));
-                    else __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
-                }
+                if (lead) wait_for(std::integral_constant<int, (NST - 1) * (L1 + L2)>{});
                 bare_barrier();
             });
         }
@@ -611,17 +663,14 @@ int launch_mm(const MmP& p, int max_items, hipStream_t stream) {
 }
 
 // launchers
+// Tile height by the expected rows of a group: 256 from 129 on, 128 below, and
+// the kernels for few rows up to kRowsMax.
 template <int EL, int MODE>
-int launch_mm_rows(const MmP& p, hipStream_t stream) {
-    const int at = (p.N + kATile - 1) / kATile;
-    auto items = [&](int bt) {
-        return (int)std::min<int64_t>(((int64_t)p.R_max / bt + std::min(p.G, p.R_max)) * at, 1 << 30);
-    };
-    const int rows = (p.R_max + p.G - 1) / p.G;              // expected rows of a group
-    if (rows > 128) return launch_mm<EL, MODE, 8>(p, items(256), stream);
-    if (rows > 64) return launch_mm<EL, MODE, 4>(p, items(128), stream);
-    if (rows > 32) return launch_mm<EL, MODE, 2>(p, items(64), stream);
-    return launch_mm<EL, MODE, 1>(p, items(32), stream);
+int launch_mm_rows(const MmP& p, int kind, hipStream_t stream) {
+    const int rows = (p.R_max + p.G - 1) / p.G;
+    if (rows <= 64) return moe_launch_mm_rows(&p, EL, kind, stream);
+    return rows > 128 ? launch_mm<EL, MODE, 8>(p, mm_items(p, 256), stream)
+                      : launch_mm<EL, MODE, 4>(p, mm_items(p, 128), stream);
 }
 
 }  // namespace
@@ -666,8 +715,9 @@ int moe_launch_mm(const MmCall& c, hipStream_t stream) {
         p.kb = (c.K + 127) / 128; p.nb = (c.N + 127) / 128;
         p.xs = c.xs; p.ws = c.wscale;
         if (c.x_src) p.xs_bytes = (uint32_t)((int64_t)c.x_rows * p.kb * 4);
-        return launch_mm_rows<kElFp8, kMmNK>(p, stream);
+        return launch_mm_rows<kElFp8, kMmNK>(p, 0, stream);
     }
-    if (c.kind == 0) return f16 ? launch_mm_rows<kElF16, kMmNK>(p, stream) : launch_mm_rows<kElBf16, kMmNK>(p, stream);
-    return f16 ? launch_mm_rows<kElF16, kMmKN>(p, stream) : launch_mm_rows<kElBf16, kMmKN>(p, stream);
+    if (c.kind == 0)
+        return f16 ? launch_mm_rows<kElF16, kMmNK>(p, 0, stream) : launch_mm_rows<kElBf16, kMmNK>(p, 0, stream);
+    return f16 ? launch_mm_rows<kElF16, kMmKN>(p, 1, stream) : launch_mm_rows<kElBf16, kMmKN>(p, 1, stream);
 }

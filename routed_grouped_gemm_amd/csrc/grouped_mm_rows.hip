@@ -1,0 +1,245 @@
+// Grouped products (see grouped_mm.hip) for few rows per group, where the
+// weights' bytes bound the call: every weight is read once per pass of BT rows.
+//
+// A workgroup of 4 waves computes 64 values of the a axis (n) for 32 or 64
+// rows; wave w owns 16 of the 64 and all rows. 64, not 256: a decode batch on
+// a few experts then gives about as many work items as two workgroups per CU
+// take at once (8 groups of N = 4096: 512), and the K loop needs no split.
+// K-tiles (64 x 128 bytes of weights, BT x 128 bytes of rows) are staged in
+// LDS by loads that write it directly, through a ring of NST stages, so that
+// about 40 KB of weights per workgroup are on their way; one barrier per
+// K-tile. Layouts and swizzles as in grouped_mm.hip.
+#include <algorithm>
+
+#include "grouped_mm.h"
+
+namespace {
+
+constexpr int kRowsThreads = 256;
+constexpr int kRowsA = 64;
+
+template <int EL, int NB>
+struct RowsGeom {
+    static constexpr int BT = 16 * NB;
+    static constexpr int NQ = BT / 32;                       // requests of a wave for the rows
+    static constexpr int QOff = kRowsA * 128;
+    static constexpr int SOff = QOff + BT * 128;             // fp8: row scales, 256 bytes per wave
+    static constexpr int Stage = SOff + (EL == kElFp8 ? 1024 : 0);
+    static constexpr int NST = (kMmLds / 2 - 4096) / Stage;  // two workgroups per CU
+    static constexpr int Loads = 2 + NQ + (EL == kElFp8 ? 1 : 0);
+};
+
+// the requests of a wave, one K-tile after another through all items
+template <int NQ>
+struct RowsReq {
+    int item, kt, step;
+    bool live;
+    MmItem c;
+    uint32_t row[NQ], srow;
+};
+
+template <int EL, int MODE, int NB, int NQ>
+MOE_DEV void rows_open(const MmP& p, const int* pass_off, const MmWhere& wh, RowsReq<NQ>& R) {
+    constexpr int BT = 16 * NB;
+    R.live = R.item < wh.n_items;
+    if (!R.live) return;
+    R.c = mm_scalar(mm_decode<EL, MODE, BT, kRowsA>(p, pass_off, wh.at, R.item));
+    R.item += wh.grid;
+    // source rows without a branch: past the item (and without a source
+    // array, whose resource is then empty) the loads return 0
+    const rsrc_t rm = make_rsrc(p.x_src + R.c.r0, p.x_src ? (uint32_t)(R.c.nrows * 4) : 0u);
+    const int first = (BT / 4) * wh.w;
+    #pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int row = first + 8 * i + (wh.lane >> 3);
+        const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, row * 4, 0, 0);
+        R.row[i] = row < R.c.nrows && s < p.x_rows ? (p.x_src ? s : (uint32_t)row) * p.x_ld : kMmNoRow;
+    }
+    if constexpr (EL == kElFp8) {
+        const int row = first + wh.lane;
+        const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, row * 4, 0, 0);
+        R.srow = wh.lane < BT / 4 && row < R.c.nrows && s < p.x_rows ? (p.x_src ? s : (uint32_t)row) * (uint32_t)(p.kb * 4)
+                                                                    : kMmNoRow;
+    }
+}
+
+// request one K-tile into its stage, then move on (nothing once the items have ended)
+template <int EL, int MODE, int NB, int NQ>
+MOE_DEV void rows_request(const MmP& p, const int* pass_off, const MmWhere& wh, RowsReq<NQ>& R, uint8_t* smem) {
+    using Geo = RowsGeom<EL, NB>;
+    constexpr int EB = EL == kElFp8 ? 1 : 2, BT = Geo::BT;
+    if (!R.live) return;
+    const int lane = mm_fresh(wh.lane), w = wh.w;
+    const MmItem& c = R.c;
+    uint8_t* st = smem + (R.step % Geo::NST) * Geo::Stage;
+    if constexpr (MODE == kMmNK) {
+        const rsrc_t r = make_rsrc(p.w + (size_t)c.g * p.w_group + (size_t)c.a0 * p.w_ld,
+                                   (uint32_t)min(kRowsA, p.N - c.a0) * p.w_ld);
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int kb = R.kt * 128 + 16 * ((lane & 7) ^ ((lane >> 4) | (4 * i)));
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                r, (mm_lds_void_t*)(st + (16 * w + 8 * i) * 128), 16,
+                kb < p.K * EB ? (uint32_t)(16 * w + 8 * i + (lane >> 3)) * p.w_ld + (uint32_t)kb : kMmInvalid, 0, 0, 0);
+        }
+    } else {
+        const int krem = p.K - R.kt * 64;
+        const rsrc_t r = make_rsrc(p.w + (size_t)c.g * p.w_group + (size_t)R.kt * 64 * p.w_ld + (size_t)c.a0 * 2,
+                                   (uint32_t)(min(krem, 64) - 1) * p.w_ld + (uint32_t)(min(kRowsA, p.N - c.a0) * 2));
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int k = 16 * w + 8 * i + (lane >> 3);
+            const int col = (((lane & 7) >> 1) ^ (k & 3)) * 16 + (lane & 1) * 8;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                r, (mm_lds_void_t*)(st + (16 * w + 8 * i) * 128), 16,
+                k < krem && c.a0 + col < p.N ? (uint32_t)k * p.w_ld + (uint32_t)(col * 2) : kMmInvalid, 0, 0, 0);
+        }
+    }
+    // gathered rows are addressed from the array's start, a group's own rows from the tile's first
+    const rsrc_t rx = make_rsrc(p.x_src ? p.x : p.x + (size_t)c.r0 * p.x_ld,
+                                p.x_src ? p.x_bytes : (uint32_t)(c.nrows - 1) * p.x_ld + (uint32_t)(p.K * EB));
+    const int first = (BT / 4) * w;
+    #pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int kb = R.kt * 128 + 16 * ((lane & 7) ^ ((lane >> 4) | (4 * (((first >> 3) + i) & 1))));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (mm_lds_void_t*)(st + Geo::QOff + (first + 8 * i) * 128), 16,
+                                                 kb < p.K * EB ? R.row[i] + (uint32_t)kb : kMmInvalid, 0, 0, 0);
+    }
+    if constexpr (EL == kElFp8) {
+        const rsrc_t rs = make_rsrc(p.x_src ? p.xs : p.xs + (size_t)c.r0 * p.kb,
+                                    p.x_src ? p.xs_bytes : (uint32_t)(c.nrows * p.kb * 4));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (mm_lds_void_t*)(st + Geo::SOff + w * 256), 4,
+                                                 R.srow + (uint32_t)(R.kt * 4), 0, 0, 0);
+    }
+    ++R.step;
+    const int kt = R.kt + 1;
+    const bool last = kt == c.nk;
+    R.kt = last ? 0 : kt;
+    if (last) rows_open<EL, MODE, NB>(p, pass_off, wh, R);
+}
+
+template <int EL, int MODE, int NB>
+__global__ __launch_bounds__(kRowsThreads, 2)
+void grouped_mm_rows_kernel(MmP p) {
+    using Geo = RowsGeom<EL, NB>;
+    constexpr int BT = Geo::BT, NST = Geo::NST;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    int* pass_off = (int*)(smem + NST * Geo::Stage);         // [G + 1] passes before group g
+
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int q = lane >> 4, j = lane & 15;
+    const int at = (p.N + kRowsA - 1) / kRowsA;
+    if (w == 0) mm_passes(p, BT, lane, pass_off);
+    __syncthreads();
+    const int n_items = __builtin_amdgcn_readfirstlane(pass_off[p.G]) * at;
+    const int grid = gridDim.x;
+    const int slot = (grid % 8 == 0) ? (blockIdx.x % 8) * (grid / 8) + blockIdx.x / 8 : blockIdx.x;
+    if (slot >= n_items) return;
+    const MmWhere wh{n_items, at, grid, lane, w};
+
+    RowsReq<Geo::NQ> R;
+    R.item = slot;
+    R.kt = R.step = 0;
+    rows_open<EL, MODE, NB>(p, pass_off, wh, R);
+    #pragma unroll 1
+    for (int i = 0; i < NST - 1; ++i) rows_request<EL, MODE, NB>(p, pass_off, wh, R, smem);
+
+    int step = 0;
+    for (int item = slot; item < n_items; item += grid) {
+        const MmItem c = mm_scalar(mm_decode<EL, MODE, BT, kRowsA>(p, pass_off, at, item));
+        const float* ws = EL == kElFp8 ? p.ws + ((size_t)c.g * p.nb + (c.a0 >> 7)) * p.kb : nullptr;
+        f32x4 acc[NB];
+        #pragma unroll
+        for (int u = 0; u < NB; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        #pragma unroll 1
+        for (int kt = 0; kt < c.nk; ++kt, ++step) {
+            // this K-tile has landed (newer ones stay in flight), and behind
+            // the barrier the previous one has been read: its stage is free
+            if (R.live) __builtin_amdgcn_s_waitcnt(waitcnt_imm(Geo::Loads * (NST - 2), 15));
+            else __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+            bare_barrier();
+            rows_request<EL, MODE, NB>(p, pass_off, wh, R, smem);
+            const uint8_t* st = smem + (step % NST) * Geo::Stage;
+            i32x4 fp[2], fq[2][NB];
+            float fs[NB], fw = 0.f;
+            #pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int ch = ((4 * s + q) ^ ((j >> 1) & 7)) * 16;
+                if constexpr (MODE == kMmNK) {
+                    fp[s] = *(const i32x4*)(st + (16 * w + j) * 128 + ch);
+                } else {
+                    const int o = (32 * s + 8 * q + (j >> 2)) * 128 + ((w ^ (j >> 2)) * 32) + (j & 3) * 8;
+                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_s16x4*)(st + o));
+                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_s16x4*)(st + o + 4 * 128));
+                    const u32x2_t l = __builtin_bit_cast(u32x2_t, lo), hh = __builtin_bit_cast(u32x2_t, hi);
+                    fp[s] = i32x4{(int)l.x, (int)l.y, (int)hh.x, (int)hh.y};
+                }
+                #pragma unroll
+                for (int u = 0; u < NB; ++u) fq[s][u] = *(const i32x4*)(st + Geo::QOff + (16 * u + j) * 128 + ch);
+            }
+            if constexpr (EL == kElFp8) {
+                #pragma unroll
+                for (int u = 0; u < NB; ++u)
+                    fs[u] = *(const float*)(st + Geo::SOff + ((16 * u + j) / (BT / 4)) * 256 + ((16 * u + j) % (BT / 4)) * 4);
+                fw = ws[kt];
+                #pragma unroll
+                for (int u = 0; u < NB; ++u) {
+                    const f32x4 d = mfma_fp8(fp[0], fp[1], fq[0][u], fq[1][u], f32x4{0.f, 0.f, 0.f, 0.f});
+                    const float sc = fs[u] * fw;
+                    #pragma unroll
+                    for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(d[v], sc, acc[u][v]);
+                }
+            } else {
+                #pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    #pragma unroll
+                    for (int u = 0; u < NB; ++u) acc[u] = mfma16x16x32<EL>(fp[s], fq[s][u], acc[u]);
+            }
+            // the reads of this stage end here, before the next barrier
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+        }
+        const int a = c.a0 + 16 * w + 4 * q;
+        const int f16 = EL == kElFp8 ? p.out_f16 : EL == kElF16;
+        #pragma unroll
+        for (int u = 0; u < NB; ++u) {
+            const int b = 16 * u + j;
+            if (b < c.nrows && a < p.N)
+                *(u32x2_t*)((uint16_t*)p.out + (size_t)(c.r0 + b) * p.out_ld + a) =
+                    u32x2_t{pack16(acc[u][0], acc[u][1], f16), pack16(acc[u][2], acc[u][3], f16)};
+        }
+    }
+}
+
+template <int EL, int MODE, int NB>
+int launch_rows(const MmP& p, hipStream_t stream) {
+    using Geo = RowsGeom<EL, NB>;
+    auto* k = &grouped_mm_rows_kernel<EL, MODE, NB>;
+    static bool ready[64] = {false};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return (int)e;
+    if (dev < 0 || dev >= 64 || !ready[dev]) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, kMmLds);
+        if (e != hipSuccess) return (int)e;
+        if (dev >= 0 && dev < 64) ready[dev] = true;
+    }
+    const int grid = std::max(1, std::min(mm_items(p, Geo::BT, kRowsA), 2 * device_cu_count()));
+    k<<<grid, kRowsThreads, (size_t)(Geo::Stage * Geo::NST + (p.G + 1) * 4), stream>>>(p);
+    return (int)hipGetLastError();
+}
+
+template <int EL, int MODE>
+int launch_few(const MmP& p, hipStream_t stream) {
+    const int rows = (p.R_max + p.G - 1) / p.G;
+    return rows > 32 ? launch_rows<EL, MODE, 4>(p, stream) : launch_rows<EL, MODE, 2>(p, stream);
+}
+
+}  // namespace
+
+int moe_launch_mm_rows(const void* params, int el, int kind, hipStream_t stream) {
+    const MmP& p = *(const MmP*)params;
+    if (el == kElFp8) return launch_few<kElFp8, kMmNK>(p, stream);
+    if (el == kElF16) return kind ? launch_few<kElF16, kMmKN>(p, stream) : launch_few<kElF16, kMmNK>(p, stream);
+    return kind ? launch_few<kElBf16, kMmKN>(p, stream) : launch_few<kElBf16, kMmNK>(p, stream);
+}
