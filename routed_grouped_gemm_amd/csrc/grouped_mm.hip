@@ -61,15 +61,17 @@ struct MmGeom {
 
 // A stream of requests: the a operand with the first half of the b operand, or
 // the second half, one K-tile after another through all items. A wave takes an
-// eighth of each: 32 rows (contiguous form) or 8 k (slow form).
+// eighth of each: 32 rows (contiguous form) or 8 k (slow form). Row sources
+// are loaded an item (wgrad: a K-tile) before their use: waiting for one would
+// drain the requests in flight.
 template <int NQ>
 struct MmReq {
-    int item, kt, step;                 // item: the one to open after this
-    bool live;
-    MmItem c;
-    uint32_t row[NQ];                   // contiguous b operand: byte offsets of this lane's rows
-    uint32_t srow;                      // fp8: byte offset of this lane's row of scales
-    uint32_t psrc, qsrc;                // wgrad: byte offsets of the source rows of k, one k per lane % 8
+    int item, kt, step;                 // item: the one to look at after n
+    bool live, nlive;
+    MmItem c, n;                        // the item requested now, and the next one
+    uint32_t row[NQ], nrow[NQ];         // contiguous b operand: byte offsets of this lane's rows; next item's sources
+    uint32_t srow, nsrow;               // fp8: byte offset of this lane's row of scales; next item's source
+    uint32_t psrc, qsrc, npsrc, nqsrc;  // wgrad: source rows of the next K-tile's k, one k per lane % 8
     uint32_t po[4], qo[NQ];             // the next request's byte offsets,
     const uint8_t *pb, *qb;             // what they count from
     uint32_t pn, qn;                    // and the bytes that may be read there
@@ -79,78 +81,67 @@ struct MmReq {
 template <int NB>
 MOE_DEV int q_first(int w, int half) { return (w >> 2) * (16 * NB) + half * (8 * NB) + (w & 3) * (2 * NB); }
 
-// the next item with K-tiles, or none
+// wgrad: sources of this wave's 8 k of K-tile kt of item c (past the group: not looked at)
+template <int MODE>
+MOE_DEV void mm_load_src(const MmP& p, const MmWhere& wh, const MmItem& c, int kt, bool with_p, uint32_t& ps, uint32_t& qs) {
+    const int k = kt * 64 + 8 * wh.w + (wh.lane & 7);
+    if (MODE == kWgrad && with_p && p.x_src)
+        ps = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.x_src + c.r0, (uint32_t)(c.nrows * 4)), k * 4, 0, 0);
+    if (p.dy_src)
+        qs = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.dy_src + c.r0, (uint32_t)(c.nrows * 4)), k * 4, 0, 0);
+}
+
+// find the next item with K-tiles and load its row sources
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_open_item(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half) {
+MOE_DEV void mm_look(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half) {
     int item = R.item;
     bool live = false;
     while (item < wh.n_items && !live) {
-        R.c = mm_decode<EL, MODE, 32 * NB>(p, pass_off, wh.at, item);
-        live = R.c.nk > 0;
+        R.n = mm_decode<EL, MODE, 32 * NB>(p, pass_off, wh.at, item);
+        live = R.n.nk > 0;
         item += wh.grid;
     }
     R.item = item;
-    R.live = live;
+    R.nlive = live;
     if (!live) return;
-    R.c = mm_scalar(R.c);
-    if constexpr (!is_wgrad(MODE)) {
-        // source rows without a branch: past the item (and without a source
-        // array, whose resource is then empty) the loads return 0
-        const rsrc_t rm = make_rsrc(p.x_src + R.c.r0, p.x_src ? (uint32_t)(R.c.nrows * 4) : 0u);
+    R.n = mm_scalar(R.n);
+    if constexpr (is_wgrad(MODE)) {
+        mm_load_src<MODE>(p, wh, R.n, 0, half == 0, R.npsrc, R.nqsrc);
+    } else {
+        // without a branch: past the item (and without a source array, whose
+        // resource is then empty) the loads return 0
+        const rsrc_t rm = make_rsrc(p.x_src + R.n.r0, p.x_src ? (uint32_t)(R.n.nrows * 4) : 0u);
+        const int first = q_first<NB>(wh.w, half);
+        #pragma unroll
+        for (int i = 0; i < NQ; ++i)
+            R.nrow[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, (first + 8 * i + (wh.lane >> 3)) * 4, 0, 0);
+        if constexpr (EL == kElFp8)
+            R.nsrow = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, (first + wh.lane) * 4, 0, 0);
+    }
+}
+// make the next item the one requested, and look for the one after
+template <int EL, int MODE, int NB, int NQ>
+MOE_DEV void mm_take(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half) {
+    R.live = R.nlive;
+    if (!R.live) return;
+    R.c = R.n;
+    if constexpr (is_wgrad(MODE)) {
+        R.psrc = R.npsrc;
+        R.qsrc = R.nqsrc;
+    } else {
         const int first = q_first<NB>(wh.w, half);
         #pragma unroll
         for (int i = 0; i < NQ; ++i) {
             const int row = first + 8 * i + (wh.lane >> 3);
-            const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, row * 4, 0, 0);
-            R.row[i] = row < R.c.nrows && s < p.x_rows ? (p.x_src ? s : (uint32_t)row) * p.x_ld : kMmNoRow;
+            R.row[i] = row < R.c.nrows && R.nrow[i] < p.x_rows ? (p.x_src ? R.nrow[i] : (uint32_t)row) * p.x_ld : kMmNoRow;
         }
         if constexpr (EL == kElFp8) {
             const int row = first + wh.lane;
-            const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, row * 4, 0, 0);
-            R.srow = wh.lane < 2 * NB && row < R.c.nrows && s < p.x_rows
-                         ? (p.x_src ? s : (uint32_t)row) * (uint32_t)(p.kb * 4) : kMmNoRow;
+            R.srow = wh.lane < 2 * NB && row < R.c.nrows && R.nsrow < p.x_rows
+                         ? (p.x_src ? R.nsrow : (uint32_t)row) * (uint32_t)(p.kb * 4) : kMmNoRow;
         }
     }
-}
-
-// wgrad: source rows of this wave's 8 k of the K-tile it requests next
-template <int MODE, int NQ>
-MOE_DEV void mm_open_src(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, bool with_p) {
-    const int k = R.kt * 64 + 8 * wh.w + (wh.lane & 7);      // past the group: row 0, never used
-    if constexpr (MODE == kWgrad) {
-        if (with_p) {
-            const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-                make_rsrc(p.x_src + R.c.r0, p.x_src ? (uint32_t)(R.c.nrows * 4) : 0u), k * 4, 0, 0);
-            R.psrc = s < p.x_rows ? s * p.x_ld : kMmNoRow;
-        }
-    }
-    const uint32_t s = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-        make_rsrc(p.dy_src + R.c.r0, p.dy_src ? (uint32_t)(R.c.nrows * 4) : 0u), k * 4, 0, 0);
-    R.qsrc = s < p.dy_rows ? s * p.dy_ld : kMmNoRow;
-}
-
-template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_start(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half, int slot) {
-    R.item = slot;
-    R.step = R.kt = 0;
-    mm_open_item<EL, MODE, NB>(p, pass_off, wh, R, half);
-    if constexpr (is_wgrad(MODE)) {
-        if (R.live) mm_open_src<MODE>(p, wh, R, half == 0);
-    }
-}
-
-// step past the K-tile just requested
-template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_advance(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half) {
-    ++R.step;
-    if (!R.live) return;
-    const int kt = R.kt + 1;
-    const bool last = kt == R.c.nk;
-    R.kt = last ? 0 : kt;
-    if (last) mm_open_item<EL, MODE, NB>(p, pass_off, wh, R, half);
-    if constexpr (is_wgrad(MODE)) {
-        if (R.live) mm_open_src<MODE>(p, wh, R, half == 0);
-    }
+    mm_look<EL, MODE, NB>(p, pass_off, wh, R, half);
 }
 
 // bounds a request to 64 rows of the slow form, or to a whole gathered array
@@ -162,14 +153,15 @@ MOE_DEV void mm_slow_bounds(const uint8_t*& base, uint32_t& bytes, uint32_t ld, 
     }
 }
 
-// Offsets of the next request (all past the resource once the items have
-// ended: such a request reads nothing and clears a stage nothing reads).
+// Offsets of a stream's next request (all past the resource once the items
+// have ended: such a request reads nothing and clears a stage nothing reads).
 // Slow form, RPI rows of LPR lanes each per request: k = 8 w + RPI i + lane / LPR.
 template <int COLS, int N>
-MOE_DEV void mm_slow_offsets(uint32_t (&o)[N], bool live, bool mapped, uint32_t src, uint32_t ld, int krem, int c0,
-                             int ncols, int half, int w, int lane) {
+MOE_DEV void mm_slow_offsets(uint32_t (&o)[N], bool live, bool mapped, uint32_t src, uint32_t rows, uint32_t ld, int krem,
+                             int c0, int ncols, int half, int w, int lane) {
     constexpr int RPI = 512 / COLS, LPR = 64 / RPI;
     const int kl = lane / LPR, p32 = (lane % LPR) >> 1;
+    const uint32_t so = src < rows && 8 * w + (lane & 7) < krem ? src * ld : kMmNoRow;
     #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int k = 8 * w + RPI * i + kl;
@@ -180,10 +172,13 @@ MOE_DEV void mm_slow_offsets(uint32_t (&o)[N], bool live, bool mapped, uint32_t 
             const int ch = p32 ^ tr_swz_half(k);
             col = (ch >> 2) * 128 + half * 64 + (ch & 3) * 16 + (lane & 1) * 8;
         }
-        const bool ok = live && k < krem && c0 + col < ncols;
-        uint32_t v = (uint32_t)k * ld + (uint32_t)(col * 2);
-        if (mapped) v = (uint32_t)__builtin_amdgcn_ds_bpermute((RPI * i + kl) * 4, (int)src) + (uint32_t)((c0 + col) * 2);
-        o[i] = ok ? v : kMmInvalid;
+        const bool ok = live && c0 + col < ncols;
+        if (mapped) {
+            const uint32_t v = (uint32_t)__builtin_amdgcn_ds_bpermute((RPI * i + kl) * 4, (int)so) + (uint32_t)((c0 + col) * 2);
+            o[i] = ok ? v : kMmInvalid;
+        } else {
+            o[i] = ok && k < krem ? (uint32_t)k * ld + (uint32_t)(col * 2) : kMmInvalid;
+        }
     }
 }
 template <int EL, int MODE, int NB, int NQ>
@@ -193,42 +188,79 @@ MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, int half)
     const MmItem& c = R.c;
     if (half == 0) {
         if constexpr (MODE == kMmNK) {
-            R.pb = p.w + (size_t)c.g * p.w_group + (size_t)c.a0 * p.w_ld;
-            R.pn = (uint32_t)min(kATile, p.N - c.a0) * p.w_ld;
+            R.pb = p.w + (size_t)c.g * p.w_group + (size_t)c.a0 * p.w_ld + (size_t)(R.kt * 128);
+            R.pn = (uint32_t)min(kATile, p.N - c.a0) * p.w_ld - (uint32_t)(R.kt * 128);
             // requests i and i + 2 differ by 16 rows (added when issued); the
             // swizzle of row 32 w + 8 i + lane / 8 depends on i's parity alone
             #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int kb = R.kt * 128 + 16 * ((lane & 7) ^ ((lane >> 4) | (4 * h)));
-                R.po[h] = R.live && kb < p.K * EB ? (uint32_t)(32 * w + 8 * h + (lane >> 3)) * p.w_ld + (uint32_t)kb : 0x80000000u;
+                const int kb = 16 * ((lane & 7) ^ ((lane >> 4) | (4 * h)));
+                R.po[h] = R.live && R.kt * 128 + kb < p.K * EB
+                              ? (uint32_t)(32 * w + 8 * h + (lane >> 3)) * p.w_ld + (uint32_t)kb : 0x80000000u;
             }
         } else if constexpr (MODE == kMmKN) {
             R.pb = p.w + (size_t)c.g * p.w_group;
             mm_slow_bounds(R.pb, R.pn, p.w_ld, false, R.kt * 64, p.K - R.kt * 64, c.a0, p.N);
-            mm_slow_offsets<256>(R.po, R.live, false, 0, p.w_ld, p.K - R.kt * 64, c.a0, p.N, 0, w, lane);
+            mm_slow_offsets<256>(R.po, R.live, false, 0, 0, p.w_ld, p.K - R.kt * 64, c.a0, p.N, 0, w, lane);
         } else if constexpr (MODE == kWgrad) {
             R.pb = p.x;
             R.pn = p.x_bytes;
             mm_slow_bounds(R.pb, R.pn, p.x_ld, p.x_src != nullptr, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.a0, p.K);
-            mm_slow_offsets<256>(R.po, R.live, p.x_src != nullptr, R.psrc, p.x_ld, c.nrows - R.kt * 64, c.a0, p.K, 0, w, lane);
+            mm_slow_offsets<256>(R.po, R.live, p.x_src != nullptr, R.psrc, p.x_rows, p.x_ld, c.nrows - R.kt * 64, c.a0,
+                                 p.K, 0, w, lane);
         }
     }
     if constexpr (is_wgrad(MODE)) {
         R.qb = p.dy;
         R.qn = p.dy_bytes;
         mm_slow_bounds(R.qb, R.qn, p.dy_ld, p.dy_src != nullptr, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.b0, p.N);
-        mm_slow_offsets<128>(R.qo, R.live, p.dy_src != nullptr, R.qsrc, p.dy_ld, c.nrows - R.kt * 64, c.b0, p.N, half, w, lane);
+        mm_slow_offsets<128>(R.qo, R.live, p.dy_src != nullptr, R.qsrc, p.dy_rows, p.dy_ld, c.nrows - R.kt * 64, c.b0, p.N,
+                             half, w, lane);
+        if (R.live && R.kt + 1 < c.nk) mm_load_src<MODE>(p, wh, c, R.kt + 1, half == 0, R.psrc, R.qsrc);
     } else {
         // gathered rows are addressed from the array's start, a group's own rows from the tile's first
-        R.qb = p.x_src ? p.x : p.x + (size_t)c.r0 * p.x_ld;
-        R.qn = p.x_src ? p.x_bytes : (uint32_t)(c.nrows - 1) * p.x_ld + (uint32_t)(p.K * EB);
+        R.qb = (p.x_src ? p.x : p.x + (size_t)c.r0 * p.x_ld) + (size_t)(R.kt * 128);
+        R.qn = (p.x_src ? p.x_bytes : (uint32_t)(c.nrows - 1) * p.x_ld + (uint32_t)(p.K * EB)) - (uint32_t)(R.kt * 128);
         const int first = q_first<NB>(w, half);
         #pragma unroll
         for (int i = 0; i < NQ; ++i) {
-            const int kb = R.kt * 128 + 16 * ((lane & 7) ^ ((lane >> 4) | (4 * (((first >> 3) + i) & 1))));
-            R.qo[i] = R.live && kb < p.K * EB ? R.row[i] + (uint32_t)kb : kMmInvalid;
+            const int kb = 16 * ((lane & 7) ^ ((lane >> 4) | (4 * (((first >> 3) + i) & 1))));
+            R.qo[i] = R.live && R.kt * 128 + kb < p.K * EB ? R.row[i] + (uint32_t)kb : kMmInvalid;
         }
     }
+}
+
+// Step past the K-tile just requested. Inside an item the offsets stay and
+// what they count from moves on (scalar additions); they are formed anew for
+// an item's first and last K-tile, and for every one of gathered wgrad rows.
+template <int EL, int MODE, int NB, int NQ>
+MOE_DEV void mm_advance(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half) {
+    ++R.step;
+    if (!R.live) return;
+    const int kt = R.kt + 1;
+    const bool last = kt == R.c.nk;
+    R.kt = last ? 0 : kt;
+    if (last) mm_take<EL, MODE, NB>(p, pass_off, wh, R, half);
+    if (last || kt == R.c.nk - 1 || (is_wgrad(MODE) && ((MODE == kWgrad && p.x_src) || p.dy_src))) {
+        mm_offsets<EL, MODE, NB>(p, wh, R, half);
+        return;
+    }
+    if (half == 0) {
+        if constexpr (MODE == kMmNK) { R.pb += 128; R.pn -= 128; }
+        else if constexpr (MODE == kMmKN) R.pb += (size_t)p.w_ld * 64;
+        else if constexpr (MODE == kWgrad) R.pb += (size_t)p.x_ld * 64;
+    }
+    if constexpr (is_wgrad(MODE)) R.qb += (size_t)p.dy_ld * 64;
+    else { R.qb += 128; R.qn -= 128; }
+}
+template <int EL, int MODE, int NB, int NQ>
+MOE_DEV void mm_start(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half, int slot) {
+    R.item = slot;
+    R.step = R.kt = 0;
+    R.c = MmItem{0, 0, 0, 0, 1, 1};
+    mm_look<EL, MODE, NB>(p, pass_off, wh, R, half);
+    mm_take<EL, MODE, NB>(p, pass_off, wh, R, half);
+    mm_offsets<EL, MODE, NB>(p, wh, R, half);
 }
 
 // Request number I of the 4 of the a operand.
@@ -573,13 +605,11 @@ void grouped_mm_kernel(MmP p) {
     mm_start<EL, MODE, NB>(p, pass_off, wh, rb, 1, slot);
     #pragma unroll 1
     for (int i = 0; i < NST; ++i) {
-        mm_offsets<EL, MODE, NB>(p, wh, ra, 0);
         mm_requests<EL, MODE, NB, 1, 0, mm_turn_requests(EL, MODE, NB, 1)>(p, wh, ra, smem);
         if (i < NST - 1) mm_advance<EL, MODE, NB>(p, pass_off, wh, ra, 0);
     }
     #pragma unroll 1
     for (int i = 0; i < NST - 1; ++i) {
-        mm_offsets<EL, MODE, NB>(p, wh, rb, 1);
         mm_requests<EL, MODE, NB, 0, 0, mm_turn_requests(EL, MODE, NB, 0)>(p, wh, rb, smem);
         if (i < NST - 2) mm_advance<EL, MODE, NB>(p, pass_off, wh, rb, 1);
     }
@@ -616,12 +646,12 @@ void grouped_mm_kernel(MmP p) {
                 }
                 if constexpr (h == 1) {
                     mm_advance<EL, MODE, NB>(p, pass_off, wh, ra, 0);
-                    mm_offsets<EL, MODE, NB>(p, wh, ra, 0);
                 } else {
                     mm_advance<EL, MODE, NB>(p, pass_off, wh, rb, 1);
-                    mm_offsets<EL, MODE, NB>(p, wh, rb, 1);
                 }
-                __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+                // the reads end before this wave's products and so a turn before
+                // the stage is requested again; only writes to LDS must be done here
+                if constexpr (MODE == kWgrad8) __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
                 if (!lead) wait_for(std::integral_constant<int, h ? (NST - 2) * L1 + (NST - 1) * L2 : (NST - 1) * L1 + (NST - 2) * L2>{});
                 bare_barrier();
                 __builtin_amdgcn_s_setprio(1);
