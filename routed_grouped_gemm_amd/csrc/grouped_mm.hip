@@ -174,19 +174,23 @@ MOE_DEV void mm_slow_offsets(uint32_t (&o)[N], bool live, bool mapped, uint32_t 
         }
         const bool ok = live && c0 + col < ncols;
         if (mapped) {
-            const uint32_t v = (uint32_t)__builtin_amdgcn_ds_bpermute((RPI * i + kl) * 4, (int)so) + (uint32_t)((c0 + col) * 2);
-            o[i] = ok ? v : kMmInvalid;
+            // (readlanes, not an LDS permute, which would wait behind the fragment reads)
+            uint32_t v = (uint32_t)__builtin_amdgcn_readlane((int)so, RPI * i);
+            #pragma unroll
+            for (int r = 1; r < RPI; ++r)
+                v = kl == r ? (uint32_t)__builtin_amdgcn_readlane((int)so, RPI * i + r) : v;
+            o[i] = ok ? v + (uint32_t)((c0 + col) * 2) : kMmInvalid;
         } else {
             o[i] = ok && k < krem ? (uint32_t)k * ld + (uint32_t)(col * 2) : kMmInvalid;
         }
     }
 }
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, int half) {
+MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, int half, bool for_p = true, bool for_q = true) {
     constexpr int EB = EL == kElFp8 ? 1 : 2;
     const int lane = mm_fresh(wh.lane), w = wh.w;
     const MmItem& c = R.c;
-    if (half == 0) {
+    if (half == 0 && for_p) {
         if constexpr (MODE == kMmNK) {
             R.pb = p.w + (size_t)c.g * p.w_group + (size_t)c.a0 * p.w_ld + (size_t)(R.kt * 128);
             R.pn = (uint32_t)min(kATile, p.N - c.a0) * p.w_ld - (uint32_t)(R.kt * 128);
@@ -210,13 +214,13 @@ MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, int half)
                                  p.K, 0, w, lane);
         }
     }
-    if constexpr (is_wgrad(MODE)) {
+    if (!for_q) {
+    } else if constexpr (is_wgrad(MODE)) {
         R.qb = p.dy;
         R.qn = p.dy_bytes;
         mm_slow_bounds(R.qb, R.qn, p.dy_ld, p.dy_src != nullptr, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.b0, p.N);
         mm_slow_offsets<128>(R.qo, R.live, p.dy_src != nullptr, R.qsrc, p.dy_rows, p.dy_ld, c.nrows - R.kt * 64, c.b0, p.N,
                              half, w, lane);
-        if (R.live && R.kt + 1 < c.nk) mm_load_src<MODE>(p, wh, c, R.kt + 1, half == 0, R.psrc, R.qsrc);
     } else {
         // gathered rows are addressed from the array's start, a group's own rows from the tile's first
         R.qb = (p.x_src ? p.x : p.x + (size_t)c.r0 * p.x_ld) + (size_t)(R.kt * 128);
@@ -241,17 +245,21 @@ MOE_DEV void mm_advance(const MmP& p, const int* pass_off, const MmWhere& wh, Mm
     const bool last = kt == R.c.nk;
     R.kt = last ? 0 : kt;
     if (last) mm_take<EL, MODE, NB>(p, pass_off, wh, R, half);
-    if (last || kt == R.c.nk - 1 || (is_wgrad(MODE) && ((MODE == kWgrad && p.x_src) || p.dy_src))) {
-        mm_offsets<EL, MODE, NB>(p, wh, R, half);
-        return;
-    }
-    if (half == 0) {
+    const bool edge = last || kt == R.c.nk - 1;
+    const bool anew_p = edge || (MODE == kWgrad && p.x_src), anew_q = edge || (is_wgrad(MODE) && p.dy_src);
+    if (anew_p || anew_q) mm_offsets<EL, MODE, NB>(p, wh, R, half, anew_p, anew_q);
+    if (half == 0 && !anew_p) {
         if constexpr (MODE == kMmNK) { R.pb += 128; R.pn -= 128; }
         else if constexpr (MODE == kMmKN) R.pb += (size_t)p.w_ld * 64;
         else if constexpr (MODE == kWgrad) R.pb += (size_t)p.x_ld * 64;
     }
-    if constexpr (is_wgrad(MODE)) R.qb += (size_t)p.dy_ld * 64;
-    else { R.qb += 128; R.qn -= 128; }
+    if (!anew_q) {
+        if constexpr (is_wgrad(MODE)) R.qb += (size_t)p.dy_ld * 64;
+        else { R.qb += 128; R.qn -= 128; }
+    }
+    if constexpr (is_wgrad(MODE)) {
+        if (R.live && R.kt + 1 < R.c.nk) mm_load_src<MODE>(p, wh, R.c, R.kt + 1, half == 0, R.psrc, R.qsrc);
+    }
 }
 template <int EL, int MODE, int NB, int NQ>
 MOE_DEV void mm_start(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half, int slot) {
@@ -261,6 +269,9 @@ MOE_DEV void mm_start(const MmP& p, const int* pass_off, const MmWhere& wh, MmRe
     mm_look<EL, MODE, NB>(p, pass_off, wh, R, half);
     mm_take<EL, MODE, NB>(p, pass_off, wh, R, half);
     mm_offsets<EL, MODE, NB>(p, wh, R, half);
+    if constexpr (is_wgrad(MODE)) {
+        if (R.live && R.c.nk > 1) mm_load_src<MODE>(p, wh, R.c, 1, half == 0, R.psrc, R.qsrc);
+    }
 }
 
 // Request number I of the 4 of the a operand.
@@ -553,39 +564,44 @@ void grouped_mm_kernel(MmP p) {
             #pragma unroll
             for (int t = 0; t < 4; ++t) acc[u][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     };
-    // sums stay in 32 bits until here: the one rounding to the output's type
+    // Sums stay in 32 bits until here: the one rounding to the output's type.
+    // Every lane stores, past an edge outside the resource (dropped), so a wave
+    // always issues 4 NB stores and the next K-tile's waits can leave them in
+    // flight.
     auto store = [&](const MmItem& c, auto f16_) __attribute__((always_inline)) {
         constexpr int f16 = decltype(f16_)::value;
+        const int es = is_wgrad(MODE) && p.out_f32 ? 4 : 2;
+        const size_t ld = is_wgrad(MODE) ? (size_t)p.K : p.out_ld;
+        const size_t row0 = is_wgrad(MODE) ? (size_t)c.g * p.N + c.b0 : (size_t)c.r0;
+        const int rows = is_wgrad(MODE) ? min(BT, p.N - c.b0) : c.nrows, cols = min(kATile, na - c.a0);
+        const rsrc_t r = make_rsrc(p.out + (row0 * ld + c.a0) * es, (uint32_t)(((size_t)(rows - 1) * ld + cols) * es));
+        // rows past the tile's are past the resource by themselves; values past
+        // the operand's end (a partial tile only) are sent there
+        const int fresh = mm_fresh(lane), a0 = 64 * wi + 4 * (fresh >> 4);
+        uint32_t o = (uint32_t)((16 * NB * ti + (fresh & 15)) * (int)ld + a0) * (uint32_t)es;
         #pragma unroll
         for (int u = 0; u < NB; ++u) {
-            const int b = 16 * NB * ti + 16 * u + j;
             #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const int a = c.a0 + 64 * wi + 16 * t + 4 * q;
                 f32x4 v = acc[u][t];
-                if constexpr (is_wgrad(MODE)) {
-                    if (c.b0 + b < p.N && a < p.K) {
-                        const size_t o = ((size_t)c.g * p.N + c.b0 + b) * p.K + a;
-                        if (p.out_f32) {
-                            f32x4* d = (f32x4*)((float*)p.out + o);
-                            if (p.accumulate) { const f32x4 e = *d; v = f32x4{v[0] + e[0], v[1] + e[1], v[2] + e[2], v[3] + e[3]}; }
-                            *d = v;
-                        } else {
-                            u32x2_t* d = (u32x2_t*)((uint16_t*)p.out + o);
-                            if (p.accumulate) {
-                                const u32x2_t e = *d;
-                                v[0] += lo16(e.x, f16); v[1] += hi16(e.x, f16);
-                                v[2] += lo16(e.y, f16); v[3] += hi16(e.y, f16);
-                            }
-                            *d = u32x2_t{pack16(v[0], v[1], f16), pack16(v[2], v[3], f16)};
-                        }
+                const uint32_t ot = cols == kATile || a0 + 16 * t < cols ? o + (uint32_t)(16 * t * es) : kMmInvalid;
+                if (is_wgrad(MODE) && p.out_f32) {
+                    if (p.accumulate) {
+                        const f32x4 e = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, ot, 0, 0));
+                        v = f32x4{v[0] + e[0], v[1] + e[1], v[2] + e[2], v[3] + e[3]};
                     }
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), r, ot, 0, 0);
                 } else {
-                    if (b < c.nrows && a < p.N)
-                        *(u32x2_t*)((uint16_t*)p.out + (size_t)(c.r0 + b) * p.out_ld + a) =
-                            u32x2_t{pack16(v[0], v[1], f16), pack16(v[2], v[3], f16)};
+                    if (is_wgrad(MODE) && p.accumulate) {
+                        const u32x2_t e = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, ot, 0, 0));
+                        v[0] += lo16(e.x, f16); v[1] += hi16(e.x, f16);
+                        v[2] += lo16(e.y, f16); v[3] += hi16(e.y, f16);
+                    }
+                    __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{pack16(v[0], v[1], f16), pack16(v[2], v[3], f16)}, r, ot, 0, 0);
                 }
             }
+            o += (uint32_t)(16 * (int)ld * es);
+            asm volatile("" : "+v"(o));                      // one row of tiles at a time: no offsets kept for all
         }
     };
 
@@ -622,13 +638,17 @@ void grouped_mm_kernel(MmP p) {
     // ones that the next turn reads have landed. Waves 0-3 wait after their
     // products, waves 4-7 (half a turn later, before this turn's requests) after
     // their reads. Requests not counted (row sources, stores) only make a wait
-    // longer; once a stream has ended its requests still count.
+    // longer; once a stream has ended its requests still count. In the first
+    // NST - 1 K-tiles after an item's stores the requests waited for are older
+    // than the stores, which then count as newer.
     constexpr int KEPT = MODE == kWgrad8 ? 8 : 0;            // requests of the 8-bit rows, one K-tile's in flight
     constexpr int L1 = mm_turn_requests(EL, MODE, NB, 1), L2 = mm_turn_requests(EL, MODE, NB, 0);
+    int stored = 0;                                          // K-tiles whose waits leave the last stores in flight
     auto wait_for = [&](auto n) __attribute__((always_inline)) {
         constexpr int N = decltype(n)::value;
-        static_assert(N + KEPT < 64, "vmcnt");
+        static_assert(N + KEPT + 4 * NB < 64, "vmcnt");
         if (MODE == kWgrad8 && !kept.live) __builtin_amdgcn_s_waitcnt(waitcnt_imm(N, 15));
+        else if (stored > 0) __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + KEPT + 4 * NB, 15));
         else __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + KEPT, 15));
     };
     int step = 0;
@@ -660,7 +680,10 @@ void grouped_mm_kernel(MmP p) {
                 if (lead) wait_for(std::integral_constant<int, (NST - 1) * (L1 + L2)>{});
                 bare_barrier();
             });
+            --stored;
         }
+        // (an item without K-tiles stores between two others' stores: not counted)
+        stored = (is_wgrad(MODE) && (p.accumulate || c.nk == 0)) ? 0 : NST - 1;
         if (!is_wgrad(MODE) || c.nk > 0 || !p.accumulate) {
             if constexpr (EL == kElFp8) {
                 if (p.out_f16) store(c, std::integral_constant<int, 1>{});

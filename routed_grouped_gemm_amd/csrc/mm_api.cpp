@@ -18,6 +18,9 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 // last 4 MiB of which mark rows that are not there
 constexpr int64_t kGatherBytes = (1ll << 32) - (1ll << 22);
 
+// largest leading dimension: 256 rows of a tile stay below 2 GiB
+constexpr int32_t kMaxLd = 1 << 22;
+
 int32_t check_dims(int32_t R_max, int32_t N, int32_t K, int32_t G, int kmult) {
     if (R_max < 0 || G < 1 || G > MOE_MAX_EXPERTS + 1) return MOE_ERR_SHAPE;
     if (N < 8 || N % 8 || N > MOE_MM_MAX_DIM || K < kmult || K % kmult || K > MOE_MM_MAX_DIM) return MOE_ERR_SHAPE;
@@ -27,7 +30,7 @@ int32_t check_dims(int32_t R_max, int32_t N, int32_t K, int32_t G, int kmult) {
 // A row operand: [rows, cols] elements of eb bytes with leading dimension ld,
 // read whole rows at a time through `src` or directly by the R_max rows.
 int32_t check_rows(const void* p, int32_t rows, int32_t cols, int32_t ld, int eb, const int32_t* src, int32_t R_max) {
-    if (rows < 0 || ld < cols || ((int64_t)ld * eb) % 16 || ld > (1 << 22)) return MOE_ERR_SHAPE;
+    if (rows < 0 || ld < cols || ((int64_t)ld * eb) % 16 || ld > kMaxLd) return MOE_ERR_SHAPE;
     if (!src && rows < R_max) return MOE_ERR_SHAPE;
     if (src && R_max > 0 && rows < 1) return MOE_ERR_SHAPE;
     if (src && (int64_t)rows * ld * eb >= kGatherBytes) return MOE_ERR_SHAPE;
@@ -65,7 +68,7 @@ MOE_EXPORT int32_t moe_grouped_mm(const void* x, int32_t x_rows, int32_t ldx, co
     if (!t16(dtype) || (flags & ~MOE_MM_W_KN)) return MOE_ERR_UNSUPPORTED;
     int32_t st = check_dims(R_max, N, K, G, 8);
     if (st) return st;
-    if (ldy < N || ldy % 4) return MOE_ERR_SHAPE;
+    if (ldy < N || ldy % 4 || ldy > kMaxLd) return MOE_ERR_SHAPE;
     if ((st = check_rows(x, x_rows, K, ldx, 2, row_src, R_max))) return st;
     if (R_max == 0) return MOE_OK;
     if (!w || !offsets || !y) return MOE_ERR_NULL;
@@ -98,7 +101,7 @@ MOE_EXPORT int32_t moe_grouped_wgrad(const void* dy, int32_t dy_rows, int32_t ld
     if ((st = check_rows(dy, dy_rows, N, ld_dy, 2, dy_src, R_max))) return st;
     if (xs) {
         // 8-bit rows are read in pieces of 8 bytes
-        if (x_rows < 0 || ldx < K || ldx % 8 || ldx > (1 << 22)) return MOE_ERR_SHAPE;
+        if (x_rows < 0 || ldx < K || ldx % 8 || ldx > kMaxLd) return MOE_ERR_SHAPE;
         if (x_rows < (x_src ? (R_max > 0 ? 1 : 0) : R_max)) return MOE_ERR_SHAPE;
         if (x_src && (int64_t)x_rows * ldx >= kGatherBytes) return MOE_ERR_SHAPE;
         if (R_max > 0 && !x) return MOE_ERR_NULL;
@@ -155,7 +158,7 @@ MOE_EXPORT int32_t moe_grouped_mm_fp8(const uint8_t* xq, const float* xs, int32_
     if (!t16(dtype)) return MOE_ERR_UNSUPPORTED;
     int32_t st = check_dims(R_max, N, K, G, 16);
     if (st) return st;
-    if (ldy < N || ldy % 4) return MOE_ERR_SHAPE;
+    if (ldy < N || ldy % 4 || ldy > kMaxLd) return MOE_ERR_SHAPE;
     if ((st = check_rows(xq, x_rows, K, K, 1, row_src, R_max))) return st;
     if (R_max == 0) return MOE_OK;
     if (!xs || !wq || !wscale || !offsets || !y) return MOE_ERR_NULL;
