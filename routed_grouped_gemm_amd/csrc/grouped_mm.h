@@ -142,12 +142,16 @@ MOE_DEV MmItem mm_decode(const MmP& p, const int* pass_off, int at, int item) {
         c.g = __builtin_amdgcn_readfirstlane(item / (at * bt));
         l = item - c.g * (at * bt);
     } else {
-        int glo = 0, ghi = p.G;                              // largest g with pass_off[g] * at <= item
-        while (ghi - glo > 1) {
-            const int mid = (glo + ghi) >> 1;
-            if (pass_off[mid] * at <= item) glo = mid; else ghi = mid;
+        // groups whose first item is at or before this one, 64 at a time; the
+        // last of them (an empty group shares its first item with the next) is it
+        int n = 0;
+        for (int g0 = 0; g0 < p.G; g0 += 64) {
+            const int g = g0 + (int)(threadIdx.x & 63);
+            const int here = __builtin_popcountll(__ballot(g < p.G && pass_off[g] * at <= item));
+            n += here;
+            if (here < 64) break;
         }
-        c.g = __builtin_amdgcn_readfirstlane(glo);
+        c.g = __builtin_amdgcn_readfirstlane(n) - 1;
         const int first = __builtin_amdgcn_readfirstlane(pass_off[c.g]);
         bt = __builtin_amdgcn_readfirstlane(pass_off[c.g + 1]) - first;
         l = item - first * at;

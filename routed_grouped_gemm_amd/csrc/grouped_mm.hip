@@ -59,22 +59,24 @@ struct MmGeom {
     static constexpr int Lds(int G) { return Stage * NST + (G + 1) * 4; }
 };
 
-// A stream of requests: the a operand with the first half of the b operand, or
-// the second half, one K-tile after another through all items. A wave takes an
-// eighth of each: 32 rows (contiguous form) or 8 k (slow form). Row sources
-// are loaded an item (wgrad: a K-tile) before their use: waiting for one would
-// drain the requests in flight.
+// The requests of a wave: one K-tile after another through all items, an
+// eighth of each operand half: 32 or 2 NB rows (contiguous form) or 8 k (slow
+// form). Turn 1 moves on to a K-tile and requests its a operand and first b
+// half, the next turn 0 its second b half. Row sources are loaded an item
+// (wgrad: a K-tile) before their use: waiting for one would drain the requests
+// in flight.
 template <int NQ>
 struct MmReq {
     int item, kt, step;                 // item: the one to look at after n
+    int at, nat;                        // numbers of c and n
     bool live, nlive;
     MmItem c, n;                        // the item requested now, and the next one
-    uint32_t row[NQ], nrow[NQ];         // contiguous b operand: byte offsets of this lane's rows; next item's sources
-    uint32_t srow, nsrow;               // fp8: byte offset of this lane's row of scales; next item's source
+    uint32_t row[2][NQ], nrow[2][NQ];   // contiguous b operand: byte offsets of this lane's rows; next item's sources
+    uint32_t srow[2], nsrow[2];         // fp8: byte offset of this lane's row of scales; next item's source
     uint32_t psrc, qsrc, npsrc, nqsrc;  // wgrad: source rows of the next K-tile's k, one k per lane % 8
-    uint32_t po[4], qo[NQ];             // the next request's byte offsets,
-    const uint8_t *pb, *qb;             // what they count from
-    uint32_t pn, qn;                    // and the bytes that may be read there
+    uint32_t po[4], qo[2][NQ];          // the next request's byte offsets,
+    const uint8_t *pb, *qb, *sb;        // what they count from
+    uint32_t pn, qn, sn;                // and the bytes that may be read there
 };
 
 // first of the rows that wave w takes of half `half` of the b tile
@@ -83,9 +85,9 @@ MOE_DEV int q_first(int w, int half) { return (w >> 2) * (16 * NB) + half * (8 *
 
 // wgrad: sources of this wave's 8 k of K-tile kt of item c (past the group: not looked at)
 template <int MODE>
-MOE_DEV void mm_load_src(const MmP& p, const MmWhere& wh, const MmItem& c, int kt, bool with_p, uint32_t& ps, uint32_t& qs) {
+MOE_DEV void mm_load_src(const MmP& p, const MmWhere& wh, const MmItem& c, int kt, uint32_t& ps, uint32_t& qs) {
     const int k = kt * 64 + 8 * wh.w + (wh.lane & 7);
-    if (MODE == kWgrad && with_p && p.x_src)
+    if (MODE == kWgrad && p.x_src)
         ps = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.x_src + c.r0, (uint32_t)(c.nrows * 4)), k * 4, 0, 0);
     if (p.dy_src)
         qs = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.dy_src + c.r0, (uint32_t)(c.nrows * 4)), k * 4, 0, 0);
@@ -93,55 +95,64 @@ MOE_DEV void mm_load_src(const MmP& p, const MmWhere& wh, const MmItem& c, int k
 
 // find the next item with K-tiles and load its row sources
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_look(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half) {
+MOE_DEV void mm_look(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R) {
     int item = R.item;
     bool live = false;
     while (item < wh.n_items && !live) {
-        R.n = mm_decode<EL, MODE, 32 * NB>(p, pass_off, wh.at, item);
+        R.n = mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, pass_off, wh.at, item));
+        R.nat = item;
         live = R.n.nk > 0;
         item += wh.grid;
     }
     R.item = item;
     R.nlive = live;
     if (!live) return;
-    R.n = mm_scalar(R.n);
     if constexpr (is_wgrad(MODE)) {
-        mm_load_src<MODE>(p, wh, R.n, 0, half == 0, R.npsrc, R.nqsrc);
+        mm_load_src<MODE>(p, wh, R.n, 0, R.npsrc, R.nqsrc);
     } else {
         // without a branch: past the item (and without a source array, whose
         // resource is then empty) the loads return 0
         const rsrc_t rm = make_rsrc(p.x_src + R.n.r0, p.x_src ? (uint32_t)(R.n.nrows * 4) : 0u);
-        const int first = q_first<NB>(wh.w, half);
         #pragma unroll
-        for (int i = 0; i < NQ; ++i)
-            R.nrow[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, (first + 8 * i + (wh.lane >> 3)) * 4, 0, 0);
-        if constexpr (EL == kElFp8)
-            R.nsrow = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, (first + wh.lane) * 4, 0, 0);
+        for (int h = 0; h < 2; ++h) {
+            const int first = q_first<NB>(wh.w, h);
+            #pragma unroll
+            for (int i = 0; i < NQ; ++i)
+                R.nrow[h][i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, (first + 8 * i + (wh.lane >> 3)) * 4, 0, 0);
+            if constexpr (EL == kElFp8)
+                R.nsrow[h] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rm, (first + wh.lane) * 4, 0, 0);
+        }
     }
 }
 // make the next item the one requested, and look for the one after
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_take(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half) {
+MOE_DEV void mm_take(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R) {
     R.live = R.nlive;
     if (!R.live) return;
     R.c = R.n;
+    R.at = R.nat;
     if constexpr (is_wgrad(MODE)) {
         R.psrc = R.npsrc;
         R.qsrc = R.nqsrc;
     } else {
-        const int first = q_first<NB>(wh.w, half);
         #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            const int row = first + 8 * i + (wh.lane >> 3);
-            R.row[i] = row < R.c.nrows && R.nrow[i] < p.x_rows ? (p.x_src ? R.nrow[i] : (uint32_t)row) * p.x_ld : kMmNoRow;
-        }
-        if constexpr (EL == kElFp8) {
-            const int row = first + wh.lane;
-            R.srow = wh.lane < 2 * NB && row < R.c.nrows && R.nsrow < p.x_rows
-                         ? (p.x_src ? R.nsrow : (uint32_t)row) * (uint32_t)(p.kb * 4) : kMmNoRow;
+        for (int h = 0; h < 2; ++h) {
+            const int first = q_first<NB>(wh.w, h);
+            #pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const int row = first + 8 * i + (wh.lane >> 3);
+                const uint32_t s = R.nrow[h][i];
+                R.row[h][i] = row < R.c.nrows && s < p.x_rows ? (p.x_src ? s : (uint32_t)row) * p.x_ld : kMmNoRow;
+            }
+            if constexpr (EL == kElFp8) {
+                const int row = first + wh.lane;
+                const uint32_t s = R.nsrow[h];
+                R.srow[h] = wh.lane < 2 * NB && row < R.c.nrows && s < p.x_rows
+                                ? (p.x_src ? s : (uint32_t)row) * (uint32_t)(p.kb * 4) : kMmNoRow;
+            }
         }
     }
-    mm_look<EL, MODE, NB>(p, pass_off, wh, R, half);
+    mm_look<EL, MODE, NB>(p, pass_off, wh, R);
 }
 
 // bounds a request to 64 rows of the slow form, or to a whole gathered array
@@ -153,8 +164,8 @@ MOE_DEV void mm_slow_bounds(const uint8_t*& base, uint32_t& bytes, uint32_t ld, 
     }
 }
 
-// Offsets of a stream's next request (all past the resource once the items
-// have ended: such a request reads nothing and clears a stage nothing reads).
+// Offsets of the next request (all past the resource once the items have
+// ended: such a request reads nothing and clears a stage nothing reads).
 // Slow form, RPI rows of LPR lanes each per request: k = 8 w + RPI i + lane / LPR.
 template <int COLS, int N>
 MOE_DEV void mm_slow_offsets(uint32_t (&o)[N], bool live, bool mapped, uint32_t src, uint32_t rows, uint32_t ld, int krem,
@@ -186,11 +197,11 @@ MOE_DEV void mm_slow_offsets(uint32_t (&o)[N], bool live, bool mapped, uint32_t 
     }
 }
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, int half, bool for_p = true, bool for_q = true) {
+MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, bool for_p, bool for_q) {
     constexpr int EB = EL == kElFp8 ? 1 : 2;
     const int lane = mm_fresh(wh.lane), w = wh.w;
     const MmItem& c = R.c;
-    if (half == 0 && for_p) {
+    if (for_p) {
         if constexpr (MODE == kMmNK) {
             R.pb = p.w + (size_t)c.g * p.w_group + (size_t)c.a0 * p.w_ld + (size_t)(R.kt * 128);
             R.pn = (uint32_t)min(kATile, p.N - c.a0) * p.w_ld - (uint32_t)(R.kt * 128);
@@ -214,22 +225,31 @@ MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, int half,
                                  p.K, 0, w, lane);
         }
     }
-    if (!for_q) {
-    } else if constexpr (is_wgrad(MODE)) {
+    if (!for_q) return;
+    if constexpr (is_wgrad(MODE)) {
         R.qb = p.dy;
         R.qn = p.dy_bytes;
         mm_slow_bounds(R.qb, R.qn, p.dy_ld, p.dy_src != nullptr, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.b0, p.N);
-        mm_slow_offsets<128>(R.qo, R.live, p.dy_src != nullptr, R.qsrc, p.dy_rows, p.dy_ld, c.nrows - R.kt * 64, c.b0, p.N,
-                             half, w, lane);
+        #pragma unroll
+        for (int h = 0; h < 2; ++h)
+            mm_slow_offsets<128>(R.qo[h], R.live, p.dy_src != nullptr, R.qsrc, p.dy_rows, p.dy_ld, c.nrows - R.kt * 64,
+                                 c.b0, p.N, h, w, lane);
     } else {
         // gathered rows are addressed from the array's start, a group's own rows from the tile's first
         R.qb = (p.x_src ? p.x : p.x + (size_t)c.r0 * p.x_ld) + (size_t)(R.kt * 128);
         R.qn = (p.x_src ? p.x_bytes : (uint32_t)(c.nrows - 1) * p.x_ld + (uint32_t)(p.K * EB)) - (uint32_t)(R.kt * 128);
-        const int first = q_first<NB>(w, half);
         #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-            const int kb = 16 * ((lane & 7) ^ ((lane >> 4) | (4 * (((first >> 3) + i) & 1))));
-            R.qo[i] = R.live && R.kt * 128 + kb < p.K * EB ? R.row[i] + (uint32_t)kb : kMmInvalid;
+        for (int h = 0; h < 2; ++h) {
+            const int first = q_first<NB>(w, h);
+            #pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const int kb = 16 * ((lane & 7) ^ ((lane >> 4) | (4 * (((first >> 3) + i) & 1))));
+                R.qo[h][i] = R.live && R.kt * 128 + kb < p.K * EB ? R.row[h][i] + (uint32_t)kb : kMmInvalid;
+            }
+        }
+        if constexpr (EL == kElFp8) {
+            R.sb = (const uint8_t*)(p.x_src ? p.xs : p.xs + (size_t)c.r0 * p.kb) + R.kt * 4;
+            R.sn = R.live ? (p.x_src ? p.xs_bytes : (uint32_t)(c.nrows * p.kb * 4)) - (uint32_t)(R.kt * 4) : 0u;
         }
     }
 }
@@ -238,17 +258,17 @@ MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, int half,
 // what they count from moves on (scalar additions); they are formed anew for
 // an item's first and last K-tile, and for every one of gathered wgrad rows.
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_advance(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half) {
+MOE_DEV void mm_advance(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R) {
     ++R.step;
     if (!R.live) return;
     const int kt = R.kt + 1;
     const bool last = kt == R.c.nk;
     R.kt = last ? 0 : kt;
-    if (last) mm_take<EL, MODE, NB>(p, pass_off, wh, R, half);
+    if (last) mm_take<EL, MODE, NB>(p, pass_off, wh, R);
     const bool edge = last || kt == R.c.nk - 1;
     const bool anew_p = edge || (MODE == kWgrad && p.x_src), anew_q = edge || (is_wgrad(MODE) && p.dy_src);
-    if (anew_p || anew_q) mm_offsets<EL, MODE, NB>(p, wh, R, half, anew_p, anew_q);
-    if (half == 0 && !anew_p) {
+    if (anew_p || anew_q) mm_offsets<EL, MODE, NB>(p, wh, R, anew_p, anew_q);
+    if (!anew_p) {
         if constexpr (MODE == kMmNK) { R.pb += 128; R.pn -= 128; }
         else if constexpr (MODE == kMmKN) R.pb += (size_t)p.w_ld * 64;
         else if constexpr (MODE == kWgrad) R.pb += (size_t)p.x_ld * 64;
@@ -256,21 +276,23 @@ MOE_DEV void mm_advance(const MmP& p, const int* pass_off, const MmWhere& wh, Mm
     if (!anew_q) {
         if constexpr (is_wgrad(MODE)) R.qb += (size_t)p.dy_ld * 64;
         else { R.qb += 128; R.qn -= 128; }
+        if constexpr (EL == kElFp8) { R.sb += 4; R.sn -= 4; }
     }
     if constexpr (is_wgrad(MODE)) {
-        if (R.live && R.kt + 1 < R.c.nk) mm_load_src<MODE>(p, wh, R.c, R.kt + 1, half == 0, R.psrc, R.qsrc);
+        if (R.live && R.kt + 1 < R.c.nk) mm_load_src<MODE>(p, wh, R.c, R.kt + 1, R.psrc, R.qsrc);
     }
 }
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_start(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int half, int slot) {
+MOE_DEV void mm_start(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int slot) {
     R.item = slot;
     R.step = R.kt = 0;
     R.c = MmItem{0, 0, 0, 0, 1, 1};
-    mm_look<EL, MODE, NB>(p, pass_off, wh, R, half);
-    mm_take<EL, MODE, NB>(p, pass_off, wh, R, half);
-    mm_offsets<EL, MODE, NB>(p, wh, R, half);
+    R.at = -1;
+    mm_look<EL, MODE, NB>(p, pass_off, wh, R);
+    mm_take<EL, MODE, NB>(p, pass_off, wh, R);
+    mm_offsets<EL, MODE, NB>(p, wh, R, true, true);
     if constexpr (is_wgrad(MODE)) {
-        if (R.live && R.c.nk > 1) mm_load_src<MODE>(p, wh, R.c, 1, half == 0, R.psrc, R.qsrc);
+        if (R.live && R.c.nk > 1) mm_load_src<MODE>(p, wh, R.c, 1, R.psrc, R.qsrc);
     }
 }
 
@@ -289,32 +311,30 @@ MOE_DEV void mm_request_p(const MmP& p, const MmWhere& wh, const MmReq<NB / 4>& 
 #endif
 }
 // Request number I of the NQ of one half of the b operand.
-template <int EL, int MODE, int NB, int I>
-MOE_DEV void mm_request_q(const MmP& p, const MmWhere& wh, const MmReq<NB / 4>& R, int half, uint8_t* smem) {
+template <int EL, int MODE, int NB, int HALF, int I>
+MOE_DEV void mm_request_q(const MmWhere& wh, const MmReq<NB / 4>& R, uint8_t* smem) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using Geo = MmGeom<EL, NB>;
     uint8_t* st = smem + (R.step % Geo::NST) * Geo::Stage + Geo::QOff;
     const rsrc_t r = make_rsrc(R.qb, R.qn);
     if constexpr (is_wgrad(MODE))
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            r, (mm_lds_void_t*)(st + half * (kPBytes / 2) + (8 * wh.w + 4 * I) * 256), 16, R.qo[I], 0, 0, 0);
+            r, (mm_lds_void_t*)(st + HALF * (kPBytes / 2) + (8 * wh.w + 4 * I) * 256), 16, R.qo[HALF][I], 0, 0, 0);
     else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void_t*)(st + (q_first<NB>(wh.w, half) + 8 * I) * 128), 16,
-                                                 R.qo[I], 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void_t*)(st + (q_first<NB>(wh.w, HALF) + 8 * I) * 128), 16,
+                                                 R.qo[HALF][I], 0, 0, 0);
 #endif
 }
 // fp8: the scales of this wave's rows of one half (the first 2 NB lanes; the
 // others clear the rest of the wave's 256 bytes)
-template <int EL, int NB, int NQ>
-MOE_DEV void mm_request_s(const MmP& p, const MmWhere& wh, const MmReq<NQ>& R, int half, uint8_t* smem) {
-#if defined(__HIP_DEVICE_COMPILE__)          // the host pass has no buffer resources
+template <int EL, int NB, int HALF>
+MOE_DEV void mm_request_s(const MmWhere& wh, const MmReq<NB / 4>& R, uint8_t* smem) {
+#if defined(__HIP_DEVICE_COMPILE__)
     using Geo = MmGeom<EL, NB>;
-    const MmItem& c = R.c;
     uint8_t* st = smem + (R.step % Geo::NST) * Geo::Stage;
-    const rsrc_t r = make_rsrc(p.x_src ? p.xs : p.xs + (size_t)c.r0 * p.kb,
-                               p.x_src ? p.xs_bytes : (uint32_t)(c.nrows * p.kb * 4));
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void_t*)(st + Geo::SOff + half * 2048 + wh.w * 256), 4,
-                                             R.live ? R.srow + (uint32_t)(R.kt * 4) : kMmInvalid, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(R.sb, R.sn),
+                                             (mm_lds_void_t*)(st + Geo::SOff + HALF * 2048 + wh.w * 256), 4, R.srow[HALF],
+                                             0, 0, 0);
 #endif
 }
 // Requests of turn H: the a operand (turn 1), half 1 - H of the b operand, its scales.
@@ -328,8 +348,8 @@ MOE_DEV void mm_requests(const MmP& p, const MmWhere& wh, const MmReq<NQ>& R, ui
     if constexpr (I0 < I1) {
         constexpr int NP = mm_turn_p(MODE, H);
         if constexpr (I0 < NP) mm_request_p<EL, MODE, NB, I0>(p, wh, R, smem);
-        else if constexpr (I0 < NP + NQ) mm_request_q<EL, MODE, NB, I0 - NP>(p, wh, R, 1 - H, smem);
-        else mm_request_s<EL, NB>(p, wh, R, 1 - H, smem);
+        else if constexpr (I0 < NP + NQ) mm_request_q<EL, MODE, NB, 1 - H, I0 - NP>(wh, R, smem);
+        else mm_request_s<EL, NB, 1 - H>(wh, R, smem);
         mm_requests<EL, MODE, NB, H, I0 + 1, I1>(p, wh, R, smem);
     }
 }
@@ -451,6 +471,11 @@ void grouped_mm_kernel(MmP p) {
     constexpr int NU = Geo::NU, NQ = Geo::NQ;
     i32x4 fp[2][4], fq[2][NU];
     float fs[NU], fw = 0.f;
+    uint32_t fwv = 0, fwn = 0;          // fp8: weight scales of this item's and the next item's K-tiles
+    auto load_fw = [&](const MmItem& c, int kt) __attribute__((always_inline)) {
+        const float* ws = p.ws + ((size_t)c.g * p.nb + min((c.a0 + 64 * wi) >> 7, p.nb - 1)) * p.kb;
+        return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(make_rsrc(ws, (uint32_t)(p.kb * 4)), (kt + lane) * 4, 0, 0);
+    };
     // 8 k of one value (k = 32 s + 8 q ..) from rows of `rb` bytes: at o + k's row
     auto read_slow = [&](const uint8_t* st, int o, int rb) __attribute__((always_inline)) {
         i32x4 v;
@@ -489,56 +514,54 @@ void grouped_mm_kernel(MmP p) {
             for (int u = 0; u < NU; ++u)
                 fs[u] = *(const float*)(st + Geo::SOff + turn * 2048 +
                                         (ti * 4 + (16 * u + j) / Geo::HRows) * 256 + ((16 * u + j) % Geo::HRows) * 4);
-            if (turn == 0) fw = p.ws[((size_t)c.g * p.nb + min((c.a0 + 64 * wi) >> 7, p.nb - 1)) * p.kb + kt];
+            if (turn == 0) {
+                // a block row's scales, 64 K-tiles to a register: one per lane
+                if ((kt & 63) == 0 && kt > 0) fwv = load_fw(c, kt);
+                fw = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)fwv, kt & 63));
+            }
         }
     };
 
     f32x4 acc[NB][4];
-    // ra: the a operand and the first half of the b operand; rb: the second half
-    MmReq<NQ> ra, rb;
+    MmReq<NQ> R;
 
+    f32x4 d[2][4];                      // fp8: products not yet added, and their scales
+    float sc = 0.f;
+    auto add_scaled = [&](int u, int from) __attribute__((always_inline)) {
+        #pragma unroll
+        for (int t = 0; t < 4; ++t)
+            #pragma unroll
+            for (int v = 0; v < 4; ++v) acc[u][t][v] = fmaf(d[from][t][v], sc, acc[u][t][v]);
+    };
     // the products of one turn, with the turn's requests between them
     auto multiply = [&](auto turn) __attribute__((always_inline)) {
         constexpr int h = decltype(turn)::value;
         constexpr int NR = mm_turn_requests(EL, MODE, NB, h);
-        MmReq<NQ>& R = h == 1 ? ra : rb;
         if constexpr (EL == kElFp8) {
             // the K-tile is one block of 128: its products go to cleared
             // registers and are added with the two scales' product, one b tile
-            // behind: 4 additions in the shadow of each matrix instruction. The
+            // behind: 4 additions in the shadow of each matrix instruction, a
+            // turn's last b tile in the next turn (finish() after the last). The
             // empty asm statements order the two (b tile u's products before
-            // and b tile u - 1's additions before u's); left alone the compiler
-            // starts every product first and spills the accumulators.
-            f32x4 d[2][4];
-            float sc = 0.f;
-            static_for<NU + 1>([&](auto uu) __attribute__((always_inline)) {
-                constexpr int u = decltype(uu)::value;
-                if constexpr (u < NU) {
-                    #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        d[u & 1][t] = mfma_fp8(fp[0][t], fp[1][t], fq[0][u], fq[1][u], f32x4{0.f, 0.f, 0.f, 0.f});
-                    mm_requests<EL, MODE, NB, h, (NR * u) / NU, (NR * (u + 1)) / NU>(p, wh, R, smem);
+            // and the additions of the one before it before u's); left alone the
+            // compiler starts every product first and spills the accumulators.
+            static_for<NU>([&](auto uu) __attribute__((always_inline)) {
+                constexpr int u = decltype(uu)::value, before = u > 0 ? h * NU + u - 1 : (1 - h) * NU + NU - 1;
+                #pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    d[u & 1][t] = mfma_fp8(fp[0][t], fp[1][t], fq[0][u], fq[1][u], f32x4{0.f, 0.f, 0.f, 0.f});
+                mm_requests<EL, MODE, NB, h, (NR * u) / NU, (NR * (u + 1)) / NU>(p, wh, R, smem);
+                add_scaled(before, (u & 1) ^ 1);
+                #pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
                 }
-                if constexpr (u > 0) {
-                    f32x4* a = acc[h * NU + u - 1];
-                    #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        #pragma unroll
-                        for (int v = 0; v < 4; ++v) a[t][v] = fmaf(d[(u - 1) & 1][t][v], sc, a[t][v]);
-                    if constexpr (u < NU) {
-                        #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                            __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-                        }
-                    }
-                    asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
-                }
-                if constexpr (u < NU) {
-                    sc = fs[u] * fw;
-                    const f32x4* e = d[u & 1];
-                    asm volatile("" : "+v"(sc) : "v"(e[0]), "v"(e[1]), "v"(e[2]), "v"(e[3]));
-                }
+                f32x4* a = acc[before];
+                asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
+                sc = fs[u] * fw;
+                const f32x4* e = d[u & 1];
+                asm volatile("" : "+v"(sc) : "v"(e[0]), "v"(e[1]), "v"(e[2]), "v"(e[3]));
                 __builtin_amdgcn_sched_barrier(0);
             });
         } else {
@@ -563,6 +586,11 @@ void grouped_mm_kernel(MmP p) {
         for (int u = 0; u < NB; ++u)
             #pragma unroll
             for (int t = 0; t < 4; ++t) acc[u][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (EL == kElFp8) {
+            sc = 0.f;
+            #pragma unroll
+            for (int t = 0; t < 4; ++t) d[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
     };
     // Sums stay in 32 bits until here: the one rounding to the output's type.
     // Every lane stores, past an edge outside the resource (dropped), so a wave
@@ -617,24 +645,21 @@ void grouped_mm_kernel(MmP p) {
         if (kept.held) kept_write(wh, kept, smem);
         if (kept.live) kept_load<NB>(p, wh, kept);
     }
-    mm_start<EL, MODE, NB>(p, pass_off, wh, ra, 0, slot);
-    mm_start<EL, MODE, NB>(p, pass_off, wh, rb, 1, slot);
+    mm_start<EL, MODE, NB>(p, pass_off, wh, R, slot);
     #pragma unroll 1
-    for (int i = 0; i < NST; ++i) {
-        mm_requests<EL, MODE, NB, 1, 0, mm_turn_requests(EL, MODE, NB, 1)>(p, wh, ra, smem);
-        if (i < NST - 1) mm_advance<EL, MODE, NB>(p, pass_off, wh, ra, 0);
-    }
-    #pragma unroll 1
-    for (int i = 0; i < NST - 1; ++i) {
-        mm_requests<EL, MODE, NB, 0, 0, mm_turn_requests(EL, MODE, NB, 0)>(p, wh, rb, smem);
-        if (i < NST - 2) mm_advance<EL, MODE, NB>(p, pass_off, wh, rb, 1);
+    for (int i = 0; i < NST; ++i) {     // the last one's second b half follows in the first turn
+        mm_requests<EL, MODE, NB, 1, 0, mm_turn_requests(EL, MODE, NB, 1)>(p, wh, R, smem);
+        if (i < NST - 1) {
+            mm_requests<EL, MODE, NB, 0, 0, mm_turn_requests(EL, MODE, NB, 0)>(p, wh, R, smem);
+            mm_advance<EL, MODE, NB>(p, pass_off, wh, R);
+        }
     }
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
     bare_barrier();
     if (!lead) bare_barrier();
 
-    // Turn 1 requests ra's K-tile NST ahead, turn 0 rb's NST - 1 ahead, both
-    // between the products. Waits: the newer requests left in flight when the
+    // Turn 1 requests K-tile NST ahead, turn 0 the second b half of NST - 1
+    // ahead, both between the products. Waits: the newer requests left in flight when the
     // ones that the next turn reads have landed. Waves 0-3 wait after their
     // products, waves 4-7 (half a turn later, before this turn's requests) after
     // their reads. Requests not counted (row sources, stores) only make a wait
@@ -652,8 +677,14 @@ void grouped_mm_kernel(MmP p) {
         else __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + KEPT, 15));
     };
     int step = 0;
+    if constexpr (EL == kElFp8) fwn = load_fw(mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, pass_off, at, slot)), 0);
     for (int item = slot; item < n_items; item += grid) {
-        const MmItem c = mm_decode<EL, MODE, 32 * NB>(p, pass_off, at, item);
+        // the item is the one being requested, unless items are very short
+        const MmItem c = R.live && R.at == item ? R.c : mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, pass_off, at, item));
+        if constexpr (EL == kElFp8) {   // the next item's scales are loaded an item ahead
+            fwv = fwn;
+            if (item + grid < n_items) fwn = load_fw(mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, pass_off, at, item + grid)), 0);
+        }
         clear();
         #pragma unroll 1
         for (int kt = 0; kt < c.nk; ++kt, ++step) {
@@ -664,11 +695,7 @@ void grouped_mm_kernel(MmP p) {
                     if (kept.held) kept_write(wh, kept, smem + (kept.step % NST) * Geo::Stage);
                     if (kept.live) kept_load<NB>(p, wh, kept);
                 }
-                if constexpr (h == 1) {
-                    mm_advance<EL, MODE, NB>(p, pass_off, wh, ra, 0);
-                } else {
-                    mm_advance<EL, MODE, NB>(p, pass_off, wh, rb, 1);
-                }
+                if constexpr (h == 1) mm_advance<EL, MODE, NB>(p, pass_off, wh, R);
                 // the reads end before this wave's products and so a turn before
                 // the stage is requested again; only writes to LDS must be done here
                 if constexpr (MODE == kWgrad8) __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
@@ -682,6 +709,7 @@ void grouped_mm_kernel(MmP p) {
             });
             --stored;
         }
+        if constexpr (EL == kElFp8) add_scaled(NB - 1, 1);
         // (an item without K-tiles stores between two others' stores: not counted)
         stored = (is_wgrad(MODE) && (p.accumulate || c.nk == 0)) ? 0 : NST - 1;
         if (!is_wgrad(MODE) || c.nk > 0 || !p.accumulate) {
