@@ -71,7 +71,7 @@ struct MmReq {
     int at, nat;                        // numbers of c and n
     bool live, nlive;
     MmItem c, n;                        // the item requested now, and the next one
-    uint32_t row[2][NQ], nrow[2][NQ];   // contiguous b operand: byte offsets of this lane's rows; next item's sources
+    uint32_t nrow[2][NQ];               // contiguous b operand: sources of this lane's rows of the next item
     uint32_t srow[2], nsrow[2];         // fp8: byte offset of this lane's row of scales; next item's source
     uint32_t psrc, qsrc, npsrc, nqsrc;  // wgrad: source rows of the next K-tile's k, one k per lane % 8
     uint32_t po[4], qo[2][NQ];          // the next request's byte offsets,
@@ -82,6 +82,13 @@ struct MmReq {
 // first of the rows that wave w takes of half `half` of the b tile
 template <int NB>
 MOE_DEV int q_first(int w, int half) { return (w >> 2) * (16 * NB) + half * (8 * NB) + (w & 3) * (2 * NB); }
+
+// byte offset in a row's 128 bytes of the chunk that this lane takes of the
+// rows of request i (the swizzle of row 8 m + lane / 8 depends on m's parity)
+template <int NB>
+MOE_DEV int q_chunk(int lane, int w, int half, int i) {
+    return 16 * ((lane & 7) ^ ((lane >> 4) | (4 * (((q_first<NB>(w, half) >> 3) + i) & 1))));
+}
 
 // wgrad: sources of this wave's 8 k of K-tile kt of item c (past the group: not looked at)
 template <int MODE>
@@ -142,7 +149,8 @@ MOE_DEV void mm_take(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq
             for (int i = 0; i < NQ; ++i) {
                 const int row = first + 8 * i + (wh.lane >> 3);
                 const uint32_t s = R.nrow[h][i];
-                R.row[h][i] = row < R.c.nrows && s < p.x_rows ? (p.x_src ? s : (uint32_t)row) * p.x_ld : kMmNoRow;
+                R.qo[h][i] = (row < R.c.nrows && s < p.x_rows ? (p.x_src ? s : (uint32_t)row) * p.x_ld : kMmNoRow) +
+                             (uint32_t)q_chunk<NB>(wh.lane, wh.w, h, i);
             }
             if constexpr (EL == kElFp8) {
                 const int row = first + wh.lane;
@@ -240,11 +248,10 @@ MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, bool for_
         R.qn = (p.x_src ? p.x_bytes : (uint32_t)(c.nrows - 1) * p.x_ld + (uint32_t)(p.K * EB)) - (uint32_t)(R.kt * 128);
         #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int first = q_first<NB>(w, h);
             #pragma unroll
             for (int i = 0; i < NQ; ++i) {
-                const int kb = 16 * ((lane & 7) ^ ((lane >> 4) | (4 * (((first >> 3) + i) & 1))));
-                R.qo[h][i] = R.live && R.kt * 128 + kb < p.K * EB ? R.row[h][i] + (uint32_t)kb : kMmInvalid;
+                const uint32_t o = R.qo[h][i];
+                R.qo[h][i] = R.live && R.kt * 128 + q_chunk<NB>(lane, w, h, i) < p.K * EB ? o : kMmInvalid;
             }
         }
         if constexpr (EL == kElFp8) {
@@ -280,6 +287,10 @@ MOE_DEV void mm_advance(const MmP& p, const int* pass_off, const MmWhere& wh, Mm
     }
     if constexpr (is_wgrad(MODE)) {
         if (R.live && R.kt + 1 < R.c.nk) mm_load_src<MODE>(p, wh, R.c, R.kt + 1, R.psrc, R.qsrc);
+        R.pb = uniform_ptr(R.pb);
+        R.qb = uniform_ptr(R.qb);
+        R.pn = (uint32_t)__builtin_amdgcn_readfirstlane((int)R.pn);
+        R.qn = (uint32_t)__builtin_amdgcn_readfirstlane((int)R.qn);
     }
 }
 template <int EL, int MODE, int NB, int NQ>
@@ -479,9 +490,7 @@ void grouped_mm_kernel(MmP p) {
     // 8 k of one value (k = 32 s + 8 q ..) from rows of `rb` bytes: at o + k's row
     auto read_slow = [&](const uint8_t* st, int o, int rb) __attribute__((always_inline)) {
         i32x4 v;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_s16x4*)(st + o));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_s16x4*)(st + o + 4 * rb));
-        const u32x2_t l = __builtin_bit_cast(u32x2_t, lo), h = __builtin_bit_cast(u32x2_t, hi);
+        const u32x2_t l = read_tr16((const mm_lds_s16x4*)(st + o)), h = read_tr16((const mm_lds_s16x4*)(st + o + 4 * rb));
         v[0] = (int)l.x; v[1] = (int)l.y; v[2] = (int)h.x; v[3] = (int)h.y;
         return v;
     };
@@ -525,43 +534,40 @@ void grouped_mm_kernel(MmP p) {
     f32x4 acc[NB][4];
     MmReq<NQ> R;
 
-    f32x4 d[2][4];                      // fp8: products not yet added, and their scales
+    f32x4 d[4];                         // fp8: products not yet added, and their scales
     float sc = 0.f;
-    auto add_scaled = [&](int u, int from) __attribute__((always_inline)) {
-        #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            #pragma unroll
-            for (int v = 0; v < 4; ++v) acc[u][t][v] = fmaf(d[from][t][v], sc, acc[u][t][v]);
-    };
+
     // the products of one turn, with the turn's requests between them
     auto multiply = [&](auto turn) __attribute__((always_inline)) {
         constexpr int h = decltype(turn)::value;
         constexpr int NR = mm_turn_requests(EL, MODE, NB, h);
         if constexpr (EL == kElFp8) {
             // the K-tile is one block of 128: its products go to cleared
-            // registers and are added with the two scales' product, one b tile
-            // behind: 4 additions in the shadow of each matrix instruction, a
-            // turn's last b tile in the next turn (finish() after the last). The
-            // empty asm statements order the two (b tile u's products before
-            // and the additions of the one before it before u's); left alone the
-            // compiler starts every product first and spills the accumulators.
+            // registers and are added with the two scales' product, four
+            // instructions behind: 4 additions in the shadow of each matrix
+            // instruction, the registers then being the next one's; a turn's
+            // last b tile in the next turn (or after the item's last). The
+            // empty asm statements order the two (the additions of the b tile
+            // before, b tile u's products); left alone the compiler starts
+            // every product first and spills the accumulators.
             static_for<NU>([&](auto uu) __attribute__((always_inline)) {
                 constexpr int u = decltype(uu)::value, before = u > 0 ? h * NU + u - 1 : (1 - h) * NU + NU - 1;
-                #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    d[u & 1][t] = mfma_fp8(fp[0][t], fp[1][t], fq[0][u], fq[1][u], f32x4{0.f, 0.f, 0.f, 0.f});
-                mm_requests<EL, MODE, NB, h, (NR * u) / NU, (NR * (u + 1)) / NU>(p, wh, R, smem);
-                add_scaled(before, (u & 1) ^ 1);
+                f32x4* a = acc[before];
                 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                    #pragma unroll
+                    for (int v = 0; v < 4; ++v) a[t][v] = fmaf(d[t][v], sc, a[t][v]);
+                    d[t] = mfma_fp8(fp[0][t], fp[1][t], fq[0][u], fq[1][u], f32x4{0.f, 0.f, 0.f, 0.f});
                 }
-                f32x4* a = acc[before];
+                mm_requests<EL, MODE, NB, h, (NR * u) / NU, (NR * (u + 1)) / NU>(p, wh, R, smem);
+                #pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                }
                 asm volatile("" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]));
                 sc = fs[u] * fw;
-                const f32x4* e = d[u & 1];
-                asm volatile("" : "+v"(sc) : "v"(e[0]), "v"(e[1]), "v"(e[2]), "v"(e[3]));
+                asm volatile("" : "+v"(sc) : "v"(d[0]), "v"(d[1]), "v"(d[2]), "v"(d[3]));
                 __builtin_amdgcn_sched_barrier(0);
             });
         } else {
@@ -589,7 +595,7 @@ void grouped_mm_kernel(MmP p) {
         if constexpr (EL == kElFp8) {
             sc = 0.f;
             #pragma unroll
-            for (int t = 0; t < 4; ++t) d[1][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < 4; ++t) d[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
     };
     // Sums stay in 32 bits until here: the one rounding to the output's type.
@@ -709,7 +715,12 @@ void grouped_mm_kernel(MmP p) {
             });
             --stored;
         }
-        if constexpr (EL == kElFp8) add_scaled(NB - 1, 1);
+        if constexpr (EL == kElFp8) {
+            #pragma unroll
+            for (int t = 0; t < 4; ++t)
+                #pragma unroll
+                for (int v = 0; v < 4; ++v) acc[NB - 1][t][v] = fmaf(d[t][v], sc, acc[NB - 1][t][v]);
+        }
         // (an item without K-tiles stores between two others' stores: not counted)
         stored = (is_wgrad(MODE) && (p.accumulate || c.nk == 0)) ? 0 : NST - 1;
         if (!is_wgrad(MODE) || c.nk > 0 || !p.accumulate) {

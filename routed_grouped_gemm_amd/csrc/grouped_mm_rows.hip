@@ -170,9 +170,7 @@ void grouped_mm_rows_kernel(MmP p) {
                     fp[s] = *(const i32x4*)(st + (16 * w + j) * 128 + ch);
                 } else {
                     const int o = (32 * s + 8 * q + (j >> 2)) * 128 + ((w ^ (j >> 2)) * 32) + (j & 3) * 8;
-                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_s16x4*)(st + o));
-                    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((mm_lds_s16x4*)(st + o + 4 * 128));
-                    const u32x2_t l = __builtin_bit_cast(u32x2_t, lo), hh = __builtin_bit_cast(u32x2_t, hi);
+                    const u32x2_t l = read_tr16((const mm_lds_s16x4*)(st + o)), hh = read_tr16((const mm_lds_s16x4*)(st + o + 4 * 128));
                     fp[s] = i32x4{(int)l.x, (int)l.y, (int)hh.x, (int)hh.y};
                 }
                 #pragma unroll
