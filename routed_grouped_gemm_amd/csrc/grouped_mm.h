@@ -106,7 +106,11 @@ MOE_DEV void bare_barrier() {
 }
 
 enum { kMmNK = 0, kMmKN = 1, kWgrad = 2, kWgrad8 = 3 };     // kWgrad8: x rows in E4M3 with block scales
-constexpr bool is_wgrad(int mode) { return mode >= kWgrad; }
+// wgrad modes also say at compile time which operand's rows are gathered (the
+// offsets of gathered rows are formed for every K-tile, others once an item)
+constexpr int kGatherX = 16, kGatherDy = 32;
+constexpr int mm_kind(int mode) { return mode & 15; }
+constexpr bool is_wgrad(int mode) { return mm_kind(mode) >= kWgrad; }
 
 constexpr int kMmThreads = 512;
 constexpr int kMmLds = 163840;              // LDS of a compute unit

@@ -94,9 +94,9 @@ MOE_DEV int q_chunk(int lane, int w, int half, int i) {
 template <int MODE>
 MOE_DEV void mm_load_src(const MmP& p, const MmWhere& wh, const MmItem& c, int kt, uint32_t& ps, uint32_t& qs) {
     const int k = kt * 64 + 8 * wh.w + (wh.lane & 7);
-    if (MODE == kWgrad && p.x_src)
+    if constexpr (mm_kind(MODE) == kWgrad && (MODE & kGatherX) != 0)
         ps = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.x_src + c.r0, (uint32_t)(c.nrows * 4)), k * 4, 0, 0);
-    if (p.dy_src)
+    if constexpr ((MODE & kGatherDy) != 0)
         qs = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.dy_src + c.r0, (uint32_t)(c.nrows * 4)), k * 4, 0, 0);
 }
 
@@ -225,11 +225,11 @@ MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, bool for_
             R.pb = p.w + (size_t)c.g * p.w_group;
             mm_slow_bounds(R.pb, R.pn, p.w_ld, false, R.kt * 64, p.K - R.kt * 64, c.a0, p.N);
             mm_slow_offsets<256>(R.po, R.live, false, 0, 0, p.w_ld, p.K - R.kt * 64, c.a0, p.N, 0, w, lane);
-        } else if constexpr (MODE == kWgrad) {
+        } else if constexpr (mm_kind(MODE) == kWgrad) {
             R.pb = p.x;
             R.pn = p.x_bytes;
-            mm_slow_bounds(R.pb, R.pn, p.x_ld, p.x_src != nullptr, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.a0, p.K);
-            mm_slow_offsets<256>(R.po, R.live, p.x_src != nullptr, R.psrc, p.x_rows, p.x_ld, c.nrows - R.kt * 64, c.a0,
+            mm_slow_bounds(R.pb, R.pn, p.x_ld, (MODE & kGatherX) != 0, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.a0, p.K);
+            mm_slow_offsets<256>(R.po, R.live, (MODE & kGatherX) != 0, R.psrc, p.x_rows, p.x_ld, c.nrows - R.kt * 64, c.a0,
                                  p.K, 0, w, lane);
         }
     }
@@ -237,10 +237,10 @@ MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, bool for_
     if constexpr (is_wgrad(MODE)) {
         R.qb = p.dy;
         R.qn = p.dy_bytes;
-        mm_slow_bounds(R.qb, R.qn, p.dy_ld, p.dy_src != nullptr, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.b0, p.N);
+        mm_slow_bounds(R.qb, R.qn, p.dy_ld, (MODE & kGatherDy) != 0, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.b0, p.N);
         #pragma unroll
         for (int h = 0; h < 2; ++h)
-            mm_slow_offsets<128>(R.qo[h], R.live, p.dy_src != nullptr, R.qsrc, p.dy_rows, p.dy_ld, c.nrows - R.kt * 64,
+            mm_slow_offsets<128>(R.qo[h], R.live, (MODE & kGatherDy) != 0, R.qsrc, p.dy_rows, p.dy_ld, c.nrows - R.kt * 64,
                                  c.b0, p.N, h, w, lane);
     } else {
         // gathered rows are addressed from the array's start, a group's own rows from the tile's first
@@ -273,12 +273,12 @@ MOE_DEV void mm_advance(const MmP& p, const int* pass_off, const MmWhere& wh, Mm
     R.kt = last ? 0 : kt;
     if (last) mm_take<EL, MODE, NB>(p, pass_off, wh, R);
     const bool edge = last || kt == R.c.nk - 1;
-    const bool anew_p = edge || (MODE == kWgrad && p.x_src), anew_q = edge || (is_wgrad(MODE) && p.dy_src);
+    const bool anew_p = edge || (mm_kind(MODE) == kWgrad && (MODE & kGatherX) != 0), anew_q = edge || (MODE & kGatherDy) != 0;
     if (anew_p || anew_q) mm_offsets<EL, MODE, NB>(p, wh, R, anew_p, anew_q);
     if (!anew_p) {
         if constexpr (MODE == kMmNK) { R.pb += 128; R.pn -= 128; }
         else if constexpr (MODE == kMmKN) R.pb += (size_t)p.w_ld * 64;
-        else if constexpr (MODE == kWgrad) R.pb += (size_t)p.x_ld * 64;
+        else if constexpr (mm_kind(MODE) == kWgrad) R.pb += (size_t)p.x_ld * 64;
     }
     if (!anew_q) {
         if constexpr (is_wgrad(MODE)) R.qb += (size_t)p.dy_ld * 64;
@@ -349,7 +349,7 @@ MOE_DEV void mm_request_s(const MmWhere& wh, const MmReq<NB / 4>& R, uint8_t* sm
 #endif
 }
 // Requests of turn H: the a operand (turn 1), half 1 - H of the b operand, its scales.
-constexpr int mm_turn_p(int mode, int turn) { return turn == 1 && mode != kWgrad8 ? 4 : 0; }
+constexpr int mm_turn_p(int mode, int turn) { return turn == 1 && mm_kind(mode) != kWgrad8 ? 4 : 0; }
 constexpr int mm_turn_requests(int el, int mode, int nb, int turn) {
     return mm_turn_p(mode, turn) + nb / 4 + (el == kElFp8 ? 1 : 0);
 }
@@ -641,7 +641,7 @@ void grouped_mm_kernel(MmP p) {
 
     // --------------------------------------------------------------- loop
     MmKept kept;
-    if constexpr (MODE == kWgrad8) {
+    if constexpr (mm_kind(MODE) == kWgrad8) {
         kept.item = slot;
         kept.step = kept.kt = 0;
         kept.held = false;
@@ -672,13 +672,13 @@ void grouped_mm_kernel(MmP p) {
     // longer; once a stream has ended its requests still count. In the first
     // NST - 1 K-tiles after an item's stores the requests waited for are older
     // than the stores, which then count as newer.
-    constexpr int KEPT = MODE == kWgrad8 ? 8 : 0;            // requests of the 8-bit rows, one K-tile's in flight
+    constexpr int KEPT = mm_kind(MODE) == kWgrad8 ? 8 : 0;            // requests of the 8-bit rows, one K-tile's in flight
     constexpr int L1 = mm_turn_requests(EL, MODE, NB, 1), L2 = mm_turn_requests(EL, MODE, NB, 0);
     int stored = 0;                                          // K-tiles whose waits leave the last stores in flight
     auto wait_for = [&](auto n) __attribute__((always_inline)) {
         constexpr int N = decltype(n)::value;
         static_assert(N + KEPT + 4 * NB < 64, "vmcnt");
-        if (MODE == kWgrad8 && !kept.live) __builtin_amdgcn_s_waitcnt(waitcnt_imm(N, 15));
+        if (mm_kind(MODE) == kWgrad8 && !kept.live) __builtin_amdgcn_s_waitcnt(waitcnt_imm(N, 15));
         else if (stored > 0) __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + KEPT + 4 * NB, 15));
         else __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + KEPT, 15));
     };
@@ -697,14 +697,14 @@ void grouped_mm_kernel(MmP p) {
             static_for<2>([&](auto turn) __attribute__((always_inline)) {
                 constexpr int h = decltype(turn)::value;
                 read_frags(step, h, c, kt);
-                if constexpr (MODE == kWgrad8 && h == 1) {
+                if constexpr (mm_kind(MODE) == kWgrad8 && h == 1) {
                     if (kept.held) kept_write(wh, kept, smem + (kept.step % NST) * Geo::Stage);
                     if (kept.live) kept_load<NB>(p, wh, kept);
                 }
                 if constexpr (h == 1) mm_advance<EL, MODE, NB>(p, pass_off, wh, R);
                 // the reads end before this wave's products and so a turn before
                 // the stage is requested again; only writes to LDS must be done here
-                if constexpr (MODE == kWgrad8) __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+                if constexpr (mm_kind(MODE) == kWgrad8) __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
                 if (!lead) wait_for(std::integral_constant<int, h ? (NST - 2) * L1 + (NST - 1) * L2 : (NST - 1) * L1 + (NST - 2) * L2>{});
                 bare_barrier();
                 __builtin_amdgcn_s_setprio(1);
@@ -765,6 +765,14 @@ int launch_mm_rows(const MmP& p, int kind, hipStream_t stream) {
                       : launch_mm<EL, MODE, 4>(p, mm_items(p, 128), stream);
 }
 
+template <int EL>
+int launch_wgrad(const MmP& p, int items, hipStream_t stream) {
+    if (p.x_src && p.dy_src) return launch_mm<EL, kWgrad | kGatherX | kGatherDy, 8>(p, items, stream);
+    if (p.x_src) return launch_mm<EL, kWgrad | kGatherX, 8>(p, items, stream);
+    if (p.dy_src) return launch_mm<EL, kWgrad | kGatherDy, 8>(p, items, stream);
+    return launch_mm<EL, kWgrad, 8>(p, items, stream);
+}
+
 }  // namespace
 
 size_t moe_mm_workspace_bytes(int kind, bool fp8, int R_max, int G, int N, int K) {
@@ -797,8 +805,10 @@ int moe_launch_mm(const MmCall& c, hipStream_t stream) {
         if (c.dy_src) p.dy_bytes = (uint32_t)((int64_t)(c.dy_rows - 1) * c.ld_dy * 2 + (int64_t)c.N * 2);
         const int64_t tiles = (int64_t)c.G * ((c.N + 255) / 256) * ((c.K + 255) / 256);
         const int items = (int)std::min<int64_t>(tiles, 1 << 30);
-        if (c.xs) return launch_mm<kElBf16, kWgrad8, 8>(p, items, stream);
-        return f16 ? launch_mm<kElF16, kWgrad, 8>(p, items, stream) : launch_mm<kElBf16, kWgrad, 8>(p, items, stream);
+        if (c.xs)                        // (the 8-bit rows' gather is no part of the request state)
+            return c.dy_src ? launch_mm<kElBf16, kWgrad8 | kGatherDy, 8>(p, items, stream)
+                            : launch_mm<kElBf16, kWgrad8, 8>(p, items, stream);
+        return f16 ? launch_wgrad<kElF16>(p, items, stream) : launch_wgrad<kElBf16>(p, items, stream);
     }
     p.w = (const uint8_t*)c.w;
     p.w_group = (size_t)c.N * c.K * eb;
