@@ -414,10 +414,13 @@ MOE_DEV void kept_load(const MmP& p, const MmWhere& wh, MmKept& X) {
             row = wh.lane < 32 ? s0 : s1;
         }
         const bool ok = k < krem && col < p.K && (!mapped || (uint32_t)row < p.x_rows);
-        X.q[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
-            rx, ok ? (uint32_t)row * p.x_ld + (uint32_t)col : kMmInvalid, 0, 0));
-        X.s[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-            rs, ok ? ((uint32_t)row * (uint32_t)p.kb + (uint32_t)(col >> 7)) * 4u : kMmInvalid, 0, 0));
+        // (opaque offsets: with visible ones the compiler makes two loads of
+        // each, the second waiting for the first)
+        uint32_t oq = ok ? (uint32_t)row * p.x_ld + (uint32_t)col : kMmInvalid;
+        uint32_t os = ok ? ((uint32_t)row * (uint32_t)p.kb + (uint32_t)(col >> 7)) * 4u : kMmInvalid;
+        asm volatile("" : "+v"(oq), "+v"(os));
+        X.q[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rx, oq, 0, 0));
+        X.s[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, os, 0, 0));
     }
     X.held = true;
     const int kt = X.kt + 1;
