@@ -36,6 +36,10 @@ struct MmP {
     const float* xs; uint32_t xs_bytes;                  // fp8: row scales [x_rows, kb]
     const float* ws;                                     // fp8: weight scales [G, nb, kb]
     int kb, nb;
+    // work split along the reduction axis: K-tiles per part, parts (rows
+    // kernel), and the fp32 partial sums (null: no splitting)
+    int part, parts, max_slots;
+    float* partial;
 };
 
 // Rows [lo, hi) of group g, held inside [0, R_max) whatever the offsets say.
@@ -122,14 +126,16 @@ MOE_DEV int kc_swz(int row) { return (row >> 1) & 7; }
 MOE_DEV int tr_swz(int k) { return (k & 3) | (((k >> 3) & 3) << 2); }
 MOE_DEV int tr_swz_half(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
 
-struct MmItem { int g, a0, b0, r0, nrows, nk; };
+// rows [r0, r0 + nrows), nk K-tiles; slot: place of its partial sums, -1: the output itself
+struct MmItem { int g, a0, b0, r0, nrows, nk, slot; };
 
 // the item's fields as scalars again (control flow that merely looks divergent
 // would otherwise turn every descriptor load into a loop over lanes)
 MOE_DEV MmItem mm_scalar(const MmItem& c) {
     return MmItem{__builtin_amdgcn_readfirstlane(c.g), __builtin_amdgcn_readfirstlane(c.a0),
                   __builtin_amdgcn_readfirstlane(c.b0), __builtin_amdgcn_readfirstlane(c.r0),
-                  __builtin_amdgcn_readfirstlane(c.nrows), __builtin_amdgcn_readfirstlane(c.nk)};
+                  __builtin_amdgcn_readfirstlane(c.nrows), __builtin_amdgcn_readfirstlane(c.nk),
+                  __builtin_amdgcn_readfirstlane(c.slot)};
 }
 
 // pass_off[g] = passes of `bt` rows before group g, pass_off[G] their number,
@@ -148,32 +154,72 @@ MOE_DEV void mm_passes(const MmP& p, int bt, int lane, int* pass_off) {
 }
 
 // Where a workgroup is: its items and this lane.
-struct MmWhere { int n_items, at, grid, lane, w; };
+struct MmWhere { int n_items, at, grid, slot, lane, w; };
 
-// work item number `item`: tiles of AT values of the a axis, BT of the b axis
+// largest index i in [0, n) with at[i] <= v (at[0] <= v, non-decreasing): 64
+// entries at a time
+MOE_DEV int last_at_most(const int* at, int n, int v) {
+    int c = 0;
+    for (int i0 = 0; i0 < n; i0 += 64) {
+        const int i = i0 + (int)(threadIdx.x & 63);
+        const int here = __builtin_popcountll(__ballot(i < n && at[i] <= v));
+        c += here;
+        if (here < 64) break;
+    }
+    return __builtin_amdgcn_readfirstlane(c) - 1;
+}
+
+// Tables of a launch in LDS. mm: at [G + 1] passes of rows before group g.
+// wgrad: groups in the order of their items, at [G + 1] units (parts of a
+// group's K-tiles) before the i-th, order [G] the i-th group; slots [G] the
+// first partial-sum slot of group g's tiles (-1: not split).
+struct MmTables { const int *at, *order, *slots; };
+
+// parts that group g's nk K-tiles are split into
+MOE_DEV int wgrad_parts(const MmP& p, int nk) { return p.part > 0 ? max(1, (nk + p.part - 1) / p.part) : 1; }
+MOE_DEV int group_ktiles(const MmP& p, int g) {
+    int lo, hi;
+    group_rows(p, g, lo, hi);
+    return (hi - lo + 63) / 64;
+}
+// number of the item that a workgroup takes in its round: wgrad's items come
+// longest first, so every other round is dealt out backwards
+template <int MODE>
+MOE_DEV int mm_nth(int round, int grid, int slot) {
+    return round * grid + (is_wgrad(MODE) && (round & 1) ? grid - 1 - slot : slot);
+}
+
+// work item number `item`: tiles of AT values of the a axis (at of them), BT of the b axis
 template <int EL, int MODE, int BT, int AT = kATile>
-MOE_DEV MmItem mm_decode(const MmP& p, const int* pass_off, int at, int item) {
+MOE_DEV MmItem mm_decode(const MmP& p, const MmTables& tb, int at, int item) {
     constexpr int KT = EL == kElFp8 ? 128 : 64;
     MmItem c;
     int lo, hi, bt, l;
+    c.slot = -1;
     if constexpr (is_wgrad(MODE)) {
         bt = (p.N + BT - 1) / BT;
-        c.g = __builtin_amdgcn_readfirstlane(item / (at * bt));
-        l = item - c.g * (at * bt);
+        const int unit = __builtin_amdgcn_readfirstlane(item / (at * bt));
+        l = item - unit * (at * bt);
+        const int i = last_at_most(tb.at, p.G, unit);
+        const int first = __builtin_amdgcn_readfirstlane(tb.at[i]), parts = __builtin_amdgcn_readfirstlane(tb.at[i + 1]) - first;
+        const int part = unit - first;
+        c.g = __builtin_amdgcn_readfirstlane(tb.order[i]);
+        const int slot0 = __builtin_amdgcn_readfirstlane(tb.slots[c.g]);
+        group_rows(p, c.g, lo, hi);
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        const int rows = __builtin_amdgcn_readfirstlane(hi) - lo, nk = (rows + KT - 1) / KT;
+        // the group's K-tiles in `parts` nearly equal runs
+        const int k0 = __builtin_amdgcn_readfirstlane((int)((int64_t)nk * part / parts));
+        c.nk = __builtin_amdgcn_readfirstlane((int)((int64_t)nk * (part + 1) / parts)) - k0;
+        c.r0 = lo + k0 * KT;
+        c.nrows = min(rows - k0 * KT, c.nk * KT);
+        if (slot0 >= 0) c.slot = slot0 + part * (at * bt) + l;
     } else {
-        // groups whose first item is at or before this one, 64 at a time; the
-        // last of them (an empty group shares its first item with the next) is it
-        int n = 0;
-        for (int g0 = 0; g0 < p.G; g0 += 64) {
-            const int g = g0 + (int)(threadIdx.x & 63);
-            const int here = __builtin_popcountll(__ballot(g < p.G && pass_off[g] * at <= item));
-            n += here;
-            if (here < 64) break;
-        }
-        c.g = __builtin_amdgcn_readfirstlane(n) - 1;
-        const int first = __builtin_amdgcn_readfirstlane(pass_off[c.g]);
-        bt = __builtin_amdgcn_readfirstlane(pass_off[c.g + 1]) - first;
+        c.g = last_at_most(tb.at, p.G, item / at);           // (an empty group shares its first pass with the next)
+        const int first = __builtin_amdgcn_readfirstlane(tb.at[c.g]);
+        bt = __builtin_amdgcn_readfirstlane(tb.at[c.g + 1]) - first;
         l = item - first * at;
+        group_rows(p, c.g, lo, hi);
     }
     // bands of four b tiles, b fastest: the items that run together on one
     // XCD share operands in its L2
@@ -182,14 +228,9 @@ MOE_DEV MmItem mm_decode(const MmP& p, const int* pass_off, int at, int item) {
     const int ai = __builtin_amdgcn_readfirstlane(l2 / h);
     c.a0 = ai * AT;
     c.b0 = (4 * __builtin_amdgcn_readfirstlane(band) + __builtin_amdgcn_readfirstlane(l2 - ai * h)) * BT;
-    group_rows(p, c.g, lo, hi);
-    c.r0 = __builtin_amdgcn_readfirstlane(lo);
-    c.nrows = __builtin_amdgcn_readfirstlane(hi) - c.r0;
-    if constexpr (is_wgrad(MODE)) {
-        c.nk = (c.nrows + KT - 1) / KT;
-    } else {
-        c.r0 += c.b0;
-        c.nrows = min(BT, c.nrows - c.b0);
+    if constexpr (!is_wgrad(MODE)) {
+        c.r0 = __builtin_amdgcn_readfirstlane(lo) + c.b0;
+        c.nrows = min(BT, __builtin_amdgcn_readfirstlane(hi) - c.r0);
         c.nk = (p.K + KT - 1) / KT;
     }
     return c;
@@ -213,5 +254,5 @@ inline int mm_items(const MmP& p, int bt, int atile = kATile) {
 }  // namespace
 
 // Products of few rows per group (grouped_mm_rows.hip); p is an MmP, el its
-// element kind, kind 0 for W [N, K] and 1 for W [K, N].
-int moe_launch_mm_rows(const void* p, int el, int kind, hipStream_t stream);
+// element kind, kind 0 for W [N, K] and 1 for W [K, N], rows its tile height.
+int moe_launch_mm_rows(const void* p, int el, int kind, int rows, hipStream_t stream);

@@ -56,7 +56,7 @@ struct MmGeom {
     static constexpr int SOff = kPBytes + BT * 128;          // fp8: row scales, 256 bytes per wave and half
     static constexpr int Stage = SOff + (EL == kElFp8 ? 4096 : 0);
     static constexpr int NST = Stage * 3 + 8320 <= kMmLds ? 3 : 2;
-    static constexpr int Lds(int G) { return Stage * NST + (G + 1) * 4; }
+    static constexpr int Lds(int G, bool wgrad) { return Stage * NST + (wgrad ? 3 * G + 1 : G + 1) * 4; }
 };
 
 // The requests of a wave: one K-tile after another through all items, an
@@ -67,7 +67,7 @@ struct MmGeom {
 // in flight.
 template <int NQ>
 struct MmReq {
-    int item, kt, step;                 // item: the one to look at after n
+    int round, kt, step;                // round: the one to look at after n
     int at, nat;                        // numbers of c and n
     bool live, nlive;
     MmItem c, n;                        // the item requested now, and the next one
@@ -102,16 +102,15 @@ MOE_DEV void mm_load_src(const MmP& p, const MmWhere& wh, const MmItem& c, int k
 
 // find the next item with K-tiles and load its row sources
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_look(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R) {
-    int item = R.item;
+MOE_DEV void mm_look(const MmP& p, const MmTables& tb, const MmWhere& wh, MmReq<NQ>& R) {
+    int round = R.round;
     bool live = false;
-    while (item < wh.n_items && !live) {
-        R.n = mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, pass_off, wh.at, item));
+    for (int item; !live && (item = mm_nth<MODE>(round, wh.grid, wh.slot)) < wh.n_items; ++round) {
+        R.n = mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, tb, wh.at, item));
         R.nat = item;
         live = R.n.nk > 0;
-        item += wh.grid;
     }
-    R.item = item;
+    R.round = round;
     R.nlive = live;
     if (!live) return;
     if constexpr (is_wgrad(MODE)) {
@@ -133,7 +132,7 @@ MOE_DEV void mm_look(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq
 }
 // make the next item the one requested, and look for the one after
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_take(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R) {
+MOE_DEV void mm_take(const MmP& p, const MmTables& tb, const MmWhere& wh, MmReq<NQ>& R) {
     R.live = R.nlive;
     if (!R.live) return;
     R.c = R.n;
@@ -160,7 +159,7 @@ MOE_DEV void mm_take(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq
             }
         }
     }
-    mm_look<EL, MODE, NB>(p, pass_off, wh, R);
+    mm_look<EL, MODE, NB>(p, tb, wh, R);
 }
 
 // bounds a request to 64 rows of the slow form, or to a whole gathered array
@@ -265,13 +264,13 @@ MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, bool for_
 // what they count from moves on (scalar additions); they are formed anew for
 // an item's first and last K-tile, and for every one of gathered wgrad rows.
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_advance(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R) {
+MOE_DEV void mm_advance(const MmP& p, const MmTables& tb, const MmWhere& wh, MmReq<NQ>& R) {
     ++R.step;
     if (!R.live) return;
     const int kt = R.kt + 1;
     const bool last = kt == R.c.nk;
     R.kt = last ? 0 : kt;
-    if (last) mm_take<EL, MODE, NB>(p, pass_off, wh, R);
+    if (last) mm_take<EL, MODE, NB>(p, tb, wh, R);
     const bool edge = last || kt == R.c.nk - 1;
     const bool anew_p = edge || (mm_kind(MODE) == kWgrad && (MODE & kGatherX) != 0), anew_q = edge || (MODE & kGatherDy) != 0;
     if (anew_p || anew_q) mm_offsets<EL, MODE, NB>(p, wh, R, anew_p, anew_q);
@@ -294,13 +293,12 @@ MOE_DEV void mm_advance(const MmP& p, const int* pass_off, const MmWhere& wh, Mm
     }
 }
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_start(const MmP& p, const int* pass_off, const MmWhere& wh, MmReq<NQ>& R, int slot) {
-    R.item = slot;
-    R.step = R.kt = 0;
-    R.c = MmItem{0, 0, 0, 0, 1, 1};
+MOE_DEV void mm_start(const MmP& p, const MmTables& tb, const MmWhere& wh, MmReq<NQ>& R) {
+    R.round = R.step = R.kt = 0;
+    R.c = MmItem{0, 0, 0, 0, 1, 1, -1};
     R.at = -1;
-    mm_look<EL, MODE, NB>(p, pass_off, wh, R);
-    mm_take<EL, MODE, NB>(p, pass_off, wh, R);
+    mm_look<EL, MODE, NB>(p, tb, wh, R);
+    mm_take<EL, MODE, NB>(p, tb, wh, R);
     mm_offsets<EL, MODE, NB>(p, wh, R, true, true);
     if constexpr (is_wgrad(MODE)) {
         if (R.live && R.c.nk > 1) mm_load_src<MODE>(p, wh, R.c, 1, R.psrc, R.qsrc);
@@ -370,7 +368,7 @@ MOE_DEV void mm_requests(const MmP& p, const MmWhere& wh, const MmReq<NQ>& R, ui
 // 8 w + 2 i + l / 32. Codes are requested two K-tiles ahead and written to LDS
 // as BF16 values (code * scale, rounded) one K-tile ahead.
 struct MmKept {
-    int item, kt, step;                 // step: of the K-tile held in q
+    int round, kt, step;                 // step: of the K-tile held in q
     bool live, held;
     MmItem c;
     int src;                            // source rows of this wave's 8 k, one per lane % 8
@@ -379,15 +377,14 @@ struct MmKept {
 };
 
 template <int NB>
-MOE_DEV void kept_open(const MmP& p, const MmWhere& wh, MmKept& X) {
-    int item = X.item;
+MOE_DEV void kept_open(const MmP& p, const MmTables& tb, const MmWhere& wh, MmKept& X) {
+    int round = X.round;
     bool live = false;
-    while (item < wh.n_items && !live) {
-        X.c = mm_decode<kElBf16, kWgrad8, 32 * NB>(p, nullptr, wh.at, item);
+    for (int item; !live && (item = mm_nth<kWgrad8>(round, wh.grid, wh.slot)) < wh.n_items; ++round) {
+        X.c = mm_decode<kElBf16, kWgrad8, 32 * NB>(p, tb, wh.at, item);
         live = X.c.nk > 0;
-        item += wh.grid;
     }
-    X.item = item;
+    X.round = round;
     X.live = live;
     X.c = mm_scalar(X.c);
 }
@@ -397,7 +394,7 @@ MOE_DEV void kept_src(const MmP& p, const MmWhere& wh, MmKept& X) {
         make_rsrc(p.x_src + X.c.r0, p.x_src ? (uint32_t)(X.c.nrows * 4) : 0u), k * 4, 0, 0);
 }
 template <int NB>
-MOE_DEV void kept_load(const MmP& p, const MmWhere& wh, MmKept& X) {
+MOE_DEV void kept_load(const MmP& p, const MmTables& tb, const MmWhere& wh, MmKept& X) {
     const int k0 = X.kt * 64, krem = X.c.nrows - k0, first = X.c.r0 + k0, rows = min(krem, 64);
     const bool mapped = p.x_src != nullptr;
     const rsrc_t rx = make_rsrc(mapped ? p.x : p.x + (size_t)first * p.x_ld,
@@ -426,7 +423,7 @@ MOE_DEV void kept_load(const MmP& p, const MmWhere& wh, MmKept& X) {
     const int kt = X.kt + 1;
     const bool last = kt == X.c.nk;
     X.kt = last ? 0 : kt;
-    if (last) kept_open<NB>(p, wh, X);
+    if (last) kept_open<NB>(p, tb, wh, X);
     if (X.live) kept_src(p, wh, X);
 }
 MOE_DEV void kept_write(const MmWhere& wh, MmKept& X, uint8_t* st) {
@@ -448,6 +445,94 @@ MOE_DEV void kept_write(const MmWhere& wh, MmKept& X, uint8_t* st) {
     ++X.step;
 }
 
+// wgrad's tables (see MmTables), by the whole workgroup; a barrier must follow.
+// Groups go by the length of their parts, longest first (up to 512 groups; with
+// more, in their own order: a rank is found by comparing with every other).
+MOE_DEV void wgrad_tables(const MmP& p, int tiles, int* at, int* order, int* slots) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    for (int g = tid; g < p.G; g += kMmThreads) {
+        const int nk = group_ktiles(p, g), n = wgrad_parts(p, nk);
+        at[g] = (nk + n - 1) / n;                            // for now: the length of its parts
+    }
+    __syncthreads();
+    for (int g = tid; g < p.G; g += kMmThreads) {
+        int rank = g;
+        if (p.G <= kMmThreads) {
+            rank = 0;
+            for (int i = 0; i < p.G; ++i) rank += at[i] > at[g] || (at[i] == at[g] && i < g) ? 1 : 0;
+        }
+        order[rank] = g;
+    }
+    __syncthreads();
+    if (tid >= 64) return;
+    int units = 0, slot = 0;
+    for (int i0 = 0; i0 < p.G; i0 += 64) {
+        const int i = i0 + lane;
+        const int n = i < p.G ? wgrad_parts(p, group_ktiles(p, order[i])) : 0;
+        const int m = i < p.G ? wgrad_parts(p, group_ktiles(p, i)) : 0, sl = m > 1 ? m * tiles : 0;
+        const int inc = wave_incl_scan(n), sinc = wave_incl_scan(sl);
+        if (i < p.G) {
+            at[i] = units + inc - n;
+            slots[i] = sl > 0 ? slot + sinc - sl : -1;
+        }
+        units += __builtin_amdgcn_readlane(inc, 63);
+        slot += __builtin_amdgcn_readlane(sinc, 63);
+    }
+    if (lane == 0) at[p.G] = units;
+    if (slot > p.max_slots) {                                // only where groups overlap: nothing is split
+        for (int i = lane; i <= p.G; i += 64) {
+            at[i] = i;
+            if (i < p.G) slots[i] = -1;
+        }
+    }
+}
+
+// The partial sums of split groups into the gradient, in the order of the
+// parts: 64 rows of one tile per workgroup. Bound by HBM (each partial tile is
+// read once).
+__global__ __launch_bounds__(256)
+void wgrad_join_kernel(MmP p) {
+    const int bt = (p.N + 255) / 256, at = (p.K + 255) / 256, tiles = at * bt;
+    const int g = blockIdx.y, tile = blockIdx.x >> 2, quarter = blockIdx.x & 3;
+    const int lane = threadIdx.x & 63;
+    const int parts = wgrad_parts(p, group_ktiles(p, g));
+    if (parts == 1) return;
+    int slot = 0, all = 0;                                   // slots of the groups before this one, and of all
+    for (int g0 = 0; g0 < p.G; g0 += 64) {
+        const int m = g0 + lane < p.G ? wgrad_parts(p, group_ktiles(p, g0 + lane)) : 0, n = m > 1 ? m * tiles : 0;
+        slot += __builtin_amdgcn_readlane(wave_incl_scan(g0 + lane < g ? n : 0), 63);
+        all += __builtin_amdgcn_readlane(wave_incl_scan(n), 63);
+    }
+    if (all > p.max_slots) return;
+    // the tile's place, as the product's items count them
+    const int band = tile / (4 * at), h = min(4, bt - 4 * band), l2 = tile - band * 4 * at;
+    const int a0 = (l2 / h) * 256, b0 = (4 * band + l2 % h) * 256;
+    const float* src = p.partial + ((size_t)slot + tile) * 65536;
+    for (int i = threadIdx.x; i < 64 * 64; i += 256) {
+        const int row = quarter * 64 + (i >> 6), col = (i & 63) * 4;
+        if (b0 + row >= p.N || a0 + col >= p.K) continue;
+        f32x4 v = *(const f32x4*)(src + row * 256 + col);
+        for (int s = 1; s < parts; ++s) {
+            const f32x4 e = *(const f32x4*)(src + (size_t)s * tiles * 65536 + row * 256 + col);
+            v = f32x4{v[0] + e[0], v[1] + e[1], v[2] + e[2], v[3] + e[3]};
+        }
+        const size_t o = ((size_t)g * p.N + b0 + row) * p.K + a0 + col;
+        if (p.out_f32) {
+            f32x4* d = (f32x4*)((float*)p.out + o);
+            if (p.accumulate) { const f32x4 e = *d; v = f32x4{v[0] + e[0], v[1] + e[1], v[2] + e[2], v[3] + e[3]}; }
+            *d = v;
+        } else {
+            u32x2_t* d = (u32x2_t*)((uint16_t*)p.out + o);
+            if (p.accumulate) {
+                const u32x2_t e = *d;
+                v[0] += lo16(e.x, p.out_f16); v[1] += hi16(e.x, p.out_f16);
+                v[2] += lo16(e.y, p.out_f16); v[3] += hi16(e.y, p.out_f16);
+            }
+            *d = u32x2_t{pack16(v[0], v[1], p.out_f16), pack16(v[2], v[3], p.out_f16)};
+        }
+    }
+}
+
 template <int EL, int MODE, int NB>
 __global__ __launch_bounds__(kMmThreads, 1)
 void grouped_mm_kernel(MmP p) {
@@ -457,7 +542,8 @@ void grouped_mm_kernel(MmP p) {
     static_assert(!Q_TR || BT == 256, "the slow form is laid out for 256 values");
 
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    int* pass_off = (int*)(smem + NST * Geo::Stage);         // mm: [G + 1] passes before group g
+    int* const tab = (int*)(smem + NST * Geo::Stage);
+    const MmTables tb{tab, tab + p.G + 1, tab + 2 * p.G + 1};
 
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -469,17 +555,19 @@ void grouped_mm_kernel(MmP p) {
     const int at = (na + kATile - 1) / kATile;
     int n_items;
     if constexpr (is_wgrad(MODE)) {
-        n_items = p.G * at * ((p.N + BT - 1) / BT);
-    } else {
-        if (w == 0) mm_passes(p, BT, lane, pass_off);
+        wgrad_tables(p, at * ((p.N + BT - 1) / BT), tab, tab + p.G + 1, tab + 2 * p.G + 1);
         __syncthreads();
-        n_items = __builtin_amdgcn_readfirstlane(pass_off[p.G]) * at;
+        n_items = __builtin_amdgcn_readfirstlane(tab[p.G]) * at * ((p.N + BT - 1) / BT);
+    } else {
+        if (w == 0) mm_passes(p, BT, lane, tab);
+        __syncthreads();
+        n_items = __builtin_amdgcn_readfirstlane(tab[p.G]) * at;
     }
     const int grid = gridDim.x;
     const int slot = (grid % 8 == 0) ? (blockIdx.x % 8) * (grid / 8) + blockIdx.x / 8 : blockIdx.x;
     if (slot >= n_items) return;
 
-    const MmWhere wh{n_items, at, grid, lane, w};
+    const MmWhere wh{n_items, at, grid, slot, lane, w};
 
     // ---------------------------------------------------------- fragments
     constexpr int NU = Geo::NU, NQ = Geo::NQ;
@@ -607,11 +695,16 @@ void grouped_mm_kernel(MmP p) {
     // flight.
     auto store = [&](const MmItem& c, auto f16_) __attribute__((always_inline)) {
         constexpr int f16 = decltype(f16_)::value;
-        const int es = is_wgrad(MODE) && p.out_f32 ? 4 : 2;
-        const size_t ld = is_wgrad(MODE) ? (size_t)p.K : p.out_ld;
+        // a part of a split group goes to its tile of partial sums
+        const bool partial = is_wgrad(MODE) && c.slot >= 0, f32 = is_wgrad(MODE) && (p.out_f32 || partial);
+        const bool add = is_wgrad(MODE) && p.accumulate && !partial;
+        const int es = f32 ? 4 : 2;
+        const size_t ld = partial ? kATile : (is_wgrad(MODE) ? (size_t)p.K : p.out_ld);
         const size_t row0 = is_wgrad(MODE) ? (size_t)c.g * p.N + c.b0 : (size_t)c.r0;
-        const int rows = is_wgrad(MODE) ? min(BT, p.N - c.b0) : c.nrows, cols = min(kATile, na - c.a0);
-        const rsrc_t r = make_rsrc(p.out + (row0 * ld + c.a0) * es, (uint32_t)(((size_t)(rows - 1) * ld + cols) * es));
+        const int rows = partial ? BT : (is_wgrad(MODE) ? min(BT, p.N - c.b0) : c.nrows);
+        const int cols = partial ? kATile : min(kATile, na - c.a0);
+        uint8_t* base = partial ? (uint8_t*)(p.partial + (size_t)c.slot * (kATile * BT)) : p.out + (row0 * ld + c.a0) * es;
+        const rsrc_t r = make_rsrc(base, (uint32_t)(((size_t)(rows - 1) * ld + cols) * es));
         // rows past the tile's are past the resource by themselves; values past
         // the operand's end (a partial tile only) are sent there
         const int fresh = mm_fresh(lane), a0 = 64 * wi + 4 * (fresh >> 4);
@@ -622,14 +715,14 @@ void grouped_mm_kernel(MmP p) {
             for (int t = 0; t < 4; ++t) {
                 f32x4 v = acc[u][t];
                 const uint32_t ot = cols == kATile || a0 + 16 * t < cols ? o + (uint32_t)(16 * t * es) : kMmInvalid;
-                if (is_wgrad(MODE) && p.out_f32) {
-                    if (p.accumulate) {
+                if (f32) {
+                    if (add) {
                         const f32x4 e = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, ot, 0, 0));
                         v = f32x4{v[0] + e[0], v[1] + e[1], v[2] + e[2], v[3] + e[3]};
                     }
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), r, ot, 0, 0);
                 } else {
-                    if (is_wgrad(MODE) && p.accumulate) {
+                    if (add) {
                         const u32x2_t e = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, ot, 0, 0));
                         v[0] += lo16(e.x, f16); v[1] += hi16(e.x, f16);
                         v[2] += lo16(e.y, f16); v[3] += hi16(e.y, f16);
@@ -645,22 +738,21 @@ void grouped_mm_kernel(MmP p) {
     // --------------------------------------------------------------- loop
     MmKept kept;
     if constexpr (mm_kind(MODE) == kWgrad8) {
-        kept.item = slot;
-        kept.step = kept.kt = 0;
+        kept.round = kept.step = kept.kt = 0;
         kept.held = false;
-        kept_open<NB>(p, wh, kept);
+        kept_open<NB>(p, tb, wh, kept);
         if (kept.live) kept_src(p, wh, kept);
-        if (kept.live) kept_load<NB>(p, wh, kept);
+        if (kept.live) kept_load<NB>(p, tb, wh, kept);
         if (kept.held) kept_write(wh, kept, smem);
-        if (kept.live) kept_load<NB>(p, wh, kept);
+        if (kept.live) kept_load<NB>(p, tb, wh, kept);
     }
-    mm_start<EL, MODE, NB>(p, pass_off, wh, R, slot);
+    mm_start<EL, MODE, NB>(p, tb, wh, R);
     #pragma unroll 1
     for (int i = 0; i < NST; ++i) {     // the last one's second b half follows in the first turn
         mm_requests<EL, MODE, NB, 1, 0, mm_turn_requests(EL, MODE, NB, 1)>(p, wh, R, smem);
         if (i < NST - 1) {
             mm_requests<EL, MODE, NB, 0, 0, mm_turn_requests(EL, MODE, NB, 0)>(p, wh, R, smem);
-            mm_advance<EL, MODE, NB>(p, pass_off, wh, R);
+            mm_advance<EL, MODE, NB>(p, tb, wh, R);
         }
     }
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
@@ -686,13 +778,13 @@ void grouped_mm_kernel(MmP p) {
         else __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + KEPT, 15));
     };
     int step = 0;
-    if constexpr (EL == kElFp8) fwn = load_fw(mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, pass_off, at, slot)), 0);
-    for (int item = slot; item < n_items; item += grid) {
+    if constexpr (EL == kElFp8) fwn = load_fw(mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, tb, at, slot)), 0);
+    for (int round = 0, item; (item = mm_nth<MODE>(round, grid, slot)) < n_items; ++round) {
         // the item is the one being requested, unless items are very short
-        const MmItem c = R.live && R.at == item ? R.c : mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, pass_off, at, item));
+        const MmItem c = R.live && R.at == item ? R.c : mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, tb, at, item));
         if constexpr (EL == kElFp8) {   // the next item's scales are loaded an item ahead
             fwv = fwn;
-            if (item + grid < n_items) fwn = load_fw(mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, pass_off, at, item + grid)), 0);
+            if (item + grid < n_items) fwn = load_fw(mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, tb, at, item + grid)), 0);
         }
         clear();
         #pragma unroll 1
@@ -702,9 +794,9 @@ void grouped_mm_kernel(MmP p) {
                 read_frags(step, h, c, kt);
                 if constexpr (mm_kind(MODE) == kWgrad8 && h == 1) {
                     if (kept.held) kept_write(wh, kept, smem + (kept.step % NST) * Geo::Stage);
-                    if (kept.live) kept_load<NB>(p, wh, kept);
+                    if (kept.live) kept_load<NB>(p, tb, wh, kept);
                 }
-                if constexpr (h == 1) mm_advance<EL, MODE, NB>(p, pass_off, wh, R);
+                if constexpr (h == 1) mm_advance<EL, MODE, NB>(p, tb, wh, R);
                 // the reads end before this wave's products and so a turn before
                 // the stage is requested again; only writes to LDS must be done here
                 if constexpr (mm_kind(MODE) == kWgrad8) __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
@@ -741,7 +833,7 @@ void grouped_mm_kernel(MmP p) {
 template <int EL, int MODE, int NB>
 int launch_mm(const MmP& p, int max_items, hipStream_t stream) {
     using Geo = MmGeom<EL, NB>;
-    const size_t lds = Geo::Lds(is_wgrad(MODE) ? 0 : p.G);
+    const size_t lds = Geo::Lds(p.G, is_wgrad(MODE));
     auto* k = &grouped_mm_kernel<EL, MODE, NB>;
     static bool ready[64] = {false};
     int dev = 0;
@@ -758,14 +850,58 @@ int launch_mm(const MmP& p, int max_items, hipStream_t stream) {
 }
 
 // launchers
-// Tile height by the expected rows of a group: 256 from 129 on, 128 below, and
-// the kernels for few rows up to kRowsMax.
 template <int EL, int MODE>
-int launch_mm_rows(const MmP& p, int kind, hipStream_t stream) {
-    const int rows = (p.R_max + p.G - 1) / p.G;
-    if (rows <= 64) return moe_launch_mm_rows(&p, EL, kind, stream);
+int launch_mm_rows(const MmP& p, int kind, int rows, hipStream_t stream) {
+    if (rows <= 64) return moe_launch_mm_rows(&p, EL, kind, rows, stream);
     return rows > 128 ? launch_mm<EL, MODE, 8>(p, mm_items(p, 256), stream)
                       : launch_mm<EL, MODE, 4>(p, mm_items(p, 128), stream);
+}
+
+// The kernel of a product and its split along K, from sizes alone (uniform
+// groups assumed: the counts are on the device). Time in rounds of workgroups,
+// nk K-tiles each, at the measured microseconds per K-tile (G = 1, K = 4096,
+// N = 4096 and 1024, R from 16 to 16384; W [K, N] and FP8 cost 1.1 to 1.3 times
+// as much in all four, so their choice is the same):
+//   256 rows x 256   1.6 (1.3 with few workgroups)   1 workgroup per CU
+//   128 rows x 256   1.0 (0.9)                       1
+//    64 rows x  64   0.54 for two on a CU (0.5)      2
+//    32 rows x  64   0.48 for two on a CU (0.45)     2
+// e.g. 512 x 4096 x 4096: 84, 58, 40 and 67 us; 4096 x 4096 x 4096: 109, 127,
+// 281, 496. Splitting (64- and 32-row tiles only) costs the joining launch and
+// its partial sums, about 5 us.
+struct MmPlan { int rows, parts; };
+MmPlan mm_plan(bool fp8, int R_max, int G, int N, int K) {
+    static const int kRowsOf[4] = {256, 128, 64, 32};
+    static const double kTile[4] = {1.6, 1.0, 0.54, 0.48}, kFew[4] = {1.3, 0.9, 0.5, 0.45};
+    if (R_max <= 0) return MmPlan{32, 1};
+    const int cus = device_cu_count(), active = std::max(1, std::min(G, R_max));
+    const int64_t per = ((int64_t)R_max + active - 1) / active;          // rows of a group
+    const int nk = (K + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
+    MmPlan best{256, 1};
+    double least = 1e30;
+    for (int i = 0; i < 4; ++i) {
+        const int cols = i < 2 ? 256 : 64, slots = i < 2 ? cus : 2 * cus;
+        const int64_t items = active * ((per + kRowsOf[i] - 1) / kRowsOf[i]) * ((N + cols - 1) / cols);
+        const int most = i < 2 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>({slots / items, nk / 8, 16}));
+        for (int parts = 1; parts <= most; parts = parts < most && 2 * parts > most ? most : 2 * parts) {
+            const int64_t rounds = (items * parts + slots - 1) / slots;
+            const double tile = items * parts <= cus ? kFew[i] : kTile[i];
+            const double t = (double)rounds * ((nk + parts - 1) / parts * tile + (i < 2 ? 4.0 : 1.0)) + (parts > 1 ? 5.0 : 0.0);
+            if (t < least) { least = t; best = MmPlan{kRowsOf[i], parts}; }
+        }
+    }
+    return best;
+}
+
+// K-tiles per part of a weight gradient: a group is split when its K-tiles
+// exceed a workgroup's even share of the whole, so that one large group, or
+// few tiles, do not leave most workgroups idle. 0: no group can be that large.
+// A split tile costs a write and a read of 256 KiB per part.
+int wgrad_part(int R_max, int G, int N, int K) {
+    const int64_t tiles = (int64_t)((N + 255) / 256) * ((K + 255) / 256), most = ((int64_t)R_max + 63) / 64;
+    const int64_t share = (tiles * (most + std::min(G, R_max) / 2) + device_cu_count() - 1) / device_cu_count();
+    const int64_t part = std::max<int64_t>(share, 8);
+    return part >= most ? 0 : (int)part;
 }
 
 template <int EL>
@@ -779,8 +915,18 @@ int launch_wgrad(const MmP& p, int items, hipStream_t stream) {
 }  // namespace
 
 size_t moe_mm_workspace_bytes(int kind, bool fp8, int R_max, int G, int N, int K) {
-    (void)kind; (void)fp8; (void)R_max; (void)G; (void)N; (void)K;
-    return 0;
+    if (kind == 2) {
+        const int part = wgrad_part(R_max, G, N, K);
+        if (part == 0) return 0;
+        // groups longer than a part are split into fewer than twice as many
+        // parts as their K-tiles make whole ones (partly filled K-tiles, one a
+        // group, included)
+        const int64_t tiles = (int64_t)((N + 255) / 256) * ((K + 255) / 256);
+        const int64_t ktiles = ((int64_t)R_max + 63) / 64 + std::min(G, R_max);
+        return (size_t)(tiles * (2 * ktiles / part)) * 65536 * 4;
+    }
+    const MmPlan plan = mm_plan(fp8, R_max, G, N, K);
+    return plan.parts > 1 ? (size_t)plan.parts * R_max * N * 4 : 0;
 }
 
 int moe_launch_mm(const MmCall& c, hipStream_t stream) {
@@ -808,11 +954,24 @@ int moe_launch_mm(const MmCall& c, hipStream_t stream) {
         if (c.dy_src) p.dy_bytes = (uint32_t)((int64_t)(c.dy_rows - 1) * c.ld_dy * 2 + (int64_t)c.N * 2);
         const int64_t tiles = (int64_t)c.G * ((c.N + 255) / 256) * ((c.K + 255) / 256);
         const int items = (int)std::min<int64_t>(tiles, 1 << 30);
+        p.part = wgrad_part(c.R_max, c.G, c.N, c.K);
+        p.partial = (float*)c.ws;
+        p.max_slots = (int)(moe_mm_workspace_bytes(2, false, c.R_max, c.G, c.N, c.K) / (65536 * 4));
+        int e;
+        const int grid = p.part > 0 ? 1 << 30 : items;       // (split groups have more items than tiles)
         if (c.xs)                        // (the 8-bit rows' gather is no part of the request state)
-            return c.dy_src ? launch_mm<kElBf16, kWgrad8 | kGatherDy, 8>(p, items, stream)
-                            : launch_mm<kElBf16, kWgrad8, 8>(p, items, stream);
-        return f16 ? launch_wgrad<kElF16>(p, items, stream) : launch_wgrad<kElBf16>(p, items, stream);
+            e = c.dy_src ? launch_mm<kElBf16, kWgrad8 | kGatherDy, 8>(p, grid, stream)
+                         : launch_mm<kElBf16, kWgrad8, 8>(p, grid, stream);
+        else
+            e = f16 ? launch_wgrad<kElF16>(p, grid, stream) : launch_wgrad<kElBf16>(p, grid, stream);
+        if (e || p.part == 0) return e;
+        const dim3 join((unsigned)(tiles / c.G * 4), (unsigned)c.G);
+        wgrad_join_kernel<<<join, 256, 0, stream>>>(p);
+        return (int)hipGetLastError();
     }
+    const MmPlan plan = mm_plan(c.fp8, c.R_max, c.G, c.N, c.K);
+    p.parts = plan.parts;
+    p.partial = (float*)c.ws;
     p.w = (const uint8_t*)c.w;
     p.w_group = (size_t)c.N * c.K * eb;
     p.w_ld = (uint32_t)((c.kind == 1 ? c.N : c.K) * eb);
@@ -820,9 +979,9 @@ int moe_launch_mm(const MmCall& c, hipStream_t stream) {
         p.kb = (c.K + 127) / 128; p.nb = (c.N + 127) / 128;
         p.xs = c.xs; p.ws = c.wscale;
         if (c.x_src) p.xs_bytes = (uint32_t)((int64_t)c.x_rows * p.kb * 4);
-        return launch_mm_rows<kElFp8, kMmNK>(p, 0, stream);
+        return launch_mm_rows<kElFp8, kMmNK>(p, 0, plan.rows, stream);
     }
     if (c.kind == 0)
-        return f16 ? launch_mm_rows<kElF16, kMmNK>(p, 0, stream) : launch_mm_rows<kElBf16, kMmNK>(p, 0, stream);
-    return f16 ? launch_mm_rows<kElF16, kMmKN>(p, 1, stream) : launch_mm_rows<kElBf16, kMmKN>(p, 1, stream);
+        return f16 ? launch_mm_rows<kElF16, kMmNK>(p, 0, plan.rows, stream) : launch_mm_rows<kElBf16, kMmNK>(p, 0, plan.rows, stream);
+    return f16 ? launch_mm_rows<kElF16, kMmKN>(p, 1, plan.rows, stream) : launch_mm_rows<kElBf16, kMmKN>(p, 1, plan.rows, stream);
 }

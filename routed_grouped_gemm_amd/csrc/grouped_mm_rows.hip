@@ -32,18 +32,31 @@ struct RowsGeom {
 // the requests of a wave, one K-tile after another through all items
 template <int NQ>
 struct RowsReq {
-    int item, kt, step;
+    int item, kt, k1, step;             // K-tiles [kt, k1) of the item are still to come
     bool live;
     MmItem c;
     uint32_t row[NQ], srow;
 };
 
+// Item number `item`: its tile, and the K-tiles [k0, k1) of its part. A part's
+// tiles go one after another before the next part's.
+template <int EL, int MODE, int BT>
+MOE_DEV MmItem rows_item(const MmP& p, const MmTables& tb, const MmWhere& wh, int item, int& part, int& k0, int& k1) {
+    const int tiles = wh.n_items / p.parts;
+    part = __builtin_amdgcn_readfirstlane(item / tiles);
+    const MmItem c = mm_scalar(mm_decode<EL, MODE, BT, kRowsA>(p, tb, wh.at, item - part * tiles));
+    k0 = __builtin_amdgcn_readfirstlane(c.nk * part / p.parts);
+    k1 = __builtin_amdgcn_readfirstlane(c.nk * (part + 1) / p.parts);
+    return c;
+}
+
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void rows_open(const MmP& p, const int* pass_off, const MmWhere& wh, RowsReq<NQ>& R) {
+MOE_DEV void rows_open(const MmP& p, const MmTables& tb, const MmWhere& wh, RowsReq<NQ>& R) {
     constexpr int BT = 16 * NB;
     R.live = R.item < wh.n_items;
     if (!R.live) return;
-    R.c = mm_scalar(mm_decode<EL, MODE, BT, kRowsA>(p, pass_off, wh.at, R.item));
+    int part;
+    R.c = rows_item<EL, MODE, BT>(p, tb, wh, R.item, part, R.kt, R.k1);
     R.item += wh.grid;
     // source rows without a branch: past the item (and without a source
     // array, whose resource is then empty) the loads return 0
@@ -65,7 +78,7 @@ MOE_DEV void rows_open(const MmP& p, const int* pass_off, const MmWhere& wh, Row
 
 // request one K-tile into its stage, then move on (nothing once the items have ended)
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void rows_request(const MmP& p, const int* pass_off, const MmWhere& wh, RowsReq<NQ>& R, uint8_t* smem) {
+MOE_DEV void rows_request(const MmP& p, const MmTables& tb, const MmWhere& wh, RowsReq<NQ>& R, uint8_t* smem) {
     using Geo = RowsGeom<EL, NB>;
     constexpr int EB = EL == kElFp8 ? 1 : 2, BT = Geo::BT;
     if (!R.live) return;
@@ -113,9 +126,9 @@ MOE_DEV void rows_request(const MmP& p, const int* pass_off, const MmWhere& wh, 
     }
     ++R.step;
     const int kt = R.kt + 1;
-    const bool last = kt == c.nk;
-    R.kt = last ? 0 : kt;
-    if (last) rows_open<EL, MODE, NB>(p, pass_off, wh, R);
+    const bool last = kt == R.k1;
+    R.kt = kt;
+    if (last) rows_open<EL, MODE, NB>(p, tb, wh, R);
 }
 
 template <int EL, int MODE, int NB>
@@ -124,42 +137,44 @@ void grouped_mm_rows_kernel(MmP p) {
     using Geo = RowsGeom<EL, NB>;
     constexpr int BT = Geo::BT, NST = Geo::NST;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    int* pass_off = (int*)(smem + NST * Geo::Stage);         // [G + 1] passes before group g
+    int* const tab = (int*)(smem + NST * Geo::Stage);        // [G + 1] passes before group g
+    const MmTables tb{tab, nullptr, nullptr};
 
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int q = lane >> 4, j = lane & 15;
     const int at = (p.N + kRowsA - 1) / kRowsA;
-    if (w == 0) mm_passes(p, BT, lane, pass_off);
+    if (w == 0) mm_passes(p, BT, lane, tab);
     __syncthreads();
-    const int n_items = __builtin_amdgcn_readfirstlane(pass_off[p.G]) * at;
+    const int n_items = __builtin_amdgcn_readfirstlane(tab[p.G]) * at * p.parts;
     const int grid = gridDim.x;
     const int slot = (grid % 8 == 0) ? (blockIdx.x % 8) * (grid / 8) + blockIdx.x / 8 : blockIdx.x;
     if (slot >= n_items) return;
-    const MmWhere wh{n_items, at, grid, lane, w};
+    const MmWhere wh{n_items, at, grid, slot, lane, w};
 
     RowsReq<Geo::NQ> R;
     R.item = slot;
-    R.kt = R.step = 0;
-    rows_open<EL, MODE, NB>(p, pass_off, wh, R);
+    R.step = 0;
+    rows_open<EL, MODE, NB>(p, tb, wh, R);
     #pragma unroll 1
-    for (int i = 0; i < NST - 1; ++i) rows_request<EL, MODE, NB>(p, pass_off, wh, R, smem);
+    for (int i = 0; i < NST - 1; ++i) rows_request<EL, MODE, NB>(p, tb, wh, R, smem);
 
     int step = 0;
     for (int item = slot; item < n_items; item += grid) {
-        const MmItem c = mm_scalar(mm_decode<EL, MODE, BT, kRowsA>(p, pass_off, at, item));
+        int part, k0, k1;
+        const MmItem c = rows_item<EL, MODE, BT>(p, tb, wh, item, part, k0, k1);
         const float* ws = EL == kElFp8 ? p.ws + ((size_t)c.g * p.nb + (c.a0 >> 7)) * p.kb : nullptr;
         f32x4 acc[NB];
         #pragma unroll
         for (int u = 0; u < NB; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
         #pragma unroll 1
-        for (int kt = 0; kt < c.nk; ++kt, ++step) {
+        for (int kt = k0; kt < k1; ++kt, ++step) {
             // this K-tile has landed (newer ones stay in flight), and behind
             // the barrier the previous one has been read: its stage is free
             if (R.live) __builtin_amdgcn_s_waitcnt(waitcnt_imm(Geo::Loads * (NST - 2), 15));
             else __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
             bare_barrier();
-            rows_request<EL, MODE, NB>(p, pass_off, wh, R, smem);
+            rows_request<EL, MODE, NB>(p, tb, wh, R, smem);
             const uint8_t* st = smem + (step % NST) * Geo::Stage;
             i32x4 fp[2], fq[2][NB];
             float fs[NB], fw = 0.f;
@@ -202,10 +217,38 @@ void grouped_mm_rows_kernel(MmP p) {
         #pragma unroll
         for (int u = 0; u < NB; ++u) {
             const int b = 16 * u + j;
-            if (b < c.nrows && a < p.N)
-                *(u32x2_t*)((uint16_t*)p.out + (size_t)(c.r0 + b) * p.out_ld + a) =
-                    u32x2_t{pack16(acc[u][0], acc[u][1], f16), pack16(acc[u][2], acc[u][3], f16)};
+            if (b < c.nrows && a < p.N) {
+                const size_t row = (size_t)(c.r0 + b);
+                if (p.parts > 1)
+                    *(f32x4*)(p.partial + ((size_t)part * p.R_max + row) * p.N + a) = acc[u];
+                else
+                    *(u32x2_t*)((uint16_t*)p.out + row * p.out_ld + a) =
+                        u32x2_t{pack16(acc[u][0], acc[u][1], f16), pack16(acc[u][2], acc[u][3], f16)};
+            }
         }
+    }
+}
+
+// The sum of a split product's parts, in their order, rounded once: 4 values
+// per lane, for the rows that belong to a group.
+__global__ __launch_bounds__(256)
+void mm_join_kernel(MmP p) {
+    int lo, hi, end;
+    group_rows(p, 0, lo, hi);
+    group_rows(p, p.G - 1, hi, end);
+    const int n4 = p.N / 4;
+    const int64_t total = (int64_t)p.R_max * n4, stride = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += stride) {
+        const int row = (int)(i / n4), a = (int)(i - (int64_t)row * n4) * 4;
+        if (row < lo || row >= end) continue;
+        const float* src = p.partial + (size_t)row * p.N + a;
+        f32x4 v = *(const f32x4*)src;
+        for (int s = 1; s < p.parts; ++s) {
+            const f32x4 e = *(const f32x4*)(src + (size_t)s * p.R_max * p.N);
+            v = f32x4{v[0] + e[0], v[1] + e[1], v[2] + e[2], v[3] + e[3]};
+        }
+        *(u32x2_t*)((uint16_t*)p.out + (size_t)row * p.out_ld + a) =
+            u32x2_t{pack16(v[0], v[1], p.out_f16), pack16(v[2], v[3], p.out_f16)};
     }
 }
 
@@ -222,22 +265,27 @@ int launch_rows(const MmP& p, hipStream_t stream) {
         if (e != hipSuccess) return (int)e;
         if (dev >= 0 && dev < 64) ready[dev] = true;
     }
-    const int grid = std::max(1, std::min(mm_items(p, Geo::BT, kRowsA), 2 * device_cu_count()));
+    const int64_t items = (int64_t)mm_items(p, Geo::BT, kRowsA) * p.parts;
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(items, 2 * device_cu_count()));
     k<<<grid, kRowsThreads, (size_t)(Geo::Stage * Geo::NST + (p.G + 1) * 4), stream>>>(p);
+    if (p.parts == 1) return (int)hipGetLastError();
+    e = hipGetLastError();
+    if (e != hipSuccess) return (int)e;
+    const int64_t lanes = (int64_t)p.R_max * (p.N / 4);
+    mm_join_kernel<<<(int)std::min<int64_t>((lanes + 255) / 256, 4 * device_cu_count()), 256, 0, stream>>>(p);
     return (int)hipGetLastError();
 }
 
 template <int EL, int MODE>
-int launch_few(const MmP& p, hipStream_t stream) {
-    const int rows = (p.R_max + p.G - 1) / p.G;
+int launch_few(const MmP& p, int rows, hipStream_t stream) {
     return rows > 32 ? launch_rows<EL, MODE, 4>(p, stream) : launch_rows<EL, MODE, 2>(p, stream);
 }
 
 }  // namespace
 
-int moe_launch_mm_rows(const void* params, int el, int kind, hipStream_t stream) {
+int moe_launch_mm_rows(const void* params, int el, int kind, int rows, hipStream_t stream) {
     const MmP& p = *(const MmP*)params;
-    if (el == kElFp8) return launch_few<kElFp8, kMmNK>(p, stream);
-    if (el == kElF16) return kind ? launch_few<kElF16, kMmKN>(p, stream) : launch_few<kElF16, kMmNK>(p, stream);
-    return kind ? launch_few<kElBf16, kMmKN>(p, stream) : launch_few<kElBf16, kMmNK>(p, stream);
+    if (el == kElFp8) return launch_few<kElFp8, kMmNK>(p, rows, stream);
+    if (el == kElF16) return kind ? launch_few<kElF16, kMmKN>(p, rows, stream) : launch_few<kElF16, kMmNK>(p, rows, stream);
+    return kind ? launch_few<kElBf16, kMmKN>(p, rows, stream) : launch_few<kElBf16, kMmNK>(p, rows, stream);
 }

@@ -84,6 +84,14 @@ MM = [
     ([0, 0, 0], 128, 128),
     ([5] * 70, 72, 96),
     ([1, 2, 700, 3], 264, 520),
+    # few tiles: the reduction axis is split and joined
+    ([16], 1024, 2048),
+    ([5, 0, 9], 136, 4096),
+    ([70], 256, 4104),
+    ([300], 264, 1544),
+    ([3000], 264, 520),
+    ([2000, 10, 1000], 256, 264),
+    ([0, 1300, 0, 0, 64, 1], 72, 136),
 ]
 
 
@@ -208,7 +216,8 @@ def decode_w(codes, scales):
 
 FP8 = [([1], 8, 16), ([0, 1, 0, 2, 0], 64, 80), ([3, 0, 5, 8], 136, 208), ([16, 1, 0, 15], 512, 512),
        ([17, 31, 33, 2], 264, 1008), ([64, 65, 40, 0], 256, 336), ([100, 128, 129, 60], 520, 272),
-       ([257, 300, 0, 511, 256], 776, 464), ([1000, 24], 1416, 2048), ([0, 0], 128, 128)]
+       ([257, 300, 0, 511, 256], 776, 464), ([1000, 24], 1416, 2048), ([0, 0], 128, 128),
+       ([16], 1024, 4096), ([5, 0, 9], 136, 8208), ([300], 264, 3088), ([600, 3], 520, 10256)]
 
 
 @pytest.mark.parametrize("dtype", T16)

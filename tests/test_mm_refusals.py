@@ -56,6 +56,24 @@ def test_grouped_wgrad():
     assert call(dy=F + 2) == SHAPE and call(x=F + 8) == SHAPE
 
 
+def test_workspace_sizes():
+    """Pure host functions, defined at every size: 0 where nothing is split or
+    the sizes are refused, bounded where a product is."""
+    lib = _lib.load()
+    for f in (lib.moe_grouped_mm_workspace_size, lib.moe_grouped_wgrad_workspace_size,
+              lib.moe_grouped_mm_fp8_workspace_size):
+        assert f(0, 4, 256, 128) == 0
+        assert f(-1, 4, 256, 128) == 0 and f(64, 0, 256, 128) == 0 and f(64, 4, 250, 128) == 0
+        for R in (1, 15, 64, 1000, 16384, 1 << 20):
+            for G in (1, 8, 2049):
+                for N, K in ((8, 16), (256, 256), (4096, 7168), (1 << 20, 1 << 20)):
+                    assert f(R, G, N, K) < 1 << 38, (R, G, N, K)
+    assert lib.moe_grouped_mm_workspace_size(16, 1, 1024, 7168) > 0
+    assert lib.moe_grouped_mm_workspace_size(16384, 8, 4096, 4096) == 0
+    assert lib.moe_grouped_wgrad_workspace_size(16384, 1, 256, 256) > 0
+    assert lib.moe_grouped_wgrad_workspace_size(4096, 64, 4096, 4096) == 0
+
+
 def test_quantisers():
     lib = _lib.load()
 
