@@ -209,8 +209,9 @@ MOE_DEV MmItem mm_decode(const MmP& p, const MmTables& tb, int at, int item) {
         lo = __builtin_amdgcn_readfirstlane(lo);
         const int rows = __builtin_amdgcn_readfirstlane(hi) - lo, nk = (rows + KT - 1) / KT;
         // the group's K-tiles in `parts` nearly equal runs
-        const int k0 = __builtin_amdgcn_readfirstlane((int)((int64_t)nk * part / parts));
-        c.nk = __builtin_amdgcn_readfirstlane((int)((int64_t)nk * (part + 1) / parts)) - k0;
+        const int each = __builtin_amdgcn_readfirstlane(nk / parts), more = nk - each * parts;
+        const int k0 = part * each + min(part, more);
+        c.nk = each + (part < more ? 1 : 0);
         c.r0 = lo + k0 * KT;
         c.nrows = min(rows - k0 * KT, c.nk * KT);
         if (slot0 >= 0) c.slot = slot0 + part * (at * bt) + l;

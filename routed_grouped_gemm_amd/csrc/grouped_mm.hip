@@ -693,12 +693,13 @@ void grouped_mm_kernel(MmP p) {
     // Every lane stores, past an edge outside the resource (dropped), so a wave
     // always issues 4 NB stores and the next K-tile's waits can leave them in
     // flight.
-    auto store = [&](const MmItem& c, auto f16_) __attribute__((always_inline)) {
-        constexpr int f16 = decltype(f16_)::value;
+    // (the variants are compiled apart: with a run-time choice inside, the waits
+    // of the adding variant's loads end up before every store of the others)
+    auto store = [&](const MmItem& c, auto f16_, auto f32_, auto add_) __attribute__((always_inline)) {
+        constexpr int f16 = decltype(f16_)::value, es = decltype(f32_)::value ? 4 : 2;
+        constexpr bool add = decltype(add_)::value;
         // a part of a split group goes to its tile of partial sums
-        const bool partial = is_wgrad(MODE) && c.slot >= 0, f32 = is_wgrad(MODE) && (p.out_f32 || partial);
-        const bool add = is_wgrad(MODE) && p.accumulate && !partial;
-        const int es = f32 ? 4 : 2;
+        const bool partial = is_wgrad(MODE) && c.slot >= 0;
         const size_t ld = partial ? kATile : (is_wgrad(MODE) ? (size_t)p.K : p.out_ld);
         const size_t row0 = is_wgrad(MODE) ? (size_t)c.g * p.N + c.b0 : (size_t)c.r0;
         const int rows = partial ? BT : (is_wgrad(MODE) ? min(BT, p.N - c.b0) : c.nrows);
@@ -714,15 +715,15 @@ void grouped_mm_kernel(MmP p) {
             #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 f32x4 v = acc[u][t];
-                const uint32_t ot = cols == kATile || a0 + 16 * t < cols ? o + (uint32_t)(16 * t * es) : kMmInvalid;
-                if (f32) {
-                    if (add) {
+                const uint32_t ot = a0 + 16 * t < cols ? o + (uint32_t)(16 * t * es) : kMmInvalid;
+                if constexpr (es == 4) {
+                    if constexpr (add) {
                         const f32x4 e = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, ot, 0, 0));
                         v = f32x4{v[0] + e[0], v[1] + e[1], v[2] + e[2], v[3] + e[3]};
                     }
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, v), r, ot, 0, 0);
                 } else {
-                    if (add) {
+                    if constexpr (add) {
                         const u32x2_t e = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, ot, 0, 0));
                         v[0] += lo16(e.x, f16); v[1] += hi16(e.x, f16);
                         v[2] += lo16(e.y, f16); v[3] += hi16(e.y, f16);
@@ -819,11 +820,19 @@ void grouped_mm_kernel(MmP p) {
         // (an item without K-tiles stores between two others' stores: not counted)
         stored = (is_wgrad(MODE) && (p.accumulate || c.nk == 0)) ? 0 : NST - 1;
         if (!is_wgrad(MODE) || c.nk > 0 || !p.accumulate) {
+            constexpr std::integral_constant<int, EL == kElF16> same{};
+            constexpr std::true_type yes{};
+            constexpr std::false_type no{};
             if constexpr (EL == kElFp8) {
-                if (p.out_f16) store(c, std::integral_constant<int, 1>{});
-                else store(c, std::integral_constant<int, 0>{});
+                if (p.out_f16) store(c, std::integral_constant<int, 1>{}, no, no);
+                else store(c, same, no, no);
+            } else if constexpr (is_wgrad(MODE)) {
+                if (c.slot >= 0 || (p.out_f32 && !p.accumulate)) store(c, same, yes, no);
+                else if (p.out_f32) store(c, same, yes, yes);
+                else if (p.accumulate) store(c, same, no, yes);
+                else store(c, same, no, no);
             } else {
-                store(c, std::integral_constant<int, EL == kElF16>{});
+                store(c, same, no, no);
             }
         }
     }
