@@ -89,13 +89,6 @@ MOE_DEV u32x2_t read_tr16(const mm_lds_s16x4* __restrict__ at) {
     return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(const_cast<mm_lds_s16x4*>(at)));
 }
 
-// a pointer known to be the same in every lane, as a scalar
-MOE_DEV const uint8_t* uniform_ptr(const uint8_t* p) {
-    const uint64_t v = (uint64_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
-    return (const uint8_t*)(((uint64_t)hi << 32) | lo);
-}
-
 // s_waitcnt immediate: vmcnt <= vm, lgkmcnt <= lgkm (15: no wait)
 constexpr int waitcnt_imm(int vm, int lgkm) { return (vm & 15) | (7 << 4) | (lgkm << 8) | ((vm >> 4) << 14); }
 

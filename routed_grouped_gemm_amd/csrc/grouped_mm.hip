@@ -167,7 +167,10 @@ MOE_DEV void mm_slow_bounds(const uint8_t*& base, uint32_t& bytes, uint32_t ld, 
                             int ncols) {
     if (!mapped) {
         base += (size_t)first * ld + (size_t)c0 * 2;
-        bytes = (uint32_t)(max(min(krem, 64), 1) - 1) * ld + (uint32_t)(min(ncols - c0, 256) * 2);
+        // (a scalar again: the clamp becomes a vector instruction, and a
+        // descriptor in vector registers a loop over lanes at every request)
+        const int rows = __builtin_amdgcn_readfirstlane(max(min(krem, 64), 1));
+        bytes = (uint32_t)(rows - 1) * ld + (uint32_t)(min(ncols - c0, 256) * 2);
     }
 }
 
@@ -286,10 +289,6 @@ MOE_DEV void mm_advance(const MmP& p, const MmTables& tb, const MmWhere& wh, MmR
     }
     if constexpr (is_wgrad(MODE)) {
         if (R.live && R.kt + 1 < R.c.nk) mm_load_src<MODE>(p, wh, R.c, R.kt + 1, R.psrc, R.qsrc);
-        R.pb = uniform_ptr(R.pb);
-        R.qb = uniform_ptr(R.qb);
-        R.pn = (uint32_t)__builtin_amdgcn_readfirstlane((int)R.pn);
-        R.qn = (uint32_t)__builtin_amdgcn_readfirstlane((int)R.qn);
     }
 }
 template <int EL, int MODE, int NB, int NQ>
@@ -902,14 +901,27 @@ MmPlan mm_plan(bool fp8, int R_max, int G, int N, int K) {
     return best;
 }
 
-// K-tiles per part of a weight gradient: a group is split when its K-tiles
-// exceed a workgroup's even share of the whole, so that one large group, or
-// few tiles, do not leave most workgroups idle. 0: no group can be that large.
-// A split tile costs a write and a read of 256 KiB per part.
+// K-tiles per part of a weight gradient (0: no group can be longer): groups
+// longer than that are split, so that few tiles, or one large group, do not
+// leave most workgroups idle. For groups of equal size, the number of parts
+// with the least time in rounds of workgroups (1.5 us a K-tile, 10 a tile) and
+// in joining (256 KiB written and read per part and tile, at 4 TB/s); at least
+// a workgroup's even share of the whole, for the groups that are larger. E.g.
+// one group of 16384 rows, 2816 x 2048 (88 tiles, 256 K-tiles): 2 parts.
 int wgrad_part(int R_max, int G, int N, int K) {
+    if (R_max <= 0) return 0;
     const int64_t tiles = (int64_t)((N + 255) / 256) * ((K + 255) / 256), most = ((int64_t)R_max + 63) / 64;
-    const int64_t share = (tiles * (most + std::min(G, R_max) / 2) + device_cu_count() - 1) / device_cu_count();
-    const int64_t part = std::max<int64_t>(share, 8);
+    const int64_t cus = device_cu_count(), active = std::min(G, R_max);
+    const int64_t share = (tiles * (most + active / 2) + cus - 1) / cus, nk = (most + active - 1) / active;
+    int64_t part = nk;
+    double least = 1e30;
+    for (int64_t n = 1; n <= 64 && n * 8 <= nk + 7; ++n) {
+        const int64_t items = tiles * active * n;
+        const double t = (double)((items + cus - 1) / cus) * (1.5 * (double)((nk + n - 1) / n) + 10.0) +
+                         (n > 1 ? 5.0 + (double)items * 0.131 : 0.0);
+        if (t < least) { least = t; part = (nk + n - 1) / n; }
+    }
+    if (part == nk) part = std::max<int64_t>({nk, share, 8});
     return part >= most ? 0 : (int)part;
 }
 
