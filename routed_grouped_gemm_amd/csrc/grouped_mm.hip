@@ -74,6 +74,7 @@ struct MmReq {
     uint32_t nrow[2][NQ];               // contiguous b operand: sources of this lane's rows of the next item
     uint32_t srow[2], nsrow[2];         // fp8: byte offset of this lane's row of scales; next item's source
     uint32_t psrc, qsrc, npsrc, nqsrc;  // wgrad: source rows of the next K-tile's k, one k per lane % 8
+    uint32_t pc[2], qc[2];              // wgrad, gathered rows: byte offsets inside a row
     uint32_t po[4], qo[2][NQ];          // the next request's byte offsets,
     const uint8_t *pb, *qb, *sb;        // what they count from
     uint32_t pn, qn, sn;                // and the bytes that may be read there
@@ -162,52 +163,67 @@ MOE_DEV void mm_take(const MmP& p, const MmTables& tb, const MmWhere& wh, MmReq<
     mm_look<EL, MODE, NB>(p, tb, wh, R);
 }
 
-// bounds a request to 64 rows of the slow form, or to a whole gathered array
-MOE_DEV void mm_slow_bounds(const uint8_t*& base, uint32_t& bytes, uint32_t ld, bool mapped, int first, int krem, int c0,
-                            int ncols) {
-    if (!mapped) {
-        base += (size_t)first * ld + (size_t)c0 * 2;
-        // (a scalar again: the clamp becomes a vector instruction, and a
-        // descriptor in vector registers a loop over lanes at every request)
-        const int rows = __builtin_amdgcn_readfirstlane(max(min(krem, 64), 1));
-        bytes = (uint32_t)(rows - 1) * ld + (uint32_t)(min(ncols - c0, 256) * 2);
-    }
+// bounds a request to 64 rows of the slow form
+MOE_DEV void mm_slow_bounds(const uint8_t*& base, uint32_t& bytes, uint32_t ld, int first, int krem, int c0, int ncols) {
+    base += (size_t)first * ld + (size_t)c0 * 2;
+    // (a scalar again: the clamp becomes a vector instruction, and a
+    // descriptor in vector registers a loop over lanes at every request)
+    const int rows = __builtin_amdgcn_readfirstlane(max(min(krem, 64), 1));
+    bytes = (uint32_t)(rows - 1) * ld + (uint32_t)(min(ncols - c0, 256) * 2);
 }
 
 // Offsets of the next request (all past the resource once the items have
 // ended: such a request reads nothing and clears a stage nothing reads).
 // Slow form, RPI rows of LPR lanes each per request: k = 8 w + RPI i + lane / LPR.
-template <int COLS, int N>
-MOE_DEV void mm_slow_offsets(uint32_t (&o)[N], bool live, bool mapped, uint32_t src, uint32_t rows, uint32_t ld, int krem,
-                             int c0, int ncols, int half, int w, int lane) {
+template <int COLS>
+MOE_DEV int mm_slow_col(int i, int half, int w, int lane) {
     constexpr int RPI = 512 / COLS, LPR = 64 / RPI;
-    const int kl = lane / LPR, p32 = (lane % LPR) >> 1;
-    const uint32_t so = src < rows && 8 * w + (lane & 7) < krem ? src * ld : kMmNoRow;
+    const int k = 8 * w + RPI * i + lane / LPR, p32 = (lane % LPR) >> 1;
+    if constexpr (COLS == 256) return (p32 ^ tr_swz(k)) * 16 + (lane & 1) * 8;
+    const int ch = p32 ^ tr_swz_half(k);
+    return (ch >> 2) * 128 + half * 64 + (ch & 3) * 16 + (lane & 1) * 8;
+}
+template <int COLS, int N>
+MOE_DEV void mm_slow_offsets(uint32_t (&o)[N], bool live, uint32_t ld, int krem, int c0, int ncols, int half, int w, int lane) {
+    constexpr int RPI = 512 / COLS, LPR = 64 / RPI;
     #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int k = 8 * w + RPI * i + kl;
-        int col;
-        if constexpr (COLS == 256) {
-            col = (p32 ^ tr_swz(k)) * 16 + (lane & 1) * 8;
-        } else {
-            const int ch = p32 ^ tr_swz_half(k);
-            col = (ch >> 2) * 128 + half * 64 + (ch & 3) * 16 + (lane & 1) * 8;
-        }
-        const bool ok = live && c0 + col < ncols;
-        if (mapped) {
-            // (readlanes, not an LDS permute, which would wait behind the fragment reads)
-            uint32_t v = (uint32_t)__builtin_amdgcn_readlane((int)so, RPI * i);
-            #pragma unroll
-            for (int r = 1; r < RPI; ++r)
-                v = kl == r ? (uint32_t)__builtin_amdgcn_readlane((int)so, RPI * i + r) : v;
-            o[i] = ok ? v + (uint32_t)((c0 + col) * 2) : kMmInvalid;
-        } else {
-            o[i] = ok && k < krem ? (uint32_t)k * ld + (uint32_t)(col * 2) : kMmInvalid;
-        }
+        const int k = 8 * w + RPI * i + lane / LPR, col = mm_slow_col<COLS>(i, half, w, lane);
+        o[i] = live && k < krem && c0 + col < ncols ? (uint32_t)k * ld + (uint32_t)(col * 2) : kMmInvalid;
     }
 }
+// The same of gathered rows, every K-tile anew: so little of it as the products
+// of the other waves hide. The part inside a row stays for an item; it is the
+// same for requests i and i + 2 (COLS 256) or all (COLS 128, one per half).
+// Columns past the end and rows past the group or the array are all ones, which
+// the saturating sum keeps.
+template <int COLS>
+MOE_DEV void mm_gather_cols(uint32_t (&c)[2], int c0, int ncols, int w, int lane) {
+    #pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int col = COLS == 256 ? mm_slow_col<COLS>(i, 0, w, lane) : mm_slow_col<COLS>(0, i, w, lane);
+        c[i] = c0 + col < ncols ? (uint32_t)((c0 + col) * 2) : 0xFFFFFFFFu;
+    }
+}
+// byte offset of the row of this lane in request i, from one source row per lane % 8
+template <int COLS>
+MOE_DEV uint32_t mm_gather_row(uint32_t so, int i, int lane) {
+    // (readlanes and masks: an LDS permute would wait behind the fragment
+    // reads, and a choice between readlanes becomes a branch)
+    constexpr int RPI = 512 / COLS;
+    const uint32_t r0 = (uint32_t)__builtin_amdgcn_readlane((int)so, RPI * i), r1 = (uint32_t)__builtin_amdgcn_readlane((int)so, RPI * i + 1);
+    if constexpr (COLS == 256) return r0 ^ ((r0 ^ r1) & (uint32_t)((int)((uint32_t)lane << 26) >> 31));
+    const uint32_t r2 = (uint32_t)__builtin_amdgcn_readlane((int)so, RPI * i + 2), r3 = (uint32_t)__builtin_amdgcn_readlane((int)so, RPI * i + 3);
+    const uint32_t odd = (uint32_t)((int)((uint32_t)lane << 27) >> 31), high = (uint32_t)((int)((uint32_t)lane << 26) >> 31);
+    const uint32_t a = r0 ^ ((r0 ^ r1) & odd), b = r2 ^ ((r2 ^ r3) & odd);
+    return a ^ ((a ^ b) & high);
+}
+MOE_DEV uint32_t mm_gather_so(uint32_t src, uint32_t rows, uint32_t ld, int krem, int w, int lane) {
+    const uint32_t o = src * ld;
+    return (src < rows) & (8 * w + (lane & 7) < krem) ? o : 0xFFFFFFFFu;
+}
 template <int EL, int MODE, int NB, int NQ>
-MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, bool for_p, bool for_q) {
+MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, bool edge, bool for_p, bool for_q) {
     constexpr int EB = EL == kElFp8 ? 1 : 2;
     const int lane = mm_fresh(wh.lane), w = wh.w;
     const MmItem& c = R.c;
@@ -225,25 +241,43 @@ MOE_DEV void mm_offsets(const MmP& p, const MmWhere& wh, MmReq<NQ>& R, bool for_
             }
         } else if constexpr (MODE == kMmKN) {
             R.pb = p.w + (size_t)c.g * p.w_group;
-            mm_slow_bounds(R.pb, R.pn, p.w_ld, false, R.kt * 64, p.K - R.kt * 64, c.a0, p.N);
-            mm_slow_offsets<256>(R.po, R.live, false, 0, 0, p.w_ld, p.K - R.kt * 64, c.a0, p.N, 0, w, lane);
+            mm_slow_bounds(R.pb, R.pn, p.w_ld, R.kt * 64, p.K - R.kt * 64, c.a0, p.N);
+            mm_slow_offsets<256>(R.po, R.live, p.w_ld, p.K - R.kt * 64, c.a0, p.N, 0, w, lane);
+        } else if constexpr (mm_kind(MODE) == kWgrad && (MODE & kGatherX) != 0) {
+            if (edge) {
+                R.pb = p.x;
+                R.pn = R.live ? p.x_bytes : 0u;
+                mm_gather_cols<256>(R.pc, c.a0, p.K, w, lane);
+            }
+            const uint32_t so = mm_gather_so(R.psrc, p.x_rows, p.x_ld, c.nrows - R.kt * 64, w, lane);
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) R.po[i] = __builtin_elementwise_add_sat(mm_gather_row<256>(so, i, lane), R.pc[i & 1]);
         } else if constexpr (mm_kind(MODE) == kWgrad) {
             R.pb = p.x;
-            R.pn = p.x_bytes;
-            mm_slow_bounds(R.pb, R.pn, p.x_ld, (MODE & kGatherX) != 0, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.a0, p.K);
-            mm_slow_offsets<256>(R.po, R.live, (MODE & kGatherX) != 0, R.psrc, p.x_rows, p.x_ld, c.nrows - R.kt * 64, c.a0,
-                                 p.K, 0, w, lane);
+            mm_slow_bounds(R.pb, R.pn, p.x_ld, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.a0, p.K);
+            mm_slow_offsets<256>(R.po, R.live, p.x_ld, c.nrows - R.kt * 64, c.a0, p.K, 0, w, lane);
         }
     }
     if (!for_q) return;
-    if constexpr (is_wgrad(MODE)) {
+    if constexpr (is_wgrad(MODE) && (MODE & kGatherDy) != 0) {
+        if (edge) {
+            R.qb = p.dy;
+            R.qn = R.live ? p.dy_bytes : 0u;
+            mm_gather_cols<128>(R.qc, c.b0, p.N, w, lane);
+        }
+        const uint32_t so = mm_gather_so(R.qsrc, p.dy_rows, p.dy_ld, c.nrows - R.kt * 64, w, lane);
+        #pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+            const uint32_t row = mm_gather_row<128>(so, i, lane);
+            #pragma unroll
+            for (int h = 0; h < 2; ++h) R.qo[h][i] = __builtin_elementwise_add_sat(row, R.qc[h]);
+        }
+    } else if constexpr (is_wgrad(MODE)) {
         R.qb = p.dy;
-        R.qn = p.dy_bytes;
-        mm_slow_bounds(R.qb, R.qn, p.dy_ld, (MODE & kGatherDy) != 0, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.b0, p.N);
+        mm_slow_bounds(R.qb, R.qn, p.dy_ld, c.r0 + R.kt * 64, c.nrows - R.kt * 64, c.b0, p.N);
         #pragma unroll
         for (int h = 0; h < 2; ++h)
-            mm_slow_offsets<128>(R.qo[h], R.live, (MODE & kGatherDy) != 0, R.qsrc, p.dy_rows, p.dy_ld, c.nrows - R.kt * 64,
-                                 c.b0, p.N, h, w, lane);
+            mm_slow_offsets<128>(R.qo[h], R.live, p.dy_ld, c.nrows - R.kt * 64, c.b0, p.N, h, w, lane);
     } else {
         // gathered rows are addressed from the array's start, a group's own rows from the tile's first
         R.qb = (p.x_src ? p.x : p.x + (size_t)c.r0 * p.x_ld) + (size_t)(R.kt * 128);
@@ -276,7 +310,7 @@ MOE_DEV void mm_advance(const MmP& p, const MmTables& tb, const MmWhere& wh, MmR
     if (last) mm_take<EL, MODE, NB>(p, tb, wh, R);
     const bool edge = last || kt == R.c.nk - 1;
     const bool anew_p = edge || (mm_kind(MODE) == kWgrad && (MODE & kGatherX) != 0), anew_q = edge || (MODE & kGatherDy) != 0;
-    if (anew_p || anew_q) mm_offsets<EL, MODE, NB>(p, wh, R, anew_p, anew_q);
+    if (anew_p || anew_q) mm_offsets<EL, MODE, NB>(p, wh, R, edge, anew_p, anew_q);
     if (!anew_p) {
         if constexpr (MODE == kMmNK) { R.pb += 128; R.pn -= 128; }
         else if constexpr (MODE == kMmKN) R.pb += (size_t)p.w_ld * 64;
@@ -298,7 +332,7 @@ MOE_DEV void mm_start(const MmP& p, const MmTables& tb, const MmWhere& wh, MmReq
     R.at = -1;
     mm_look<EL, MODE, NB>(p, tb, wh, R);
     mm_take<EL, MODE, NB>(p, tb, wh, R);
-    mm_offsets<EL, MODE, NB>(p, wh, R, true, true);
+    mm_offsets<EL, MODE, NB>(p, wh, R, true, true, true);
     if constexpr (is_wgrad(MODE)) {
         if (R.live && R.c.nk > 1) mm_load_src<MODE>(p, wh, R.c, 1, R.psrc, R.qsrc);
     }
@@ -404,11 +438,7 @@ MOE_DEV void kept_load(const MmP& p, const MmTables& tb, const MmWhere& wh, MmKe
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int k = 8 * wh.w + 2 * i + (wh.lane >> 5);
-        int row = k;
-        if (mapped) {
-            const int s0 = __builtin_amdgcn_readlane(X.src, 2 * i), s1 = __builtin_amdgcn_readlane(X.src, 2 * i + 1);
-            row = wh.lane < 32 ? s0 : s1;
-        }
+        const int row = mapped ? (int)mm_gather_row<256>((uint32_t)X.src, i, wh.lane) : k;
         const bool ok = k < krem && col < p.K && (!mapped || (uint32_t)row < p.x_rows);
         // (opaque offsets: with visible ones the compiler makes two loads of
         // each, the second waiting for the first)
