@@ -398,64 +398,87 @@ MOE_DEV void mm_requests(const MmP& p, const MmWhere& wh, const MmReq<NQ>& R, ui
 
 // wgrad from 8-bit rows: the a operand passes through registers. Every wave
 // takes 8 of a K-tile's 64 rows: lane l of piece i holds 8 codes of row
-// 8 w + 2 i + l / 32. Codes are requested two K-tiles ahead and written to LDS
-// as BF16 values (code * scale, rounded) one K-tile ahead.
+// 8 w + 2 i + l / 32. Codes are requested two K-tiles ahead between the products
+// of turn 1 and written to LDS as BF16 values (code * scale, rounded) between
+// those of the next turn 0: a wave that did so in its reading turn would hold
+// up the other waves' products (8 groups of 16384 x 2816 x 2048: 298 -> 210 us).
 struct MmKept {
-    int round, kt, step;                 // step: of the K-tile held in q
-    bool live, held;
+    int round, kt;                      // K-tile to request next
+    bool live;
     MmItem c;
-    int src;                            // source rows of this wave's 8 k, one per lane % 8
+    uint32_t src;                       // source rows of this wave's 8 k, one per lane % 8
     u32x2_t q[4];
     float s[4];
 };
 
-template <int NB>
+template <int MODE, int NB>
 MOE_DEV void kept_open(const MmP& p, const MmTables& tb, const MmWhere& wh, MmKept& X) {
     int round = X.round;
     bool live = false;
-    for (int item; !live && (item = mm_nth<kWgrad8>(round, wh.grid, wh.slot)) < wh.n_items; ++round) {
-        X.c = mm_decode<kElBf16, kWgrad8, 32 * NB>(p, tb, wh.at, item);
-        live = X.c.nk > 0;
+    MmItem c = X.c;
+    for (int item; !live && (item = mm_nth<MODE>(round, wh.grid, wh.slot)) < wh.n_items; ++round) {
+        c = mm_decode<kElBf16, MODE, 32 * NB>(p, tb, wh.at, item);
+        live = c.nk > 0;
     }
     X.round = round;
     X.live = live;
-    X.c = mm_scalar(X.c);
+    X.c = mm_scalar(c);
 }
+template <int MODE>
 MOE_DEV void kept_src(const MmP& p, const MmWhere& wh, MmKept& X) {
-    const int k = X.kt * 64 + 8 * wh.w + (wh.lane & 7);
-    X.src = __builtin_amdgcn_raw_buffer_load_b32(
-        make_rsrc(p.x_src + X.c.r0, p.x_src ? (uint32_t)(X.c.nrows * 4) : 0u), k * 4, 0, 0);
-}
-template <int NB>
-MOE_DEV void kept_load(const MmP& p, const MmTables& tb, const MmWhere& wh, MmKept& X) {
-    const int k0 = X.kt * 64, krem = X.c.nrows - k0, first = X.c.r0 + k0, rows = min(krem, 64);
-    const bool mapped = p.x_src != nullptr;
-    const rsrc_t rx = make_rsrc(mapped ? p.x : p.x + (size_t)first * p.x_ld,
-                                mapped ? p.x_bytes : (uint32_t)(rows - 1) * p.x_ld + (uint32_t)p.K);
-    const rsrc_t rs = make_rsrc(mapped ? p.xs : p.xs + (size_t)first * p.kb,
-                                mapped ? p.xs_bytes : (uint32_t)(rows * p.kb * 4));
-    const int col = X.c.a0 + (wh.lane & 31) * 8;
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int k = 8 * wh.w + 2 * i + (wh.lane >> 5);
-        const int row = mapped ? (int)mm_gather_row<256>((uint32_t)X.src, i, wh.lane) : k;
-        const bool ok = k < krem && col < p.K && (!mapped || (uint32_t)row < p.x_rows);
-        // (opaque offsets: with visible ones the compiler makes two loads of
-        // each, the second waiting for the first)
-        uint32_t oq = ok ? (uint32_t)row * p.x_ld + (uint32_t)col : kMmInvalid;
-        uint32_t os = ok ? ((uint32_t)row * (uint32_t)p.kb + (uint32_t)(col >> 7)) * 4u : kMmInvalid;
-        asm volatile("" : "+v"(oq), "+v"(os));
-        X.q[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rx, oq, 0, 0));
-        X.s[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, os, 0, 0));
+    if constexpr ((MODE & kGatherX) != 0) {
+        const int k = X.kt * 64 + 8 * wh.w + (wh.lane & 7);
+        X.src = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(make_rsrc(p.x_src + X.c.r0, (uint32_t)(X.c.nrows * 4)), k * 4, 0, 0);
     }
-    X.held = true;
+}
+// request the K-tile's codes and scales (nothing once the items have ended)
+template <int MODE>
+MOE_DEV void kept_load(const MmP& p, const MmWhere& wh, MmKept& X) {
+    const int lane = mm_fresh(wh.lane), w = wh.w;
+    const int k0 = X.kt * 64, krem = X.c.nrows - k0, first = X.c.r0 + k0;
+    const int col = X.c.a0 + (lane & 31) * 8;
+    if constexpr ((MODE & kGatherX) != 0) {
+        const rsrc_t rx = make_rsrc(p.x, X.live ? p.x_bytes : 0u), rs = make_rsrc(p.xs, X.live ? p.xs_bytes : 0u);
+        const uint32_t cq = col < p.K ? (uint32_t)col : 0xFFFFFFFFu, cs = (uint32_t)(col >> 7) * 4u;
+        const uint32_t oq = mm_gather_so(X.src, p.x_rows, p.x_ld, krem, w, lane);
+        const uint32_t os = mm_gather_so(X.src, p.x_rows, (uint32_t)p.kb * 4u, krem, w, lane);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            X.q[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
+                rx, __builtin_elementwise_add_sat(mm_gather_row<256>(oq, i, lane), cq), 0, 0));
+            // (columns past the end read some scale of the row: their codes are zero)
+            X.s[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                rs, __builtin_elementwise_add_sat(mm_gather_row<256>(os, i, lane), cs), 0, 0));
+        }
+    } else {
+        // rows past the group are past the resource
+        const int rows = __builtin_amdgcn_readfirstlane(max(min(krem, 64), 1));
+        const rsrc_t rx = make_rsrc(p.x + (size_t)first * p.x_ld, X.live ? (uint32_t)(rows - 1) * p.x_ld + (uint32_t)p.K : 0u);
+        const rsrc_t rs = make_rsrc(p.xs + (size_t)first * p.kb, X.live ? (uint32_t)(rows * p.kb * 4) : 0u);
+        const uint32_t k = (uint32_t)(8 * w + (lane >> 5));
+        // (opaque: with a visible choice the compiler makes two loads of each,
+        // the second waiting for the first)
+        uint32_t oq = col < p.K ? k * p.x_ld + (uint32_t)col : 0x80000000u;
+        const uint32_t os = (k * (uint32_t)p.kb + (uint32_t)(col >> 7)) * 4u;
+        asm("" : "+v"(oq));
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            X.q[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rx, oq + (uint32_t)(2 * i) * p.x_ld, 0, 0));
+            X.s[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, os + (uint32_t)(2 * i) * (uint32_t)p.kb * 4u, 0, 0));
+        }
+    }
+}
+// step past the K-tile just requested
+template <int MODE, int NB>
+MOE_DEV void kept_next(const MmP& p, const MmTables& tb, const MmWhere& wh, MmKept& X) {
+    if (!X.live) return;
     const int kt = X.kt + 1;
     const bool last = kt == X.c.nk;
     X.kt = last ? 0 : kt;
-    if (last) kept_open<NB>(p, tb, wh, X);
-    if (X.live) kept_src(p, wh, X);
+    if (last) kept_open<MODE, NB>(p, tb, wh, X);
+    if (X.live) kept_src<MODE>(p, wh, X);
 }
-MOE_DEV void kept_write(const MmWhere& wh, MmKept& X, uint8_t* st) {
+MOE_DEV void kept_write(const MmWhere& wh, const MmKept& X, uint8_t* st) {
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int k = 8 * wh.w + 2 * i + (wh.lane >> 5), c = wh.lane & 31;
@@ -470,8 +493,6 @@ MOE_DEV void kept_write(const MmWhere& wh, MmKept& X, uint8_t* st) {
         }
         *(i32x4*)(st + k * 512 + (((c >> 1) ^ tr_swz(k)) * 32) + (c & 1) * 16) = o;
     }
-    X.held = false;
-    ++X.step;
 }
 
 // wgrad's tables (see MmTables), by the whole workgroup; a barrier must follow.
@@ -657,6 +678,9 @@ void grouped_mm_kernel(MmP p) {
     f32x4 d[4];                         // fp8: products not yet added, and their scales
     float sc = 0.f;
 
+    MmKept kept;
+    int step = 0;
+
     // the products of one turn, with the turn's requests between them
     auto multiply = [&](auto turn) __attribute__((always_inline)) {
         constexpr int h = decltype(turn)::value;
@@ -691,7 +715,10 @@ void grouped_mm_kernel(MmP p) {
                 __builtin_amdgcn_sched_barrier(0);
             });
         } else {
+            constexpr bool kKept = mm_kind(MODE) == kWgrad8;
             mm_requests<EL, MODE, NB, h, 0, NR>(p, wh, R, smem);
+            if constexpr (kKept && h == 0) kept_write(wh, kept, smem + ((step + 1) % NST) * Geo::Stage);
+            if constexpr (kKept && h == 1) kept_load<MODE>(p, wh, kept);
             #pragma unroll
             for (int s = 0; s < 2; ++s)
                 #pragma unroll
@@ -699,10 +726,24 @@ void grouped_mm_kernel(MmP p) {
                     #pragma unroll
                     for (int t = 0; t < 4; ++t)
                         acc[h * NU + u][t] = mfma16x16x32<EL>(fp[s][t], fq[s][u], acc[h * NU + u][t]);
-            #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 8 * NU / (NR + 1), 0);
-                __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+            if constexpr (kKept && h == 0) {
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {                // a piece's conversions and its write
+                    if (i < NR) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+                    #pragma unroll
+                    for (int m = 0; m < 8; ++m) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+                    }
+                    __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+                }
+            } else {
+                constexpr int NM = NR + (kKept ? 8 : 0);     // requests in all
+                #pragma unroll
+                for (int i = 0; i < NM; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 8 * NU / (NM + 1), 0);
+                    __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+                }
             }
         }
     };
@@ -766,15 +807,16 @@ void grouped_mm_kernel(MmP p) {
     };
 
     // --------------------------------------------------------------- loop
-    MmKept kept;
     if constexpr (mm_kind(MODE) == kWgrad8) {
-        kept.round = kept.step = kept.kt = 0;
-        kept.held = false;
-        kept_open<NB>(p, tb, wh, kept);
-        if (kept.live) kept_src(p, wh, kept);
-        if (kept.live) kept_load<NB>(p, tb, wh, kept);
-        if (kept.held) kept_write(wh, kept, smem);
-        if (kept.live) kept_load<NB>(p, tb, wh, kept);
+        kept.round = kept.kt = 0;
+        kept.src = 0;
+        kept.c = MmItem{0, 0, 0, 0, 1, 1, -1};
+        kept_open<MODE, NB>(p, tb, wh, kept);
+        if (kept.live) kept_src<MODE>(p, wh, kept);
+        kept_load<MODE>(p, wh, kept);
+        kept_write(wh, kept, smem);
+        kept_next<MODE, NB>(p, tb, wh, kept);
+        kept_load<MODE>(p, wh, kept);
     }
     mm_start<EL, MODE, NB>(p, tb, wh, R);
     #pragma unroll 1
@@ -797,17 +839,15 @@ void grouped_mm_kernel(MmP p) {
     // longer; once a stream has ended its requests still count. In the first
     // NST - 1 K-tiles after an item's stores the requests waited for are older
     // than the stores, which then count as newer.
-    constexpr int KEPT = mm_kind(MODE) == kWgrad8 ? 8 : 0;            // requests of the 8-bit rows, one K-tile's in flight
+    constexpr int KEPT = mm_kind(MODE) == kWgrad8 ? 8 : 0;            // requests of the 8-bit rows in turn 1
     constexpr int L1 = mm_turn_requests(EL, MODE, NB, 1), L2 = mm_turn_requests(EL, MODE, NB, 0);
     int stored = 0;                                          // K-tiles whose waits leave the last stores in flight
     auto wait_for = [&](auto n) __attribute__((always_inline)) {
         constexpr int N = decltype(n)::value;
-        static_assert(N + KEPT + 4 * NB < 64, "vmcnt");
-        if (mm_kind(MODE) == kWgrad8 && !kept.live) __builtin_amdgcn_s_waitcnt(waitcnt_imm(N, 15));
-        else if (stored > 0) __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + KEPT + 4 * NB, 15));
-        else __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + KEPT, 15));
+        static_assert(N + 4 * NB < 64, "vmcnt");
+        if (stored > 0) __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + 4 * NB, 15));
+        else __builtin_amdgcn_s_waitcnt(waitcnt_imm(N, 15));
     };
-    int step = 0;
     if constexpr (EL == kElFp8) fwn = load_fw(mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, tb, at, slot)), 0);
     for (int round = 0, item; (item = mm_nth<MODE>(round, grid, slot)) < n_items; ++round) {
         // the item is the one being requested, unless items are very short
@@ -822,20 +862,19 @@ void grouped_mm_kernel(MmP p) {
             static_for<2>([&](auto turn) __attribute__((always_inline)) {
                 constexpr int h = decltype(turn)::value;
                 read_frags(step, h, c, kt);
-                if constexpr (mm_kind(MODE) == kWgrad8 && h == 1) {
-                    if (kept.held) kept_write(wh, kept, smem + (kept.step % NST) * Geo::Stage);
-                    if (kept.live) kept_load<NB>(p, tb, wh, kept);
-                }
+                if constexpr (mm_kind(MODE) == kWgrad8 && h == 0) kept_next<MODE, NB>(p, tb, wh, kept);
                 if constexpr (h == 1) mm_advance<EL, MODE, NB>(p, tb, wh, R);
                 // the reads end before this wave's products and so a turn before
-                // the stage is requested again; only writes to LDS must be done here
-                if constexpr (mm_kind(MODE) == kWgrad8) __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-                if (!lead) wait_for(std::integral_constant<int, h ? (NST - 2) * L1 + (NST - 1) * L2 : (NST - 1) * L1 + (NST - 2) * L2>{});
+                // the stage is requested again
+                if (!lead) wait_for(std::integral_constant<int, h ? (NST - 2) * (L1 + KEPT) + (NST - 1) * L2
+                                                                  : (NST - 1) * (L1 + KEPT) + (NST - 2) * L2>{});
                 bare_barrier();
                 __builtin_amdgcn_s_setprio(1);
                 multiply(turn);
                 __builtin_amdgcn_s_setprio(0);
-                if (lead) wait_for(std::integral_constant<int, (NST - 1) * (L1 + L2)>{});
+                if (lead) wait_for(std::integral_constant<int, (NST - 1) * (L1 + KEPT + L2)>{});
+                // (writes to LDS are done before the barrier)
+                if constexpr (mm_kind(MODE) == kWgrad8 && h == 0) __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
                 bare_barrier();
             });
             --stored;
@@ -955,12 +994,12 @@ int wgrad_part(int R_max, int G, int N, int K) {
     return part >= most ? 0 : (int)part;
 }
 
-template <int EL>
+template <int EL, int KIND>
 int launch_wgrad(const MmP& p, int items, hipStream_t stream) {
-    if (p.x_src && p.dy_src) return launch_mm<EL, kWgrad | kGatherX | kGatherDy, 8>(p, items, stream);
-    if (p.x_src) return launch_mm<EL, kWgrad | kGatherX, 8>(p, items, stream);
-    if (p.dy_src) return launch_mm<EL, kWgrad | kGatherDy, 8>(p, items, stream);
-    return launch_mm<EL, kWgrad, 8>(p, items, stream);
+    if (p.x_src && p.dy_src) return launch_mm<EL, KIND | kGatherX | kGatherDy, 8>(p, items, stream);
+    if (p.x_src) return launch_mm<EL, KIND | kGatherX, 8>(p, items, stream);
+    if (p.dy_src) return launch_mm<EL, KIND | kGatherDy, 8>(p, items, stream);
+    return launch_mm<EL, KIND, 8>(p, items, stream);
 }
 
 }  // namespace
@@ -1010,11 +1049,8 @@ int moe_launch_mm(const MmCall& c, hipStream_t stream) {
         p.max_slots = (int)(moe_mm_workspace_bytes(2, false, c.R_max, c.G, c.N, c.K) / (65536 * 4));
         int e;
         const int grid = p.part > 0 ? 1 << 30 : items;       // (split groups have more items than tiles)
-        if (c.xs)                        // (the 8-bit rows' gather is no part of the request state)
-            e = c.dy_src ? launch_mm<kElBf16, kWgrad8 | kGatherDy, 8>(p, grid, stream)
-                         : launch_mm<kElBf16, kWgrad8, 8>(p, grid, stream);
-        else
-            e = f16 ? launch_wgrad<kElF16>(p, grid, stream) : launch_wgrad<kElBf16>(p, grid, stream);
+        if (c.xs) e = launch_wgrad<kElBf16, kWgrad8>(p, grid, stream);
+        else e = f16 ? launch_wgrad<kElF16, kWgrad>(p, grid, stream) : launch_wgrad<kElBf16, kWgrad>(p, grid, stream);
         if (e || p.part == 0) return e;
         const dim3 join((unsigned)(tiles / c.G * 4), (unsigned)c.G);
         wgrad_join_kernel<<<join, 256, 0, stream>>>(p);
