@@ -15,6 +15,13 @@
  *   combine  per-token sum of its rows, BF16                      moe_combine
  *   layer    all of the above in one call                         moe_layer
  *
+ * and, for training and for checkpoints in other formats, grouped products of
+ * 16-bit operands (moe_grouped_mm: forward and the gradient of the rows;
+ * moe_grouped_wgrad: the gradient of the weights), of FP8 operands with a
+ * scale per 128 (moe_quantize_block, moe_quantize_block_weights,
+ * moe_grouped_mm_fp8), and the gated activation that keeps its input in 8 bits
+ * for the backward pass (moe_glu_checkpoint, moe_glu_checkpoint_backward).
+ *
  * Conventions, for every entry point:
  *  - Tensor pointers are DEVICE pointers owned by the caller. Row-major,
  *    densely packed unless a leading dimension is stated.
@@ -37,7 +44,8 @@
  * are packed two per byte, element 2i in the low nibble.
  *
  * Design limits (GC-MoE page, "Limitations", the paper's Appendix A):
- * I <= 4096, I % 128 == 0, H % 256 == 0, k + s <= 32, E_tot <= 2048.
+ * I <= 4096, I % 128 == 0, H % 256 == 0, k + s <= 32, E_tot <= 2048. The
+ * 16-bit, block-128 FP8 and 8-bit checkpoint calls state their own.
  */
 #ifndef MOE_H
 #define MOE_H
@@ -418,8 +426,9 @@ int32_t moe_layer_workspace_offsets(int32_t T, int32_t E_tot, int32_t k, int32_t
  *                      of the forward product, the gradient of its rows)
  *   moe_grouped_wgrad  dW_g[n][k] = sum_{r in g} dy[t(r)][n] * x[s(r)][k]
  *
- * for every row r in [offsets[g], offsets[g+1]) (offsets are held inside
- * [0, R_max]). s(r) = row_src[r] (or x_src), t(r) = dy_src[r], each r itself
+ * for every row r in [offsets[g], offsets[g+1]). Offsets ascend; others are
+ * held inside [0, R_max], so that nothing outside the arrays is touched, but
+ * which rows of y are then written is not defined. s(r) = row_src[r] (or x_src), t(r) = dy_src[r], each r itself
  * when NULL, so token-order arrays are read through moe_permute's row_src
  * without a gathered copy. Rows of y that belong to no group are left as they
  * were. A group without rows has dW_g = 0 (unchanged with
@@ -437,7 +446,9 @@ int32_t moe_layer_workspace_offsets(int32_t T, int32_t E_tot, int32_t k, int32_t
  * the decoded values are rounded to BF16 (exact for its power-of-two scales).
  * dtype MOE_T_BF16 only; ldx % 8 == 0 and rows at multiples of 8 bytes.
  *
- * ws: workspace of the matching size function (may be 0).
+ * No output may overlap an input (or, in these calls, another output).
+ * ws: workspace of the matching size function (may be 0), one for each call in
+ * flight. Results are the same bits every time.
  */
 #define MOE_T_BF16 0
 #define MOE_T_F16  1
@@ -481,8 +492,9 @@ int32_t moe_quantize_block_weights(const void* w, int32_t dtype, int32_t G, int3
                                    uint8_t* q, float* s, hipStream_t stream);
 
 /*
- * The grouped product of block-scaled operands (any finite fp32 scales, so
- * weights quantised elsewhere can be used as they are):
+ * The grouped product of block-scaled operands (any fp32 scales, so weights
+ * quantised elsewhere can be used as they are; the product of a row's and a
+ * weight block's scale is formed in fp32 and must be finite and normal):
  *   y[r][n] = sum_b xs[s(r)][b] * ws_g[n / 128][b] * sum_{k in block b} xq[s(r)][k] * wq_g[n][k]
  * blocks of 128 along K, the inner sums on the FP8 matrix instructions, the
  * outer one in fp32, one rounding to dtype (MOE_T_BF16 or MOE_T_F16).
@@ -517,7 +529,7 @@ int32_t moe_grouped_mm_fp8(const uint8_t* xq, const float* xs, int32_t x_rows, c
  *           the input of the second product's weight gradient
  *   dw[r]   = sum_i dh * a(clamp(g)) * clamp(u)  (fp32, NULL: not written)
  * n_rows: NULL, or a device count: rows from *n_rows on are left as they were.
- * I % 8 == 0.
+ * I % 8 == 0. No output may overlap an input.
  */
 int32_t moe_glu_checkpoint(const void* pre, int32_t dtype, int32_t rows, int32_t I, int32_t ld,
                            const float* row_w, const int32_t* n_rows, const moe_epilogue* epi, void* h,

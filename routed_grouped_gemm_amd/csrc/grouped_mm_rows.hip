@@ -9,6 +9,11 @@
 // LDS by loads that write it directly, through a ring of NST stages, so that
 // about 40 KB of weights per workgroup are on their way; one barrier per
 // K-tile. Layouts and swizzles as in grouped_mm.hip.
+//
+// Measured: 16 rows on 7 of 8 experts, 4096 x 7168 in BF16 (411 MB) 70 to 75 us,
+// 5.5 to 5.9 TB/s; the same in FP8 (206 MB) 44 us, 4.7 TB/s; 16 rows of one
+// expert, 1024 x 7168 (15 MB), 16 us of which about 5 are the joining launch,
+// against 47 us unsplit.
 #include <algorithm>
 
 #include "grouped_mm.h"
