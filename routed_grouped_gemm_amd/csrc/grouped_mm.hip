@@ -674,7 +674,12 @@ void grouped_mm_kernel(MmP p) {
                                         (ti * 4 + (16 * u + j) / Geo::HRows) * 256 + ((16 * u + j) % Geo::HRows) * 4);
             if (turn == 0) {
                 // a block row's scales, 64 K-tiles to a register: one per lane
-                if ((kt & 63) == 0 && kt > 0) fwv = load_fw(c, kt);
+                // (used here, so that the wait for it is here: behind the
+                // branch it would drain the requests of every K-tile)
+                if ((kt & 63) == 0 && kt > 0) {
+                    fwv = load_fw(c, kt);
+                    asm volatile("" : "+v"(fwv));
+                }
                 fw = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)fwv, kt & 63));
             }
         }
@@ -862,6 +867,7 @@ void grouped_mm_kernel(MmP p) {
         const MmItem c = R.live && R.at == item ? R.c : mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, tb, at, item));
         if constexpr (EL == kElFp8) {   // the next item's scales are loaded an item ahead
             fwv = fwn;
+            asm volatile("" : "+v"(fwv));
             if (item + grid < n_items) fwn = load_fw(mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, tb, at, item + grid)), 0);
         }
         clear();

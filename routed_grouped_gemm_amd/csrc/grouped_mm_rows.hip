@@ -10,10 +10,10 @@
 // about 40 KB of weights per workgroup are on their way; one barrier per
 // K-tile. Layouts and swizzles as in grouped_mm.hip.
 //
-// Measured: 16 rows on 7 of 8 experts, 4096 x 7168 in BF16 (411 MB) 70 to 75 us,
-// 5.5 to 5.9 TB/s; the same in FP8 (206 MB) 44 us, 4.7 TB/s; 16 rows of one
-// expert, 1024 x 7168 (15 MB), 16 us of which about 5 are the joining launch,
-// against 47 us unsplit.
+// Measured, weights not in any cache: 2 rows on each of 8 experts, 4096 x 7168
+// in BF16 (470 MB) 76 us, 6.2 TB/s, in FP8 (235 MB) 41 us, 5.7 TB/s, W [K, N]
+// 95 us; 16 rows of one expert, 1024 x 7168 (15 MB), 16 us of which about 5 are
+// the joining launch, against 47 us unsplit.
 #include <algorithm>
 
 #include "grouped_mm.h"
@@ -81,7 +81,11 @@ MOE_DEV void rows_open(const MmP& p, const MmTables& tb, const MmWhere& wh, Rows
     }
 }
 
-// request one K-tile into its stage, then move on (nothing once the items have ended)
+// request one K-tile into its stage, then move on (nothing once the items have
+// ended). Tiles of 32 rows are chosen where a group's rows are one pass, so each
+// weight is read once: those loads are non-temporal (84 -> 76 us for the BF16
+// decode above). With 64 rows several passes share the weights through the
+// caches (512 x 4096 x 4096: 40 us, non-temporal 43).
 template <int EL, int MODE, int NB, int NQ>
 MOE_DEV void rows_request(const MmP& p, const MmTables& tb, const MmWhere& wh, RowsReq<NQ>& R, uint8_t* smem) {
     using Geo = RowsGeom<EL, NB>;
@@ -98,7 +102,7 @@ MOE_DEV void rows_request(const MmP& p, const MmTables& tb, const MmWhere& wh, R
             const int kb = R.kt * 128 + 16 * ((lane & 7) ^ ((lane >> 4) | (4 * i)));
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 r, (mm_lds_void_t*)(st + (16 * w + 8 * i) * 128), 16,
-                kb < p.K * EB ? (uint32_t)(16 * w + 8 * i + (lane >> 3)) * p.w_ld + (uint32_t)kb : kMmInvalid, 0, 0, 0);
+                kb < p.K * EB ? (uint32_t)(16 * w + 8 * i + (lane >> 3)) * p.w_ld + (uint32_t)kb : kMmInvalid, 0, 0, NB == 2 ? 2 : 0);
         }
     } else {
         const int krem = p.K - R.kt * 64;
@@ -110,7 +114,7 @@ MOE_DEV void rows_request(const MmP& p, const MmTables& tb, const MmWhere& wh, R
             const int col = (((lane & 7) >> 1) ^ (k & 3)) * 16 + (lane & 1) * 8;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 r, (mm_lds_void_t*)(st + (16 * w + 8 * i) * 128), 16,
-                k < krem && c.a0 + col < p.N ? (uint32_t)k * p.w_ld + (uint32_t)(col * 2) : kMmInvalid, 0, 0, 0);
+                k < krem && c.a0 + col < p.N ? (uint32_t)k * p.w_ld + (uint32_t)(col * 2) : kMmInvalid, 0, 0, NB == 2 ? 2 : 0);
         }
     }
     // gathered rows are addressed from the array's start, a group's own rows from the tile's first
@@ -157,6 +161,19 @@ void grouped_mm_rows_kernel(MmP p) {
     if (slot >= n_items) return;
     const MmWhere wh{n_items, at, grid, slot, lane, w};
 
+    // fp8: the weight scales of a part's K-tiles, one per lane, loaded an item
+    // ahead (a load in the K loop would be waited for in every K-tile)
+    uint32_t fwv = 0, fwn = 0;
+    auto load_fw = [&](const MmItem& c, int kt) __attribute__((always_inline)) {
+        const float* ws = p.ws + ((size_t)c.g * p.nb + (c.a0 >> 7)) * p.kb;
+        return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(make_rsrc(ws, (uint32_t)(p.kb * 4)), (kt + lane) * 4, 0, 0);
+    };
+    if constexpr (EL == kElFp8) {
+        int part, k0, k1;
+        const MmItem c = rows_item<EL, MODE, BT>(p, tb, wh, slot, part, k0, k1);
+        fwn = load_fw(c, k0);
+    }
+
     RowsReq<Geo::NQ> R;
     R.item = slot;
     R.step = 0;
@@ -168,7 +185,15 @@ void grouped_mm_rows_kernel(MmP p) {
     for (int item = slot; item < n_items; item += grid) {
         int part, k0, k1;
         const MmItem c = rows_item<EL, MODE, BT>(p, tb, wh, item, part, k0, k1);
-        const float* ws = EL == kElFp8 ? p.ws + ((size_t)c.g * p.nb + (c.a0 >> 7)) * p.kb : nullptr;
+        if constexpr (EL == kElFp8) {
+            fwv = fwn;
+            asm volatile("" : "+v"(fwv));
+            if (item + grid < n_items) {
+                int npart, nk0, nk1;
+                const MmItem n = rows_item<EL, MODE, BT>(p, tb, wh, item + grid, npart, nk0, nk1);
+                fwn = load_fw(n, nk0);
+            }
+        }
         f32x4 acc[NB];
         #pragma unroll
         for (int u = 0; u < NB; ++u) acc[u] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -200,7 +225,13 @@ void grouped_mm_rows_kernel(MmP p) {
                 #pragma unroll
                 for (int u = 0; u < NB; ++u)
                     fs[u] = *(const float*)(st + Geo::SOff + ((16 * u + j) / (BT / 4)) * 256 + ((16 * u + j) % (BT / 4)) * 4);
-                fw = ws[kt];
+                // (used here, so that the wait for it is here: behind the
+                // branch it would drain the requests of every K-tile)
+                if (((kt - k0) & 63) == 0 && kt > k0) {
+                    fwv = load_fw(c, kt);
+                    asm volatile("" : "+v"(fwv));
+                }
+                fw = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)fwv, (kt - k0) & 63));
                 #pragma unroll
                 for (int u = 0; u < NB; ++u) {
                     const f32x4 d = mfma_fp8(fp[0], fp[1], fq[0][u], fq[1][u], f32x4{0.f, 0.f, 0.f, 0.f});
