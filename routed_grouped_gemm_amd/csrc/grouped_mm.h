@@ -48,6 +48,15 @@ MOE_DEV void group_rows(const MmP& p, int g, int& lo, int& hi) {
     hi = min(max(p.offsets[g + 1], lo), p.R_max);
 }
 
+// The same of one group for the whole wave, by scalar loads: waiting for a
+// vector load would drain the requests in flight at every item.
+MOE_DEV void group_rows_scalar(const MmP& p, int g, int& lo, int& hi) {
+    typedef const __attribute__((address_space(4))) int32_t* const_i32;
+    const const_i32 at = (const_i32)(uintptr_t)p.offsets + __builtin_amdgcn_readfirstlane(g);
+    lo = min(max(at[0], 0), p.R_max);
+    hi = min(max(at[1], lo), p.R_max);
+}
+
 // two floats -> two packed 16-bit values, round to nearest even
 MOE_DEV uint32_t pack16(float a, float b, int f16) {
     if (f16) {
@@ -198,7 +207,7 @@ MOE_DEV MmItem mm_decode(const MmP& p, const MmTables& tb, int at, int item) {
         const int part = unit - first;
         c.g = __builtin_amdgcn_readfirstlane(tb.order[i]);
         const int slot0 = __builtin_amdgcn_readfirstlane(tb.slots[c.g]);
-        group_rows(p, c.g, lo, hi);
+        group_rows_scalar(p, c.g, lo, hi);
         lo = __builtin_amdgcn_readfirstlane(lo);
         const int rows = __builtin_amdgcn_readfirstlane(hi) - lo, nk = (rows + KT - 1) / KT;
         // the group's K-tiles in `parts` nearly equal runs
@@ -213,7 +222,7 @@ MOE_DEV MmItem mm_decode(const MmP& p, const MmTables& tb, int at, int item) {
         const int first = __builtin_amdgcn_readfirstlane(tb.at[c.g]);
         bt = __builtin_amdgcn_readfirstlane(tb.at[c.g + 1]) - first;
         l = item - first * at;
-        group_rows(p, c.g, lo, hi);
+        group_rows_scalar(p, c.g, lo, hi);
     }
     // bands of four b tiles, b fastest: the items that run together on one
     // XCD share operands in its L2
