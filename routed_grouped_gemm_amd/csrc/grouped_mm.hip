@@ -42,7 +42,7 @@
 // first K-tiles are in flight during an item's epilogue.
 //
 // Measured, one group, BF16: 16384 x 4096 x 4096 430 us (1280 TFLOP/s) with W
-// [N, K], 405 (1355) with W [K, N], FP8 270 (2035); weight gradients of 16384 x
+// [N, K], 405 (1355) with W [K, N], FP8 261 to 271 (2030 to 2100); weight gradients of 16384 x
 // 2816 x 2048 in 8 equal groups 187 us (1010), from 8-bit rows 210. The matrix
 // cores are busy 48% (few, uneven items) to 62% of the cycles, and the clock
 // falls to 1.8 to 2.1 GHz under them; no LDS bank conflicts, LDS active 18 to
