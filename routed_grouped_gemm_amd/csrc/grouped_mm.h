@@ -122,6 +122,7 @@ constexpr int kMmThreads = 512;
 constexpr int kMmLds = 163840;              // LDS of a compute unit
 constexpr int kATile = 256;
 constexpr int kPBytes = kATile * 128;       // one K-tile of the a operand
+constexpr int kMmOut = 8 * 1024;            // stores pass through it
 
 // chunk swizzle of a row in the contiguous form, and of a k in the slow form
 MOE_DEV int kc_swz(int row) { return (row >> 1) & 7; }
@@ -175,7 +176,7 @@ MOE_DEV int last_at_most(const int* at, int n, int v) {
 // wgrad: groups in the order of their items, at [G + 1] units (parts of a
 // group's K-tiles) before the i-th, order [G] the i-th group; slots [G] the
 // first partial-sum slot of group g's tiles (-1: not split).
-struct MmTables { const int *at, *order, *slots; };
+struct MmTables { const int* at; const uint16_t* order; const int* slots; };
 
 // parts that group g's nk K-tiles are split into
 MOE_DEV int wgrad_parts(const MmP& p, int nk) { return p.part > 0 ? max(1, (nk + p.part - 1) / p.part) : 1; }

@@ -63,8 +63,9 @@ struct MmGeom {
     static constexpr int QOff = kPBytes;
     static constexpr int SOff = kPBytes + BT * 128;          // fp8: row scales, 256 bytes per wave and half
     static constexpr int Stage = SOff + (EL == kElFp8 ? 4096 : 0);
-    static constexpr int NST = Stage * 3 + 8320 <= kMmLds ? 3 : 2;
-    static constexpr int Lds(int G, bool wgrad) { return Stage * NST + (wgrad ? 3 * G + 1 : G + 1) * 4; }
+    // beside the stages: 1 KiB a wave for its stores, and the tables
+    static constexpr int NST = Stage * 3 + 2 * kMmOut <= kMmLds ? 3 : 2;
+    static constexpr int Lds(int G, bool wgrad) { return Stage * NST + kMmOut + (G + 1) * 4 + (wgrad ? 6 * G : 0); }
 };
 
 // The requests of a wave: one K-tile after another through all items, an
@@ -506,7 +507,7 @@ MOE_DEV void kept_write(const MmWhere& wh, const MmKept& X, uint8_t* st) {
 // wgrad's tables (see MmTables), by the whole workgroup; a barrier must follow.
 // Groups go by the length of their parts, longest first (up to 512 groups; with
 // more, in their own order: a rank is found by comparing with every other).
-MOE_DEV void wgrad_tables(const MmP& p, int tiles, int* at, int* order, int* slots) {
+MOE_DEV void wgrad_tables(const MmP& p, int tiles, int* at, uint16_t* order, int* slots) {
     const int tid = threadIdx.x, lane = tid & 63;
     for (int g = tid; g < p.G; g += kMmThreads) {
         const int nk = group_ktiles(p, g), n = wgrad_parts(p, nk);
@@ -519,7 +520,7 @@ MOE_DEV void wgrad_tables(const MmP& p, int tiles, int* at, int* order, int* slo
             rank = 0;
             for (int i = 0; i < p.G; ++i) rank += at[i] > at[g] || (at[i] == at[g] && i < g) ? 1 : 0;
         }
-        order[rank] = g;
+        order[rank] = (uint16_t)g;
     }
     __syncthreads();
     if (tid >= 64) return;
@@ -600,8 +601,9 @@ void grouped_mm_kernel(MmP p) {
     static_assert(!Q_TR || BT == 256, "the slow form is laid out for 256 values");
 
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    int* const tab = (int*)(smem + NST * Geo::Stage);
-    const MmTables tb{tab, tab + p.G + 1, tab + 2 * p.G + 1};
+    int* const tab = (int*)(smem + NST * Geo::Stage + kMmOut);
+    uint16_t* const order = (uint16_t*)(tab + 2 * p.G + 1);
+    const MmTables tb{tab, order, tab + p.G + 1};
 
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -613,7 +615,7 @@ void grouped_mm_kernel(MmP p) {
     const int at = (na + kATile - 1) / kATile;
     int n_items;
     if constexpr (is_wgrad(MODE)) {
-        wgrad_tables(p, at * ((p.N + BT - 1) / BT), tab, tab + p.G + 1, tab + 2 * p.G + 1);
+        wgrad_tables(p, at * ((p.N + BT - 1) / BT), tab, order, tab + p.G + 1);
         __syncthreads();
         n_items = __builtin_amdgcn_readfirstlane(tab[p.G]) * at * ((p.N + BT - 1) / BT);
     } else {
@@ -773,9 +775,14 @@ void grouped_mm_kernel(MmP p) {
         }
     };
     // Sums stay in 32 bits until here: the one rounding to the output's type.
+    // The values pass through LDS, 16 rows x 64 bytes at a time (two tiles in 16
+    // bits or one in 32), so that 4 neighbouring lanes store 64 bytes of a row:
+    // stored as they come out of the products, 16 neighbouring lanes hold 16
+    // rows, and an item of any length took XX us longer. A wave's LDS accesses
+    // are done in order, so one piece of LDS serves all its passes without waits.
     // Every lane stores, past an edge outside the resource (dropped), so a wave
-    // always issues 4 NB stores and the next K-tile's waits can leave them in
-    // flight.
+    // always issues 2 NB (4 NB) stores and the next K-tile's waits can leave them
+    // in flight.
     // (the variants are compiled apart: with a run-time choice inside, the waits
     // of the adding variant's loads end up before every store of the others)
     auto store = [&](const MmItem& c, auto f16_, auto f32_, auto add_) __attribute__((always_inline)) {
@@ -791,14 +798,30 @@ void grouped_mm_kernel(MmP p) {
         const rsrc_t r = make_rsrc(base, (uint32_t)(((size_t)(rows - 1) * ld + cols) * es));
         // rows past the tile's are past the resource by themselves; values past
         // the operand's end (a partial tile only) are sent there
-        const int fresh = mm_fresh(lane), a0 = 64 * wi + 4 * (fresh >> 4);
-        uint32_t o = (uint32_t)((16 * NB * ti + (fresh & 15)) * (int)ld + a0) * (uint32_t)es;
+        constexpr bool pair = es == 2 && !add;
+        const int fresh = mm_fresh(lane), wr = fresh & 15, wq = fresh >> 4, rr = fresh >> 2, rc = fresh & 3;
+        uint8_t* const out = smem + NST * Geo::Stage + w * (kMmOut / 8);
+        uint8_t* const put = out + wr * 64;                  // 16-byte chunks swizzled by row / 4
+        const uint8_t* const got = out + rr * 64 + (rc ^ ((rr >> 2) & 3)) * 16;
+        const int a0 = 64 * wi + (pair ? 8 : 4) * rc;
+        uint32_t o = (uint32_t)((16 * NB * ti + rr) * (int)ld + a0) * (uint32_t)es;
         #pragma unroll
         for (int u = 0; u < NB; ++u) {
             #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                f32x4 v = acc[u][t];
+            for (int t = 0; t < 4; t += pair ? 2 : 1) {
                 const uint32_t ot = a0 + 16 * t < cols ? o + (uint32_t)(16 * t * es) : kMmInvalid;
+                if constexpr (pair) {
+                    #pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const f32x4& v = acc[u][t + k];
+                        *(u32x2_t*)(put + ((2 * k + (wq >> 1)) ^ ((wr >> 2) & 3)) * 16 + (wq & 1) * 8) =
+                            u32x2_t{pack16(v[0], v[1], f16), pack16(v[2], v[3], f16)};
+                    }
+                    __builtin_amdgcn_raw_buffer_store_b128(*(const i32x4*)got, r, ot, 0, 0);
+                    continue;
+                }
+                *(f32x4*)(put + (wq ^ ((wr >> 2) & 3)) * 16) = acc[u][t];
+                f32x4 v = *(const f32x4*)got;
                 if constexpr (es == 4) {
                     if constexpr (add) {
                         const f32x4 e = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, ot, 0, 0));
@@ -854,11 +877,12 @@ void grouped_mm_kernel(MmP p) {
     // than the stores, which then count as newer.
     constexpr int KEPT = mm_kind(MODE) == kWgrad8 ? 8 : 0;            // requests of the 8-bit rows in turn 1
     constexpr int L1 = mm_turn_requests(EL, MODE, NB, 1), L2 = mm_turn_requests(EL, MODE, NB, 0);
+    constexpr int STORES = is_wgrad(MODE) ? 4 * NB : 2 * NB;
     int stored = 0;                                          // K-tiles whose waits leave the last stores in flight
     auto wait_for = [&](auto n) __attribute__((always_inline)) {
         constexpr int N = decltype(n)::value;
-        static_assert(N + 4 * NB < 64, "vmcnt");
-        if (stored > 0) __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + 4 * NB, 15));
+        static_assert(N + STORES < 64, "vmcnt");
+        if (stored > 0) __builtin_amdgcn_s_waitcnt(waitcnt_imm(N + STORES, 15));
         else __builtin_amdgcn_s_waitcnt(waitcnt_imm(N, 15));
     };
     if constexpr (EL == kElFp8) fwn = load_fw(mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, tb, at, slot)), 0);
@@ -899,8 +923,9 @@ void grouped_mm_kernel(MmP p) {
                 #pragma unroll
                 for (int v = 0; v < 4; ++v) acc[NB - 1][t][v] = fmaf(d[t][v], sc, acc[NB - 1][t][v]);
         }
-        // (an item without K-tiles stores between two others' stores: not counted)
-        stored = (is_wgrad(MODE) && (p.accumulate || c.nk == 0)) ? 0 : NST - 1;
+        // (an item without K-tiles stores between two others' stores: not
+        // counted, nor the fewer stores of a weight gradient in 16 bits)
+        stored = is_wgrad(MODE) && (p.accumulate || c.nk == 0 || (c.slot < 0 && !p.out_f32)) ? 0 : NST - 1;
         if (!is_wgrad(MODE) || c.nk > 0 || !p.accumulate) {
             constexpr std::integral_constant<int, EL == kElF16> same{};
             constexpr std::true_type yes{};
@@ -944,7 +969,8 @@ int launch_mm(const MmP& p, int max_items, hipStream_t stream) {
 template <int EL, int MODE>
 int launch_mm_rows(const MmP& p, int kind, int rows, hipStream_t stream) {
     if (rows <= 64) return moe_launch_mm_rows(&p, EL, kind, rows, stream);
-    return rows > 128 ? launch_mm<EL, MODE, 8>(p, mm_items(p, 256), stream)
+    // (three stages of 128 rows leave LDS for 2047 groups)
+    return rows > 128 || MmGeom<EL, 4>::Lds(p.G, false) > kMmLds ? launch_mm<EL, MODE, 8>(p, mm_items(p, 256), stream)
                       : launch_mm<EL, MODE, 4>(p, mm_items(p, 128), stream);
 }
 
