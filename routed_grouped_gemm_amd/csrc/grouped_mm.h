@@ -156,8 +156,9 @@ MOE_DEV void mm_passes(const MmP& p, int bt, int lane, int* pass_off) {
     if (lane == 0) pass_off[p.G] = run;
 }
 
-// Where a workgroup is: its items and this lane.
-struct MmWhere { int n_items, at, grid, slot, lane, w; };
+// Where a workgroup is: its items and this lane. dealt: how wgrad's items are
+// dealt out (mm_nth).
+struct MmWhere { int n_items, at, grid, slot, lane, w, dealt; };
 
 // largest index i in [0, n) with at[i] <= v (at[0] <= v, non-decreasing): 64
 // entries at a time
@@ -185,11 +186,17 @@ MOE_DEV int group_ktiles(const MmP& p, int g) {
     group_rows(p, g, lo, hi);
     return (hi - lo + 63) / 64;
 }
-// number of the item that a workgroup takes in its round: wgrad's items come
-// longest first, so every other round is dealt out backwards
+// Number of the item that a workgroup takes in its round. wgrad's items come
+// longest first and are dealt out backwards in some rounds: dealt 0, every
+// other whole round; dealt 1, every round but the first.
+MOE_DEV int wgrad_nth(int round, int n_items, int grid, int slot, int dealt) {
+    const bool back = dealt ? round > 0 : (round & 1) && (round + 1) * grid <= n_items;
+    return round * grid + (back ? grid - 1 - slot : slot);
+}
 template <int MODE>
-MOE_DEV int mm_nth(int round, int grid, int slot) {
-    return round * grid + (is_wgrad(MODE) && (round & 1) ? grid - 1 - slot : slot);
+MOE_DEV int mm_nth(int round, const MmWhere& wh) {
+    if constexpr (is_wgrad(MODE)) return wgrad_nth(round, wh.n_items, wh.grid, wh.slot, wh.dealt);
+    return round * wh.grid + wh.slot;
 }
 
 // work item number `item`: tiles of AT values of the a axis (at of them), BT of the b axis

@@ -159,7 +159,7 @@ void grouped_mm_rows_kernel(MmP p) {
     const int grid = gridDim.x;
     const int slot = (grid % 8 == 0) ? (blockIdx.x % 8) * (grid / 8) + blockIdx.x / 8 : blockIdx.x;
     if (slot >= n_items) return;
-    const MmWhere wh{n_items, at, grid, slot, lane, w};
+    const MmWhere wh{n_items, at, grid, slot, lane, w, 0};
 
     // fp8: the weight scales of a part's K-tiles, one per lane, loaded an item
     // ahead (a load in the K loop would be waited for in every K-tile)
