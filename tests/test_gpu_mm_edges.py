@@ -212,3 +212,42 @@ def test_bindings_refuse():
     with pytest.raises(moe.MoeError):                # too many groups
         moe.moe_grouped_mm(x, torch.zeros((2050, 8, 64), dtype=BF, device="cuda"), torch.zeros(2051, dtype=torch.int32, device="cuda"))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("R,counts", [(1200, [300, 900]), (500, [130, 0, 129, 100]), (20, [3, 17])])
+def test_outputs_at_multiples_of_8_bytes(R, counts):
+    """Rows of y that start at odd multiples of 8 bytes, columns beside them
+    untouched, with every tile height."""
+    banner(f"8-byte rows {R} {counts}")
+    g, N, K = gen(R), 264, 144
+    o = torch.cat([i32([0]), i32(counts).cumsum(0).to(torch.int32)])
+    x, w = randn(g, (R, K), BF), randn(g, (len(counts), N, K), BF, 0.1)
+    xq, xs = moe.moe_quantize_block(x)
+    wq, ws = moe.moe_quantize_block_weights(w)
+    used = sum(counts)
+    for what in ("mm", "kn", "fp8"):
+        yb = torch.full((R + 2, N + 12), -7.0, dtype=BF, device="cuda")
+        y = yb[1:1 + R, 4:4 + N]
+        if what == "fp8":
+            moe.moe_grouped_mm_fp8(xq, xs, wq, ws, o, out=y)
+            ref, mag = ref_mm(decode(xq, xs), decode_w(wq, ws), o, None, False)
+        else:
+            moe.moe_grouped_mm(x, w.transpose(1, 2).contiguous() if what == "kn" else w, o, w_kn=what == "kn", out=y)
+            ref, mag = ref_mm(x, w, o, None, False)
+        check(y[:used].contiguous(), ref[:used], mag[:used], K, what, extra=MFMA_REL if what == "fp8" else 0.0)
+        y[:used] = -7.0
+        assert (yb == -7).all(), what
+
+
+def test_more_groups_than_three_stages_leave_tables_for():
+    """2049 groups at a size that asks for tiles of 128 rows."""
+    banner("2049 groups, 128 rows")
+    g, G, N, K, per = gen(16), 2049, 256, 512, 100
+    R = G * per
+    x = randn(g, (R, K), BF)
+    w = randn(g, (G, N, K), BF, 0.1)
+    y = moe.moe_grouped_mm(x, w, torch.arange(0, R + 1, per, device="cuda", dtype=torch.int32))
+    for e in (0, 1, 1023, 2047, 2048):
+        a, b = x[e * per:(e + 1) * per].double(), w[e].double().t()
+        check(y[e * per:(e + 1) * per], a @ b, a.abs() @ b.abs(), K, f"group {e}")
+    assert y.isfinite().all()
