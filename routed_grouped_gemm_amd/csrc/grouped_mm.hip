@@ -41,13 +41,13 @@
 // Persistent grid; the requests run ahead across items, so the next item's
 // first K-tiles are in flight during an item's epilogue.
 //
-// Measured, one group, BF16: 16384 x 4096 x 4096 430 us (1280 TFLOP/s) with W
-// [N, K], 405 (1355) with W [K, N], FP8 261 to 271 (2030 to 2100); weight gradients of 16384 x
-// 2816 x 2048 in 8 equal groups 187 us (1010), from 8-bit rows 210. The matrix
-// cores are busy 48% (few, uneven items) to 62% of the cycles, and the clock
-// falls to 1.8 to 2.1 GHz under them; no LDS bank conflicts, LDS active 18 to
-// 23%. FP8 has the same LDS traffic and matrix cycles per K-tile, and 4
-// additions with the block's scale per matrix instruction besides (48%).
+// Measured, one group, BF16: 16384 x 4096 x 4096 413 us (1330 TFLOP/s) with W
+// [N, K], 395 (1390) with W [K, N], FP8 250 (2200); weight gradients of 16384 x
+// 2816 x 2048 in 8 equal groups 187 us (1010), from 8-bit rows 209. The matrix
+// cores are busy half of the cycles (few, uneven items) to 62%, and the clock
+// falls to 1.8 to 2.1 GHz under them; the LDS is active for about a quarter, bank
+// conflicts come from the stores alone. FP8 has the same LDS traffic and matrix cycles per K-tile, and
+// 4 additions with the block's scale per matrix instruction besides.
 #include <algorithm>
 
 #include "grouped_mm.h"
