@@ -437,7 +437,7 @@ int32_t moe_layer_workspace_offsets(int32_t T, int32_t E_tot, int32_t k, int32_t
  * dtype: MOE_T_BF16 or MOE_T_F16, of x, w, dy and y. dW is of the same type,
  * or fp32 with MOE_WGRAD_F32. Leading dimensions are in elements; rows start
  * at multiples of 16 bytes (8 bytes for y). N % 8 == 0, K % 8 == 0, both at
- * most MOE_MM_MAX_DIM; G <= 2049. With a source array (row_src, x_src,
+ * most MOE_MM_MAX_DIM; R_max <= MOE_MM_MAX_ROWS; G <= 2049. With a source array (row_src, x_src,
  * dy_src) the indexed array must stay below 2^32 - 2^22 bytes; sources outside
  * it read as zero rows.
  *
@@ -454,6 +454,7 @@ int32_t moe_layer_workspace_offsets(int32_t T, int32_t E_tot, int32_t k, int32_t
 #define MOE_T_F16  1
 #define MOE_T_F32  2
 #define MOE_MM_MAX_DIM (1 << 20)
+#define MOE_MM_MAX_ROWS ((1 << 29) - 1)
 #define MOE_MM_W_KN           (1u << 16)
 #define MOE_WGRAD_ACCUMULATE  (1u << 17)
 #define MOE_WGRAD_F32         (1u << 18)

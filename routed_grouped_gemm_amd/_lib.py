@@ -21,6 +21,7 @@ MOE_LAYER_TOKEN_RING = 1 << 11
 MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 MOE_T_BF16, MOE_T_F16, MOE_T_F32 = 0, 1, 2
 MOE_MM_MAX_DIM = 1 << 20
+MOE_MM_MAX_ROWS = (1 << 29) - 1
 MOE_MM_W_KN = 1 << 16
 MOE_WGRAD_ACCUMULATE = 1 << 17
 MOE_WGRAD_F32 = 1 << 18

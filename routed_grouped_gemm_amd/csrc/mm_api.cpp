@@ -21,8 +21,12 @@ constexpr int64_t kGatherBytes = (1ll << 32) - (1ll << 22);
 // largest leading dimension: 256 rows of a tile stay below 2 GiB
 constexpr int32_t kMaxLd = 1 << 22;
 
+// bound on the rows of a call: row counts rounded up to a tile and the byte
+// sizes of source arrays stay inside signed 32 bits
+constexpr int32_t kMaxRows = MOE_MM_MAX_ROWS;
+
 int32_t check_dims(int32_t R_max, int32_t N, int32_t K, int32_t G, int kmult) {
-    if (R_max < 0 || G < 1 || G > MOE_MAX_EXPERTS + 1) return MOE_ERR_SHAPE;
+    if (R_max < 0 || R_max > kMaxRows || G < 1 || G > MOE_MAX_EXPERTS + 1) return MOE_ERR_SHAPE;
     if (N < 8 || N % 8 || N > MOE_MM_MAX_DIM || K < kmult || K % kmult || K > MOE_MM_MAX_DIM) return MOE_ERR_SHAPE;
     return MOE_OK;
 }

@@ -1,0 +1,39 @@
+"""Limits of the grouped products, weight gradients and their workspaces,
+answered from scalars and pointers alone (nothing is launched)."""
+from routed_grouped_gemm_amd import _lib
+
+F = 0x1000                                          # stands for a device pointer; never dereferenced
+OK, NULL, SHAPE, UNSUP, WS = (_lib.MOE_OK, _lib.MOE_ERR_NULL, _lib.MOE_ERR_SHAPE, _lib.MOE_ERR_UNSUPPORTED,
+                              _lib.MOE_ERR_WORKSPACE)
+BF16, F16 = _lib.MOE_T_BF16, _lib.MOE_T_F16
+
+
+def mm(R=64, N=256, K=128, G=4, src=None, ws=F, ws_bytes=1 << 40, x_rows=None):
+    return _lib.load().moe_grouped_mm(F, R if x_rows is None else x_rows, K, src, F, BF16, F, R, N, K, G, 0, F, N, ws,
+                                      ws_bytes, None)
+
+
+def fp8(R=64, N=256, K=128, G=4, src=None, ws=F, ws_bytes=1 << 40, x_rows=None):
+    return _lib.load().moe_grouped_mm_fp8(F, F, R if x_rows is None else x_rows, src, F, F, F, R, N, K, G, BF16, F, N,
+                                          ws, ws_bytes, None)
+
+
+def wgrad(R=64, N=256, K=128, G=4, src=None, xs=None, ws=F, ws_bytes=1 << 40, x_rows=None):
+    return _lib.load().moe_grouped_wgrad(F, R, N, None, F, R if x_rows is None else x_rows, K, src, xs, BF16, F, R, N,
+                                         K, G, 0, F, ws, ws_bytes, None)
+
+
+def test_rows_past_the_limit():
+    """Row counts that 32-bit arithmetic on the device does not hold (a tile more
+    than the rows, four bytes a source) are refused, with and without sources."""
+    lib = _lib.load()
+    most = _lib.MOE_MM_MAX_ROWS
+    assert most == 2**29 - 1
+    for R in (most + 1, 1 << 30, 2**31 - 64, 2**31 - 1):
+        for src in (None, F):
+            at = dict(R=R, N=8, K=16, G=1, src=src, x_rows=64 if src else R)
+            assert mm(**at) == SHAPE and fp8(**at) == SHAPE, (R, src)
+            assert wgrad(**at) == SHAPE and wgrad(xs=F, **at) == SHAPE, (R, src)
+        for f in (lib.moe_grouped_mm_workspace_size, lib.moe_grouped_wgrad_workspace_size,
+                  lib.moe_grouped_mm_fp8_workspace_size):
+            assert f(R, 1, 64, 64) == 0
