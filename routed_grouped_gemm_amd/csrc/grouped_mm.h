@@ -142,18 +142,23 @@ MOE_DEV MmItem mm_scalar(const MmItem& c) {
 }
 
 // pass_off[g] = passes of `bt` rows before group g, pass_off[G] their number,
-// in LDS; one wave writes them (a barrier must follow)
-MOE_DEV void mm_passes(const MmP& p, int bt, int lane, int* pass_off) {
-    int run = 0;
+// in LDS; one wave writes them (a barrier must follow). per: items of a pass.
+// Rows are below 2^29 and a pass is 32 or more, so 64 groups' passes fit 32
+// bits; the items of all do wherever y is an array that exists, but groups that
+// overlap (offsets that do not ascend) can have more: then there are none.
+MOE_DEV void mm_passes(const MmP& p, int bt, int per, int lane, int* pass_off) {
+    int64_t run = 0;
     for (int g0 = 0; g0 < p.G; g0 += 64) {
         int lo = 0, hi = 0;
         if (g0 + lane < p.G) group_rows(p, g0 + lane, lo, hi);
         const int n = (hi - lo + bt - 1) / bt;
         const int inc = wave_incl_scan(n);
-        if (g0 + lane < p.G) pass_off[g0 + lane] = run + inc - n;
+        if (g0 + lane < p.G) pass_off[g0 + lane] = (int)run + inc - n;
         run += __builtin_amdgcn_readlane(inc, 63);
     }
-    if (lane == 0) pass_off[p.G] = run;
+    if (lane == 0) pass_off[p.G] = (int)run;
+    if (run * per > (1 << 30))
+        for (int g = lane; g <= p.G; g += 64) pass_off[g] = 0;
 }
 
 // Where a workgroup is: its items and this lane. dealt: how wgrad's items are

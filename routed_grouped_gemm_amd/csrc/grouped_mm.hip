@@ -650,7 +650,7 @@ void grouped_mm_kernel(MmP p) {
         __syncthreads();
         n_items = __builtin_amdgcn_readfirstlane(tab[p.G]) * at * ((p.N + BT - 1) / BT);
     } else {
-        if (w == 0) mm_passes(p, BT, lane, tab);
+        if (w == 0) mm_passes(p, BT, at, lane, tab);
         __syncthreads();
         n_items = __builtin_amdgcn_readfirstlane(tab[p.G]) * at;
     }

@@ -153,7 +153,7 @@ void grouped_mm_rows_kernel(MmP p) {
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int q = lane >> 4, j = lane & 15;
     const int at = (p.N + kRowsA - 1) / kRowsA;
-    if (w == 0) mm_passes(p, BT, lane, tab);
+    if (w == 0) mm_passes(p, BT, at * p.parts, lane, tab);
     __syncthreads();
     const int n_items = __builtin_amdgcn_readfirstlane(tab[p.G]) * at * p.parts;
     const int grid = gridDim.x;
