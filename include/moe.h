@@ -447,8 +447,8 @@ int32_t moe_layer_workspace_offsets(int32_t T, int32_t E_tot, int32_t k, int32_t
  * dtype MOE_T_BF16 only; ldx % 8 == 0 and rows at multiples of 8 bytes.
  *
  * No output may overlap an input (or, in these calls, another output).
- * ws: workspace of the matching size function (may be 0), one for each call in
- * flight. Results are the same bits every time.
+ * ws: workspace of the matching size function (may be 0) at a multiple of 16
+ * bytes, one for each call in flight. Results are the same bits every time.
  */
 #define MOE_T_BF16 0
 #define MOE_T_F16  1

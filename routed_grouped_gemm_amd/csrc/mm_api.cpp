@@ -43,9 +43,10 @@ int32_t check_rows(const void* p, int32_t rows, int32_t cols, int32_t ld, int eb
     return MOE_OK;
 }
 
+// partial sums are stored and loaded 16 bytes at a time
 int32_t check_ws(size_t need, const void* ws, size_t ws_bytes) {
     if (ws_bytes < need || (need && !ws)) return MOE_ERR_WORKSPACE;
-    return MOE_OK;
+    return need && !aligned(ws, 16) ? MOE_ERR_SHAPE : MOE_OK;
 }
 
 bool t16(int32_t dtype) { return dtype == MOE_T_BF16 || dtype == MOE_T_F16; }

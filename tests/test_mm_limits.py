@@ -37,3 +37,20 @@ def test_rows_past_the_limit():
         for f in (lib.moe_grouped_mm_workspace_size, lib.moe_grouped_wgrad_workspace_size,
                   lib.moe_grouped_mm_fp8_workspace_size):
             assert f(R, 1, 64, 64) == 0
+
+
+def test_workspace_is_checked():
+    """A call that splits its sums refuses a workspace that is missing, too small
+    or not at a multiple of 16 bytes (partial sums go there 16 bytes at a time)."""
+    lib = _lib.load()
+    few = dict(R=16, G=1, N=1024, K=4096)            # few tiles: split
+    need = {mm: lib.moe_grouped_mm_workspace_size(16, 1, 1024, 4096),
+            fp8: lib.moe_grouped_mm_fp8_workspace_size(16, 1, 1024, 4096)}
+    one = dict(R=16384, G=1, N=256, K=256)
+    need[wgrad] = lib.moe_grouped_wgrad_workspace_size(16384, 1, 256, 256)
+    for f, at in ((mm, few), (fp8, few), (wgrad, one)):
+        assert need[f] > 0
+        assert f(ws=None, ws_bytes=need[f], **at) == WS and f(ws_bytes=need[f] - 1, **at) == WS, f.__name__
+        assert f(ws=None, ws_bytes=0, **at) == WS
+        for odd in (1, 4, 8):
+            assert f(ws=F + odd, ws_bytes=need[f] + 16, **at) == SHAPE, (f.__name__, odd)
