@@ -312,6 +312,12 @@ def moe_grouped_w2(w2: PackedWeights, counts, offsets, hq, hs, H: int,
 
 # ----------------------------------------------------------------- combine
 def moe_combine(y, slot_row, H: int, row_w=None, out=None, stream=None):
+    """y: BF16 rows [R, H] (bfloat16, or their bits as uint16 or int16). Returns
+    the tokens' sums, BF16 bits in uint16 [T, H]."""
+    if y.dtype not in (torch.bfloat16, torch.uint16, torch.int16):
+        raise MoeError(f"y must be BF16 (bfloat16, or its bits as uint16 or int16), got {y.dtype}")
+    if not y.is_contiguous() or (y.dim() > 1 and y.shape[-1] != H):
+        raise MoeError(f"y must be contiguous rows of {H}, got {tuple(y.shape)} with strides {y.stride()}")
     T, ks = slot_row.shape
     with _on(stream):
         if out is None:
