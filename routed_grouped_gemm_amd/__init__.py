@@ -515,6 +515,16 @@ def _offsets(offsets, G: int, device) -> None:
     _dense(offsets, (G + 1,), torch.int32, "offsets", device)
 
 
+def _n_rows(src, t, name: str) -> int:
+    """Rows that a call reads of t, directly or through src (whose type and
+    device are checked once all operands give the same number)."""
+    if src is None:
+        return t.shape[0]
+    if src.dim() != 1:
+        raise MoeError(f"{name} must be 1-D, got {tuple(src.shape)}")
+    return src.shape[0]
+
+
 def moe_grouped_mm(x, w, offsets, w_kn: bool = False, row_src=None, out=None, stream=None):
     """y[r] = x[r] . W_g^T for the rows r of group g (offsets, int32 [G + 1] on
     the device): w [G, N, K], or [G, K, N] with w_kn. x [R, K], or [T, K] read
@@ -527,7 +537,7 @@ def moe_grouped_mm(x, w, offsets, w_kn: bool = False, row_src=None, out=None, st
     _dense(w, w.shape, x.dtype, "w", dev)
     G, N = w.shape[0], w.shape[2 if w_kn else 1]
     _offsets(offsets, G, dev)
-    R = T if row_src is None else row_src.shape[0]
+    R = _n_rows(row_src, x, "row_src")
     _dense(row_src, (R,), torch.int32, "row_src", dev)
     with _at(dev, stream):
         if out is None:
@@ -554,9 +564,11 @@ def moe_grouped_wgrad(dy, x, offsets, dy_src=None, x_src=None, x_scales=None, ou
     _mat(x, (torch.uint8,) if x_scales is not None else (dy.dtype,), "x", dev)
     K = x.shape[1]
     _dense(x_scales, (x.shape[0], -(-K // 128)), torch.float32, "x_scales", dev)
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise MoeError(f"offsets must be 1-D with at least 2 elements, got {tuple(offsets.shape)}")
     G = offsets.shape[0] - 1
     _offsets(offsets, G, dev)
-    n = {t.shape[0] for t in (dy if dy_src is None else dy_src, x if x_src is None else x_src)}
+    n = {_n_rows(dy_src, dy, "dy_src"), _n_rows(x_src, x, "x_src")}
     if len(n) != 1:
         raise MoeError(f"dy and x give different numbers of rows: {sorted(n)}")
     R = n.pop()
@@ -631,7 +643,7 @@ def moe_grouped_mm_fp8(xq, xs, wq, ws, offsets, row_src=None, out=None, out_dtyp
     _dense(wq, (G, N, K), torch.uint8, "wq", dev)
     _dense(ws, (G, -(-N // 128), kb), torch.float32, "ws", dev)
     _offsets(offsets, G, dev)
-    R = T if row_src is None else row_src.shape[0]
+    R = _n_rows(row_src, xq, "row_src")
     _dense(row_src, (R,), torch.int32, "row_src", dev)
     if out is not None:
         out_dtype = out.dtype
