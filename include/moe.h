@@ -510,6 +510,18 @@ int32_t moe_grouped_mm_fp8(const uint8_t* xq, const float* xs, int32_t x_rows, c
                            int32_t R_max, int32_t N, int32_t K, int32_t G, int32_t dtype, void* y,
                            int32_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/*
+ * How a call of these sizes runs, from host scalars alone (the current
+ * device's compute units enter). moe_grouped_mm_plan (fp8 != 0: of
+ * moe_grouped_mm_fp8): rows of a tile (32 or 64: the weight-streaming kernel;
+ * 128 or 256: the LDS-tiled kernel) and the parts that the reduction axis is
+ * split into. moe_grouped_wgrad_plan: rows of a part, longer groups being split
+ * (0: no group can be longer). The order of a sum follows from these.
+ */
+int32_t moe_grouped_mm_plan(int32_t R_max, int32_t G, int32_t N, int32_t K, int32_t fp8,
+                            int32_t* tile_rows, int32_t* parts);
+int32_t moe_grouped_wgrad_plan(int32_t R_max, int32_t G, int32_t N, int32_t K, int32_t* part_rows);
+
 /* ---- the gated activation with its input kept in 8 bits -------------------------- */
 /*
  * moe_glu_checkpoint: pre = [g | u] rows of 2I (dtype MOE_T_BF16 or MOE_T_F16,

@@ -591,6 +591,20 @@ def moe_grouped_wgrad(dy, x, offsets, dy_src=None, x_src=None, x_scales=None, ou
     return out
 
 
+def moe_grouped_mm_plan(R_max: int, G: int, N: int, K: int, fp8: bool = False) -> tuple[int, int]:
+    """(rows of a tile, parts of the reduction axis) of a grouped product of these sizes."""
+    rows, parts = C.c_int32(), C.c_int32()
+    _check(lib.moe_grouped_mm_plan(R_max, G, N, K, int(fp8), C.byref(rows), C.byref(parts)), "moe_grouped_mm_plan")
+    return rows.value, parts.value
+
+
+def moe_grouped_wgrad_plan(R_max: int, G: int, N: int, K: int) -> int:
+    """Rows of a part of a weight gradient's groups (0: no group can be longer)."""
+    rows = C.c_int32()
+    _check(lib.moe_grouped_wgrad_plan(R_max, G, N, K, C.byref(rows)), "moe_grouped_wgrad_plan")
+    return rows.value
+
+
 def moe_quantize_block(x, n_rows=None, codes=None, scales=None, stream=None):
     """Rows of x (bf16, fp16 or fp32 [R, K]) to E4M3 codes uint8 [R, K] and
     power-of-two scales f32 [R, ceil(K/128)]. n_rows: an int32 device tensor

@@ -88,6 +88,8 @@ SIGNATURES = {
     "moe_quantize_block_weights": (I32, [P, I32, I32, I32, I32, P, P, P]),
     "moe_grouped_mm_fp8_workspace_size": (SZ, [I32, I32, I32, I32]),
     "moe_grouped_mm_fp8": (I32, [P, P, I32, P, P, P, P, I32, I32, I32, I32, I32, P, I32, P, SZ, P]),
+    "moe_grouped_mm_plan": (I32, [I32, I32, I32, I32, I32, C.POINTER(I32), C.POINTER(I32)]),
+    "moe_grouped_wgrad_plan": (I32, [I32, I32, I32, I32, C.POINTER(I32)]),
     "moe_glu_checkpoint": (I32, [P, I32, I32, I32, I32, P, P, EP, P, P, P, P]),
     "moe_glu_checkpoint_backward": (I32, [P, P, P, I32, I32, I32, I32, P, P, EP, P, P, P, P]),
 }

@@ -1007,8 +1007,7 @@ int launch_mm(const MmP& p, int max_items, hipStream_t stream) {
 template <int EL, int MODE>
 int launch_mm_rows(const MmP& p, int kind, int rows, hipStream_t stream) {
     if (rows <= 64) return moe_launch_mm_rows(&p, EL, kind, rows, stream);
-    // (three stages of 128 rows leave LDS for 2047 groups)
-    return rows > 128 || MmGeom<EL, 4>::Lds(p.G, false) > kMmLds ? launch_mm<EL, MODE, 8>(p, mm_items(p, 256), stream)
+    return rows > 128 ? launch_mm<EL, MODE, 8>(p, mm_items(p, 256), stream)
                       : launch_mm<EL, MODE, 4>(p, mm_items(p, 128), stream);
 }
 
@@ -1045,6 +1044,9 @@ MmPlan mm_plan(bool fp8, int R_max, int G, int N, int K) {
             if (t < least) { least = t; best = MmPlan{kRowsOf[i], parts}; }
         }
     }
+    // (three stages of 128 rows leave LDS for the tables of 2047 groups)
+    const int lds = fp8 ? MmGeom<kElFp8, 4>::Lds(G, false) : MmGeom<kElBf16, 4>::Lds(G, false);
+    if (best.rows == 128 && lds > kMmLds) best.rows = 256;
     return best;
 }
 
@@ -1081,6 +1083,13 @@ int launch_wgrad(const MmP& p, int items, hipStream_t stream) {
 }
 
 }  // namespace
+
+void moe_mm_plan(bool fp8, int R_max, int G, int N, int K, int* tile_rows, int* parts) {
+    const MmPlan plan = mm_plan(fp8, R_max, G, N, K);
+    *tile_rows = plan.rows;
+    *parts = plan.parts;
+}
+int moe_wgrad_plan(int R_max, int G, int N, int K) { return wgrad_part(R_max, G, N, K) * 64; }
 
 size_t moe_mm_workspace_bytes(int kind, bool fp8, int R_max, int G, int N, int K) {
     if (kind == 2) {

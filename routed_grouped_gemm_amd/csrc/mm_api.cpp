@@ -179,6 +179,23 @@ MOE_EXPORT int32_t moe_grouped_mm_fp8(const uint8_t* xq, const float* xs, int32_
     return hip_status(moe_launch_mm(c, stream));
 }
 
+MOE_EXPORT int32_t moe_grouped_mm_plan(int32_t R_max, int32_t G, int32_t N, int32_t K, int32_t fp8,
+                                       int32_t* tile_rows, int32_t* parts) {
+    const int32_t st = check_dims(R_max, N, K, G, fp8 ? 16 : 8);
+    if (st) return st;
+    if (!tile_rows || !parts) return MOE_ERR_NULL;
+    moe_mm_plan(fp8 != 0, R_max, G, N, K, tile_rows, parts);
+    return MOE_OK;
+}
+
+MOE_EXPORT int32_t moe_grouped_wgrad_plan(int32_t R_max, int32_t G, int32_t N, int32_t K, int32_t* part_rows) {
+    const int32_t st = check_dims(R_max, N, K, G, 8);
+    if (st) return st;
+    if (!part_rows) return MOE_ERR_NULL;
+    *part_rows = moe_wgrad_plan(R_max, G, N, K);
+    return MOE_OK;
+}
+
 MOE_EXPORT int32_t moe_glu_checkpoint(const void* pre, int32_t dtype, int32_t rows, int32_t I, int32_t ld,
                                       const float* row_w, const int32_t* n_rows, const moe_epilogue* epi, void* h,
                                       uint8_t* q, float* s, hipStream_t stream) {

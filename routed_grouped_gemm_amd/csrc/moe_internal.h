@@ -140,6 +140,8 @@ struct MmCall {
     void* out; int ldy;
     void* ws; size_t ws_bytes;
 };
+void moe_mm_plan(bool fp8, int R_max, int G, int N, int K, int* tile_rows, int* parts);
+int moe_wgrad_plan(int R_max, int G, int N, int K);          // rows of a part, 0: no group is split
 size_t moe_mm_workspace_bytes(int kind, bool fp8, int R_max, int G, int N, int K);
 int moe_launch_mm(const MmCall& c, hipStream_t stream);
 

@@ -54,3 +54,36 @@ def test_workspace_is_checked():
         assert f(ws=None, ws_bytes=0, **at) == WS
         for odd in (1, 4, 8):
             assert f(ws=F + odd, ws_bytes=need[f] + 16, **at) == SHAPE, (f.__name__, odd)
+
+
+def test_plans():
+    """Pure host functions: a tile height, a split only of few-row tiles, a
+    workspace exactly where something is split, and refusals as the calls'."""
+    import ctypes as C
+
+    lib = _lib.load()
+    rows, parts, part = C.c_int32(), C.c_int32(), C.c_int32()
+    out = C.byref(rows), C.byref(parts)
+    seen = set()
+    for f, size in ((0, lib.moe_grouped_mm_workspace_size), (1, lib.moe_grouped_mm_fp8_workspace_size)):
+        for R in (0, 1, 16, 300, 2600, 9000, 100000):
+            for G in (1, 8, 40, 2049):
+                for N, K in ((8, 16), (264, 528), (2056, 336), (4096, 7168)):
+                    assert lib.moe_grouped_mm_plan(R, G, N, K, f, *out) == OK
+                    assert rows.value in (32, 64, 128, 256) and parts.value >= 1
+                    assert parts.value == 1 or rows.value <= 64
+                    assert (size(R, G, N, K) > 0) == (parts.value > 1 and R > 0)
+                    seen.add((f, rows.value, parts.value > 1))
+        assert {r for g, r, _ in seen if g == f} == {32, 64, 128, 256}
+        assert lib.moe_grouped_mm_plan(64, 4, 252, 128, f, *out) == SHAPE
+        assert lib.moe_grouped_mm_plan(64, 4, 256, 128, f, None, out[1]) == NULL
+        assert lib.moe_grouped_mm_plan(64, 4, 256, 128, f, out[0], None) == NULL
+    assert lib.moe_grouped_mm_plan(64, 4, 256, 136, 1, *out) == SHAPE
+    for R in (0, 1, 64, 5000, 16384):
+        for G in (1, 8, 2049):
+            for N, K in ((8, 8), (256, 256), (2816, 2048)):
+                assert lib.moe_grouped_wgrad_plan(R, G, N, K, C.byref(part)) == OK
+                assert part.value % 64 == 0 and 0 <= part.value < max(R, 1) + 64
+                assert (lib.moe_grouped_wgrad_workspace_size(R, G, N, K) > 0) == (part.value > 0)
+    assert lib.moe_grouped_wgrad_plan(64, 0, 256, 256, C.byref(part)) == SHAPE
+    assert lib.moe_grouped_wgrad_plan(64, 4, 256, 256, None) == NULL
