@@ -541,6 +541,7 @@ int32_t moe_grouped_wgrad_plan(int32_t R_max, int32_t G, int32_t N, int32_t K, i
  *   h[r]    as the forward forms it, from the decoded values (NULL: not written);
  *           the input of the second product's weight gradient
  *   dw[r]   = sum_i dh * a(clamp(g)) * clamp(u)  (fp32, NULL: not written)
+ * A NaN in g or u stays one through every activation.
  * n_rows: NULL, or a device count: rows from *n_rows on are left as they were.
  * I % 8 == 0. No output may overlap an input.
  */

@@ -178,6 +178,16 @@ MOE_DEV float clamp_to(float v, float lim) {
     return v < -lim ? -lim : (v > lim ? lim : v);
 }
 
+// The activations of moe_device.h with a NaN gate kept by the squared ReLU too
+// (a maximum with 0 turns it into 0, and a diverged step would look sound).
+MOE_DEV float gate_value(float z, int act, float beta) {
+    return act == MOE_ACT_SRELU && z != z ? z : act_value(z, act, beta);
+}
+MOE_DEV void gate_and_grad(float z, int act, float beta, float& a, float& da) {
+    act_and_grad(z, act, beta, a, da);
+    if (act == MOE_ACT_SRELU && z != z) a = da = z;
+}
+
 // h = a(clamp(g)) clamp(u) w and the block codes of g and u: a lane holds 8
 // of each, 16 lanes a block of each half
 template <int T>
@@ -216,7 +226,7 @@ void glu_forward_kernel(GluP p) {
             float h[8];
             #pragma unroll
             for (int k = 0; k < 8; ++k)
-                h[k] = act_value(clamp_to(g.v[k], p.limit), p.act, p.beta) * clamp_to(u.v[k], p.limit) * w;
+                h[k] = gate_value(clamp_to(g.v[k], p.limit), p.act, p.beta) * clamp_to(u.v[k], p.limit) * w;
             store8<T>(p.h + (row * I + c * 8) * 2, h);
         }
     }
@@ -247,7 +257,7 @@ void glu_backward_kernel(GluP p) {
                 const float mu = !(lim > 0.f) || fabsf(u.v[k]) <= lim ? 1.f : 0.f;
                 const float gc = clamp_to(g.v[k], lim), uc = clamp_to(u.v[k], lim);
                 float a, da;
-                act_and_grad(gc, p.act, p.beta, a, da);
+                gate_and_grad(gc, p.act, p.beta, a, da);
                 const float dw = d.v[k] * w;
                 dg[k] = dw * uc * da * mg;
                 du[k] = dw * a * mu;
