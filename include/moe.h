@@ -443,12 +443,25 @@ int32_t moe_layer_workspace_offsets(int32_t T, int32_t E_tot, int32_t k, int32_t
  *
  * x as an 8-bit checkpoint (moe_grouped_wgrad, xs non-NULL): x holds E4M3
  * codes and xs [x_rows, ceil(K/128)] the scales moe_quantize_block wrote;
- * the decoded values are rounded to BF16 (exact for its power-of-two scales).
- * dtype MOE_T_BF16 only; ldx % 8 == 0 and rows at multiples of 8 bytes.
+ * the decoded values are rounded to BF16 (exact for power-of-two scales of
+ * 2^-117 and more: 4 significant bits, no value below BF16's normal range).
+ * dtype MOE_T_BF16 only (decoded values can be past FP16's range, and dy has
+ * the type of the decoded rows); ldx % 8 == 0 and rows at multiples of 8 bytes.
+ *
+ * In a training step of these calls the combine of FP16 rows is the caller's:
+ * moe_combine sums BF16 rows.
  *
  * No output may overlap an input (or, in these calls, another output).
  * ws: workspace of the matching size function (may be 0) at a multiple of 16
- * bytes, one for each call in flight. Results are the same bits every time.
+ * bytes, one for each call in flight. A product's is at most 8 MiB (fp32 sums
+ * of the parts of a few tiles). A weight gradient's is 256 KiB for each part of
+ * a group and 256 x 256 tile of its dW: 115 MB for 16384 rows in 8 groups, 2816
+ * x 2048; with 100000s of rows up to about 10 times dW in fp32, several GB.
+ * Results are the same bits every time.
+ *
+ * The launch follows R_max / G, which stands for the rows of a group (the
+ * counts are on the device): where far fewer rows are used than R_max, pass
+ * R_max as close to offsets[G] as the host knows it.
  */
 #define MOE_T_BF16 0
 #define MOE_T_F16  1
@@ -498,7 +511,10 @@ int32_t moe_quantize_block_weights(const void* w, int32_t dtype, int32_t G, int3
  * weight block's scale is formed in fp32 and must be finite and normal):
  *   y[r][n] = sum_b xs[s(r)][b] * ws_g[n / 128][b] * sum_{k in block b} xq[s(r)][k] * wq_g[n][k]
  * blocks of 128 along K, the inner sums on the FP8 matrix instructions, the
- * outer one in fp32, one rounding to dtype (MOE_T_BF16 or MOE_T_F16).
+ * outer one in fp32, one rounding to dtype (MOE_T_BF16 or MOE_T_F16). The
+ * instruction drops products below about 2^-15 of the largest near them: beside
+ * the rounding, an output is off by about 1e-5 of its sum of |terms| (Gaussian
+ * codes), 1e-4 where a block's codes spread over the whole range of E4M3.
  * xq [x_rows, K], xs [x_rows, ceil(K/128)], wq [G, N, K],
  * wscale [G, ceil(N/128), ceil(K/128)], y [R_max, N] with leading dimension
  * ldy. Groups, row_src and untouched rows as in moe_grouped_mm; G = 1 with

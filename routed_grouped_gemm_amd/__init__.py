@@ -3,8 +3,11 @@
 A thin PyTorch binding over libmoe (include/moe.h). Every function here only
 marshals arguments (device pointers, sizes, the current HIP stream) and calls
 the C ABI of the same name; all computation runs in the library's HIP kernels.
-PyTorch provides device memory and streams. Importing the package fails if the
-library has not been built (python routed_grouped_gemm_amd/build.py).
+PyTorch provides device memory and streams. No call records a gradient: the
+gradients of the products and of the activation are calls of their own
+(moe_grouped_mm with w_kn, moe_grouped_wgrad, moe_glu_checkpoint_backward), and
+outputs do not require one whatever the inputs do. Importing the package fails
+if the library has not been built (python routed_grouped_gemm_amd/build.py).
 """
 from __future__ import annotations
 
@@ -529,7 +532,8 @@ def moe_grouped_mm(x, w, offsets, w_kn: bool = False, row_src=None, out=None, st
     """y[r] = x[r] . W_g^T for the rows r of group g (offsets, int32 [G + 1] on
     the device): w [G, N, K], or [G, K, N] with w_kn. x [R, K], or [T, K] read
     through row_src (int32 [R]). bf16 or fp16; returns [R, N] of that type,
-    rows of no group unwritten."""
+    rows of no group unwritten. Records no gradient: the rows' is this call with
+    w_kn the other way, the weights' is moe_grouped_wgrad."""
     _mat(x, _T16, "x")
     dev, (T, K) = x.device, x.shape
     if w.dim() != 3 or w.shape[1 if w_kn else 2] != K:
@@ -558,7 +562,7 @@ def moe_grouped_wgrad(dy, x, offsets, dy_src=None, x_src=None, x_scales=None, ou
     (float32, or dy's type). dy [R, N] and x [R, K], or token-order arrays
     read through dy_src / x_src (int32 [R]). With x_scales, x is an 8-bit
     checkpoint (codes and scales of moe_quantize_block). accumulate adds to
-    `out`, which must then be given."""
+    `out`, which must then be given. Records no gradient."""
     _mat(dy, _T16, "dy")
     dev, N = dy.device, dy.shape[1]
     _mat(x, (torch.uint8,) if x_scales is not None else (dy.dtype,), "x", dev)
@@ -608,7 +612,7 @@ def moe_grouped_wgrad_plan(R_max: int, G: int, N: int, K: int) -> int:
 def moe_quantize_block(x, n_rows=None, codes=None, scales=None, stream=None):
     """Rows of x (bf16, fp16 or fp32 [R, K]) to E4M3 codes uint8 [R, K] and
     power-of-two scales f32 [R, ceil(K/128)]. n_rows: an int32 device tensor
-    of one element; rows from it on are left unwritten."""
+    of one element; rows from it on are left unwritten. Records no gradient."""
     _mat(x, _T_ANY, "x")
     dev, (R, K) = x.device, x.shape
     _dense(n_rows, () if n_rows is not None and n_rows.dim() == 0 else (1,), torch.int32, "n_rows", dev)
@@ -626,7 +630,7 @@ def moe_quantize_block(x, n_rows=None, codes=None, scales=None, stream=None):
 
 def moe_quantize_block_weights(w, codes=None, scales=None, stream=None):
     """w [G, N, K] (bf16, fp16 or fp32) to E4M3 codes uint8 [G, N, K] and
-    power-of-two scales f32 [G, ceil(N/128), ceil(K/128)]."""
+    power-of-two scales f32 [G, ceil(N/128), ceil(K/128)]. Records no gradient."""
     if w.device.type != "cuda" or w.dtype not in _T_ANY or w.dim() != 3 or not w.is_contiguous():
         raise MoeError("w must be a contiguous 3-D device tensor of bf16, fp16 or fp32")
     dev, (G, N, K) = w.device, w.shape
@@ -646,7 +650,8 @@ def moe_quantize_block_weights(w, codes=None, scales=None, stream=None):
 def moe_grouped_mm_fp8(xq, xs, wq, ws, offsets, row_src=None, out=None, out_dtype=torch.bfloat16, stream=None):
     """Grouped product of block-scaled FP8 operands: xq uint8 [R, K] (or [T, K]
     read through row_src) with xs f32 [.., ceil(K/128)], wq uint8 [G, N, K]
-    with ws f32 [G, ceil(N/128), ceil(K/128)]. Returns [R, N] bf16 or fp16."""
+    with ws f32 [G, ceil(N/128), ceil(K/128)]. Returns [R, N] bf16 or fp16.
+    Records no gradient."""
     if xq.device.type != "cuda" or xq.dim() != 2 or wq.dim() != 3 or wq.shape[2] != xq.shape[1]:
         raise MoeError("xq must be a 2-D device tensor and wq [G, N, K] of the same K")
     dev, (T, K) = xq.device, xq.shape
@@ -680,7 +685,8 @@ def moe_glu_checkpoint(pre, row_w=None, n_rows=None, epi: Epilogue | None = None
                        codes=None, scales=None, stream=None):
     """pre = [gate | up] rows [R, 2I] (bf16 or fp16) to h = act(gate) * up * w
     [R, I] and, with keep, pre in 8 bits: codes uint8 [R, 2I], scales f32
-    [R, 2, ceil(I/128)]. Returns (h, codes, scales)."""
+    [R, 2, ceil(I/128)]. Returns (h, codes, scales). Records no gradient: that is
+    moe_glu_checkpoint_backward."""
     _mat(pre, _T16, "pre")
     dev, R, I = pre.device, pre.shape[0], pre.shape[1] // 2
     if pre.shape[1] % 2:

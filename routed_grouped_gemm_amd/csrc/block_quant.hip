@@ -10,9 +10,11 @@
 //
 // All kernels here are bound by HBM: they read and write each byte once, 16
 // bytes (8 for codes) per lane and request. Measured (a large copy: 5.2 TB/s):
-// rows of 8192 x 7168 BF16 31 us, 5.7 TB/s; the activation of 49152 x 1408 104
-// us (562 MB, 5.4 TB/s), its backward of 24576 x 2048 FP16 88 to 95 us (510 MB,
-// 5.4 to 5.8 TB/s). With a few rows the call is host time, about 12 us.
+// rows of 8192 x 7168 BF16 31 us, 5.7 TB/s; weights of 8 x 4096 x 7168 BF16 138 us
+// (705 MB, 5.1 TB/s), FP32 of half the groups 109 us (5.4); the activation of
+// 49152 x 1408 107 us (558 MB, 5.2 TB/s), without codes 77 to 82 (415 MB, 5.1 to
+// 5.4), its backward of 24576 x 2048 FP16 95 us (506 MB, 5.3). With a few rows
+// the call is host time, about 14 us.
 #include <algorithm>
 
 #include "grouped_mm.h"

@@ -47,7 +47,8 @@
 // cores are busy half of the cycles (few, uneven items) to 62%, and the clock
 // falls to 1.8 to 2.1 GHz under them; the LDS is active for about a quarter, bank
 // conflicts come from the stores alone. FP8 has the same LDS traffic and matrix cycles per K-tile, and
-// 4 additions with the block's scale per matrix instruction besides.
+// 4 additions with the block's scale per matrix instruction besides (and sums the
+// 128 products of a block as the instruction does, see mfma_fp8).
 #include <algorithm>
 
 #include "grouped_mm.h"
@@ -640,7 +641,7 @@ void grouped_mm_kernel(MmP p) {
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int q = lane >> 4, j = lane & 15;
     const int wi = w & 3, ti = w >> 2;
-    const bool lead = w < 4;                                 // waves 0-3 issue the requests
+    const bool lead = w < 4;                                 // the half that multiplies first, half a step ahead
 
     const int na = is_wgrad(MODE) ? p.K : p.N;               // extent of the contiguous output axis
     const int at = (na + kATile - 1) / kATile;

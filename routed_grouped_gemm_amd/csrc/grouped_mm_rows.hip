@@ -82,10 +82,14 @@ MOE_DEV void rows_open(const MmP& p, const MmTables& tb, const MmWhere& wh, Rows
 }
 
 // request one K-tile into its stage, then move on (nothing once the items have
-// ended). Tiles of 32 rows are chosen where a group's rows are one pass, so each
-// weight is read once: those loads are non-temporal (84 -> 76 us for the BF16
-// decode above). With 64 rows several passes share the weights through the
-// caches (512 x 4096 x 4096: 40 us, non-temporal 43).
+// ended). Tiles of 32 rows serve groups of about one pass each, whose weights
+// are then read once: their weight loads are non-temporal (83 -> 77 us for the
+// BF16 decode above; 128 rows on one of 33 groups and 4 on the others, 2816 x
+// 2048, 89 -> 83). Where such a tile is chosen for a group of many passes that
+// costs little (264 x 520, 94 passes 11.7 -> 11.5 us; 264 x 1544, 10 passes 15.7
+// -> 16.2; 200 of 256 rows on one of 8 groups, 4096 x 4096, 75.7 -> 79.0). With
+// 64 rows several passes share the weights through the caches (512 x 4096 x
+// 4096: 40 us, non-temporal 43).
 template <int EL, int MODE, int NB, int NQ>
 MOE_DEV void rows_request(const MmP& p, const MmTables& tb, const MmWhere& wh, RowsReq<NQ>& R, uint8_t* smem) {
     using Geo = RowsGeom<EL, NB>;

@@ -1,6 +1,7 @@
 // C ABI of the 16-bit and block-scaled FP8 grouped products, the block
-// quantisers and the checkpointed activation: argument validation only (no
-// HIP API is touched before a call is found valid).
+// quantisers and the checkpointed activation: argument validation only
+// (nothing is launched before a call is found valid; the workspace a product
+// needs follows from its plan, which asks for the device's compute units).
 #include <hip/hip_runtime.h>
 #include <math.h>
 
@@ -100,6 +101,8 @@ MOE_EXPORT int32_t moe_grouped_wgrad(const void* dy, int32_t dy_rows, int32_t ld
                                      int32_t N, int32_t K, int32_t G, uint32_t flags, void* dw, void* ws,
                                      size_t ws_bytes, hipStream_t stream) {
     if (!t16(dtype) || (flags & ~(MOE_WGRAD_ACCUMULATE | MOE_WGRAD_F32))) return MOE_ERR_UNSUPPORTED;
+    // (codes times scales reach past fp16's range, and the product's operands
+    // are of one type: 8-bit rows are decoded to bf16, with bf16 gradients)
     if (xs && dtype != MOE_T_BF16) return MOE_ERR_UNSUPPORTED;
     int32_t st = check_dims(R_max, N, K, G, 8);
     if (st) return st;
