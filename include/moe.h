@@ -129,6 +129,7 @@ extern "C" {
 #define MOE_ACT_SWIGLU 0
 #define MOE_ACT_GEGLU  1
 #define MOE_ACT_SRELU  2
+#define MOE_ACT_NONE   3    /* a(z) = z: products with an epilogue and moe_layer_few only */
 typedef struct moe_epilogue {
     int32_t      act;        /* MOE_ACT_*                                        */
     float        beta;       /* Swish slope (MOE_ACT_SWIGLU only), e.g. 1.0f     */
@@ -568,6 +569,108 @@ int32_t moe_glu_checkpoint_backward(const uint8_t* q, const float* s, const void
                                     int32_t rows, int32_t I, int32_t ld_dh, const float* row_w,
                                     const int32_t* n_rows, const moe_epilogue* epi, void* dpre, void* h,
                                     float* dw, hipStream_t stream);
+
+/* ---- the layer for a few tokens ------------------------------------------------- */
+/*
+ * The whole routed layer for at most MOE_FEW_MAX_TOKENS tokens on 16-bit token
+ * rows, in two launches, with plain (not prepacked) weights: 16-bit ones as
+ * moe_grouped_mm takes them, or E4M3 codes with a scale per 128 x 128 as
+ * moe_quantize_block_weights writes them (any fp32 scales). For longer batches
+ * use moe_route, moe_permute, the grouped products and moe_combine.
+ *
+ *   out[t] = residual[t] + sum_j w_j (h_j W2_g^T + b2_g)     over t's local experts g = e_j
+ *   h_j    = a(clamp(g)) clamp(u),  [g | u] = x[t] W1_g^T + b1_g
+ *
+ * with the router's choice and weights w as moe_route (MOE_ROUTE_RENORM in
+ * flags) on logits [T, E_tot], local experts [e0, e0 + E_loc), and a shared
+ * expert (group E_loc, every token, weight 1) where shared_w1 and shared_w2 are
+ * given. w_j h_j is rounded to dtype between the products; every sum is fp32, in
+ * a fixed order; one rounding to dtype at the end. A token without a local
+ * expert gets its residual, or 0.
+ *
+ * dtype: MOE_T_BF16 or MOE_T_F16, of x, residual, out and 16-bit weights.
+ * w1 [E_loc, 2I, H] (gate rows, then up rows), w2 [E_loc, H, I], shared_w1
+ * [2I, H], shared_w2 [H, I]. Scales: all NULL for 16-bit weights, else
+ * w1_scales [E_loc, ceil(2I/128), ceil(H/128)], w2_scales [E_loc, ceil(H/128),
+ * ceil(I/128)], the shared expert's alike. Code times scale is never formed in
+ * 16 bits: the codes are exact there, the scale multiplies fp32 sums.
+ * epi: act, beta, limit as moe_epilogue (MOE_ACT_NONE too), bias f32 [G][2I]
+ * with G = E_loc + s; save_pre must be NULL. NULL: SwiGLU, beta = 1. bias2:
+ * NULL or f32 [G][H]. residual: NULL or [T, H] rows of ld_res; out itself may
+ * be given. No other output may overlap an input.
+ * H and I are multiples of 8 (16 for E4M3), at most 65536, 2 I H weights below
+ * 4 GiB - 4 MiB; x rows and weights start at multiples of 16 bytes. T = 0
+ * enqueues nothing. ws: moe_layer_few_workspace_size bytes at a multiple of 16,
+ * one for each call in flight.
+ */
+#define MOE_FEW_MAX_TOKENS 32
+typedef struct moe_few_args {
+    const float*   logits;                   /* [T, E_tot] f32 */
+    int32_t        T, E_tot, k;
+    int32_t        e0, E_loc;
+    int32_t        dtype;
+    const void*    x;                        /* [T, H], leading dimension ldx */
+    int32_t        ldx;
+    int32_t        H, I;
+    uint32_t       flags;
+    const void*    w1;
+    const void*    w2;
+    const float*   w1_scales;
+    const float*   w2_scales;
+    const void*    shared_w1;                /* NULL: no shared expert */
+    const void*    shared_w2;
+    const float*   shared_w1_scales;
+    const float*   shared_w2_scales;
+    const moe_epilogue* epi;
+    const float*   bias2;
+    const void*    residual;
+    void*          out;                      /* [T, H], leading dimension ld_out */
+    int32_t        ld_res, ld_out;
+} moe_few_args;
+
+size_t  moe_layer_few_workspace_size(int32_t T, int32_t k, int32_t E_loc, int32_t I, int32_t s);
+int32_t moe_layer_few(const moe_few_args* a, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---- gradients of biases and of the router ---------------------------------------- */
+/*
+ * moe_grouped_bias_grad: db_g[n] = sum over the rows r of group g of
+ * row_w[r] * dy[dy_src[r]][n], fp32 [G, N] (row_w NULL: 1; dy_src NULL: row r
+ * itself; sources outside dy count as zero rows). With MOE_WGRAD_ACCUMULATE it
+ * adds to what db holds; without, a group without rows has 0. The same bits
+ * every time. Groups, dtype and dy's leading dimension as in moe_grouped_wgrad;
+ * db starts at a multiple of 16 bytes and overlaps no input. ws as there.
+ */
+size_t  moe_grouped_bias_grad_workspace_size(int32_t R_max, int32_t G, int32_t N);
+int32_t moe_grouped_bias_grad(const void* dy, int32_t dy_rows, int32_t ld_dy, const int32_t* dy_src,
+                              const float* row_w, int32_t dtype, const int32_t* offsets, int32_t R_max,
+                              int32_t N, int32_t G, uint32_t flags, float* db, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+
+/*
+ * moe_route_backward: the gradient of the router's logits from that of the
+ * routing weights. With p = softmax(logits[t]), e_j = topk_idx[t][j] and D_j
+ * the gradient of weight j:
+ *   dlogits[e] = p_e ([sum of D_j over e_j = e] - sum_j D_j p_{e_j})
+ *   with MOE_ROUTE_RENORM: the sum over e_j = e of w_j (D_j - sum_i D_i w_i),
+ *                          w_j = p_{e_j} / sum_i p_{e_i}
+ *   + p_e (prob_grad[e] - sum_i prob_grad[i] p_i)      (prob_grad non-NULL, f32 [E_tot])
+ *   + 2 z_coef lse p_e,  lse = log sum exp logits[t]
+ * prob_grad is the gradient of a loss in the sum of p over the tokens, e.g. the
+ * balance loss c E sum_e f_e mean_t p_te: c E f_e / T. z_coef: of the loss
+ * z_coef sum_t lse_t^2.
+ * D_j = dw[t * k + j], or with slot_row (leading dimension ld_slot >= k, as
+ * moe_permute writes it: k + s) dw[slot_row[t * ld_slot + j]], 0 where that is
+ * outside [0, dw_rows): the experts of other GPUs. The call is linear in dw,
+ * prob_grad and z_coef, so the parts of several GPUs may be added. Indices
+ * outside [0, E_tot) count as not chosen. A logit of -inf has p = 0 and no
+ * gradient, a row of them only likewise; NaN or +inf make the row's gradient
+ * NaN (with MOE_ROUTE_RENORM and no other term, at least the chosen experts').
+ * dlogits f32 [T, E_tot], fp32 throughout. 1 <= k <= min(E_tot, 32).
+ */
+int32_t moe_route_backward(const float* logits, int32_t T, int32_t E_tot, int32_t k, uint32_t flags,
+                           const int32_t* topk_idx, const float* dw, int32_t dw_rows, const int32_t* slot_row,
+                           int32_t ld_slot, const float* prob_grad, float z_coef, float* dlogits,
+                           hipStream_t stream);
 
 #ifdef __cplusplus
 }

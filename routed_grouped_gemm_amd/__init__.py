@@ -17,13 +17,13 @@ import ctypes as C
 import torch
 
 from . import _lib
-from ._lib import (MOE_ACT_GEGLU, MOE_ACT_SRELU, MOE_ACT_SWIGLU, MOE_FMT_MXFP4,  # noqa: F401
-                   MOE_FMT_MXFP8, MOE_GEMM_PASS, MOE_GEMM_STREAMED, MOE_GEMM_TILED,
+from ._lib import (MOE_ACT_GEGLU, MOE_ACT_NONE, MOE_ACT_SRELU, MOE_ACT_SWIGLU,  # noqa: F401
+                   MOE_FEW_MAX_TOKENS, MOE_FMT_MXFP4, MOE_FMT_MXFP8, MOE_GEMM_PASS, MOE_GEMM_STREAMED, MOE_GEMM_TILED,
                    MOE_LAYER_SEPARATE_KERNELS,
                    MOE_LAYER_TOKEN_RING, MOE_MM_W_KN, MOE_ROUTE_RENORM,
                    MOE_SCALE_RULE_CEIL, MOE_T_BF16, MOE_T_F16, MOE_T_F32, MOE_W1_WRITE_TRANSPOSE,
                    MOE_WEIGHT_AT_COMBINE, MOE_WGRAD_ACCUMULATE, MOE_WGRAD_F32,
-                   moe_epilogue, moe_layer_args, moe_weights)
+                   moe_epilogue, moe_few_args, moe_layer_args, moe_weights)
 
 lib = _lib.load()
 
@@ -729,4 +729,133 @@ def moe_glu_checkpoint_backward(codes, scales, dh, row_w=None, n_rows=None, epi:
         _check(lib.moe_glu_checkpoint_backward(_p(codes), _p(scales), _p(dh), _T16[dh.dtype], R, I, _ld(dh),
                                                _p(row_w), _p(n_rows), _eref(epi), _p(out["dpre"]), _p(out["h"]),
                                                _p(out["dw"]), _raw_stream(dev)), "moe_glu_checkpoint_backward")
+    return out
+
+
+# ------------------------------------------------- the layer for a few tokens
+def _few_pair(w1, w2, s1, s2, n: int, H: int, I: int, dtype, eight: bool, name: str, dev) -> None:
+    """Check one pair of weight arrays (and scales) of moe_layer_few."""
+    wt = torch.uint8 if eight else dtype
+    for w, s, shape, which in ((w1, s1, (n, 2 * I, H), "w1"), (w2, s2, (n, H, I), "w2")):
+        if w is None:
+            raise MoeError(f"{name}{which} is missing")
+        _dense(w, shape, wt, name + which, dev)
+        if eight != (s is not None):
+            raise MoeError(f"scales must be given for all weights or for none ({name}{which})")
+        _dense(s, (n, -(-shape[1] // 128), -(-shape[2] // 128)), torch.float32, f"{name}{which} scales", dev)
+
+
+def moe_layer_few(logits, x, w1, w2, k: int, e0: int = 0, w1_scales=None, w2_scales=None, shared=None,
+                  epi: Epilogue | None = None, bias2=None, residual=None, flags: int = 0, out=None, ws=None, stream=None):
+    """The whole layer for at most MOE_FEW_MAX_TOKENS tokens x [T, H] (bf16 or
+    fp16), logits f32 [T, E]: w1 [E_loc, 2I, H] and w2 [E_loc, H, I] of x's type,
+    or E4M3 codes (uint8) with w1_scales and w2_scales as
+    moe_quantize_block_weights returns them. shared: (w1 [1, 2I, H], w1 scales or
+    None, w2 [1, H, I], w2 scales or None). epi: activation, clamp, bias f32
+    [G, 2I]; bias2 f32 [G, H] (G counts the shared expert); residual [T, H].
+    flags: MOE_ROUTE_RENORM. ws: a uint8 workspace of
+    moe_layer_few_workspace_size bytes. Returns [T, H] of x's type."""
+    _mat(x, _T16, "x")
+    dev, (T, H) = x.device, x.shape
+    if logits.dim() != 2 or logits.shape[0] != T:
+        raise MoeError(f"logits must be [{T}, E], got {tuple(logits.shape)}")
+    E = logits.shape[1]
+    _dense(logits, (T, E), torch.float32, "logits", dev)
+    if w1.dim() != 3 or w1.shape[1] % 2:
+        raise MoeError(f"w1 must be [E_loc, 2I, H], got {tuple(w1.shape)}")
+    G, I, eight = w1.shape[0], w1.shape[1] // 2, w1_scales is not None
+    _few_pair(w1, w2, w1_scales, w2_scales, G, H, I, x.dtype, eight, "", dev)
+    args = moe_few_args()
+    s = 0
+    if shared is not None:
+        a, sa, b, sb = shared
+        _few_pair(a, b, sa, sb, 1, H, I, x.dtype, eight, "shared ", dev)
+        args.shared_w1, args.shared_w1_scales, args.shared_w2, args.shared_w2_scales = _p(a), _p(sa), _p(b), _p(sb)
+        s = 1
+    if epi is not None:
+        _dense(epi.bias, (G + s, 2 * I), torch.float32, "bias", dev)
+        args.epi = C.pointer(epi.desc)
+    _dense(bias2, (G + s, H), torch.float32, "bias2", dev)
+    if residual is not None:
+        if _mat(residual, (x.dtype,), "residual", dev).shape != (T, H):
+            raise MoeError(f"residual must be [{T}, {H}], got {tuple(residual.shape)}")
+        args.residual, args.ld_res = _p(residual), _ld(residual)
+    with _at(dev, stream):
+        if out is None:
+            out = torch.empty((T, H), dtype=x.dtype, device=dev)
+        elif _mat(out, (x.dtype,), "out", dev).shape != (T, H):
+            raise MoeError(f"out must be [{T}, {H}], got {tuple(out.shape)}")
+        if ws is None:
+            ws = torch.empty(max(int(lib.moe_layer_few_workspace_size(T, k, G, I, s)), 1), dtype=torch.uint8, device=dev)
+        elif ws.dim() != 1:
+            raise MoeError("ws must be 1-D")
+        else:
+            _dense(ws, ws.shape, torch.uint8, "ws", dev)
+        args.logits, args.T, args.E_tot, args.k, args.e0, args.E_loc = _p(logits), T, E, k, e0, G
+        args.dtype, args.x, args.ldx, args.H, args.I, args.flags = _T16[x.dtype], _p(x), _ld(x), H, I, flags
+        args.w1, args.w2, args.w1_scales, args.w2_scales = _p(w1), _p(w2), _p(w1_scales), _p(w2_scales)
+        args.bias2, args.out, args.ld_out = _p(bias2), _p(out), _ld(out)
+        _check(lib.moe_layer_few(C.byref(args), _p(ws), ws.shape[0], _raw_stream(dev)), "moe_layer_few")
+    return out
+
+
+def moe_layer_few_workspace_size(T: int, k: int, E_loc: int, I: int, shared: bool = False) -> int:
+    return int(lib.moe_layer_few_workspace_size(T, k, E_loc, I, int(bool(shared))))
+
+
+# --------------------------------------- gradients of biases and of the router
+def moe_grouped_bias_grad(dy, offsets, dy_src=None, row_w=None, out=None, accumulate: bool = False, stream=None):
+    """db_g = sum over the rows r of group g of row_w[r] * dy[r] (or
+    dy[dy_src[r]]): f32 [G, N]. accumulate adds to `out`, which must then be given."""
+    _mat(dy, _T16, "dy")
+    dev, N = dy.device, dy.shape[1]
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise MoeError(f"offsets must be 1-D with at least 2 elements, got {tuple(offsets.shape)}")
+    G = offsets.shape[0] - 1
+    _offsets(offsets, G, dev)
+    R = _n_rows(dy_src, dy, "dy_src")
+    _dense(dy_src, (R,), torch.int32, "dy_src", dev)
+    _dense(row_w, (R,), torch.float32, "row_w", dev)
+    if accumulate and out is None:
+        raise MoeError("accumulate needs out")
+    with _at(dev, stream):
+        if out is None:
+            out = torch.empty((G, N), dtype=torch.float32, device=dev)
+        _dense(out, (G, N), torch.float32, "out", dev)
+        nws = int(lib.moe_grouped_bias_grad_workspace_size(R, G, N))
+        ws = _ws(nws, dev)
+        _check(lib.moe_grouped_bias_grad(_p(dy), dy.shape[0], _ld(dy), _p(dy_src), _p(row_w), _T16[dy.dtype], _p(offsets),
+                                         R, N, G, MOE_WGRAD_ACCUMULATE if accumulate else 0, _p(out), _p(ws), nws,
+                                         _raw_stream(dev)), "moe_grouped_bias_grad")
+    return out
+
+
+def moe_route_backward(logits, topk_idx, dw, slot_row=None, prob_grad=None, z_coef: float = 0.0, flags: int = 0, out=None,
+                       stream=None):
+    """The logits' gradient f32 [T, E] from that of the routing weights: dw f32
+    [T, k], or with slot_row (moe_permute's, int32 [T, k + s]) the grouped rows'
+    f32 [R]. prob_grad f32 [E]: gradient of a loss in sum_t softmax(logits[t]);
+    z_coef: of a loss z_coef * sum_t logsumexp(logits[t])^2. flags as given to
+    moe_route."""
+    if logits.device.type != "cuda" or logits.dim() != 2 or topk_idx.dim() != 2:
+        raise MoeError("logits and topk_idx must be 2-D device tensors")
+    dev, (T, E) = logits.device, logits.shape
+    k = topk_idx.shape[1]
+    _dense(logits, (T, E), torch.float32, "logits", dev)
+    _dense(topk_idx, (T, k), torch.int32, "topk_idx", dev)
+    if slot_row is None:
+        _dense(dw, (T, k), torch.float32, "dw", dev)
+    else:
+        if slot_row.dim() != 2 or slot_row.shape[1] < k or dw.dim() != 1:
+            raise MoeError(f"slot_row must be [{T}, {k} or more] and dw 1-D, got {tuple(slot_row.shape)}, {tuple(dw.shape)}")
+        _dense(slot_row, (T, slot_row.shape[1]), torch.int32, "slot_row", dev)
+        _dense(dw, dw.shape, torch.float32, "dw", dev)
+    _dense(prob_grad, (E,), torch.float32, "prob_grad", dev)
+    with _at(dev, stream):
+        if out is None:
+            out = torch.empty((T, E), dtype=torch.float32, device=dev)
+        _dense(out, (T, E), torch.float32, "out", dev)
+        _check(lib.moe_route_backward(_p(logits), T, E, k, flags, _p(topk_idx), _p(dw), dw.numel(), _p(slot_row),
+                                      slot_row.shape[1] if slot_row is not None else 0, _p(prob_grad), z_coef, _p(out),
+                                      _raw_stream(dev)), "moe_route_backward")
     return out

@@ -33,7 +33,8 @@ class moe_weights(C.Structure):
                 ("bytes", C.c_size_t)]
 
 
-MOE_ACT_SWIGLU, MOE_ACT_GEGLU, MOE_ACT_SRELU = 0, 1, 2
+MOE_ACT_SWIGLU, MOE_ACT_GEGLU, MOE_ACT_SRELU, MOE_ACT_NONE = 0, 1, 2, 3
+MOE_FEW_MAX_TOKENS = 32
 
 
 class moe_epilogue(C.Structure):
@@ -51,9 +52,20 @@ class moe_layer_args(C.Structure):
                 ("epi", C.POINTER(moe_epilogue))]
 
 
+class moe_few_args(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("T", C.c_int32), ("E_tot", C.c_int32), ("k", C.c_int32),
+                ("e0", C.c_int32), ("E_loc", C.c_int32), ("dtype", C.c_int32), ("x", C.c_void_p),
+                ("ldx", C.c_int32), ("H", C.c_int32), ("I", C.c_int32), ("flags", C.c_uint32),
+                ("w1", C.c_void_p), ("w2", C.c_void_p), ("w1_scales", C.c_void_p), ("w2_scales", C.c_void_p),
+                ("shared_w1", C.c_void_p), ("shared_w2", C.c_void_p), ("shared_w1_scales", C.c_void_p),
+                ("shared_w2_scales", C.c_void_p), ("epi", C.POINTER(moe_epilogue)), ("bias2", C.c_void_p),
+                ("residual", C.c_void_p), ("out", C.c_void_p), ("ld_res", C.c_int32), ("ld_out", C.c_int32)]
+
+
 P, I32, U32, SZ = C.c_void_p, C.c_int32, C.c_uint32, C.c_size_t
 WP = C.POINTER(moe_weights)
 EP = C.POINTER(moe_epilogue)
+F32 = C.c_float
 
 # name -> (restype, argtypes), in the order of include/moe.h
 SIGNATURES = {
@@ -92,6 +104,11 @@ SIGNATURES = {
     "moe_grouped_wgrad_plan": (I32, [I32, I32, I32, I32, C.POINTER(I32)]),
     "moe_glu_checkpoint": (I32, [P, I32, I32, I32, I32, P, P, EP, P, P, P, P]),
     "moe_glu_checkpoint_backward": (I32, [P, P, P, I32, I32, I32, I32, P, P, EP, P, P, P, P]),
+    "moe_layer_few_workspace_size": (SZ, [I32, I32, I32, I32, I32]),
+    "moe_layer_few": (I32, [C.POINTER(moe_few_args), P, SZ, P]),
+    "moe_grouped_bias_grad_workspace_size": (SZ, [I32, I32, I32]),
+    "moe_grouped_bias_grad": (I32, [P, I32, I32, P, P, I32, P, I32, I32, I32, U32, P, P, SZ, P]),
+    "moe_route_backward": (I32, [P, I32, I32, I32, U32, P, P, I32, P, I32, P, F32, P, P]),
 }
 
 _lib = None

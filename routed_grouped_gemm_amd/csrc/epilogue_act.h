@@ -1,0 +1,56 @@
+// Activations of the product epilogues (grouped_mm_act.hip, few_layer.hip): the
+// gated unit a(clamp(g)) clamp(u) and the plain a(clamp(z)), and their
+// derivatives. Internal to libmoe.
+#pragma once
+#include "moe_device.h"
+
+namespace {
+
+// clamp to +-lim (lim > 0); a NaN stays one
+MOE_DEV float epi_clamp(float v, float lim) {
+    if (!(lim > 0.f)) return v;
+    return v < -lim ? -lim : (v > lim ? lim : v);
+}
+MOE_DEV float epi_inside(float v, float lim) { return !(lim > 0.f) || fabsf(v) <= lim ? 1.f : 0.f; }
+
+// Phi(z) by erfc, which keeps its relative precision where Phi is small (1 +
+// erf loses it: at z = -4 an error of 1e-3 of the value, past FP16's half step)
+MOE_DEV float epi_phi(float z) { return 0.5f * erfcf(z * -0.70710678118654752f); }
+
+// Swish (z sigmoid(beta z)), exact GELU, squared ReLU (a NaN stays one), or z
+template <int ACT>
+MOE_DEV float epi_act(float z, float beta) {
+    if constexpr (ACT == MOE_ACT_GEGLU) return z * epi_phi(z);
+    if constexpr (ACT == MOE_ACT_SRELU) return z < 0.f ? 0.f : z * z;
+    if constexpr (ACT == MOE_ACT_NONE) return z;
+    return z * __builtin_amdgcn_rcpf(1.0f + __expf(-beta * z));
+}
+template <int ACT>
+MOE_DEV void epi_act_grad(float z, float beta, float& a, float& da) {
+    if constexpr (ACT == MOE_ACT_GEGLU) {
+        const float phi = epi_phi(z);
+        a = z * phi;
+        da = phi + z * (0.39894228040143268f * __expf(-0.5f * z * z));
+    } else if constexpr (ACT == MOE_ACT_SRELU) {
+        a = z < 0.f ? 0.f : z * z;
+        da = z < 0.f ? 0.f : 2.0f * z;
+    } else if constexpr (ACT == MOE_ACT_NONE) {
+        a = z;
+        da = 1.f;
+    } else {
+        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-beta * z));
+        a = z * s;
+        da = s + beta * a * (1.0f - s);
+    }
+}
+
+// f(std::integral_constant<int, act>) of a run-time activation
+template <typename F>
+MOE_DEV void with_act(int act, F&& f) {
+    if (act == MOE_ACT_SWIGLU) f(std::integral_constant<int, MOE_ACT_SWIGLU>{});
+    else if (act == MOE_ACT_GEGLU) f(std::integral_constant<int, MOE_ACT_GEGLU>{});
+    else if (act == MOE_ACT_SRELU) f(std::integral_constant<int, MOE_ACT_SRELU>{});
+    else f(std::integral_constant<int, MOE_ACT_NONE>{});
+}
+
+}  // namespace

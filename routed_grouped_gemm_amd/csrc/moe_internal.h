@@ -161,3 +161,27 @@ struct GluCall {
 };
 int moe_launch_glu_forward(const GluCall& c, hipStream_t stream);
 int moe_launch_glu_backward(const GluCall& c, hipStream_t stream);
+
+// The layer for a few tokens (few_layer.hip): workspace bytes and the launch (a: checked by the caller).
+size_t moe_few_bytes(int T, int k, int G, int s, int I);
+int moe_launch_few(const moe_few_args& a, void* ws, hipStream_t stream);
+
+// Bias gradients (bias_grad.hip).
+struct BiasGradCall {
+    int dtype;
+    const void* dy; int dy_rows, ld_dy; const int32_t* dy_src;
+    const float* row_w; const int32_t* offsets;
+    int R_max, N, G;
+    bool accumulate;
+    float* out; void* ws;
+};
+size_t moe_bias_grad_bytes(int R_max, int N);
+int moe_launch_bias_grad(const BiasGradCall& c, hipStream_t stream);
+
+// The router's gradient (router_grad.hip).
+struct RouteGradCall {
+    const float* logits; int T, E_tot, k; uint32_t flags;
+    const int32_t* topk_idx; const float* dw; int dw_rows; const int32_t* slot_row; int ld_slot;
+    const float* prob_grad; float z_coef; float* dlogits;
+};
+int moe_launch_route_backward(const RouteGradCall& c, hipStream_t stream);
