@@ -570,6 +570,64 @@ int32_t moe_glu_checkpoint_backward(const uint8_t* q, const float* s, const void
                                     const int32_t* n_rows, const moe_epilogue* epi, void* dpre, void* h,
                                     float* dw, hipStream_t stream);
 
+/* ---- products with an epilogue -------------------------------------------------- */
+/*
+ * moe_grouped_mm_act: the grouped product of 16-bit operands with bias,
+ * activation, row weight and residual in its epilogue, for every row r of a
+ * group:
+ *   z    = x[s(r)] . W_g^T + bias_g                                   (N values)
+ *   y[r] = residual[r] + row_w[r] * a(clamp(z))                       (N values)
+ *   with MOE_MM_GATED, z = [g | u] (W [G, 2I, K]: gate rows, then up rows, N = 2I):
+ *   y[r] = residual[r] + row_w[r] * a(clamp(g)) * clamp(u)            (I values)
+ * in fp32 up to one rounding. Operands, groups, leading dimensions and
+ * untouched rows as in moe_grouped_mm (MOE_MM_W_KN: not with MOE_MM_GATED);
+ * a group of G = 1 with offsets {0, R} is a dense layer. epi: activation
+ * (MOE_ACT_NONE too), beta, limit, bias f32 [G][N], and save_pre, which receives
+ * z (before the clamp) in dtype, dense [R_max, N]; NULL: SwiGLU with beta = 1
+ * where gated, no activation else. row_w f32 [R_max] or NULL (1). residual:
+ * rows of dtype with leading dimension ld_res (a multiple of 4, rows at
+ * multiples of 8 bytes), or NULL; y itself may be given (ld_res = ldy), no other
+ * output may overlap an input. A gated group's weights stay below 4 GiB - 4 MiB,
+ * N % 16 == 0. bias and save_pre start at multiples of 16 bytes.
+ *
+ * moe_grouped_mm_dact: its backward pass up to the pre-activation, where y went
+ * through the product W2 (dy its output's gradient): with dh[r] = dy[t(r)] . W_g
+ * (W [G, K, N] with MOE_MM_W_KN, W2 as the forward product holds it: K its
+ * outputs, N = I; or W [G, N, K]), never stored, and w = row_w[r]:
+ *   dpre[r] = dh w a'(clamp(z)) [|z| <= limit]                        [R_max, N]
+ *   h[r]    = w a(clamp(z)),  dw[r] = sum_n dh a(clamp(z))
+ *   with MOE_MM_GATED, pre [R_max, 2N] = [g | u]:
+ *   dpre[r] = [dg | du],  dg = dh w clamp(u) a'(clamp(g)) [|g| <= limit],
+ *                         du = dh w a(clamp(g)) [|u| <= limit]        [R_max, 2N]
+ *   h[r]    = w a(clamp(g)) clamp(u),  dw[r] = sum_n dh a(clamp(g)) clamp(u)
+ * pre: what save_pre holds (leading dimension ld_pre, a multiple of 4, rows at
+ * multiples of 8 bytes). dpre and h (or NULL) in dtype, dense, from multiples of
+ * 16 bytes; dw f32 [R_max] (or NULL). epi as in the forward call; its bias is
+ * part of pre and save_pre is not used. h is the input of the second product's
+ * weight gradient, dpre that of the first one's (moe_grouped_wgrad), of its rows'
+ * gradient (moe_grouped_mm) and of its bias's (moe_grouped_bias_grad). Where W2
+ * adds a bias b2 behind the row weight, dw lacks the term dy . b2.
+ *
+ * An infinite pre-activation follows the formulas in fp32 (Swish and GELU of
+ * -inf are NaN). Workspaces at multiples of 16 bytes, one for each call in
+ * flight; the same bits every time.
+ */
+#define MOE_MM_GATED          (1u << 19)
+
+size_t  moe_grouped_mm_act_workspace_size(int32_t R_max, int32_t G, int32_t N, int32_t K);
+int32_t moe_grouped_mm_act(const void* x, int32_t x_rows, int32_t ldx, const int32_t* row_src,
+                           const void* w, int32_t dtype, const int32_t* offsets, int32_t R_max,
+                           int32_t N, int32_t K, int32_t G, uint32_t flags, const moe_epilogue* epi,
+                           const float* row_w, const void* residual, int32_t ld_res, void* y, int32_t ldy,
+                           void* ws, size_t ws_bytes, hipStream_t stream);
+
+size_t  moe_grouped_mm_dact_workspace_size(int32_t R_max, int32_t G, int32_t N, int32_t K);
+int32_t moe_grouped_mm_dact(const void* dy, int32_t dy_rows, int32_t ld_dy, const int32_t* dy_src,
+                            const void* w, int32_t dtype, const int32_t* offsets, int32_t R_max, int32_t N,
+                            int32_t K, int32_t G, uint32_t flags, const moe_epilogue* epi, const void* pre,
+                            int32_t ld_pre, const float* row_w, void* dpre, void* h, float* dw, void* ws,
+                            size_t ws_bytes, hipStream_t stream);
+
 /* ---- the layer for a few tokens ------------------------------------------------- */
 /*
  * The whole routed layer for at most MOE_FEW_MAX_TOKENS tokens on 16-bit token

@@ -20,7 +20,7 @@ from . import _lib
 from ._lib import (MOE_ACT_GEGLU, MOE_ACT_NONE, MOE_ACT_SRELU, MOE_ACT_SWIGLU,  # noqa: F401
                    MOE_FEW_MAX_TOKENS, MOE_FMT_MXFP4, MOE_FMT_MXFP8, MOE_GEMM_PASS, MOE_GEMM_STREAMED, MOE_GEMM_TILED,
                    MOE_LAYER_SEPARATE_KERNELS,
-                   MOE_LAYER_TOKEN_RING, MOE_MM_W_KN, MOE_ROUTE_RENORM,
+                   MOE_LAYER_TOKEN_RING, MOE_MM_GATED, MOE_MM_W_KN, MOE_ROUTE_RENORM,
                    MOE_SCALE_RULE_CEIL, MOE_T_BF16, MOE_T_F16, MOE_T_F32, MOE_W1_WRITE_TRANSPOSE,
                    MOE_WEIGHT_AT_COMBINE, MOE_WGRAD_ACCUMULATE, MOE_WGRAD_F32,
                    moe_epilogue, moe_few_args, moe_layer_args, moe_weights)
@@ -729,6 +729,94 @@ def moe_glu_checkpoint_backward(codes, scales, dh, row_w=None, n_rows=None, epi:
         _check(lib.moe_glu_checkpoint_backward(_p(codes), _p(scales), _p(dh), _T16[dh.dtype], R, I, _ld(dh),
                                                _p(row_w), _p(n_rows), _eref(epi), _p(out["dpre"]), _p(out["h"]),
                                                _p(out["dw"]), _raw_stream(dev)), "moe_glu_checkpoint_backward")
+    return out
+
+
+# --------------------------------------------------- products with an epilogue
+def moe_grouped_mm_act(x, w, offsets, epi: Epilogue | None = None, gated: bool = False, w_kn: bool = False, row_src=None,
+                       row_w=None, residual=None, keep_pre: bool = False, out=None, pre=None, stream=None):
+    """moe_grouped_mm with bias, activation, row weight and residual in its
+    epilogue: z = x[r] . W_g^T + bias_g, y[r] = residual[r] + row_w[r] * a(z), or
+    with gated (w [G, 2I, K]: gate rows, then up rows) a(gate) * up. epi:
+    activation, slope, clamp and bias f32 [G, N] (None: SwiGLU where gated, no
+    activation else). Returns y [R, N] (gated: [R, I]) of x's type; with
+    keep_pre, (y, z [R, N] of x's type). residual may be `out`. Records no
+    gradient: moe_grouped_mm_dact, moe_grouped_wgrad, moe_grouped_mm and
+    moe_grouped_bias_grad form it."""
+    _mat(x, _T16, "x")
+    dev, (T, K) = x.device, x.shape
+    if w.dim() != 3 or w.shape[1 if w_kn else 2] != K:
+        raise MoeError(f"w {tuple(w.shape)} does not fit rows of {K}")
+    _dense(w, w.shape, x.dtype, "w", dev)
+    G, N = w.shape[0], w.shape[2 if w_kn else 1]
+    if gated and (w_kn or N % 2):
+        raise MoeError("a gated product needs w [G, 2I, K]")
+    cols = N // 2 if gated else N
+    _offsets(offsets, G, dev)
+    R = _n_rows(row_src, x, "row_src")
+    _dense(row_src, (R,), torch.int32, "row_src", dev)
+    _dense(row_w, (R,), torch.float32, "row_w", dev)
+    if epi is None:
+        epi = Epilogue(act=MOE_ACT_SWIGLU if gated else MOE_ACT_NONE)
+    if epi.save_pre is not None:
+        raise MoeError("the pre-activation is kept with keep_pre (and pre), not with save_pre")
+    _dense(epi.bias, (G, N), torch.float32, "bias", dev)
+    if pre is not None and not keep_pre:
+        raise MoeError("pre is written only with keep_pre")
+    if residual is not None and _mat(residual, (x.dtype,), "residual", dev).shape != (R, cols):
+        raise MoeError(f"residual must be [{R}, {cols}], got {tuple(residual.shape)}")
+    with _at(dev, stream):
+        if out is None:
+            out = torch.empty((R, cols), dtype=x.dtype, device=dev)
+        elif _mat(out, (x.dtype,), "out", dev).shape != (R, cols):
+            raise MoeError(f"out must be [{R}, {cols}], got {tuple(out.shape)}")
+        if keep_pre and pre is None:
+            pre = torch.empty((R, N), dtype=x.dtype, device=dev)
+        _dense(pre, (R, N), x.dtype, "pre", dev)
+        e = epi.desc
+        desc = moe_epilogue(e.act, e.beta, e.limit, 0, e.bias, _p(pre))
+        nws = int(lib.moe_grouped_mm_act_workspace_size(R, G, N, K))
+        ws = _ws(nws, dev)
+        flags = (MOE_MM_W_KN if w_kn else 0) | (MOE_MM_GATED if gated else 0)
+        _check(lib.moe_grouped_mm_act(_p(x), T, _ld(x), _p(row_src), _p(w), _T16[x.dtype], _p(offsets), R, N, K, G, flags,
+                                      C.byref(desc), _p(row_w), _p(residual), _ld(residual) if residual is not None else 0,
+                                      _p(out), _ld(out), _p(ws), nws, _raw_stream(dev)), "moe_grouped_mm_act")
+    return (out, pre) if keep_pre else out
+
+
+def moe_grouped_mm_dact(dy, w, offsets, pre, epi: Epilogue | None = None, gated: bool = True, w_kn: bool = True, dy_src=None,
+                        row_w=None, want_h: bool = True, want_dw: bool = True, stream=None):
+    """The backward pass of moe_grouped_mm_act up to the pre-activation: dh = dy[r]
+    . W_g (w [G, K, N] with w_kn: the second product's weights as they are; else
+    [G, N, K]) and the activation's gradient from pre [R, 2N] (gated) or [R, N].
+    Returns a dict: dpre, shaped as pre; h [R, N], the activation's output
+    with the row weight; dw f32 [R], the row weight's gradient (None where not
+    wanted)."""
+    _mat(dy, _T16, "dy")
+    dev, (T, K) = dy.device, dy.shape
+    if w.dim() != 3 or w.shape[1 if w_kn else 2] != K:
+        raise MoeError(f"w {tuple(w.shape)} does not fit rows of {K}")
+    _dense(w, w.shape, dy.dtype, "w", dev)
+    G, N = w.shape[0], w.shape[2 if w_kn else 1]
+    _offsets(offsets, G, dev)
+    R = _n_rows(dy_src, dy, "dy_src")
+    _dense(dy_src, (R,), torch.int32, "dy_src", dev)
+    _dense(row_w, (R,), torch.float32, "row_w", dev)
+    wide = 2 * N if gated else N
+    if _mat(pre, (dy.dtype,), "pre", dev).shape != (R, wide):
+        raise MoeError(f"pre must be [{R}, {wide}], got {tuple(pre.shape)}")
+    if epi is None:
+        epi = Epilogue(act=MOE_ACT_SWIGLU if gated else MOE_ACT_NONE)
+    with _at(dev, stream):
+        out = dict(dpre=torch.empty((R, wide), dtype=dy.dtype, device=dev),
+                   h=torch.empty((R, N), dtype=dy.dtype, device=dev) if want_h else None,
+                   dw=torch.empty(R, dtype=torch.float32, device=dev) if want_dw else None)
+        nws = int(lib.moe_grouped_mm_dact_workspace_size(R, G, N, K))
+        ws = _ws(nws, dev)
+        flags = (MOE_MM_W_KN if w_kn else 0) | (MOE_MM_GATED if gated else 0)
+        _check(lib.moe_grouped_mm_dact(_p(dy), T, _ld(dy), _p(dy_src), _p(w), _T16[dy.dtype], _p(offsets), R, N, K, G, flags,
+                                       epi.ref(), _p(pre), _ld(pre), _p(row_w), _p(out["dpre"]), _p(out["h"]),
+                                       _p(out["dw"]), _p(ws), nws, _raw_stream(dev)), "moe_grouped_mm_dact")
     return out
 
 

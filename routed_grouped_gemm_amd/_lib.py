@@ -25,6 +25,7 @@ MOE_MM_MAX_ROWS = (1 << 29) - 1
 MOE_MM_W_KN = 1 << 16
 MOE_WGRAD_ACCUMULATE = 1 << 17
 MOE_WGRAD_F32 = 1 << 18
+MOE_MM_GATED = 1 << 19
 
 
 class moe_weights(C.Structure):
@@ -104,6 +105,11 @@ SIGNATURES = {
     "moe_grouped_wgrad_plan": (I32, [I32, I32, I32, I32, C.POINTER(I32)]),
     "moe_glu_checkpoint": (I32, [P, I32, I32, I32, I32, P, P, EP, P, P, P, P]),
     "moe_glu_checkpoint_backward": (I32, [P, P, P, I32, I32, I32, I32, P, P, EP, P, P, P, P]),
+    "moe_grouped_mm_act_workspace_size": (SZ, [I32, I32, I32, I32]),
+    "moe_grouped_mm_act": (I32, [P, I32, I32, P, P, I32, P, I32, I32, I32, I32, U32, EP, P, P, I32, P, I32, P, SZ, P]),
+    "moe_grouped_mm_dact_workspace_size": (SZ, [I32, I32, I32, I32]),
+    "moe_grouped_mm_dact": (I32, [P, I32, I32, P, P, I32, P, I32, I32, I32, I32, U32, EP, P, I32, P, P, P, P, P, SZ,
+                                  P]),
     "moe_layer_few_workspace_size": (SZ, [I32, I32, I32, I32, I32]),
     "moe_layer_few": (I32, [C.POINTER(moe_few_args), P, SZ, P]),
     "moe_grouped_bias_grad_workspace_size": (SZ, [I32, I32, I32]),

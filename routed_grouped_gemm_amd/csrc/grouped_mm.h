@@ -1,5 +1,5 @@
-// Pieces shared by the grouped-product kernels (grouped_mm.hip, the LDS-tiled
-// kernel, and grouped_mm_rows.hip, the weight-streaming kernel for few rows):
+// Pieces shared by the grouped-product kernels (grouped_mm_tiled.h, the LDS-tiled
+// kernel, and grouped_mm_rows.h, the weight-streaming kernel for few rows):
 // element kinds, the parameter block and MFMA wrappers. Internal to libmoe.
 #pragma once
 #include "gemm_common.h"
@@ -40,6 +40,16 @@ struct MmP {
     // kernel), and the fp32 partial sums (null: no splitting)
     int part, parts, max_slots;
     float* partial;
+    // the epilogues (grouped_mm_act.h): activation, bias f32 [G, weight rows],
+    // row weights, residual rows [R, N], pre-activation rows (written by the
+    // forward epilogues, read by the backward one, whose h and dpre are dense)
+    int act; float beta, limit;
+    const float* bias; const float* row_w;
+    const uint8_t* res; size_t res_ld;                       // elements per row
+    uint8_t* pre; size_t pre_ld;
+    uint8_t* h;
+    float* dw_part; float* dw;                               // partial row sums [16- or 64-column parts][R_max]
+    int gated;
 };
 
 // Rows [lo, hi) of group g, held inside [0, R_max) whatever the offsets say.
@@ -124,11 +134,18 @@ constexpr int kGatherX = 16, kGatherDy = 32;
 constexpr int mm_kind(int mode) { return mode & 15; }
 constexpr bool is_wgrad(int mode) { return mm_kind(mode) >= kWgrad; }
 
+// Epilogue of a product: none; bias, activation, row weight and residual of a
+// plain or a gated (W: gate rows, then up rows) product; the activation's
+// gradient from the pre-activation (the product being that of its outputs').
+enum { kEpiNone = 0, kEpiAct = 1, kEpiGated = 2, kEpiGrad = 3 };
+
 constexpr int kMmThreads = 512;
 constexpr int kMmLds = 163840;              // LDS of a compute unit
 constexpr int kATile = 256;
 constexpr int kPBytes = kATile * 128;       // one K-tile of the a operand
 constexpr int kMmOut = 8 * 1024;            // stores pass through it
+// output columns of a tile of the a operand (gated: 128 gate and 128 up rows)
+constexpr int a_tile(int epi) { return epi == kEpiGated ? kATile / 2 : kATile; }
 
 // chunk swizzle of a row in the contiguous form, and of a k in the slow form
 MOE_DEV int kc_swz(int row) { return (row >> 1) & 7; }

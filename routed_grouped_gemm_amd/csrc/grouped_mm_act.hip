@@ -1,0 +1,71 @@
+// Grouped 16-bit products with bias, activation, row weight and residual in
+// their epilogue (grouped_mm_epi.h): on the LDS-tiled kernel, on the
+// weight-streaming kernel for few rows per group, or split along K there and
+// joined by act_join_kernel. The choice is that of the plain product with as
+// many weight rows (gated: 2 N).
+//
+// The matrix instructions bound the large calls. Measured: gated 24576 x 2816 x
+// 2048 in 16 uneven groups, gathered, with bias, weights and kept
+// pre-activation 331 us (850 TFLOP/s), 8191 x 4104 x 4096 in FP16 with bias and
+// residual, W [K, N] 329 us.
+#include "grouped_mm_act.h"
+
+namespace {
+
+template <int F16, int EPI>
+__global__ __launch_bounds__(256)
+void act_join_kernel(MmP p) {
+    constexpr int PER = EPI == kEpiGated ? 2 : 4;            // outputs of 4 sums
+    int lo, end;
+    all_rows(p, lo, end);
+    const int n4 = p.N / PER;
+    const size_t wide = (size_t)p.N * (4 / PER);
+    const int64_t total = (int64_t)p.R_max * n4, stride = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += stride) {
+        const int row = (int)(i / n4), a = (int)(i - (int64_t)row * n4);
+        if (row < lo || row >= end) continue;
+        int g = 0;
+        if (p.bias) {                                        // the last group that starts at or before the row
+            int top = p.G - 1;
+            while (g < top) {
+                const int mid = (g + top + 1) >> 1;
+                if (p.offsets[mid] <= row) g = mid;
+                else top = mid - 1;
+            }
+        }
+        const f32x4 z = join_parts(p.partial + (size_t)row * wide + 4 * a, (size_t)p.R_max * wide, p.parts);
+        rows_forward<F16, EPI>(p, g, (size_t)row, PER * a, z);
+    }
+}
+
+template <int EL, int MODE, int EPI>
+int launch_act(const MmP& p, int rows, hipStream_t stream) {
+    const int e = launch_epi<EL, MODE, EPI>(p, rows, stream);
+    if (e || p.parts == 1) return e;
+    const int64_t lanes = (int64_t)p.R_max * (p.N / (EPI == kEpiGated ? 2 : 4));
+    const int grid = (int)std::min<int64_t>((lanes + 255) / 256, 4 * device_cu_count());
+    act_join_kernel<EL == kElF16, EPI><<<grid, 256, 0, stream>>>(p);
+    return (int)hipGetLastError();
+}
+
+template <int EL>
+int launch_type(const MmActCall& c, const MmP& p, int rows, hipStream_t stream) {
+    if (c.gated) return launch_act<EL, kMmNK, kEpiGated>(p, rows, stream);
+    return c.kn ? launch_act<EL, kMmKN, kEpiAct>(p, rows, stream) : launch_act<EL, kMmNK, kEpiAct>(p, rows, stream);
+}
+
+}  // namespace
+
+size_t moe_mm_act_bytes(int R_max, int G, int weight_rows, int K) { return moe_mm_workspace_bytes(0, false, R_max, G, weight_rows, K); }
+
+int moe_launch_mm_act(const MmActCall& c, hipStream_t stream) {
+    MmP p = epi_params(c, c.x, c.x_rows, c.ldx, c.x_src);
+    p.out = (uint8_t*)c.out; p.out_ld = (size_t)c.ldy;
+    p.res = (const uint8_t*)c.res; p.res_ld = (size_t)c.ld_res;
+    p.pre = (uint8_t*)c.pre; p.pre_ld = (size_t)c.N * (c.gated ? 2 : 1);
+    p.partial = (float*)c.ws;
+    int rows, parts;
+    moe_mm_plan(false, c.R_max, c.G, c.N * (c.gated ? 2 : 1), c.K, &rows, &parts);
+    p.parts = parts;
+    return c.dtype == MOE_T_F16 ? launch_type<kElF16>(c, p, rows, stream) : launch_type<kElBf16>(c, p, rows, stream);
+}

@@ -57,6 +57,88 @@ MOE_EXPORT int32_t moe_layer_few(const moe_few_args* a, void* ws, size_t ws_byte
     return hip_status(moe_launch_few(*a, ws, stream));
 }
 
+// a 16-bit array that is read or written beside the operands: 8-byte pieces of rows
+static bool bad_rows(const void* p, int32_t ld, int32_t cols) { return ld < cols || ld % 4 || ld > kMaxLd || !aligned(p, 8); }
+
+// sizes of a product with an epilogue; n: its output columns
+static int32_t check_act_dims(int32_t R_max, int32_t N, int32_t K, int32_t G, uint32_t flags) {
+    const int32_t st = check_dims(R_max, N, K, G, 8);
+    if (st) return st;
+    if (!(flags & MOE_MM_GATED)) return MOE_OK;
+    // gate and up rows of a group are addressed together, by 32-bit offsets
+    return N % 16 || (int64_t)N * K * 2 >= kGatherBytes ? MOE_ERR_SHAPE : MOE_OK;
+}
+
+MOE_EXPORT size_t moe_grouped_mm_act_workspace_size(int32_t R_max, int32_t G, int32_t N, int32_t K) {
+    if (check_dims(R_max, N, K, G, 8)) return 0;
+    return moe_mm_act_bytes(R_max, G, N, K);
+}
+
+MOE_EXPORT int32_t moe_grouped_mm_act(const void* x, int32_t x_rows, int32_t ldx, const int32_t* row_src, const void* w,
+                                      int32_t dtype, const int32_t* offsets, int32_t R_max, int32_t N, int32_t K,
+                                      int32_t G, uint32_t flags, const moe_epilogue* epi, const float* row_w,
+                                      const void* residual, int32_t ld_res, void* y, int32_t ldy, void* ws,
+                                      size_t ws_bytes, hipStream_t stream) {
+    const bool gated = (flags & MOE_MM_GATED) != 0, kn = (flags & MOE_MM_W_KN) != 0;
+    if (!t16(dtype) || (flags & ~(MOE_MM_W_KN | MOE_MM_GATED)) || (gated && kn)) return MOE_ERR_UNSUPPORTED;
+    int32_t st = check_act(epi);
+    if (st) return st;
+    if ((st = check_act_dims(R_max, N, K, G, flags))) return st;
+    const int32_t cols = gated ? N / 2 : N;
+    if (ldy < cols || ldy % 4 || ldy > kMaxLd) return MOE_ERR_SHAPE;
+    if (residual && bad_rows(residual, ld_res, cols)) return MOE_ERR_SHAPE;
+    if ((st = check_rows(x, x_rows, K, ldx, 2, row_src, R_max))) return st;
+    if (R_max == 0) return MOE_OK;
+    if (!w || !offsets || !y) return MOE_ERR_NULL;
+    if (!aligned(w, 16) || !aligned(y, 8)) return MOE_ERR_SHAPE;
+    if (epi && (!aligned(epi->bias, 16) || !aligned(epi->save_pre, 16))) return MOE_ERR_SHAPE;
+    if ((st = check_ws(moe_mm_act_bytes(R_max, G, N, K), ws, ws_bytes))) return st;
+    MmActCall c{};
+    c.dtype = dtype; c.gated = gated; c.kn = kn;
+    c.x = x; c.x_rows = x_rows; c.ldx = ldx; c.x_src = row_src;
+    c.w = w; c.offsets = offsets;
+    c.R_max = R_max; c.N = cols; c.K = K; c.G = G;
+    c.act = epi ? epi->act : (gated ? MOE_ACT_SWIGLU : MOE_ACT_NONE);
+    c.beta = epi ? epi->beta : 1.0f; c.limit = epi ? epi->limit : 0.0f;
+    c.bias = epi ? epi->bias : nullptr; c.pre = epi ? epi->save_pre : nullptr;
+    c.row_w = row_w; c.res = residual; c.ld_res = ld_res;
+    c.out = y; c.ldy = ldy; c.ws = ws;
+    return hip_status(moe_launch_mm_act(c, stream));
+}
+
+MOE_EXPORT size_t moe_grouped_mm_dact_workspace_size(int32_t R_max, int32_t G, int32_t N, int32_t K) {
+    if (check_dims(R_max, N, K, G, 8)) return 0;
+    return moe_mm_dact_bytes(R_max, G, N, K);
+}
+
+MOE_EXPORT int32_t moe_grouped_mm_dact(const void* dy, int32_t dy_rows, int32_t ld_dy, const int32_t* dy_src,
+                                       const void* w, int32_t dtype, const int32_t* offsets, int32_t R_max, int32_t N,
+                                       int32_t K, int32_t G, uint32_t flags, const moe_epilogue* epi, const void* pre,
+                                       int32_t ld_pre, const float* row_w, void* dpre, void* h, float* dw, void* ws,
+                                       size_t ws_bytes, hipStream_t stream) {
+    const bool gated = (flags & MOE_MM_GATED) != 0;
+    if (!t16(dtype) || (flags & ~(MOE_MM_W_KN | MOE_MM_GATED))) return MOE_ERR_UNSUPPORTED;
+    int32_t st = check_act(epi);
+    if (st) return st;
+    if ((st = check_dims(R_max, N, K, G, 8))) return st;
+    if (bad_rows(pre, ld_pre, gated ? 2 * N : N)) return MOE_ERR_SHAPE;
+    if ((st = check_rows(dy, dy_rows, K, ld_dy, 2, dy_src, R_max))) return st;
+    if (R_max == 0) return MOE_OK;
+    if (!w || !offsets || !pre || !dpre) return MOE_ERR_NULL;
+    if (!aligned(w, 16) || !aligned(dpre, 16) || !aligned(h, 16)) return MOE_ERR_SHAPE;
+    if ((st = check_ws(moe_mm_dact_bytes(R_max, G, N, K), ws, ws_bytes))) return st;
+    MmActCall c{};
+    c.dtype = dtype; c.grad = true; c.gated = gated; c.kn = (flags & MOE_MM_W_KN) != 0;
+    c.x = dy; c.x_rows = dy_rows; c.ldx = ld_dy; c.x_src = dy_src;
+    c.w = w; c.offsets = offsets;
+    c.R_max = R_max; c.N = N; c.K = K; c.G = G;
+    c.act = epi ? epi->act : (gated ? MOE_ACT_SWIGLU : MOE_ACT_NONE);
+    c.beta = epi ? epi->beta : 1.0f; c.limit = epi ? epi->limit : 0.0f;
+    c.row_w = row_w; c.pre = const_cast<void*>(pre); c.ld_pre = ld_pre;
+    c.out = dpre; c.h = h; c.dw = dw; c.ws = ws;
+    return hip_status(moe_launch_mm_dact(c, stream));
+}
+
 MOE_EXPORT size_t moe_grouped_bias_grad_workspace_size(int32_t R_max, int32_t G, int32_t N) {
     if (check_dims(R_max, N, 8, G, 8)) return 0;
     return moe_bias_grad_bytes(R_max, N);

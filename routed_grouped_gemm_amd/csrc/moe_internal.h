@@ -185,3 +185,25 @@ struct RouteGradCall {
     const float* prob_grad; float z_coef; float* dlogits;
 };
 int moe_launch_route_backward(const RouteGradCall& c, hipStream_t stream);
+
+// Products with an epilogue (grouped_mm_act.hip) and the activation's gradient
+// in one (grouped_mm_dact.hip). N: output columns (gated forward: half the
+// weight rows); grad: x is dy, w holds [K, N] (kn) or [N, K], pre is read.
+struct MmActCall {
+    int dtype;
+    bool grad, gated, kn;
+    const void* x; int x_rows, ldx; const int32_t* x_src;
+    const void* w; const int32_t* offsets;
+    int R_max, N, K, G;
+    int act; float beta, limit;
+    const float* bias; const float* row_w;
+    const void* res; int ld_res;
+    void* pre; int ld_pre;           // forward: written, dense
+    void* out; int ldy;              // gradient: dpre, dense
+    void* h; float* dw;              // gradient
+    void* ws;
+};
+size_t moe_mm_act_bytes(int R_max, int G, int weight_rows, int K);
+int moe_launch_mm_act(const MmActCall& c, hipStream_t stream);
+size_t moe_mm_dact_bytes(int R_max, int G, int N, int K);
+int moe_launch_mm_dact(const MmActCall& c, hipStream_t stream);

@@ -100,3 +100,53 @@ def test_bindings_refuse_host_tensors():
               lambda: moe.moe_route_backward(x.float(), off[None], x.float())):
         with pytest.raises(moe.MoeError):
             f()
+
+
+def test_grouped_mm_act():
+    lib = _lib.load()
+
+    def call(x=F, x_rows=64, ldx=128, src=None, w=F, dtype=BF16, off=F, R=64, N=256, K=128, G=4, flags=0, epi=None, rw=None,
+             res=None, ld_res=0, y=F, ldy=256, ws=F, ws_bytes=1 << 40):
+        return lib.moe_grouped_mm_act(x, x_rows, ldx, src, w, dtype, off, R, N, K, G, flags,
+                                      None if epi is None else C.byref(epi), rw, res, ld_res, y, ldy, ws, ws_bytes, None)
+
+    gated = _lib.MOE_MM_GATED
+    assert call(dtype=F32) == UNSUP and call(flags=_lib.MOE_WGRAD_F32) == UNSUP
+    assert call(flags=gated | _lib.MOE_MM_W_KN) == UNSUP
+    assert call(epi=_lib.moe_epilogue(4, 1.0, 0.0, 0, None, None)) == UNSUP
+    assert call(epi=_lib.moe_epilogue(-1, 1.0, 0.0, 0, None, None)) == UNSUP
+    assert call(epi=_lib.moe_epilogue(0, float("nan"), 0.0, 0, None, None)) == SHAPE
+    assert call(epi=_lib.moe_epilogue(0, 1.0, -0.5, 0, None, None)) == SHAPE
+    assert call(epi=_lib.moe_epilogue(0, 1.0, 0.0, 0, F + 8, None)) == SHAPE and call(epi=_lib.moe_epilogue(0, 1.0, 0.0, 0, None, F + 8)) == SHAPE
+    assert call(N=252) == SHAPE and call(N=264, ldy=264, flags=gated) == SHAPE and call(K=132, ldx=136) == SHAPE
+    assert call(N=1 << 16, K=1 << 15, ldx=1 << 15, ldy=1 << 15, flags=gated) == SHAPE       # 4 GiB of a group's weights
+    assert call(G=0) == SHAPE and call(G=2050) == SHAPE and call(R=-1) == SHAPE and call(x_rows=63) == SHAPE
+    assert call(ldy=248) == SHAPE and call(ldy=258) == SHAPE and call(ldy=120, flags=gated) == SHAPE
+    assert call(res=F, ld_res=252) == SHAPE and call(res=F, ld_res=258) == SHAPE and call(res=F + 4, ld_res=256) == SHAPE
+    assert call(x=None) == NULL and call(w=None) == NULL and call(off=None) == NULL and call(y=None) == NULL
+    assert call(x=F + 8) == SHAPE and call(w=F + 8) == SHAPE and call(y=F + 4) == SHAPE
+    assert call(R=16, G=1, K=4096, ldx=4096, ws_bytes=0) == WS and call(R=16, G=1, K=4096, ldx=4096, ws=F + 8) == SHAPE
+    assert call(R=0, x=None, x_rows=0, w=None, off=None, y=None) == OK
+
+
+def test_grouped_mm_dact():
+    lib = _lib.load()
+
+    def call(dy=F, rows=64, ld=128, src=None, w=F, dtype=BF16, off=F, R=64, N=256, K=128, G=4, flags=_lib.MOE_MM_GATED,
+             epi=None, pre=F, ld_pre=512, rw=None, dpre=F, h=F, dw=F, ws=F, ws_bytes=1 << 40):
+        return lib.moe_grouped_mm_dact(dy, rows, ld, src, w, dtype, off, R, N, K, G, flags,
+                                       None if epi is None else C.byref(epi), pre, ld_pre, rw, dpre, h, dw, ws, ws_bytes, None)
+
+    assert call(dtype=F32) == UNSUP and call(flags=_lib.MOE_WGRAD_F32) == UNSUP
+    assert call(epi=_lib.moe_epilogue(7, 1.0, 0.0, 0, None, None)) == UNSUP
+    assert call(epi=_lib.moe_epilogue(0, 1.0, float("nan"), 0, None, None)) == SHAPE
+    assert call(N=252, ld_pre=504) == SHAPE and call(K=132, ld=136) == SHAPE and call(G=0) == SHAPE and call(R=-1) == SHAPE
+    assert call(ld_pre=508) == SHAPE and call(ld_pre=514) == SHAPE and call(pre=F + 4) == SHAPE
+    assert call(rows=63) == SHAPE and call(ld=120) == SHAPE and call(rows=1 << 24, src=F) == SHAPE
+    for n in ("dy", "w", "off", "pre", "dpre"):
+        assert call(**{n: None}) == NULL, n
+    assert call(dy=F + 8) == SHAPE and call(w=F + 8) == SHAPE and call(dpre=F + 8) == SHAPE and call(h=F + 8) == SHAPE
+    assert call(ws_bytes=0) == WS and call(ws=F + 8) == SHAPE
+    assert call(R=0, dy=None, rows=0, w=None, off=None, pre=None, dpre=None, h=None, dw=None, ws=None, ws_bytes=0) == OK
+    for f in (lib.moe_grouped_mm_act_workspace_size, lib.moe_grouped_mm_dact_workspace_size):
+        assert f(-1, 4, 256, 128) == 0 and f(64, 0, 256, 128) == 0 and f(64, 4, 250, 128) == 0
