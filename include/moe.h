@@ -686,7 +686,7 @@ typedef struct moe_few_args {
     int32_t        ld_res, ld_out;
 } moe_few_args;
 
-size_t  moe_layer_few_workspace_size(int32_t T, int32_t k, int32_t E_loc, int32_t I, int32_t s);
+size_t  moe_layer_few_workspace_size(int32_t T, int32_t k, int32_t E_loc, int32_t H, int32_t I, int32_t s);
 int32_t moe_layer_few(const moe_few_args* a, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ---- gradients of biases and of the router ---------------------------------------- */

@@ -874,7 +874,7 @@ def moe_layer_few(logits, x, w1, w2, k: int, e0: int = 0, w1_scales=None, w2_sca
         elif _mat(out, (x.dtype,), "out", dev).shape != (T, H):
             raise MoeError(f"out must be [{T}, {H}], got {tuple(out.shape)}")
         if ws is None:
-            ws = torch.empty(max(int(lib.moe_layer_few_workspace_size(T, k, G, I, s)), 1), dtype=torch.uint8, device=dev)
+            ws = torch.empty(max(int(lib.moe_layer_few_workspace_size(T, k, G, H, I, s)), 1), dtype=torch.uint8, device=dev)
         elif ws.dim() != 1:
             raise MoeError("ws must be 1-D")
         else:
@@ -887,8 +887,8 @@ def moe_layer_few(logits, x, w1, w2, k: int, e0: int = 0, w1_scales=None, w2_sca
     return out
 
 
-def moe_layer_few_workspace_size(T: int, k: int, E_loc: int, I: int, shared: bool = False) -> int:
-    return int(lib.moe_layer_few_workspace_size(T, k, E_loc, I, int(bool(shared))))
+def moe_layer_few_workspace_size(T: int, k: int, E_loc: int, H: int, I: int, shared: bool = False) -> int:
+    return int(lib.moe_layer_few_workspace_size(T, k, E_loc, H, I, int(bool(shared))))
 
 
 # --------------------------------------- gradients of biases and of the router

@@ -110,7 +110,7 @@ SIGNATURES = {
     "moe_grouped_mm_dact_workspace_size": (SZ, [I32, I32, I32, I32]),
     "moe_grouped_mm_dact": (I32, [P, I32, I32, P, P, I32, P, I32, I32, I32, I32, U32, EP, P, I32, P, P, P, P, P, SZ,
                                   P]),
-    "moe_layer_few_workspace_size": (SZ, [I32, I32, I32, I32, I32]),
+    "moe_layer_few_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32]),
     "moe_layer_few": (I32, [C.POINTER(moe_few_args), P, SZ, P]),
     "moe_grouped_bias_grad_workspace_size": (SZ, [I32, I32, I32]),
     "moe_grouped_bias_grad": (I32, [P, I32, I32, P, P, I32, P, I32, I32, I32, U32, P, P, SZ, P]),

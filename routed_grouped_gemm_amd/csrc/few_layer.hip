@@ -34,7 +34,7 @@
 
 namespace {
 
-constexpr int kFewWaves = 8;
+constexpr int kFewWaves = 16;
 constexpr int kFewThreads = 64 * kFewWaves;
 
 struct FewP {
@@ -51,26 +51,27 @@ struct FewP {
     // workspace
     uint16_t* h;                                             // [R, I]
     float* row_w;                                            // [R]
-    int32_t* slot;                                           // [T, k + s] row of each slot, -1
-    int32_t* active;                                         // number of groups with rows, then they
+    int32_t* active;                                         // groups with rows, rows used, then the groups
     int16_t* rowmap;                                         // [active][T] row of a token in the group, -1
+    int blocks, cols;                                        // few_w2: blocks of `cols` (at most 16) columns
 };
 
-// Reads the units (128 bytes of 16 weight rows, and the matching k of NT x 16
-// token rows) of one wave. A batch is UB units.
-template <bool F8, int NT>
+// Units of a wave in flight (a slot of the ring each), the 16-byte pieces of a
+// token row in a unit and its k. XL: token rows are in LDS, otherwise they are
+// requested with the weights.
+template <bool F8, int NT, bool XL>
 struct FewGeom {
-    static constexpr int UB = NT == 1 ? 2 : 1;
-    static constexpr int NB = F8 ? 4 : 2;                    // 16-byte pieces of a token row in a unit
-    static constexpr int UK = F8 ? 128 : 64;                 // k of a unit
+    static constexpr int NB = F8 ? 4 : 2;
+    static constexpr int UK = F8 ? 128 : 64;
+    static constexpr int Ring = XL ? 4 : (NT == 1 ? 3 : 2);
 };
-template <bool F8, int NT>
-struct FewBatch {
-    using Geo = FewGeom<F8, NT>;
-    i32x4 a[Geo::UB][2];
-    i32x4 b[Geo::UB][NT][Geo::NB];
-    float sc[Geo::UB][2];                                    // scales (few_w1: gate, up; few_w2: the first)
-    int row[Geo::UB][NT];                                    // few_w2: the token's row, -1
+template <bool F8, int NT, bool XL>
+struct FewSlot {
+    i32x4 a[2];
+    i32x4 b[XL ? 1 : NT][XL ? 1 : FewGeom<F8, NT, XL>::NB];
+    uint32_t sc[2];                                          // scales of this lane's results (few_w1: gate, up)
+    int row[NT];                                             // few_w2: the token's row, -1,
+    int at[XL ? NT : 1];                                     // and the place of its first piece in LDS
 };
 
 // E4M3 codes (8 of them) as 16-bit values, exactly
@@ -93,17 +94,17 @@ MOE_DEV i32x4 few_decode(int lo, int hi) {
     return v;
 }
 
-// the products of one unit with one tile of 16 token rows
-template <int EL, bool F8>
-MOE_DEV f32x4 few_unit(const i32x4 (&a)[2], const i32x4* b) {
+// the products of one unit with one tile of 16 token rows (piece(i): piece i of this lane's token row)
+template <int EL, bool F8, typename Piece>
+MOE_DEV f32x4 few_unit(const i32x4 (&a)[2], Piece&& piece) {
     f32x4 d = {0.f, 0.f, 0.f, 0.f};
     #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if constexpr (F8) {
-            d = mfma16x16x32<EL>(few_decode<EL>(a[h][0], a[h][1]), b[2 * h], d);
-            d = mfma16x16x32<EL>(few_decode<EL>(a[h][2], a[h][3]), b[2 * h + 1], d);
+            d = mfma16x16x32<EL>(few_decode<EL>(a[h][0], a[h][1]), piece(2 * h), d);
+            d = mfma16x16x32<EL>(few_decode<EL>(a[h][2], a[h][3]), piece(2 * h + 1), d);
         } else {
-            d = mfma16x16x32<EL>(a[h], b[h], d);
+            d = mfma16x16x32<EL>(a[h], piece(h), d);
         }
     }
     return d;
@@ -124,10 +125,13 @@ MOE_DEV uint32_t few_koff_w(int u, int h, int q, int K) {
     const int b = u * 128 + 64 * h + 16 * q;
     return b < (F8 ? K : 2 * K) ? (uint32_t)b : kMmInvalid;
 }
+// (LDS rows are padded with zeros, so only loads from memory ask for the end)
+template <bool F8>
+MOE_DEV int few_kbyte_x(int u, int i, int q) { return F8 ? u * 256 + 128 * (i >> 1) + 32 * q + 16 * (i & 1) : u * 128 + 64 * i + 16 * q; }
 template <bool F8>
 MOE_DEV uint32_t few_koff_x(int u, int i, int q, int K) {
-    const int k = F8 ? u * 128 + 64 * (i >> 1) + 16 * q + 8 * (i & 1) : u * 64 + 32 * i + 8 * q;
-    return k < K ? (uint32_t)(2 * k) : kMmInvalid;
+    const int b = few_kbyte_x<F8>(u, i, q);
+    return b < 2 * K ? (uint32_t)b : kMmInvalid;
 }
 // the sum of two offsets, past every resource if one of them is
 MOE_DEV uint32_t few_add(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
@@ -138,9 +142,9 @@ struct FewTables { int *sidx; float* sw; int *counts, *offsets, *row_src; float*
 
 __host__ __device__ inline size_t few_table_ints(int T, int k, int G, int s) {
     const size_t R = (size_t)T * (k + s);
-    return 2 * (size_t)T * k + (size_t)G + (G + 1) + 2 * R + R + ((size_t)G < R ? G : R) + 1;
+    return 2 * (size_t)T * k + (size_t)G + (G + 1) + 2 * R + R + ((size_t)G < R ? G : R) + 2;
 }
-MOE_DEV FewTables few_tables(int* lds, int T, int k, int G, int s) {
+MOE_DEV FewTables few_tables(int* lds, int* scratch, int T, int k, int G, int s) {
     const int R = T * (k + s);
     FewTables t;
     t.sidx = lds; lds += T * k;
@@ -150,12 +154,13 @@ MOE_DEV FewTables few_tables(int* lds, int T, int k, int G, int s) {
     t.row_src = lds; lds += R;
     t.row_w = (float*)lds; lds += R;
     t.slot = lds; lds += R;
-    t.active = lds; lds += min(G, R) + 1;
-    t.scratch = lds;
+    t.active = lds;                                          // their number, the groups, rows of the longest
+    t.scratch = scratch;
     return t;
 }
 
-MOE_DEV void few_route(const FewP& p, const FewTables& t) {
+// Returns the rows of the longest group.
+MOE_DEV int few_route(const FewP& p, const FewTables& t) {
     if (p.E <= 64 && p.k <= 32) route_block<kFewWaves, 32, 2>(p.logits, p.T, p.E, p.k, p.renorm != 0, t.sidx, t.sw, nullptr, nullptr);
     else if (p.E <= 256 && p.k <= 32) route_block<kFewWaves, 32, 8>(p.logits, p.T, p.E, p.k, p.renorm != 0, t.sidx, t.sw, nullptr, nullptr);
     else if (p.E <= 512) route_block<kFewWaves, 64, 8>(p.logits, p.T, p.E, p.k, p.renorm != 0, t.sidx, t.sw, nullptr, nullptr);
@@ -167,263 +172,406 @@ MOE_DEV void few_route(const FewP& p, const FewTables& t) {
     // the groups with rows, in their order (at most one a row)
     if (threadIdx.x < 64) {
         const int lane = threadIdx.x;
-        int n = 0;
+        int n = 0, most = 0;
         for (int g0 = 0; g0 < p.G; g0 += 64) {
-            const bool has = g0 + lane < p.G && t.counts[g0 + lane] > 0;
-            const uint64_t m = __ballot(has);
-            if (has) t.active[1 + n + __popcll(m & lanemask_lt(lane))] = g0 + lane;
+            const int rows = g0 + lane < p.G ? t.counts[g0 + lane] : 0;
+            const uint64_t m = __ballot(rows > 0);
+            if (rows > 0) t.active[1 + n + __popcll(m & lanemask_lt(lane))] = g0 + lane;
             n += __popcll(m);
+            most = max(most, rows);
         }
-        if (lane == 0) t.active[0] = n;
+        most = (int)wave_umax((uint32_t)most);
+        if (lane == 0) { t.active[0] = n; t.active[n + 1] = most; }
     }
     __syncthreads();
+    return __builtin_amdgcn_readfirstlane(t.active[t.active[0] + 1]);
+}
+
+// One 16-bit row into LDS, zeros up to `bytes` (a multiple of 1 KiB): piece c of
+// a row by one wave, loads that write LDS directly.
+MOE_DEV void few_stage(const rsrc_t& r, uint32_t row_off, int row_bytes, int c, uint8_t* dst, int lane) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const int b = c * 1024 + lane * 16;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (mm_lds_void_t*)(dst + c * 1024), 16,
+                                             b < row_bytes ? row_off + (uint32_t)b : kMmInvalid, 0, 0, 0);
+#endif
+}
+
+// Keeps the order of requests, where a wait counts the younger ones.
+MOE_DEV void few_fence() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // ------------------------------------------------------------------ few_w1
-template <int EL, bool F8, int NT>
-__global__ __launch_bounds__(kFewThreads, 4)
-void few_w1_kernel(FewP p) {
-    using Geo = FewGeom<F8, NT>;
-    constexpr int UB = Geo::UB;
-    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    float* const part = (float*)smem;                        // [2][8 waves][NT][4][64]
-    const FewTables tb = few_tables((int*)(smem + 2 * kFewWaves * NT * 1024), p.T, p.k, p.G, p.s);
+// bytes of a token row in LDS: all units of all waves, and 64 so that rows start in other banks
+template <bool F8>
+__host__ __device__ inline int few_row_lds(int units) { return (units + kFewWaves - 1) / kFewWaves * kFewWaves * (F8 ? 256 : 128) + 64; }
+
+template <int EL, bool F8, int NT, bool XL>
+MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* part, uint8_t* rows) {
+    using Geo = FewGeom<F8, NT, XL>;
+    constexpr int RING = Geo::Ring;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int q = lane >> 4, j = lane & 15;
+    // items of `ob` outputs of a group (8, or fewer where that fills the grid's
+    // last round better); a workgroup takes a contiguous run, so few groups
+    int ob = 8, least = 1 << 30;
+    #pragma unroll
+    for (int o = 8; o >= 2; o -= 2) {
+        const int rounds = (n_act * ((p.I + o - 1) / o) + (int)gridDim.x - 1) / (int)gridDim.x;
+        if (rounds * (o + 1) < least) { least = rounds * (o + 1); ob = o; }
+    }
+    const int cb = (p.I + ob - 1) / ob, n_items = n_act * cb;
+    const int first = (int)((int64_t)n_items * blockIdx.x / gridDim.x), end = (int)((int64_t)n_items * (blockIdx.x + 1) / gridDim.x);
+    if (first >= end) return;
+    const int wrow = p.H * (F8 ? 1 : 2);                     // bytes of a weight row
+    const int units = (p.H + Geo::UK - 1) / Geo::UK, upw = (units + kFewWaves - 1) / kFewWaves;
+    const int nsb = (2 * p.I + 127) >> 7, ksb = (p.H + 127) >> 7;
+    const int stride = few_row_lds<F8>(units);
+    const rsrc_t rx = make_rsrc(p.x, p.x_bytes);
+    const int R1 = p.T * (p.k + p.s) - 1;
 
-    few_route(p, tb);
+    // the loader: one unit after another through all items
+    struct { int item, i; bool live; const uint8_t* w; const float* s; uint32_t ro, sg, su, xo[NT]; } L;
+    auto open = [&]() __attribute__((always_inline)) {
+        L.i = 0;
+        L.live = L.item < end;
+        const int item = L.live ? L.item : first;
+        const int ai = __builtin_amdgcn_readfirstlane(item / cb), c0 = (item - ai * cb) * ob;
+        const int g = __builtin_amdgcn_readfirstlane(tb.active[1 + ai]);
+        const int sh = g < p.E_loc ? 0 : 1, gi = sh ? 0 : g;
+        L.w = p.w1[sh] + (size_t)gi * (size_t)(2 * p.I) * (size_t)wrow;
+        const int o = 2 * (j >> 2) + (j & 1), col = c0 + o;
+        L.ro = o < ob && col < p.I ? (uint32_t)(((j >> 1) & 1) * p.I + col) * (uint32_t)wrow : kMmNoRow;
+        if constexpr (F8) {                                  // (an even column and the next one are of one block)
+            L.s = p.s1[sh] + (size_t)gi * nsb * ksb;
+            const int c = min(c0 + 2 * q, p.I - 2);
+            L.sg = (uint32_t)((c >> 7) * ksb);
+            L.su = (uint32_t)(((p.I + c) >> 7) * ksb);
+        }
+        if constexpr (!XL) {
+            const int lo = tb.offsets[g], n = tb.counts[g];
+            #pragma unroll
+            for (int t = 0; t < NT; ++t)
+                L.xo[t] = 16 * t + j < n ? (uint32_t)tb.row_src[min(lo + 16 * t + j, R1)] * p.x_ld : kMmNoRow;
+        }
+    };
+    auto load = [&](FewSlot<F8, NT, XL>& S) __attribute__((always_inline)) {
+        const rsrc_t rw = make_rsrc(L.w, L.live ? (uint32_t)(2 * p.I) * (uint32_t)wrow : 0u);
+        const int u = L.i * kFewWaves + w;
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) S.a[h] = few_load_w(rw, few_add(L.ro, few_koff_w<F8>(u, h, q, p.H)));
+        if constexpr (!XL) {
+            #pragma unroll
+            for (int t = 0; t < NT; ++t)
+                #pragma unroll
+                for (int i = 0; i < Geo::NB; ++i) S.b[t][i] = few_load(rx, few_add(L.xo[t], few_koff_x<F8>(u, i, q, p.H)));
+        }
+        if constexpr (F8) {
+            const rsrc_t rs = make_rsrc(L.s, L.live ? (uint32_t)(nsb * ksb) * 4u : 0u);
+            const uint32_t kb = (uint32_t)min(u, ksb - 1);
+            S.sc[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, (L.sg + kb) * 4u, 0, 0);
+            S.sc[1] = __builtin_amdgcn_raw_buffer_load_b32(rs, (L.su + kb) * 4u, 0, 0);
+        }
+        if (++L.i == upw) {
+            ++L.item;
+            open();
+        }
+    };
+    // the group's token rows into LDS; a wait for the requests and a barrier must follow
+    auto stage = [&](int g) __attribute__((always_inline)) {
+        const int lo = tb.offsets[g], n = tb.counts[g], chunks = stride / 1024;
+        for (int c = w; c < n * chunks; c += kFewWaves) {
+            const int r = c / chunks;
+            const int src = __builtin_amdgcn_readfirstlane(tb.row_src[lo + r]);
+            few_stage(rx, (uint32_t)src * p.x_ld, 2 * p.H, c - r * chunks, rows + r * stride, lane);
+        }
+    };
+
+    int ai = first / cb, c8 = first - ai * cb, i = 0, left = end - first, turn = 0;
+    int g = __builtin_amdgcn_readfirstlane(tb.active[1 + ai]);
+    if constexpr (XL) stage(g);
+    few_fence();
+    L.item = first;
+    open();
+    FewSlot<F8, NT, XL> ring[RING];
+    static_for<RING>([&](auto s) __attribute__((always_inline)) { load(ring[decltype(s)::value]); });
+    if constexpr (XL) {                                      // (the rows were requested before the ring's units)
+        few_fence();
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(RING * (F8 ? 4 : 2), 15));
+        bare_barrier();
+    }
+    const uint8_t* xrow[NT];
+    auto rows_of = [&]() __attribute__((always_inline)) {    // (lanes past the group's rows read its last: not stored)
+        #pragma unroll
+        for (int t = 0; t < NT; ++t) xrow[t] = rows + max(0, min(16 * t + j, tb.counts[g] - 1)) * stride;
+    };
+    rows_of();
+    f32x4 acc[NT];
+    #pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    bool done = false;
+    while (!done) {
+        static_for<RING>([&](auto s) __attribute__((always_inline)) {
+            if (done) return;
+            FewSlot<F8, NT, XL>& S = ring[decltype(s)::value];
+            const int u = i * kFewWaves + w;
+            float sc[2] = {1.f, 1.f};
+            if constexpr (F8) {
+                sc[0] = __uint_as_float(S.sc[0]);
+                sc[1] = __uint_as_float(S.sc[1]);
+            }
+            #pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const f32x4 d = few_unit<EL, F8>(S.a, [&](int x) __attribute__((always_inline)) {
+                    if constexpr (XL) return *(const i32x4*)(xrow[t] + few_kbyte_x<F8>(u, x, q));
+                    else return S.b[t][x];
+                });
+                #pragma unroll
+                for (int v = 0; v < 4; ++v) acc[t][v] = F8 ? fmaf(d[v], sc[v >> 1], acc[t][v]) : acc[t][v] + d[v];
+            }
+            load(S);
+            if (++i < upw) return;
+            i = 0;
+            // an item's end: the waves' sums through LDS, two buffers in turn: one barrier an item
+            float* const mine = part + turn * (kFewWaves * NT * 256);
+            turn ^= 1;
+            #pragma unroll
+            for (int t = 0; t < NT; ++t)
+                #pragma unroll
+                for (int v = 0; v < 4; ++v) mine[(w * NT + t) * 256 + v * 64 + lane] = acc[t][v];
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+            bare_barrier();
+            // thread (tile, output of a pair, lane of the result): gate v, up v + 2
+            const int e = threadIdx.x, t = e >> 7, v = (e >> 6) & 1, l = e & 63, r = 16 * t + (l & 15), o8 = 2 * (l >> 4) + v, c = ob * c8 + o8;
+            if (e < NT * 128 && o8 < ob && c < p.I && r < tb.counts[g]) {
+                float z = 0.f, y = 0.f;
+                #pragma unroll
+                for (int x = 0; x < kFewWaves; ++x) {
+                    z += mine[(x * NT + t) * 256 + v * 64 + l];
+                    y += mine[(x * NT + t) * 256 + (v + 2) * 64 + l];
+                }
+                if (p.b1) {
+                    z += p.b1[(size_t)g * 2 * p.I + c];
+                    y += p.b1[(size_t)g * 2 * p.I + p.I + c];
+                }
+                z = epi_clamp(z, p.limit);
+                float a = 0.f;
+                with_act(p.act, [&](auto act) { a = epi_act<decltype(act)::value>(z, p.beta); });
+                const int row = tb.offsets[g] + r;
+                const float o = a * epi_clamp(y, p.limit) * tb.row_w[row];
+                p.h[(size_t)row * p.I + c] = (uint16_t)pack16(o, 0.f, EL == kElF16);
+            }
+            #pragma unroll
+            for (int x = 0; x < NT; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (--left == 0) {
+                done = true;
+                return;
+            }
+            if (++c8 == cb) {                                // the next group (every wave is past its products)
+                c8 = 0;
+                ++ai;
+                g = __builtin_amdgcn_readfirstlane(tb.active[1 + ai]);
+                if constexpr (XL) {
+                    stage(g);
+                    few_fence();
+                    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+                    bare_barrier();
+                }
+                rows_of();
+            }
+        });
+    }
+}
+
+template <int EL, bool F8, bool TWO>
+__global__ __launch_bounds__(kFewThreads, 4)
+void few_w1_kernel(FewP p, int lds_rows) {
+    constexpr int NTM = TWO ? 2 : 1;
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    float* const part = (float*)smem;                        // [2][16 waves][NT][4][64]
+    uint8_t* const rows = smem + 2 * kFewWaves * NTM * 1024; // [lds_rows]
+    const FewTables tb = few_tables((int*)(rows + lds_rows), (int*)smem, p.T, p.k, p.G, p.s);   // (scratch: before the sums)
+    const int most = few_route(p, tb);
     const int n_act = __builtin_amdgcn_readfirstlane(tb.active[0]);
-    if (blockIdx.x == 0) {                                   // for few_w2
-        for (int i = threadIdx.x; i <= n_act; i += kFewThreads) p.active[i] = tb.active[i];
-        for (int i = threadIdx.x; i < p.T * (p.k + p.s); i += kFewThreads) p.slot[i] = tb.slot[i];
-        const int R = tb.offsets[p.G];
-        for (int i = threadIdx.x; i < R; i += kFewThreads) p.row_w[i] = tb.row_w[i];
-        for (int i = threadIdx.x; i < n_act * p.T; i += kFewThreads) {
+    if (blockIdx.x == gridDim.x - 1) {                       // for few_w2
+        const int tid = threadIdx.x;
+        if (tid == 0) { p.active[0] = n_act; p.active[1] = tb.offsets[p.G]; }
+        for (int i = tid; i < n_act; i += kFewThreads) p.active[2 + i] = tb.active[1 + i];
+        for (int i = tid; i < p.T * (p.k + p.s); i += kFewThreads) p.row_w[i] = tb.row_w[i];
+        for (int i = tid; i < n_act * p.T; i += kFewThreads) {
             const int g = tb.active[1 + i / p.T], t = i % p.T;
             int row = -1;
             for (int r = tb.offsets[g]; r < tb.offsets[g] + tb.counts[g]; ++r) row = tb.row_src[r] == t ? r : row;
             p.rowmap[i] = (int16_t)row;
         }
     }
-    const int cb = p.I / 8, n_items = n_act * cb, grid = gridDim.x;
-    if ((int)blockIdx.x >= n_items) return;
-
-    const int wrow = p.H * (F8 ? 1 : 2);                     // bytes of a weight row
-    const int units = (p.H + Geo::UK - 1) / Geo::UK;
-    const int nb = ((units + kFewWaves - 1) / kFewWaves + UB - 1) / UB, batches = (nb + 1) & ~1;
-    const int nsb = (2 * p.I + 127) >> 7, ksb = (p.H + 127) >> 7;
-
-    // the loader: one batch after another through all items
-    struct { int item, b; bool live; const uint8_t* w; const float* s; int up_s; uint32_t ro, xo[NT]; } L;
-    auto open = [&]() __attribute__((always_inline)) {
-        L.b = 0;
-        L.live = L.item < n_items;
-        const int item = L.live ? L.item : 0;
-        const int ai = __builtin_amdgcn_readfirstlane(item / cb), c0 = (item - ai * cb) * 8;
-        const int g = __builtin_amdgcn_readfirstlane(tb.active[1 + ai]);
-        const int sh = g < p.E_loc ? 0 : 1, gi = sh ? 0 : g;
-        L.w = p.w1[sh] + (size_t)gi * (size_t)(2 * p.I) * (size_t)wrow;
-        const int col = c0 + 2 * (j >> 2) + (j & 1);
-        L.ro = (uint32_t)(((j >> 1) & 1) * p.I + col) * (uint32_t)wrow;
-        if constexpr (F8) {
-            L.s = p.s1[sh] + ((size_t)gi * nsb + (c0 >> 7)) * ksb;
-            L.up_s = (((p.I + c0) >> 7) - (c0 >> 7)) * ksb;
-        }
-        const int lo = tb.offsets[g], n = tb.counts[g];
-        #pragma unroll
-        for (int i = 0; i < NT; ++i)
-            L.xo[i] = 16 * i + j < n ? (uint32_t)tb.row_src[min(lo + 16 * i + j, p.T * (p.k + p.s) - 1)] * p.x_ld : kMmNoRow;
-    };
-    auto load = [&](FewBatch<F8, NT>& B) __attribute__((always_inline)) {
-        const rsrc_t rw = make_rsrc(L.w, L.live ? (uint32_t)(2 * p.I) * (uint32_t)wrow : 0u);
-        const rsrc_t rx = make_rsrc(p.x, L.live ? p.x_bytes : 0u);
-        #pragma unroll
-        for (int i = 0; i < UB; ++i) {
-            const int u = (L.b * UB + i) * kFewWaves + w;
-            #pragma unroll
-            for (int h = 0; h < 2; ++h) B.a[i][h] = few_load_w(rw, few_add(L.ro, few_koff_w<F8>(u, h, q, p.H)));
-            #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                #pragma unroll
-                for (int h = 0; h < Geo::NB; ++h) B.b[i][t][h] = few_load(rx, few_add(L.xo[t], few_koff_x<F8>(u, h, q, p.H)));
-            if constexpr (F8) {
-                const rsrc_t rs = make_rsrc(L.s, L.live ? (uint32_t)(L.up_s + ksb) * 4u : 0u);
-                const int kb = min(u, ksb - 1);
-                B.sc[i][0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, kb * 4, 0, 0));
-                B.sc[i][1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, (L.up_s + kb) * 4, 0, 0));
-            }
-        }
-        if (++L.b == batches) {
-            L.item += grid;
-            open();
-        }
-    };
-    f32x4 acc[NT];
-    auto multiply = [&](const FewBatch<F8, NT>& B) __attribute__((always_inline)) {
-        #pragma unroll
-        for (int i = 0; i < UB; ++i)
-            #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const f32x4 d = few_unit<EL, F8>(B.a[i], B.b[i][t]);
-                #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[t][v] = F8 ? fmaf(d[v], B.sc[i][v >> 1], acc[t][v]) : acc[t][v] + d[v];
-            }
-    };
-
-    FewBatch<F8, NT> b0, b1;
-    L.item = blockIdx.x;
-    open();
-    load(b0);
-    int turn = 0;
-    for (int item = blockIdx.x; item < n_items; item += grid, turn ^= 1) {
-        #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        #pragma unroll 1
-        for (int b = 0; b < batches; b += 2) {
-            load(b1);
-            multiply(b0);
-            load(b0);                                        // the next item's first, at the end
-            multiply(b1);
-        }
-        // the waves' sums through LDS, two buffers in turn: one barrier an item
-        float* const mine = part + turn * (kFewWaves * NT * 256);
-        #pragma unroll
-        for (int t = 0; t < NT; ++t)
-            #pragma unroll
-            for (int v = 0; v < 4; ++v) mine[(w * NT + t) * 256 + v * 64 + lane] = acc[t][v];
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-        bare_barrier();
-        const int ai = __builtin_amdgcn_readfirstlane(item / cb), c0 = (item - ai * cb) * 8;
-        const int g = __builtin_amdgcn_readfirstlane(tb.active[1 + ai]);
-        const int lo = tb.offsets[g], n = tb.counts[g];
-        // thread (tile, output v of a pair, lane of the result): gate v, up v + 2
-        for (int e = threadIdx.x; e < NT * 128; e += kFewThreads) {
-            const int t = e >> 7, v = (e >> 6) & 1, l = e & 63, r = 16 * t + (l & 15), c = c0 + 2 * (l >> 4) + v;
-            if (r >= n) continue;
-            float z = 0.f, u = 0.f;
-            #pragma unroll
-            for (int i = 0; i < kFewWaves; ++i) {
-                z += mine[(i * NT + t) * 256 + v * 64 + l];
-                u += mine[(i * NT + t) * 256 + (v + 2) * 64 + l];
-            }
-            if (p.b1) {
-                z += p.b1[(size_t)g * 2 * p.I + c];
-                u += p.b1[(size_t)g * 2 * p.I + p.I + c];
-            }
-            z = epi_clamp(z, p.limit);
-            float a = 0.f;
-            with_act(p.act, [&](auto act) { a = epi_act<decltype(act)::value>(z, p.beta); });
-            const float o = a * epi_clamp(u, p.limit) * tb.row_w[lo + r];
-            p.h[(size_t)(lo + r) * p.I + c] = (uint16_t)pack16(o, 0.f, EL == kElF16);
-        }
+    // the longest group decides: one tile of 16 rows or two, rows in LDS where they fit
+    const int stride = few_row_lds<F8>((p.H + (F8 ? 127 : 63)) / (F8 ? 128 : 64));
+    const bool fit = (int64_t)most * stride <= lds_rows;
+    if (TWO && most > 16) {
+        if (fit) few_w1_body<EL, F8, NTM, true>(p, tb, n_act, part, rows);
+        else few_w1_body<EL, F8, NTM, false>(p, tb, n_act, part, rows);
+    } else {
+        if (fit) few_w1_body<EL, F8, 1, true>(p, tb, n_act, part, rows);
+        else few_w1_body<EL, F8, 1, false>(p, tb, n_act, part, rows);
     }
 }
 
 // ------------------------------------------------------------------ few_w2
-template <int EL, bool F8, int NT>
-__global__ __launch_bounds__(kFewThreads, 4)
-void few_w2_kernel(FewP p) {
-    using Geo = FewGeom<F8, NT>;
-    constexpr int UB = Geo::UB;
-    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    float* const part = (float*)smem;                        // [8 waves][NT][4][64]
-    int* const active = (int*)(smem + kFewWaves * NT * 1024);
+template <int EL, bool F8, int NT, bool XL>
+MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, int n_act, int R, float* part, uint8_t* rows) {
+    using Geo = FewGeom<F8, NT, XL>;
+    constexpr int RING = Geo::Ring;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int q = lane >> 4, j = lane & 15;
-    const int n_act = __builtin_amdgcn_readfirstlane(p.active[0]);
-    int16_t* const map = (int16_t*)(active + n_act);
-    for (int i = threadIdx.x; i < n_act; i += kFewThreads) active[i] = p.active[1 + i];
-    for (int i = threadIdx.x; i < n_act * p.T; i += kFewThreads) map[i] = p.rowmap[i];
-    __syncthreads();
-
-    const int n0 = blockIdx.x * 16;
     const int wrow = p.I * (F8 ? 1 : 2);
     const int upg = (p.I + Geo::UK - 1) / Geo::UK;           // units of a group
     const int units = n_act * upg;
-    const int nb = ((units + kFewWaves - 1) / kFewWaves + UB - 1) / UB;
     const int nsb = (p.H + 127) >> 7, ksb = (p.I + 127) >> 7;
-    // (rows past H read the last row: their sums are not stored)
-    const uint32_t ro = (uint32_t)min(n0 + j, p.H - 1) * (uint32_t)wrow;
-    const size_t h_rows = (size_t)p.T * (p.k + p.s);
+    const int stride = (upg * (F8 ? 256 : 128) + 1023) / 1024 * 1024 + 64;
+    const int upw = max(1, (units + kFewWaves - 1) / kFewWaves);      // rounds of units of a block of columns
+    const rsrc_t rh = make_rsrc(p.h, (uint32_t)((size_t)R * p.I * 2));
 
-    int ai = w / upg, ku = w - ai * upg;                     // this wave's next unit
-    auto load = [&](FewBatch<F8, NT>& B) __attribute__((always_inline)) {
+    struct { int block, i, ai, ku, sb; bool live; uint32_t ro; } L;
+    auto open = [&]() __attribute__((always_inline)) {
+        L.i = 0;
+        L.live = L.block < p.blocks;
+        const int n = (L.live ? L.block : 0) * p.cols + j;
+        L.ro = j < p.cols && n < p.H ? (uint32_t)n * (uint32_t)wrow : kMmNoRow;
+        // (columns 4 q .. 4 q + 3 are of one block of scales: blocks of E4M3 columns are multiples of 4)
+        L.sb = (min(n - j + 4 * q, p.H - 1) >> 7) * ksb;
+        L.ai = w / upg;
+        L.ku = w - L.ai * upg;
+    };
+    auto load = [&](FewSlot<F8, NT, XL>& S) __attribute__((always_inline)) {
+        const bool live = L.live && L.ai < n_act;
+        const int g = live ? __builtin_amdgcn_readfirstlane(active[L.ai]) : 0;
+        const int sh = g < p.E_loc ? 0 : 1, gi = sh ? 0 : g;
+        const rsrc_t rw = make_rsrc(p.w2[sh] + (size_t)gi * (size_t)p.H * (size_t)wrow, live ? (uint32_t)p.H * (uint32_t)wrow : 0u);
         #pragma unroll
-        for (int i = 0; i < UB; ++i) {
-            const bool live = ai < n_act;
-            const int g = live ? __builtin_amdgcn_readfirstlane(active[ai]) : 0;
-            const int sh = g < p.E_loc ? 0 : 1, gi = sh ? 0 : g;
-            const rsrc_t rw = make_rsrc(p.w2[sh] + (size_t)gi * (size_t)p.H * (size_t)wrow, live ? (uint32_t)p.H * (uint32_t)wrow : 0u);
-            const rsrc_t rh = make_rsrc(p.h, live ? (uint32_t)(h_rows * p.I * 2) : 0u);
-            #pragma unroll
-            for (int h = 0; h < 2; ++h) B.a[i][h] = few_load_w(rw, few_add(ro, few_koff_w<F8>(ku, h, q, p.I)));
-            #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int row = live && 16 * t + j < p.T ? map[ai * p.T + 16 * t + j] : -1;
-                B.row[i][t] = row;
+        for (int h = 0; h < 2; ++h) S.a[h] = few_load_w(rw, few_add(L.ro, few_koff_w<F8>(L.ku, h, q, p.I)));
+        #pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int row = live && 16 * t + j < p.T ? map[L.ai * p.T + 16 * t + j] : -1;
+            S.row[t] = row;
+            if constexpr (!XL) {
                 const uint32_t o = row >= 0 ? (uint32_t)row * (uint32_t)(p.I * 2) : kMmNoRow;
                 #pragma unroll
-                for (int h = 0; h < Geo::NB; ++h) B.b[i][t][h] = few_load(rh, few_add(o, few_koff_x<F8>(ku, h, q, p.I)));
+                for (int i = 0; i < Geo::NB; ++i) S.b[t][i] = few_load(rh, few_add(o, few_koff_x<F8>(L.ku, i, q, p.I)));
+            } else {
+                S.at[t] = max(row, 0) * stride + few_kbyte_x<F8>(L.ku, 0, q);
             }
-            if constexpr (F8) {
-                const rsrc_t rs = make_rsrc(p.s2[sh] + ((size_t)gi * nsb + (n0 >> 7)) * ksb, live ? (uint32_t)ksb * 4u : 0u);
-                B.sc[i][0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, ku * 4, 0, 0));
-            }
-            ku += kFewWaves;
-            while (ku >= upg) { ku -= upg; ++ai; }
-            ai = __builtin_amdgcn_readfirstlane(ai);
-            ku = __builtin_amdgcn_readfirstlane(ku);
+        }
+        if constexpr (F8) {
+            const rsrc_t rs = make_rsrc(p.s2[sh] + (size_t)gi * nsb * ksb, live ? (uint32_t)(nsb * ksb) * 4u : 0u);
+            S.sc[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, (L.sb + L.ku) * 4, 0, 0);
+        }
+        L.ku += kFewWaves;
+        while (L.ku >= upg) { L.ku -= upg; ++L.ai; }
+        L.ai = __builtin_amdgcn_readfirstlane(L.ai);
+        L.ku = __builtin_amdgcn_readfirstlane(L.ku);
+        if (++L.i == upw) {
+            L.block += gridDim.x;
+            open();
         }
     };
+
+    if constexpr (XL) {
+        const int chunks = stride / 1024;
+        for (int c = w; c < R * chunks; c += kFewWaves) {
+            const int r = c / chunks;
+            few_stage(rh, (uint32_t)r * (uint32_t)(p.I * 2), 2 * p.I, c - r * chunks, rows + r * stride, lane);
+        }
+    }
+    few_fence();
+    L.block = blockIdx.x;
+    open();
+    FewSlot<F8, NT, XL> ring[RING];
+    static_for<RING>([&](auto s) __attribute__((always_inline)) { load(ring[decltype(s)::value]); });
+    if constexpr (XL) {
+        few_fence();
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(RING * (F8 ? 3 : 2), 15));
+        bare_barrier();
+    }
     f32x4 acc[NT];
     #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto multiply = [&](const FewBatch<F8, NT>& B) __attribute__((always_inline)) {
-        #pragma unroll
-        for (int i = 0; i < UB; ++i)
+    int block = blockIdx.x, i = 0;
+    bool done = false;
+    while (!done) {
+        static_for<RING>([&](auto s) __attribute__((always_inline)) {
+            if (done) return;
+            FewSlot<F8, NT, XL>& S = ring[decltype(s)::value];
             #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const f32x4 d = few_unit<EL, F8>(B.a[i], B.b[i][t]);
-                const bool in = B.row[i][t] >= 0;
+                const f32x4 d = few_unit<EL, F8>(S.a, [&](int x) __attribute__((always_inline)) {
+                    if constexpr (XL) return *(const i32x4*)(rows + S.at[t] + few_kbyte_x<F8>(0, x, 0));
+                    else return S.b[t][x];
+                });
+                const bool in = S.row[t] >= 0;
                 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const float s = F8 ? fmaf(d[v], B.sc[i][0], acc[t][v]) : acc[t][v] + d[v];
-                    acc[t][v] = in ? s : acc[t][v];
+                    const float y = F8 ? fmaf(d[v], __uint_as_float(S.sc[0]), acc[t][v]) : acc[t][v] + d[v];
+                    acc[t][v] = in ? y : acc[t][v];
                 }
             }
-    };
-    FewBatch<F8, NT> b0, b1;
-    load(b0);
-    #pragma unroll 1
-    for (int b = 0; b < nb; b += 2) {
-        load(b1);
-        multiply(b0);
-        load(b0);
-        multiply(b1);
-    }
-    #pragma unroll
-    for (int t = 0; t < NT; ++t)
-        #pragma unroll
-        for (int v = 0; v < 4; ++v) part[(w * NT + t) * 256 + v * 64 + lane] = acc[t][v];
-    __syncthreads();
-    // thread (token, column): the waves' sums in their order
-    for (int e = threadIdx.x; e < NT * 256; e += kFewThreads) {
-        const int t = e >> 4, c = e & 15, n = n0 + c;
-        if (t >= p.T || n >= p.H) continue;
-        float o = 0.f;
-        #pragma unroll
-        for (int i = 0; i < kFewWaves; ++i) o += part[(i * NT + (t >> 4)) * 256 + (c & 3) * 64 + (c >> 2) * 16 + (t & 15)];
-        if (p.b2) {
-            for (int a = 0; a < n_act; ++a) {
-                const int row = map[a * p.T + t];
-                if (row >= 0) o = fmaf(p.row_w[row], p.b2[(size_t)active[a] * p.H + n], o);
+            load(S);
+            if (++i < upw) return;
+            i = 0;
+            #pragma unroll
+            for (int t = 0; t < NT; ++t)
+                #pragma unroll
+                for (int v = 0; v < 4; ++v) part[(w * NT + t) * 256 + v * 64 + lane] = acc[t][v];
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+            bare_barrier();
+            // thread (token, column): the waves' sums in their order
+            const int e = threadIdx.x, t = e >> 4, c = e & 15, n = block * p.cols + c;
+            if (e < NT * 256 && t < p.T && c < p.cols && n < p.H) {
+                float o = 0.f;
+                #pragma unroll
+                for (int x = 0; x < kFewWaves; ++x) o += part[(x * NT + (t >> 4)) * 256 + (c & 3) * 64 + (c >> 2) * 16 + (t & 15)];
+                if (p.b2) {
+                    for (int a = 0; a < n_act; ++a) {
+                        const int row = map[a * p.T + t];
+                        if (row >= 0) o = fmaf(p.row_w[row], p.b2[(size_t)active[a] * p.H + n], o);
+                    }
+                }
+                if (p.res) o += lo16(p.res[(size_t)t * p.ld_res + n], EL == kElF16);
+                p.out[(size_t)t * p.ld_out + n] = (uint16_t)pack16(o, 0.f, EL == kElF16);
             }
-        }
-        if (p.res) o += lo16(p.res[(size_t)t * p.ld_res + n], EL == kElF16);
-        p.out[(size_t)t * p.ld_out + n] = (uint16_t)pack16(o, 0.f, EL == kElF16);
+            #pragma unroll
+            for (int x = 0; x < NT; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+            block += gridDim.x;
+            done = block >= p.blocks;
+            if (!done) {                                     // the sums have been read before the next are written
+                __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+                bare_barrier();
+            }
+        });
     }
+}
+
+template <int EL, bool F8, int NT>
+__global__ __launch_bounds__(kFewThreads, 4)
+void few_w2_kernel(FewP p, int lds_rows, int most) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    float* const part = (float*)smem;                        // [16 waves][NT][4][64]
+    uint8_t* const rows = smem + kFewWaves * NT * 1024;      // [lds_rows]
+    int* const active = (int*)(rows + lds_rows);             // [2 + most], then the map
+    int16_t* const map = (int16_t*)(active + 2 + most);
+    // all of the tables at once, whatever they hold past the active groups
+    for (int i = threadIdx.x; i < most + 2; i += kFewThreads) active[i] = p.active[i];
+    for (int i = threadIdx.x; i < (most * p.T + 1) / 2; i += kFewThreads) ((int*)map)[i] = ((const int*)p.rowmap)[i];
+    __syncthreads();
+    const int n_act = __builtin_amdgcn_readfirstlane(active[0]), R = __builtin_amdgcn_readfirstlane(active[1]);
+    const int upg = (p.I + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
+    const int64_t stride = (upg * (F8 ? 256 : 128) + 1023) / 1024 * 1024 + 64;
+    if (max(R, 1) * stride <= lds_rows) few_w2_body<EL, F8, NT, true>(p, active + 2, map, n_act, R, part, rows);
+    else few_w2_body<EL, F8, NT, false>(p, active + 2, map, n_act, R, part, rows);
 }
 
 template <typename K>
@@ -439,44 +587,60 @@ int few_ready(K* k, bool (&ready)[64]) {
     return 0;
 }
 
+// LDS left for token rows: a compute unit's, less the sums and the tables (few_w1:
+// at least 55 KiB; grouping's scratch, at most 89 KiB, lies in both before they are used)
 template <int EL, bool F8, int NT>
 int launch_few(const FewP& p, hipStream_t stream) {
     static bool ready1[64] = {false}, ready2[64] = {false};
-    auto* k1 = &few_w1_kernel<EL, F8, NT>;
+    auto* k1 = &few_w1_kernel<EL, F8, NT == 2>;
     auto* k2 = &few_w2_kernel<EL, F8, NT>;
     int e = few_ready(k1, ready1);
     if (e || (e = few_ready(k2, ready2))) return e;
     const int64_t rows = (int64_t)p.T * (p.k + p.s), most = std::min<int64_t>(p.G, rows);
+    const int cus = device_cu_count();
     const int64_t items = most * (p.I / 8);
-    const int grid = (int)std::min<int64_t>(items, 2 * device_cu_count());
-    const size_t scratch = block_lds_ints(kFewWaves, p.G, p.E_loc);
-    const size_t lds1 = (size_t)2 * kFewWaves * NT * 1024 + (few_table_ints(p.T, p.k, p.G, p.s) + scratch) * 4;
-    const size_t lds2 = (size_t)kFewWaves * NT * 1024 + (size_t)most * 4 + (((size_t)most * p.T * 2 + 3) & ~(size_t)3);
-    k1<<<grid, kFewThreads, lds1, stream>>>(p);
+    const int grid1 = (int)std::min<int64_t>(items, cus), grid2 = std::min(p.blocks, cus);
+    const int64_t fix1 = (int64_t)2 * kFewWaves * NT * 1024 +
+                         (int64_t)few_table_ints(p.T, p.k, p.G, p.s) * 4;
+    const int64_t fix2 = (int64_t)kFewWaves * NT * 1024 + (2 + most) * 4 + (most * p.T + 1) / 2 * 4;
+    const int rows1 = (int)((kMmLds - fix1) / 16 * 16), rows2 = (int)((kMmLds - fix2) / 16 * 16);
+    k1<<<grid1, kFewThreads, (size_t)(fix1 + rows1), stream>>>(p, rows1);
     if ((e = (int)hipGetLastError())) return e;
-    k2<<<(unsigned)((p.H + 15) / 16), kFewThreads, lds2, stream>>>(p);
+    k2<<<grid2, kFewThreads, (size_t)(fix2 + rows2), stream>>>(p, rows2, (int)most);
     return (int)hipGetLastError();
+}
+
+// Columns of few_w2's blocks: up to 16, fewer where that fills the last round of
+// workgroups better (a round costs its columns and about one more).
+int few_cols(int H, bool eight) {
+    const int cus = device_cu_count(), step = eight ? 4 : 1;
+    int best = 16;
+    int64_t least = 1ll << 60;
+    for (int c = 16; c >= 4; c -= step) {
+        const int64_t cost = ((H + c - 1) / c + cus - 1) / cus * (c + 1);
+        if (cost < least) { least = cost; best = c; }
+    }
+    return best;
 }
 
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-// byte offsets of the workspace's regions: h, row_w, slot, active, rowmap, end
-void few_regions(int T, int k, int G, int s, int I, size_t (&at)[6]) {
+// byte offsets of the workspace's regions: h, row_w, active, rowmap, end
+void few_regions(int T, int k, int G, int s, int I, size_t (&at)[5]) {
     const size_t R = (size_t)T * (k + s), most = std::min<size_t>(G, R);
     at[0] = 0;
     at[1] = at[0] + up16(R * I * 2);
     at[2] = at[1] + up16(R * 4);
-    at[3] = at[2] + up16(R * 4);
-    at[4] = at[3] + up16((most + 1) * 4);
-    at[5] = at[4] + up16(most * T * 2);
+    at[3] = at[2] + up16((most + 2) * 4);
+    at[4] = at[3] + up16(most * T * 2 + 2);
 }
 
 }  // namespace
 
 size_t moe_few_bytes(int T, int k, int G, int s, int I) {
-    size_t at[6];
+    size_t at[5];
     few_regions(T, k, G, s, I, at);
-    return at[5];
+    return at[4];
 }
 
 int moe_launch_few(const moe_few_args& a, void* ws, hipStream_t stream) {
@@ -494,11 +658,12 @@ int moe_launch_few(const moe_few_args& a, void* ws, hipStream_t stream) {
     p.b1 = a.epi ? a.epi->bias : nullptr; p.b2 = a.bias2;
     p.res = (const uint16_t*)a.residual; p.ld_res = (size_t)a.ld_res;
     p.out = (uint16_t*)a.out; p.ld_out = (size_t)a.ld_out;
-    size_t at[6];
+    p.cols = few_cols(a.H, a.w1_scales != nullptr); p.blocks = (a.H + p.cols - 1) / p.cols;
+    size_t at[5];
     few_regions(p.T, p.k, p.G, p.s, p.I, at);
     uint8_t* b = (uint8_t*)ws;
-    p.h = (uint16_t*)(b + at[0]); p.row_w = (float*)(b + at[1]); p.slot = (int32_t*)(b + at[2]);
-    p.active = (int32_t*)(b + at[3]); p.rowmap = (int16_t*)(b + at[4]);
+    p.h = (uint16_t*)(b + at[0]); p.row_w = (float*)(b + at[1]); p.active = (int32_t*)(b + at[2]);
+    p.rowmap = (int16_t*)(b + at[3]);
     const bool f8 = a.w1_scales != nullptr, two = a.T > 16;
     if (a.dtype == MOE_T_F16) {
         if (f8) return two ? launch_few<kElF16, true, 2>(p, stream) : launch_few<kElF16, true, 1>(p, stream);

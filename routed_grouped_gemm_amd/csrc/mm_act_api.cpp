@@ -25,8 +25,9 @@ constexpr int32_t kFewMaxDim = 65536;
 
 }  // namespace
 
-MOE_EXPORT size_t moe_layer_few_workspace_size(int32_t T, int32_t k, int32_t E_loc, int32_t I, int32_t s) {
-    if (check_few_sizes(T, k, E_loc, s) || I < 8 || I > kFewMaxDim) return 0;
+MOE_EXPORT size_t moe_layer_few_workspace_size(int32_t T, int32_t k, int32_t E_loc, int32_t H, int32_t I,
+                                               int32_t s) {
+    if (check_few_sizes(T, k, E_loc, s) || H < 8 || H > kFewMaxDim || I < 8 || I > kFewMaxDim) return 0;
     return moe_few_bytes(T, k, E_loc + s, s, I);
 }
 

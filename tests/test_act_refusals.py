@@ -51,8 +51,8 @@ def test_layer_few():
     assert call(ws_bytes=16) == WS and call(ws=None) == WS and call(ws=F + 8) == SHAPE
     assert call(T=0, logits=None, x=None, out=None, ws=None, ws_bytes=0) == OK
     size = lib.moe_layer_few_workspace_size
-    assert size(33, 2, 8, 128, 0) == 0 and size(4, 2, 8, 128, 2) == 0 and size(4, 0, 8, 128, 0) == 0
-    assert size(32, 31, 2048, 65536, 1) < 1 << 28 and size(1, 1, 1, 8, 0) > 0
+    assert size(33, 2, 8, 256, 128, 0) == 0 and size(4, 2, 8, 256, 128, 2) == 0 and size(4, 0, 8, 256, 128, 0) == 0
+    assert size(32, 31, 2048, 65536, 65536, 1) < 1 << 28 and size(1, 1, 1, 8, 8, 0) > 0
 
 
 def test_bias_grad():
