@@ -203,6 +203,17 @@ MOE_DEV void few_fence() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// `steps` units in turns of the ring. The last turn is a whole one too (its units
+// past the end are not there: nothing is loaded or stored for them), because with
+// a way out between two slots the compiler sees paths on which slots are skipped,
+// and waits for requests that are long to come.
+template <int RING, typename Slot, typename Step>
+MOE_DEV void few_turns(Slot (&ring)[RING], int steps, Step&& step) {
+    #pragma unroll 1
+    for (; steps > 0; steps -= RING)
+        static_for<RING>([&](auto s) __attribute__((always_inline)) { step(ring[decltype(s)::value]); });
+}
+
 // ------------------------------------------------------------------ few_w1
 // bytes of a token row in LDS: all units of all waves, and 64 so that rows start in other banks
 template <bool F8>
@@ -312,78 +323,71 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
     f32x4 acc[NT];
     #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    bool done = false;
-    while (!done) {
-        static_for<RING>([&](auto s) __attribute__((always_inline)) {
-            if (done) return;
-            FewSlot<F8, NT, XL>& S = ring[decltype(s)::value];
-            const int u = i * kFewWaves + w;
-            float sc[2] = {1.f, 1.f};
-            if constexpr (F8) {
-                sc[0] = __uint_as_float(S.sc[0]);
-                sc[1] = __uint_as_float(S.sc[1]);
-            }
+    auto step = [&](FewSlot<F8, NT, XL>& S) __attribute__((always_inline)) {
+        const int u = i * kFewWaves + w;
+        float sc[2] = {1.f, 1.f};
+        if constexpr (F8) {
+            sc[0] = __uint_as_float(S.sc[0]);
+            sc[1] = __uint_as_float(S.sc[1]);
+        }
+        #pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const f32x4 d = few_unit<EL, F8>(S.a, [&](int x) __attribute__((always_inline)) {
+                if constexpr (XL) return *(const i32x4*)(xrow[t] + few_kbyte_x<F8>(u, x, q));
+                else return S.b[t][x];
+            });
             #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const f32x4 d = few_unit<EL, F8>(S.a, [&](int x) __attribute__((always_inline)) {
-                    if constexpr (XL) return *(const i32x4*)(xrow[t] + few_kbyte_x<F8>(u, x, q));
-                    else return S.b[t][x];
-                });
-                #pragma unroll
-                for (int v = 0; v < 4; ++v) acc[t][v] = F8 ? fmaf(d[v], sc[v >> 1], acc[t][v]) : acc[t][v] + d[v];
-            }
-            load(S);
-            if (++i < upw) return;
-            i = 0;
-            // an item's end: the waves' sums through LDS, two buffers in turn: one barrier an item
-            float* const mine = part + turn * (kFewWaves * NT * 256);
-            turn ^= 1;
+            for (int v = 0; v < 4; ++v) acc[t][v] = F8 ? fmaf(d[v], sc[v >> 1], acc[t][v]) : acc[t][v] + d[v];
+        }
+        load(S);
+        if (++i < upw || left == 0) return;
+        i = 0;
+        // an item's end: the waves' sums through LDS, two buffers in turn: one barrier an item
+        float* const mine = part + turn * (kFewWaves * NT * 256);
+        turn ^= 1;
+        #pragma unroll
+        for (int t = 0; t < NT; ++t)
             #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                #pragma unroll
-                for (int v = 0; v < 4; ++v) mine[(w * NT + t) * 256 + v * 64 + lane] = acc[t][v];
-            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-            bare_barrier();
-            // thread (tile, output of a pair, lane of the result): gate v, up v + 2
-            const int e = threadIdx.x, t = e >> 7, v = (e >> 6) & 1, l = e & 63, r = 16 * t + (l & 15), o8 = 2 * (l >> 4) + v, c = ob * c8 + o8;
-            if (e < NT * 128 && o8 < ob && c < p.I && r < tb.counts[g]) {
-                float z = 0.f, y = 0.f;
-                #pragma unroll
-                for (int x = 0; x < kFewWaves; ++x) {
-                    z += mine[(x * NT + t) * 256 + v * 64 + l];
-                    y += mine[(x * NT + t) * 256 + (v + 2) * 64 + l];
-                }
-                if (p.b1) {
-                    z += p.b1[(size_t)g * 2 * p.I + c];
-                    y += p.b1[(size_t)g * 2 * p.I + p.I + c];
-                }
-                z = epi_clamp(z, p.limit);
-                float a = 0.f;
-                with_act(p.act, [&](auto act) { a = epi_act<decltype(act)::value>(z, p.beta); });
-                const int row = tb.offsets[g] + r;
-                const float o = a * epi_clamp(y, p.limit) * tb.row_w[row];
-                p.h[(size_t)row * p.I + c] = (uint16_t)pack16(o, 0.f, EL == kElF16);
-            }
+            for (int v = 0; v < 4; ++v) mine[(w * NT + t) * 256 + v * 64 + lane] = acc[t][v];
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+        bare_barrier();
+        // thread (tile, output of a pair, lane of the result): gate v, up v + 2
+        const int e = threadIdx.x, t = e >> 7, v = (e >> 6) & 1, l = e & 63, r = 16 * t + (l & 15), o8 = 2 * (l >> 4) + v, c = ob * c8 + o8;
+        if (e < NT * 128 && o8 < ob && c < p.I && r < tb.counts[g]) {
+            float z = 0.f, y = 0.f;
             #pragma unroll
-            for (int x = 0; x < NT; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (--left == 0) {
-                done = true;
-                return;
+            for (int x = 0; x < kFewWaves; ++x) {
+                z += mine[(x * NT + t) * 256 + v * 64 + l];
+                y += mine[(x * NT + t) * 256 + (v + 2) * 64 + l];
             }
-            if (++c8 == cb) {                                // the next group (every wave is past its products)
-                c8 = 0;
-                ++ai;
-                g = __builtin_amdgcn_readfirstlane(tb.active[1 + ai]);
-                if constexpr (XL) {
-                    stage(g);
-                    few_fence();
-                    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
-                    bare_barrier();
-                }
-                rows_of();
+            if (p.b1) {
+                z += p.b1[(size_t)g * 2 * p.I + c];
+                y += p.b1[(size_t)g * 2 * p.I + p.I + c];
             }
-        });
-    }
+            z = epi_clamp(z, p.limit);
+            float a = 0.f;
+            with_act(p.act, [&](auto act) { a = epi_act<decltype(act)::value>(z, p.beta); });
+            const int row = tb.offsets[g] + r;
+            const float o = a * epi_clamp(y, p.limit) * tb.row_w[row];
+            p.h[(size_t)row * p.I + c] = (uint16_t)pack16(o, 0.f, EL == kElF16);
+        }
+        #pragma unroll
+        for (int x = 0; x < NT; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        --left;
+        if (++c8 == cb && left > 0) {                                // the next group (every wave is past its products)
+            c8 = 0;
+            ++ai;
+            g = __builtin_amdgcn_readfirstlane(tb.active[1 + ai]);
+            if constexpr (XL) {
+                stage(g);
+                few_fence();
+                __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+                bare_barrier();
+            }
+            rows_of();
+        }
+    };
+    few_turns(ring, left * upw, step);
 }
 
 template <int EL, bool F8, bool TWO>
@@ -501,58 +505,52 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
     #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     int block = blockIdx.x, i = 0;
-    bool done = false;
-    while (!done) {
-        static_for<RING>([&](auto s) __attribute__((always_inline)) {
-            if (done) return;
-            FewSlot<F8, NT, XL>& S = ring[decltype(s)::value];
+    auto step = [&](FewSlot<F8, NT, XL>& S) __attribute__((always_inline)) {
+        #pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const f32x4 d = few_unit<EL, F8>(S.a, [&](int x) __attribute__((always_inline)) {
+                if constexpr (XL) return *(const i32x4*)(rows + S.at[t] + few_kbyte_x<F8>(0, x, 0));
+                else return S.b[t][x];
+            });
+            const bool in = S.row[t] >= 0;
             #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const f32x4 d = few_unit<EL, F8>(S.a, [&](int x) __attribute__((always_inline)) {
-                    if constexpr (XL) return *(const i32x4*)(rows + S.at[t] + few_kbyte_x<F8>(0, x, 0));
-                    else return S.b[t][x];
-                });
-                const bool in = S.row[t] >= 0;
-                #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const float y = F8 ? fmaf(d[v], __uint_as_float(S.sc[0]), acc[t][v]) : acc[t][v] + d[v];
-                    acc[t][v] = in ? y : acc[t][v];
+            for (int v = 0; v < 4; ++v) {
+                const float y = F8 ? fmaf(d[v], __uint_as_float(S.sc[0]), acc[t][v]) : acc[t][v] + d[v];
+                acc[t][v] = in ? y : acc[t][v];
+            }
+        }
+        load(S);
+        if (++i < upw || block >= p.blocks) return;
+        i = 0;
+        #pragma unroll
+        for (int t = 0; t < NT; ++t)
+            #pragma unroll
+            for (int v = 0; v < 4; ++v) part[(w * NT + t) * 256 + v * 64 + lane] = acc[t][v];
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+        bare_barrier();
+        // thread (token, column): the waves' sums in their order
+        const int e = threadIdx.x, t = e >> 4, c = e & 15, n = block * p.cols + c;
+        if (e < NT * 256 && t < p.T && c < p.cols && n < p.H) {
+            float o = 0.f;
+            #pragma unroll
+            for (int x = 0; x < kFewWaves; ++x) o += part[(x * NT + (t >> 4)) * 256 + (c & 3) * 64 + (c >> 2) * 16 + (t & 15)];
+            if (p.b2) {
+                for (int a = 0; a < n_act; ++a) {
+                    const int row = map[a * p.T + t];
+                    if (row >= 0) o = fmaf(p.row_w[row], p.b2[(size_t)active[a] * p.H + n], o);
                 }
             }
-            load(S);
-            if (++i < upw) return;
-            i = 0;
-            #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                #pragma unroll
-                for (int v = 0; v < 4; ++v) part[(w * NT + t) * 256 + v * 64 + lane] = acc[t][v];
-            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-            bare_barrier();
-            // thread (token, column): the waves' sums in their order
-            const int e = threadIdx.x, t = e >> 4, c = e & 15, n = block * p.cols + c;
-            if (e < NT * 256 && t < p.T && c < p.cols && n < p.H) {
-                float o = 0.f;
-                #pragma unroll
-                for (int x = 0; x < kFewWaves; ++x) o += part[(x * NT + (t >> 4)) * 256 + (c & 3) * 64 + (c >> 2) * 16 + (t & 15)];
-                if (p.b2) {
-                    for (int a = 0; a < n_act; ++a) {
-                        const int row = map[a * p.T + t];
-                        if (row >= 0) o = fmaf(p.row_w[row], p.b2[(size_t)active[a] * p.H + n], o);
-                    }
-                }
-                if (p.res) o += lo16(p.res[(size_t)t * p.ld_res + n], EL == kElF16);
-                p.out[(size_t)t * p.ld_out + n] = (uint16_t)pack16(o, 0.f, EL == kElF16);
-            }
-            #pragma unroll
-            for (int x = 0; x < NT; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
-            block += gridDim.x;
-            done = block >= p.blocks;
-            if (!done) {                                     // the sums have been read before the next are written
-                __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-                bare_barrier();
-            }
-        });
-    }
+            if (p.res) o += lo16(p.res[(size_t)t * p.ld_res + n], EL == kElF16);
+            p.out[(size_t)t * p.ld_out + n] = (uint16_t)pack16(o, 0.f, EL == kElF16);
+        }
+        #pragma unroll
+        for (int x = 0; x < NT; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
+        block += gridDim.x;
+        // the sums have been read before the next are written
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+        bare_barrier();
+    };
+    few_turns(ring, (p.blocks - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * upw, step);
 }
 
 template <int EL, bool F8, int NT>
