@@ -118,12 +118,22 @@ MOE_DEV i32x4 few_load_w(const rsrc_t& r, uint32_t o) {
     return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 2));
 }
 
-// byte offset in a weight row of this lane's piece h of unit u, and of piece i
-// of a token row; past the row: kMmInvalid
+// byte offset in a weight row of this lane's piece of unit u, and of piece i of
+// a token row; past the row: kMmInvalid
 template <bool F8>
-MOE_DEV uint32_t few_koff_w(int u, int h, int q, int K) {
-    const int b = u * 128 + 64 * h + 16 * q;
+MOE_DEV uint32_t few_koff_w(int u, int lane, int K) {
+    const int b = u * 128 + 16 * (lane & 7);
     return b < (F8 ? K : 2 * K) ? (uint32_t)b : kMmInvalid;
+}
+// A unit of weights from the lanes that loaded it (8 lanes a row: whole lines)
+// to those that multiply it (16 rows, 4 lanes each), through 2 KiB of LDS a wave,
+// 16-byte pieces swizzled by row. A wave's LDS accesses are done in order.
+MOE_DEV void few_swap(uint8_t* ex, int lane, const i32x4 (&in)[2], i32x4 (&out)[2]) {
+    const int r = lane >> 3, j = lane & 15, q = lane >> 4;
+    *(i32x4*)(ex + r * 128 + ((lane & 7) ^ kc_swz(r)) * 16) = in[0];
+    *(i32x4*)(ex + (8 + r) * 128 + ((lane & 7) ^ kc_swz(8 + r)) * 16) = in[1];
+    out[0] = *(const i32x4*)(ex + j * 128 + (q ^ kc_swz(j)) * 16);
+    out[1] = *(const i32x4*)(ex + j * 128 + ((4 + q) ^ kc_swz(j)) * 16);
 }
 // (LDS rows are padded with zeros, so only loads from memory ask for the end)
 template <bool F8>
@@ -220,7 +230,7 @@ template <bool F8>
 __host__ __device__ inline int few_row_lds(int units) { return (units + kFewWaves - 1) / kFewWaves * kFewWaves * (F8 ? 256 : 128) + 64; }
 
 template <int EL, bool F8, int NT, bool XL>
-MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* part, uint8_t* rows) {
+MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* part, uint8_t* swap, uint8_t* rows) {
     using Geo = FewGeom<F8, NT, XL>;
     constexpr int RING = Geo::Ring;
     const int lane = threadIdx.x & 63;
@@ -242,10 +252,11 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
     const int nsb = (2 * p.I + 127) >> 7, ksb = (p.H + 127) >> 7;
     const int stride = few_row_lds<F8>(units);
     const rsrc_t rx = make_rsrc(p.x, p.x_bytes);
+    uint8_t* const ex = swap + w * 2048;
     const int R1 = p.T * (p.k + p.s) - 1;
 
     // the loader: one unit after another through all items
-    struct { int item, i; bool live; const uint8_t* w; const float* s; uint32_t ro, sg, su, xo[NT]; } L;
+    struct { int item, i; bool live; const uint8_t* w; const float* s; uint32_t ro[2], sg, su, xo[NT]; } L;
     auto open = [&]() __attribute__((always_inline)) {
         L.i = 0;
         L.live = L.item < end;
@@ -254,8 +265,11 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
         const int g = __builtin_amdgcn_readfirstlane(tb.active[1 + ai]);
         const int sh = g < p.E_loc ? 0 : 1, gi = sh ? 0 : g;
         L.w = p.w1[sh] + (size_t)gi * (size_t)(2 * p.I) * (size_t)wrow;
-        const int o = 2 * (j >> 2) + (j & 1), col = c0 + o;
-        L.ro = o < ob && col < p.I ? (uint32_t)(((j >> 1) & 1) * p.I + col) * (uint32_t)wrow : kMmNoRow;
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = 8 * h + (lane >> 3), o = 2 * (r >> 2) + (r & 1), col = c0 + o;
+            L.ro[h] = o < ob && col < p.I ? (uint32_t)(((r >> 1) & 1) * p.I + col) * (uint32_t)wrow : kMmNoRow;
+        }
         if constexpr (F8) {                                  // (an even column and the next one are of one block)
             L.s = p.s1[sh] + (size_t)gi * nsb * ksb;
             const int c = min(c0 + 2 * q, p.I - 2);
@@ -273,7 +287,7 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
         const rsrc_t rw = make_rsrc(L.w, L.live ? (uint32_t)(2 * p.I) * (uint32_t)wrow : 0u);
         const int u = L.i * kFewWaves + w;
         #pragma unroll
-        for (int h = 0; h < 2; ++h) S.a[h] = few_load_w(rw, few_add(L.ro, few_koff_w<F8>(u, h, q, p.H)));
+        for (int h = 0; h < 2; ++h) S.a[h] = few_load_w(rw, few_add(L.ro[h], few_koff_w<F8>(u, lane, p.H)));
         if constexpr (!XL) {
             #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -330,9 +344,11 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
             sc[0] = __uint_as_float(S.sc[0]);
             sc[1] = __uint_as_float(S.sc[1]);
         }
+        i32x4 a[2];
+        few_swap(ex, lane, S.a, a);
         #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const f32x4 d = few_unit<EL, F8>(S.a, [&](int x) __attribute__((always_inline)) {
+            const f32x4 d = few_unit<EL, F8>(a, [&](int x) __attribute__((always_inline)) {
                 if constexpr (XL) return *(const i32x4*)(xrow[t] + few_kbyte_x<F8>(u, x, q));
                 else return S.b[t][x];
             });
@@ -396,7 +412,8 @@ void few_w1_kernel(FewP p, int lds_rows) {
     constexpr int NTM = TWO ? 2 : 1;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     float* const part = (float*)smem;                        // [2][16 waves][NT][4][64]
-    uint8_t* const rows = smem + 2 * kFewWaves * NTM * 1024; // [lds_rows]
+    uint8_t* const swap = smem + 2 * kFewWaves * NTM * 1024; // [16 waves][2 KiB]
+    uint8_t* const rows = swap + kFewWaves * 2048;           // [lds_rows]
     const FewTables tb = few_tables((int*)(rows + lds_rows), (int*)smem, p.T, p.k, p.G, p.s);   // (scratch: before the sums)
     const int most = few_route(p, tb);
     const int n_act = __builtin_amdgcn_readfirstlane(tb.active[0]);
@@ -416,17 +433,17 @@ void few_w1_kernel(FewP p, int lds_rows) {
     const int stride = few_row_lds<F8>((p.H + (F8 ? 127 : 63)) / (F8 ? 128 : 64));
     const bool fit = (int64_t)most * stride <= lds_rows;
     if (TWO && most > 16) {
-        if (fit) few_w1_body<EL, F8, NTM, true>(p, tb, n_act, part, rows);
-        else few_w1_body<EL, F8, NTM, false>(p, tb, n_act, part, rows);
+        if (fit) few_w1_body<EL, F8, NTM, true>(p, tb, n_act, part, swap, rows);
+        else few_w1_body<EL, F8, NTM, false>(p, tb, n_act, part, swap, rows);
     } else {
-        if (fit) few_w1_body<EL, F8, 1, true>(p, tb, n_act, part, rows);
-        else few_w1_body<EL, F8, 1, false>(p, tb, n_act, part, rows);
+        if (fit) few_w1_body<EL, F8, 1, true>(p, tb, n_act, part, swap, rows);
+        else few_w1_body<EL, F8, 1, false>(p, tb, n_act, part, swap, rows);
     }
 }
 
 // ------------------------------------------------------------------ few_w2
 template <int EL, bool F8, int NT, bool XL>
-MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, int n_act, int R, float* part, uint8_t* rows) {
+MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, int n_act, int R, float* part, uint8_t* swap, uint8_t* rows) {
     using Geo = FewGeom<F8, NT, XL>;
     constexpr int RING = Geo::Ring;
     const int lane = threadIdx.x & 63;
@@ -437,17 +454,22 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
     const int units = n_act * upg;
     const int nsb = (p.H + 127) >> 7, ksb = (p.I + 127) >> 7;
     const int stride = (upg * (F8 ? 256 : 128) + 1023) / 1024 * 1024 + 64;
+    uint8_t* const ex = swap + w * 2048;
     const int upw = max(1, (units + kFewWaves - 1) / kFewWaves);      // rounds of units of a block of columns
     const rsrc_t rh = make_rsrc(p.h, (uint32_t)((size_t)R * p.I * 2));
 
-    struct { int block, i, ai, ku, sb; bool live; uint32_t ro; } L;
+    struct { int block, i, ai, ku, sb; bool live; uint32_t ro[2]; } L;
     auto open = [&]() __attribute__((always_inline)) {
         L.i = 0;
         L.live = L.block < p.blocks;
-        const int n = (L.live ? L.block : 0) * p.cols + j;
-        L.ro = j < p.cols && n < p.H ? (uint32_t)n * (uint32_t)wrow : kMmNoRow;
+        const int n0 = (L.live ? L.block : 0) * p.cols;
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = 8 * h + (lane >> 3);
+            L.ro[h] = r < p.cols && n0 + r < p.H ? (uint32_t)(n0 + r) * (uint32_t)wrow : kMmNoRow;
+        }
         // (columns 4 q .. 4 q + 3 are of one block of scales: blocks of E4M3 columns are multiples of 4)
-        L.sb = (min(n - j + 4 * q, p.H - 1) >> 7) * ksb;
+        L.sb = (min(n0 + 4 * q, p.H - 1) >> 7) * ksb;
         L.ai = w / upg;
         L.ku = w - L.ai * upg;
     };
@@ -457,7 +479,7 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
         const int sh = g < p.E_loc ? 0 : 1, gi = sh ? 0 : g;
         const rsrc_t rw = make_rsrc(p.w2[sh] + (size_t)gi * (size_t)p.H * (size_t)wrow, live ? (uint32_t)p.H * (uint32_t)wrow : 0u);
         #pragma unroll
-        for (int h = 0; h < 2; ++h) S.a[h] = few_load_w(rw, few_add(L.ro, few_koff_w<F8>(L.ku, h, q, p.I)));
+        for (int h = 0; h < 2; ++h) S.a[h] = few_load_w(rw, few_add(L.ro[h], few_koff_w<F8>(L.ku, lane, p.I)));
         #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int row = live && 16 * t + j < p.T ? map[L.ai * p.T + 16 * t + j] : -1;
@@ -506,9 +528,11 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
     for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     int block = blockIdx.x, i = 0;
     auto step = [&](FewSlot<F8, NT, XL>& S) __attribute__((always_inline)) {
+        i32x4 a[2];
+        few_swap(ex, lane, S.a, a);
         #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const f32x4 d = few_unit<EL, F8>(S.a, [&](int x) __attribute__((always_inline)) {
+            const f32x4 d = few_unit<EL, F8>(a, [&](int x) __attribute__((always_inline)) {
                 if constexpr (XL) return *(const i32x4*)(rows + S.at[t] + few_kbyte_x<F8>(0, x, 0));
                 else return S.b[t][x];
             });
@@ -558,7 +582,8 @@ __global__ __launch_bounds__(kFewThreads, 4)
 void few_w2_kernel(FewP p, int lds_rows, int most) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     float* const part = (float*)smem;                        // [16 waves][NT][4][64]
-    uint8_t* const rows = smem + kFewWaves * NT * 1024;      // [lds_rows]
+    uint8_t* const swap = smem + kFewWaves * NT * 1024;      // [16 waves][2 KiB]
+    uint8_t* const rows = swap + kFewWaves * 2048;           // [lds_rows]
     int* const active = (int*)(rows + lds_rows);             // [2 + most], then the map
     int16_t* const map = (int16_t*)(active + 2 + most);
     // all of the tables at once, whatever they hold past the active groups
@@ -568,8 +593,8 @@ void few_w2_kernel(FewP p, int lds_rows, int most) {
     const int n_act = __builtin_amdgcn_readfirstlane(active[0]), R = __builtin_amdgcn_readfirstlane(active[1]);
     const int upg = (p.I + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
     const int64_t stride = (upg * (F8 ? 256 : 128) + 1023) / 1024 * 1024 + 64;
-    if (max(R, 1) * stride <= lds_rows) few_w2_body<EL, F8, NT, true>(p, active + 2, map, n_act, R, part, rows);
-    else few_w2_body<EL, F8, NT, false>(p, active + 2, map, n_act, R, part, rows);
+    if (max(R, 1) * stride <= lds_rows) few_w2_body<EL, F8, NT, true>(p, active + 2, map, n_act, R, part, swap, rows);
+    else few_w2_body<EL, F8, NT, false>(p, active + 2, map, n_act, R, part, swap, rows);
 }
 
 template <typename K>
@@ -586,7 +611,7 @@ int few_ready(K* k, bool (&ready)[64]) {
 }
 
 // LDS left for token rows: a compute unit's, less the sums and the tables (few_w1:
-// at least 55 KiB; grouping's scratch, at most 89 KiB, lies in both before they are used)
+// at least 22 KiB; grouping's scratch, at most 89 KiB, lies in both before they are used)
 template <int EL, bool F8, int NT>
 int launch_few(const FewP& p, hipStream_t stream) {
     static bool ready1[64] = {false}, ready2[64] = {false};
@@ -598,9 +623,9 @@ int launch_few(const FewP& p, hipStream_t stream) {
     const int cus = device_cu_count();
     const int64_t items = most * (p.I / 8);
     const int grid1 = (int)std::min<int64_t>(items, cus), grid2 = std::min(p.blocks, cus);
-    const int64_t fix1 = (int64_t)2 * kFewWaves * NT * 1024 +
+    const int64_t fix1 = (int64_t)2 * kFewWaves * NT * 1024 + kFewWaves * 2048 +
                          (int64_t)few_table_ints(p.T, p.k, p.G, p.s) * 4;
-    const int64_t fix2 = (int64_t)kFewWaves * NT * 1024 + (2 + most) * 4 + (most * p.T + 1) / 2 * 4;
+    const int64_t fix2 = (int64_t)kFewWaves * NT * 1024 + kFewWaves * 2048 + (2 + most) * 4 + (most * p.T + 1) / 2 * 4;
     const int rows1 = (int)((kMmLds - fix1) / 16 * 16), rows2 = (int)((kMmLds - fix2) / 16 * 16);
     k1<<<grid1, kFewThreads, (size_t)(fix1 + rows1), stream>>>(p, rows1);
     if ((e = (int)hipGetLastError())) return e;
