@@ -42,8 +42,7 @@ struct FewP {
     int T, E, k, e0, E_loc, s, G, renorm;
     const uint8_t* x; uint32_t x_ld, x_bytes;                // bytes
     int H, I;
-    const uint8_t* w1[2]; const uint8_t* w2[2];              // routed groups, shared group
-    const float* s1[2]; const float* s2[2];
+    uint64_t w1, w1s, w2, w2s, s1, s1s, s2, s2s;             // addresses of weights and scales: routed groups, the shared one
     int act; float beta, limit;
     const float* b1; const float* b2;
     const uint16_t* res; size_t ld_res;
@@ -53,6 +52,7 @@ struct FewP {
     float* row_w;                                            // [R]
     int32_t* active;                                         // groups with rows, rows used, then the groups
     int16_t* rowmap;                                         // [active][T] row of a token in the group, -1
+    int cb8, cb6, cb4, cb2; float per_grid;                  // few_w1: items of 8, 6, 4, 2 outputs of a group; 1 / grid
     int blocks, cols;                                        // few_w2: blocks of `cols` (at most 16) columns
 };
 
@@ -63,7 +63,7 @@ template <bool F8, int NT, bool XL>
 struct FewGeom {
     static constexpr int NB = F8 ? 4 : 2;
     static constexpr int UK = F8 ? 128 : 64;
-    static constexpr int Ring = XL ? 4 : (NT == 1 ? 3 : 2);
+    static constexpr int Ring = XL ? (F8 && NT == 2 ? 3 : 4) : (NT == 1 ? 3 : 2);
 };
 template <bool F8, int NT, bool XL>
 struct FewSlot {
@@ -110,6 +110,23 @@ MOE_DEV f32x4 few_unit(const i32x4 (&a)[2], Piece&& piece) {
     return d;
 }
 
+// An address that is the same in the whole wave, as the compiler is to know too
+// (a resource in vector registers is a loop over lanes at every request).
+MOE_DEV const uint8_t* few_uniform(uint64_t a) {
+    return (const uint8_t*)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a) |
+                            (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32);
+}
+// Weights (or scales) of the groups, `bytes` a group and the shared one apart: scalars,
+// taken from the parameters once (a choice between two of those becomes a load
+// from a chosen address, and the parameters then live in scratch memory).
+struct FewGroups {
+    uint64_t at, shared;
+    size_t bytes;
+    int E_loc;
+    MOE_DEV FewGroups(uint64_t a, uint64_t s, size_t n, int e)
+        : at((uint64_t)few_uniform(a)), shared((uint64_t)few_uniform(s)), bytes(n), E_loc(__builtin_amdgcn_readfirstlane(e)) {}
+    MOE_DEV const uint8_t* of(int g) const { return (const uint8_t*)(g < E_loc ? at + (uint64_t)g * bytes : shared); }
+};
 MOE_DEV i32x4 few_load(const rsrc_t& r, uint32_t o) {
     return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
 }
@@ -146,55 +163,205 @@ MOE_DEV uint32_t few_koff_x(int u, int i, int q, int K) {
 // the sum of two offsets, past every resource if one of them is
 MOE_DEV uint32_t few_add(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
 
-// Routes the T tokens and groups their local assignments, by the whole
-// workgroup, into LDS. Returns the layout's tables.
-struct FewTables { int *sidx; float* sw; int *counts, *offsets, *row_src; float* row_w; int *slot, *active, *scratch; };
-
+// What a workgroup knows of the routing, in LDS. Rows are the local assignments in
+// the order of (token, choice), then the shared expert's tokens, so every
+// workgroup numbers them alike; active groups are in the order of their first row.
+struct FewTables {
+    int* idx; float* w;                                      // [T k] choices and weights
+    int *group, *cnt, *first;                                // [most] active groups, their rows, first member
+    int* member;                                             // [R] rows by group (in any order inside one)
+    int* token; float* row_w;                                // [R] of a row
+    int *of, *num;                                           // [G] place among the active groups; rows so far
+    int* wave;                                               // [3 x 16] sums of waves; [48] active, [49] rows, [50] rows of the longest
+};
+constexpr int kFewWaveInts = 52;
 __host__ __device__ inline size_t few_table_ints(int T, int k, int G, int s) {
-    const size_t R = (size_t)T * (k + s);
-    return 2 * (size_t)T * k + (size_t)G + (G + 1) + 2 * R + R + ((size_t)G < R ? G : R) + 2;
+    const size_t R = (size_t)T * (k + s), most = (size_t)G < R ? G : R;
+    return 2 * (size_t)T * k + 3 * most + 3 * R + 2 * (size_t)G + kFewWaveInts;
 }
-MOE_DEV FewTables few_tables(int* lds, int* scratch, int T, int k, int G, int s) {
-    const int R = T * (k + s);
+MOE_DEV FewTables few_tables(int* lds, int T, int k, int G, int s) {
+    const int R = T * (k + s), most = min(G, R);
     FewTables t;
-    t.sidx = lds; lds += T * k;
-    t.sw = (float*)lds; lds += T * k;
-    t.counts = lds; lds += G;
-    t.offsets = lds; lds += G + 1;
-    t.row_src = lds; lds += R;
+    t.idx = lds; lds += T * k;
+    t.w = (float*)lds; lds += T * k;
+    t.group = lds; lds += most;
+    t.cnt = lds; lds += most;
+    t.first = lds; lds += most;
+    t.member = lds; lds += R;
+    t.token = lds; lds += R;
     t.row_w = (float*)lds; lds += R;
-    t.slot = lds; lds += R;
-    t.active = lds;                                          // their number, the groups, rows of the longest
-    t.scratch = scratch;
+    t.of = lds; lds += G;
+    t.num = lds; lds += G;
+    t.wave = lds;
     return t;
 }
+// sum of the waves' values before this wave's, and of all
+MOE_DEV int few_before(const int* wave, int w, int& all) {
+    int run = 0;
+    all = 0;
+    #pragma unroll
+    for (int i = 0; i < kFewWaves; ++i) {
+        run += i < w ? wave[i] : 0;
+        all += wave[i];
+    }
+    return run;
+}
 
-// Returns the rows of the longest group.
-MOE_DEV int few_route(const FewP& p, const FewTables& t) {
-    if (p.E <= 64 && p.k <= 32) route_block<kFewWaves, 32, 2>(p.logits, p.T, p.E, p.k, p.renorm != 0, t.sidx, t.sw, nullptr, nullptr);
-    else if (p.E <= 256 && p.k <= 32) route_block<kFewWaves, 32, 8>(p.logits, p.T, p.E, p.k, p.renorm != 0, t.sidx, t.sw, nullptr, nullptr);
-    else if (p.E <= 512) route_block<kFewWaves, 64, 8>(p.logits, p.T, p.E, p.k, p.renorm != 0, t.sidx, t.sw, nullptr, nullptr);
-    else route_block<kFewWaves, 64, 32>(p.logits, p.T, p.E, p.k, p.renorm != 0, t.sidx, t.sw, nullptr, nullptr);
-    __syncthreads();
-    permute_in_block<kFewWaves>([&](int a) { return t.sidx[a]; }, [&](int a) { return t.sw[a]; }, p.T, p.k, p.e0, p.E_loc,
-                                p.s, t.counts, t.offsets, nullptr, t.row_src, t.row_w, t.slot, t.scratch);
-    __syncthreads();
-    // the groups with rows, in their order (at most one a row)
-    if (threadIdx.x < 64) {
-        const int lane = threadIdx.x;
-        int n = 0, most = 0;
-        for (int g0 = 0; g0 < p.G; g0 += 64) {
-            const int rows = g0 + lane < p.G ? t.counts[g0 + lane] : 0;
-            const uint64_t m = __ballot(rows > 0);
-            if (rows > 0) t.active[1 + n + __popcll(m & lanemask_lt(lane))] = g0 + lane;
-            n += __popcll(m);
-            most = max(most, rows);
+// The grouping of up to 64 N assignments by one wave, without barriers (every
+// instruction of a workgroup's 16 waves costs 16 cycles of a SIMD: the whole
+// workgroup's way, below, takes 1.8 us): lane l of slot i has assignment 64 i + l; the
+// lanes with the same group are found by a ballot per bit of its number.
+template <int N>
+MOE_DEV void few_group_wave(const FewP& p, const FewTables& t, int lane) {
+    const int Tk = p.T * p.k, all = Tk + p.s * p.T;
+    int g[N], tok[N], c[N], pos[N], ai[N], first[N];
+    uint64_t eq[N][N], rows[N], lead[N];
+    #pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int a = 64 * i + lane;
+        tok[i] = a < Tk ? a / p.k : a - Tk;
+        g[i] = -1;
+        if (a < Tk) {
+            const int e = t.idx[a] - p.e0;
+            if ((uint32_t)e < (uint32_t)p.E_loc) g[i] = e;
+        } else if (a < all) {
+            g[i] = p.E_loc;
         }
-        most = (int)wave_umax((uint32_t)most);
-        if (lane == 0) { t.active[0] = n; t.active[n + 1] = most; }
+        rows[i] = __ballot(g[i] >= 0);
+    }
+    #pragma unroll
+    for (int i = 0; i < N; ++i)
+        #pragma unroll
+        for (int j = 0; j < N; ++j) eq[i][j] = rows[j];
+    for (int b = 0; b < group_bits(p.G); ++b)
+        #pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const uint64_t m = __ballot((g[j] >> b) & 1);
+            #pragma unroll
+            for (int i = 0; i < N; ++i) eq[i][j] &= ((g[i] >> b) & 1) ? m : ~m;
+        }
+    int before = 0, n_act = 0, n_rows = 0, most = 0;
+    #pragma unroll
+    for (int i = 0; i < N; ++i) {
+        c[i] = pos[i] = 0;
+        #pragma unroll
+        for (int j = 0; j < N; ++j) {
+            c[i] += __popcll(eq[i][j]);
+            if (j < i) pos[i] += __popcll(eq[i][j]);
+        }
+        pos[i] += __popcll(eq[i][i] & lanemask_lt(lane));
+        lead[i] = __ballot(g[i] >= 0 && pos[i] == 0);
+        ai[i] = n_act + __popcll(lead[i] & lanemask_lt(lane));
+        n_act += __popcll(lead[i]);
+        const int mine = (lead[i] >> lane) & 1 ? c[i] : 0, inc = wave_incl_scan(mine);
+        first[i] = before + inc - mine;
+        before += __builtin_amdgcn_readlane(inc, 63);
+        most = max(most, (int)wave_umax((uint32_t)mine));
+    }
+    #pragma unroll
+    for (int i = 0; i < N; ++i) {
+        // the group's leader: the lowest lane of its first slot
+        int f = 0;
+        #pragma unroll
+        for (int j = N - 1; j >= 0; --j) {
+            const int v = __shfl(first[j], eq[i][j] ? __ffsll((unsigned long long)eq[i][j]) - 1 : 0, 64);
+            f = eq[i][j] ? v : f;
+        }
+        const int row = n_rows + __popcll(rows[i] & lanemask_lt(lane));
+        n_rows += __popcll(rows[i]);
+        if (g[i] >= 0) {
+            t.token[row] = tok[i];
+            t.row_w[row] = 64 * i + lane < Tk ? t.w[64 * i + lane] : 1.f;
+            t.member[f + pos[i]] = row;
+            if (pos[i] == 0) {
+                t.group[ai[i]] = g[i];
+                t.cnt[ai[i]] = c[i];
+                t.first[ai[i]] = f;
+            }
+        }
+    }
+    if (lane == 0) { t.wave[3 * kFewWaves] = n_act; t.wave[3 * kFewWaves + 1] = n_rows; t.wave[3 * kFewWaves + 2] = most; }
+}
+
+// Routes the T tokens and groups their local assignments, by the whole
+// workgroup; an assignment to a thread (T (k + s) <= 32 x 32).
+MOE_DEV void few_route(const FewP& p, const FewTables& t) {
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    for (int i = tid; i < p.G; i += kFewThreads) {
+        t.num[i] = 0;
+        t.of[i] = kFewThreads;
+    }
+    const bool r = p.renorm != 0;
+    if (p.E <= 64) route_block<kFewWaves, 32, 2>(p.logits, p.T, p.E, p.k, r, t.idx, t.w, nullptr, nullptr);
+    else if (p.E <= 256) route_block<kFewWaves, 32, 8>(p.logits, p.T, p.E, p.k, r, t.idx, t.w, nullptr, nullptr);
+    else if (p.E <= 512) route_block<kFewWaves, 64, 8>(p.logits, p.T, p.E, p.k, r, t.idx, t.w, nullptr, nullptr);
+    else route_block<kFewWaves, 64, 32>(p.logits, p.T, p.E, p.k, r, t.idx, t.w, nullptr, nullptr);
+    __syncthreads();
+    // thread a: assignment a of the routed ones, then the shared expert's tokens
+    const int Tk = p.T * p.k, all = Tk + p.s * p.T, a = tid;
+    if (all <= 128) {
+        if (w == 0) {
+            if (all <= 64) few_group_wave<1>(p, t, lane);
+            else few_group_wave<2>(p, t, lane);
+        }
+        __syncthreads();
+        return;
+    }
+    int g = -1, tok = 0, pos = 0;
+    float wt = 1.f;
+    if (a < Tk) {
+        tok = a / p.k;
+        wt = t.w[a];
+        const int e = t.idx[a] - p.e0;
+        g = (uint32_t)e < (uint32_t)p.E_loc ? e : -1;
+        if (g >= 0) {
+            pos = atomicAdd(t.num + g, 1);
+            atomicMin(t.of + g, a);
+        }
+    } else if (a < all) {
+        tok = pos = a - Tk;
+        g = p.E_loc;
+    }
+    if (tid == 0 && p.s) {
+        t.num[p.E_loc] = p.T;
+        t.of[p.E_loc] = Tk;
     }
     __syncthreads();
-    return __builtin_amdgcn_readfirstlane(t.active[t.active[0] + 1]);
+    // a group's first row in order speaks for it (pos goes by the atomics' order)
+    const bool leads = g >= 0 && t.of[g] == a;
+    const uint64_t rows = __ballot(g >= 0), lead = __ballot(leads);
+    if (lane == 0) { t.wave[w] = __popcll(rows); t.wave[kFewWaves + w] = __popcll(lead); }
+    __syncthreads();
+    int n_rows, n_act;
+    const int row = few_before(t.wave, w, n_rows) + __popcll(rows & lanemask_lt(lane));
+    const int ai = few_before(t.wave + kFewWaves, w, n_act) + __popcll(lead & lanemask_lt(lane));
+    if (g >= 0) {
+        t.token[row] = tok;
+        t.row_w[row] = wt;
+        if (leads) {
+            t.group[ai] = g;
+            t.of[g] = ai;
+        }
+    }
+    __syncthreads();
+    // first member of each active group: a scan of their rows, one group to a thread
+    const int c = tid < n_act ? t.num[t.group[tid]] : 0, inc = wave_incl_scan(c);
+    const int most = (int)wave_umax((uint32_t)c);
+    if (lane == 63) t.wave[2 * kFewWaves + w] = inc;
+    if (lane == 0) t.wave[w] = most;
+    __syncthreads();
+    if (tid < n_act) {
+        int n;
+        t.first[tid] = few_before(t.wave + 2 * kFewWaves, w, n) + inc - c;
+        t.cnt[tid] = c;
+    }
+    if (tid < 64) {
+        const int m = (int)wave_umax(lane < kFewWaves ? (uint32_t)t.wave[lane] : 0u);
+        if (lane == 0) { t.wave[3 * kFewWaves] = n_act; t.wave[3 * kFewWaves + 1] = n_rows; t.wave[3 * kFewWaves + 2] = m; }
+    }
+    __syncthreads();
+    if (g >= 0) t.member[t.first[t.of[g]] + pos] = row;
+    __syncthreads();
 }
 
 // One 16-bit row into LDS, zeros up to `bytes` (a multiple of 1 KiB): piece c of
@@ -229,7 +396,9 @@ MOE_DEV void few_turns(Slot (&ring)[RING], int steps, Step&& step) {
 template <bool F8>
 __host__ __device__ inline int few_row_lds(int units) { return (units + kFewWaves - 1) / kFewWaves * kFewWaves * (F8 ? 256 : 128) + 64; }
 
-template <int EL, bool F8, int NT, bool XL>
+// XL: token rows are read from LDS, all of them if ALL (staged by the caller), else
+// each group's in turn.
+template <int EL, bool F8, int NT, bool XL, bool ALL>
 MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* part, uint8_t* swap, uint8_t* rows) {
     using Geo = FewGeom<F8, NT, XL>;
     constexpr int RING = Geo::Ring;
@@ -238,49 +407,54 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
     const int q = lane >> 4, j = lane & 15;
     // items of `ob` outputs of a group (8, or fewer where that fills the grid's
     // last round better); a workgroup takes a contiguous run, so few groups
-    int ob = 8, least = 1 << 30;
-    #pragma unroll
-    for (int o = 8; o >= 2; o -= 2) {
-        const int rounds = (n_act * ((p.I + o - 1) / o) + (int)gridDim.x - 1) / (int)gridDim.x;
-        if (rounds * (o + 1) < least) { least = rounds * (o + 1); ob = o; }
-    }
-    const int cb = (p.I + ob - 1) / ob, n_items = n_act * cb;
-    const int first = (int)((int64_t)n_items * blockIdx.x / gridDim.x), end = (int)((int64_t)n_items * (blockIdx.x + 1) / gridDim.x);
+    int ob = 8, cb = __builtin_amdgcn_readfirstlane(p.cb8);
+    float least = ceilf((float)(n_act * cb) * p.per_grid) * 9.f;
+    auto consider = [&](int o, int c) __attribute__((always_inline)) {
+        const int n = __builtin_amdgcn_readfirstlane(c);
+        const float cost = ceilf((float)(n_act * n) * p.per_grid) * (float)(o + 1);
+        if (cost < least) { least = cost; ob = o; cb = n; }
+    };
+    consider(6, p.cb6);
+    consider(4, p.cb4);
+    consider(2, p.cb2);
+    ob = __builtin_amdgcn_readfirstlane(ob);
+    cb = __builtin_amdgcn_readfirstlane(cb);
+    const int n_items = n_act * cb, grid = gridDim.x, each = n_items / grid, more = n_items - each * grid;
+    const int first = (int)blockIdx.x * each + min((int)blockIdx.x, more), end = first + each + ((int)blockIdx.x < more ? 1 : 0);
     if (first >= end) return;
     const int wrow = p.H * (F8 ? 1 : 2);                     // bytes of a weight row
     const int units = (p.H + Geo::UK - 1) / Geo::UK, upw = (units + kFewWaves - 1) / kFewWaves;
     const int nsb = (2 * p.I + 127) >> 7, ksb = (p.H + 127) >> 7;
+    const FewGroups w_of(p.w1, p.w1s, (size_t)(2 * p.I) * (size_t)wrow, p.E_loc), s_of(p.s1, p.s1s, (size_t)(nsb * ksb) * 4, p.E_loc);
     const int stride = few_row_lds<F8>(units);
     const rsrc_t rx = make_rsrc(p.x, p.x_bytes);
     uint8_t* const ex = swap + w * 2048;
-    const int R1 = p.T * (p.k + p.s) - 1;
 
     // the loader: one unit after another through all items
-    struct { int item, i; bool live; const uint8_t* w; const float* s; uint32_t ro[2], sg, su, xo[NT]; } L;
+    struct { int ai, c, left, i; bool live; const uint8_t *w, *s; uint32_t ro[2], sg, su, xo[NT]; } L;
     auto open = [&]() __attribute__((always_inline)) {
         L.i = 0;
-        L.live = L.item < end;
-        const int item = L.live ? L.item : first;
-        const int ai = __builtin_amdgcn_readfirstlane(item / cb), c0 = (item - ai * cb) * ob;
-        const int g = __builtin_amdgcn_readfirstlane(tb.active[1 + ai]);
-        const int sh = g < p.E_loc ? 0 : 1, gi = sh ? 0 : g;
-        L.w = p.w1[sh] + (size_t)gi * (size_t)(2 * p.I) * (size_t)wrow;
+        L.live = L.left > 0;
+        const int ai = min(L.ai, n_act - 1), c0 = L.c * ob;
+        const int g = __builtin_amdgcn_readfirstlane(tb.group[ai]);
+        L.w = w_of.of(g);
         #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = 8 * h + (lane >> 3), o = 2 * (r >> 2) + (r & 1), col = c0 + o;
-            L.ro[h] = o < ob && col < p.I ? (uint32_t)(((r >> 1) & 1) * p.I + col) * (uint32_t)wrow : kMmNoRow;
+            const uint32_t at = (uint32_t)((r & 2 ? p.I : 0) + col) * (uint32_t)wrow;
+            L.ro[h] = (o < ob) & (col < p.I) ? at : kMmNoRow;
         }
         if constexpr (F8) {                                  // (an even column and the next one are of one block)
-            L.s = p.s1[sh] + (size_t)gi * nsb * ksb;
+            L.s = s_of.of(g);
             const int c = min(c0 + 2 * q, p.I - 2);
             L.sg = (uint32_t)((c >> 7) * ksb);
             L.su = (uint32_t)(((p.I + c) >> 7) * ksb);
         }
         if constexpr (!XL) {
-            const int lo = tb.offsets[g], n = tb.counts[g];
+            const int lo = tb.first[ai], n = tb.cnt[ai];
             #pragma unroll
             for (int t = 0; t < NT; ++t)
-                L.xo[t] = 16 * t + j < n ? (uint32_t)tb.row_src[min(lo + 16 * t + j, R1)] * p.x_ld : kMmNoRow;
+                L.xo[t] = 16 * t + j < n ? (uint32_t)tb.token[tb.member[lo + min(16 * t + j, n - 1)]] * p.x_ld : kMmNoRow;
         }
     };
     auto load = [&](FewSlot<F8, NT, XL>& S) __attribute__((always_inline)) {
@@ -301,25 +475,26 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
             S.sc[1] = __builtin_amdgcn_raw_buffer_load_b32(rs, (L.su + kb) * 4u, 0, 0);
         }
         if (++L.i == upw) {
-            ++L.item;
+            --L.left;
+            if (++L.c == cb) { L.c = 0; ++L.ai; }
             open();
         }
     };
     // the group's token rows into LDS; a wait for the requests and a barrier must follow
-    auto stage = [&](int g) __attribute__((always_inline)) {
-        const int lo = tb.offsets[g], n = tb.counts[g], chunks = stride / 1024;
-        for (int c = w; c < n * chunks; c += kFewWaves) {
-            const int r = c / chunks;
-            const int src = __builtin_amdgcn_readfirstlane(tb.row_src[lo + r]);
-            few_stage(rx, (uint32_t)src * p.x_ld, 2 * p.H, c - r * chunks, rows + r * stride, lane);
+    auto stage = [&](int ai) __attribute__((always_inline)) {
+        const int lo = tb.first[ai], n = tb.cnt[ai], chunks = stride / 1024;
+        for (int r = 0; r < n; ++r) {
+            const int tok = __builtin_amdgcn_readfirstlane(tb.token[tb.member[lo + r]]);
+            for (int c = w; c < chunks; c += kFewWaves) few_stage(rx, (uint32_t)tok * p.x_ld, 2 * p.H, c, rows + r * stride, lane);
         }
     };
 
-    int ai = first / cb, c8 = first - ai * cb, i = 0, left = end - first, turn = 0;
-    int g = __builtin_amdgcn_readfirstlane(tb.active[1 + ai]);
-    if constexpr (XL) stage(g);
+    int ai = __builtin_amdgcn_readfirstlane(first / cb), c8 = first - ai * cb, i = 0, left = end - first, turn = 0;
+    if constexpr (XL && !ALL) stage(ai);
     few_fence();
-    L.item = first;
+    L.ai = ai;
+    L.c = c8;
+    L.left = left;
     open();
     FewSlot<F8, NT, XL> ring[RING];
     static_for<RING>([&](auto s) __attribute__((always_inline)) { load(ring[decltype(s)::value]); });
@@ -329,9 +504,16 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
         bare_barrier();
     }
     const uint8_t* xrow[NT];
+    int g, lo, n;
     auto rows_of = [&]() __attribute__((always_inline)) {    // (lanes past the group's rows read its last: not stored)
+        g = __builtin_amdgcn_readfirstlane(tb.group[ai]);
+        lo = __builtin_amdgcn_readfirstlane(tb.first[ai]);
+        n = __builtin_amdgcn_readfirstlane(tb.cnt[ai]);
         #pragma unroll
-        for (int t = 0; t < NT; ++t) xrow[t] = rows + max(0, min(16 * t + j, tb.counts[g] - 1)) * stride;
+        for (int t = 0; t < NT; ++t) {
+            const int r = min(16 * t + j, n - 1);
+            xrow[t] = rows + (ALL ? tb.token[tb.member[lo + r]] : r) * stride;
+        }
     };
     rows_of();
     f32x4 acc[NT];
@@ -369,7 +551,7 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
         bare_barrier();
         // thread (tile, output of a pair, lane of the result): gate v, up v + 2
         const int e = threadIdx.x, t = e >> 7, v = (e >> 6) & 1, l = e & 63, r = 16 * t + (l & 15), o8 = 2 * (l >> 4) + v, c = ob * c8 + o8;
-        if (e < NT * 128 && o8 < ob && c < p.I && r < tb.counts[g]) {
+        if (e < NT * 128 && o8 < ob && c < p.I && r < n) {
             float z = 0.f, y = 0.f;
             #pragma unroll
             for (int x = 0; x < kFewWaves; ++x) {
@@ -383,7 +565,7 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
             z = epi_clamp(z, p.limit);
             float a = 0.f;
             with_act(p.act, [&](auto act) { a = epi_act<decltype(act)::value>(z, p.beta); });
-            const int row = tb.offsets[g] + r;
+            const int row = tb.member[lo + r];
             const float o = a * epi_clamp(y, p.limit) * tb.row_w[row];
             p.h[(size_t)row * p.I + c] = (uint16_t)pack16(o, 0.f, EL == kElF16);
         }
@@ -393,9 +575,8 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
         if (++c8 == cb && left > 0) {                                // the next group (every wave is past its products)
             c8 = 0;
             ++ai;
-            g = __builtin_amdgcn_readfirstlane(tb.active[1 + ai]);
-            if constexpr (XL) {
-                stage(g);
+            if constexpr (XL && !ALL) {
+                stage(ai);
                 few_fence();
                 __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
                 bare_barrier();
@@ -414,30 +595,42 @@ void few_w1_kernel(FewP p, int lds_rows) {
     float* const part = (float*)smem;                        // [2][16 waves][NT][4][64]
     uint8_t* const swap = smem + 2 * kFewWaves * NTM * 1024; // [16 waves][2 KiB]
     uint8_t* const rows = swap + kFewWaves * 2048;           // [lds_rows]
-    const FewTables tb = few_tables((int*)(rows + lds_rows), (int*)smem, p.T, p.k, p.G, p.s);   // (scratch: before the sums)
-    const int most = few_route(p, tb);
-    const int n_act = __builtin_amdgcn_readfirstlane(tb.active[0]);
+    const FewTables tb = few_tables((int*)(rows + lds_rows), p.T, p.k, p.G, p.s);
+    // the token rows, if all of them fit, are on their way while the tokens are routed
+    const int stride = few_row_lds<F8>((p.H + (F8 ? 127 : 63)) / (F8 ? 128 : 64));
+    const bool all = (int64_t)p.T * stride <= lds_rows;
+    if (all) {
+        const rsrc_t rx = make_rsrc(p.x, p.x_bytes);
+        const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), chunks = stride / 1024;
+        for (int t = 0; t < p.T; ++t)
+            for (int c = w; c < chunks; c += kFewWaves)
+                few_stage(rx, (uint32_t)t * p.x_ld, 2 * p.H, c, rows + t * stride, threadIdx.x & 63);
+    }
+    few_route(p, tb);
+    const int n_act = __builtin_amdgcn_readfirstlane(tb.wave[3 * kFewWaves]), R = tb.wave[3 * kFewWaves + 1];
+    const int most = __builtin_amdgcn_readfirstlane(tb.wave[3 * kFewWaves + 2]);
     if (blockIdx.x == gridDim.x - 1) {                       // for few_w2
         const int tid = threadIdx.x;
-        if (tid == 0) { p.active[0] = n_act; p.active[1] = tb.offsets[p.G]; }
-        for (int i = tid; i < n_act; i += kFewThreads) p.active[2 + i] = tb.active[1 + i];
-        for (int i = tid; i < p.T * (p.k + p.s); i += kFewThreads) p.row_w[i] = tb.row_w[i];
+        if (tid == 0) { p.active[0] = n_act; p.active[1] = R; }
+        for (int i = tid; i < n_act; i += kFewThreads) p.active[2 + i] = tb.group[i];
+        for (int i = tid; i < R; i += kFewThreads) p.row_w[i] = tb.row_w[i];
         for (int i = tid; i < n_act * p.T; i += kFewThreads) {
-            const int g = tb.active[1 + i / p.T], t = i % p.T;
+            const int a = i / p.T, t = i - a * p.T;
             int row = -1;
-            for (int r = tb.offsets[g]; r < tb.offsets[g] + tb.counts[g]; ++r) row = tb.row_src[r] == t ? r : row;
+            for (int m = tb.first[a]; m < tb.first[a] + tb.cnt[a]; ++m) row = tb.token[tb.member[m]] == t ? tb.member[m] : row;
             p.rowmap[i] = (int16_t)row;
         }
     }
     // the longest group decides: one tile of 16 rows or two, rows in LDS where they fit
-    const int stride = few_row_lds<F8>((p.H + (F8 ? 127 : 63)) / (F8 ? 128 : 64));
     const bool fit = (int64_t)most * stride <= lds_rows;
     if (TWO && most > 16) {
-        if (fit) few_w1_body<EL, F8, NTM, true>(p, tb, n_act, part, swap, rows);
-        else few_w1_body<EL, F8, NTM, false>(p, tb, n_act, part, swap, rows);
+        if (all) few_w1_body<EL, F8, NTM, true, true>(p, tb, n_act, part, swap, rows);
+        else if (fit) few_w1_body<EL, F8, NTM, true, false>(p, tb, n_act, part, swap, rows);
+        else few_w1_body<EL, F8, NTM, false, false>(p, tb, n_act, part, swap, rows);
     } else {
-        if (fit) few_w1_body<EL, F8, 1, true>(p, tb, n_act, part, swap, rows);
-        else few_w1_body<EL, F8, 1, false>(p, tb, n_act, part, swap, rows);
+        if (all) few_w1_body<EL, F8, 1, true, true>(p, tb, n_act, part, swap, rows);
+        else if (fit) few_w1_body<EL, F8, 1, true, false>(p, tb, n_act, part, swap, rows);
+        else few_w1_body<EL, F8, 1, false, false>(p, tb, n_act, part, swap, rows);
     }
 }
 
@@ -453,6 +646,7 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
     const int upg = (p.I + Geo::UK - 1) / Geo::UK;           // units of a group
     const int units = n_act * upg;
     const int nsb = (p.H + 127) >> 7, ksb = (p.I + 127) >> 7;
+    const FewGroups w_of(p.w2, p.w2s, (size_t)p.H * (size_t)wrow, p.E_loc), s_of(p.s2, p.s2s, (size_t)(nsb * ksb) * 4, p.E_loc);
     const int stride = (upg * (F8 ? 256 : 128) + 1023) / 1024 * 1024 + 64;
     uint8_t* const ex = swap + w * 2048;
     const int upw = max(1, (units + kFewWaves - 1) / kFewWaves);      // rounds of units of a block of columns
@@ -476,8 +670,7 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
     auto load = [&](FewSlot<F8, NT, XL>& S) __attribute__((always_inline)) {
         const bool live = L.live && L.ai < n_act;
         const int g = live ? __builtin_amdgcn_readfirstlane(active[L.ai]) : 0;
-        const int sh = g < p.E_loc ? 0 : 1, gi = sh ? 0 : g;
-        const rsrc_t rw = make_rsrc(p.w2[sh] + (size_t)gi * (size_t)p.H * (size_t)wrow, live ? (uint32_t)p.H * (uint32_t)wrow : 0u);
+        const rsrc_t rw = make_rsrc(w_of.of(g), live ? (uint32_t)p.H * (uint32_t)wrow : 0u);
         #pragma unroll
         for (int h = 0; h < 2; ++h) S.a[h] = few_load_w(rw, few_add(L.ro[h], few_koff_w<F8>(L.ku, lane, p.I)));
         #pragma unroll
@@ -493,7 +686,7 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
             }
         }
         if constexpr (F8) {
-            const rsrc_t rs = make_rsrc(p.s2[sh] + (size_t)gi * nsb * ksb, live ? (uint32_t)(nsb * ksb) * 4u : 0u);
+            const rsrc_t rs = make_rsrc(s_of.of(g), live ? (uint32_t)(nsb * ksb) * 4u : 0u);
             S.sc[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, (L.sb + L.ku) * 4, 0, 0);
         }
         L.ku += kFewWaves;
@@ -559,9 +752,11 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
             #pragma unroll
             for (int x = 0; x < kFewWaves; ++x) o += part[(x * NT + (t >> 4)) * 256 + (c & 3) * 64 + (c >> 2) * 16 + (t & 15)];
             if (p.b2) {
+                #pragma unroll 8
                 for (int a = 0; a < n_act; ++a) {
                     const int row = map[a * p.T + t];
-                    if (row >= 0) o = fmaf(p.row_w[row], p.b2[(size_t)active[a] * p.H + n], o);
+                    const float y = fmaf(p.row_w[max(row, 0)], p.b2[(size_t)active[a] * p.H + n], o);
+                    o = row >= 0 ? y : o;
                 }
             }
             if (p.res) o += lo16(p.res[(size_t)t * p.ld_res + n], EL == kElF16);
@@ -610,10 +805,9 @@ int few_ready(K* k, bool (&ready)[64]) {
     return 0;
 }
 
-// LDS left for token rows: a compute unit's, less the sums and the tables (few_w1:
-// at least 22 KiB; grouping's scratch, at most 89 KiB, lies in both before they are used)
+// LDS left for token rows: a compute unit's, less the sums and the tables
 template <int EL, bool F8, int NT>
-int launch_few(const FewP& p, hipStream_t stream) {
+int launch_few(FewP& p, hipStream_t stream) {
     static bool ready1[64] = {false}, ready2[64] = {false};
     auto* k1 = &few_w1_kernel<EL, F8, NT == 2>;
     auto* k2 = &few_w2_kernel<EL, F8, NT>;
@@ -627,6 +821,8 @@ int launch_few(const FewP& p, hipStream_t stream) {
                          (int64_t)few_table_ints(p.T, p.k, p.G, p.s) * 4;
     const int64_t fix2 = (int64_t)kFewWaves * NT * 1024 + kFewWaves * 2048 + (2 + most) * 4 + (most * p.T + 1) / 2 * 4;
     const int rows1 = (int)((kMmLds - fix1) / 16 * 16), rows2 = (int)((kMmLds - fix2) / 16 * 16);
+    p.cb8 = p.I / 8; p.cb6 = (p.I + 5) / 6; p.cb4 = p.I / 4; p.cb2 = p.I / 2;
+    p.per_grid = 1.0f / (float)grid1;
     k1<<<grid1, kFewThreads, (size_t)(fix1 + rows1), stream>>>(p, rows1);
     if ((e = (int)hipGetLastError())) return e;
     k2<<<grid2, kFewThreads, (size_t)(fix2 + rows2), stream>>>(p, rows2, (int)most);
@@ -673,10 +869,10 @@ int moe_launch_few(const moe_few_args& a, void* ws, hipStream_t stream) {
     p.G = p.E_loc + p.s; p.renorm = (a.flags & MOE_ROUTE_RENORM) != 0;
     p.x = (const uint8_t*)a.x; p.x_ld = (uint32_t)a.ldx * 2; p.x_bytes = (uint32_t)(a.T - 1) * p.x_ld + (uint32_t)a.H * 2;
     p.H = a.H; p.I = a.I;
-    p.w1[0] = (const uint8_t*)a.w1; p.w1[1] = (const uint8_t*)a.shared_w1;
-    p.w2[0] = (const uint8_t*)a.w2; p.w2[1] = (const uint8_t*)a.shared_w2;
-    p.s1[0] = a.w1_scales; p.s1[1] = a.shared_w1_scales;
-    p.s2[0] = a.w2_scales; p.s2[1] = a.shared_w2_scales;
+    p.w1 = (uint64_t)a.w1; p.w1s = (uint64_t)a.shared_w1;
+    p.w2 = (uint64_t)a.w2; p.w2s = (uint64_t)a.shared_w2;
+    p.s1 = (uint64_t)a.w1_scales; p.s1s = (uint64_t)a.shared_w1_scales;
+    p.s2 = (uint64_t)a.w2_scales; p.s2s = (uint64_t)a.shared_w2_scales;
     p.act = a.epi ? a.epi->act : MOE_ACT_SWIGLU; p.beta = a.epi ? a.epi->beta : 1.0f; p.limit = a.epi ? a.epi->limit : 0.0f;
     p.b1 = a.epi ? a.epi->bias : nullptr; p.b2 = a.bias2;
     p.res = (const uint16_t*)a.residual; p.ld_res = (size_t)a.ld_res;
