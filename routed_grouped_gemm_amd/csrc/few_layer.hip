@@ -6,14 +6,17 @@
 //           experts that have tokens, [g | u] = x[src r] W1_g^T + b1_g
 //   few_w2  out[t] = residual[t] + sum over t's rows r of (h[r] W2_g^T + w_r b2_g)
 //
-// Bound by the weights of the active experts, read once. Both kernels give 16
-// rows of weights to a workgroup of 8 waves, which split the reduction axis:
-// unit i (128 bytes of each row, so that the eight take 1 KiB of a row side by
-// side) goes to wave i % 8. A lane's 16 bytes are its operand of the 16x16x32
-// matrix instruction as they come (any order of k serves if both operands have
-// it), so weights pass through registers alone, with two batches of units in
-// flight in each wave and no barrier but the one that joins the eight waves'
-// sums. E4M3 codes become 16-bit values exactly, the scale of a unit's 128
+// Bound by the weights of the active experts, read once. In both kernels a
+// workgroup of 16 waves, one on a compute unit, walks over 16 rows of weights at
+// a time; the waves split the reduction axis: unit i (128 bytes of each of the 16
+// rows) goes to wave i % 16 (few_w1: i % split, 16 / split runs of rows at once,
+// so that a wave has some units before each barrier). A wave keeps four units in
+// flight (128 KiB in a compute unit) and requests whole lines, 8 lanes a row: with
+// 4 lanes a row, the layout of the matrix instruction's operand, the same bytes
+// took a quarter longer. The operand's layout is made by passing a unit through 2
+// KiB of LDS a wave. The other operand, the token rows or h, is in LDS where it
+// fits (all tokens, or the rows of a group at a time), else loaded with the
+// weights. E4M3 codes become 16-bit values exactly; the scale of a unit's 128
 // columns multiplies its fp32 sums.
 //
 // few_w1's 16 rows are 8 of the gate and the same 8 of the up projection, in
@@ -23,9 +26,13 @@
 // with 0: another token's infinities stay out), so the sum over experts stays in
 // fp32 registers and nothing has to be combined afterwards.
 //
-// Measured: one token on 6 of 64 experts of 2048 x 1408 in BF16 (104 MB) 36 us;
-// 16 tokens on 32 local experts of 256, 7168 x 2048 in E4M3 (about 560 MB) 146
-// us; 8 tokens on 9 experts of 512 x 264 22 us, host time.
+// Measured (a plain read of memory: 6.9 TB/s): one token on 6 of 64 experts of
+// 2048 x 1408 in BF16 (104 MB) 28 us, of which the weights stream for 14 at 7
+// TB/s; the rest is the start of two kernels (routing 2, grouping 1, first
+// requests 3, the second's tables and first requests 3). 16 tokens on 12 of 32
+// local experts of 7168 x 2048 in E4M3 (528 MB) 95 us, on 16 in BF16 (1.4 GB) 214
+// us, 6.6 TB/s. 32 tokens on 21 of them in BF16 308 us, E4M3 206 us (h does not
+// fit LDS). 8 tokens on 8 experts of 4096 x 4096 128 us, 6.3 TB/s.
 #include <algorithm>
 
 #include "epilogue_act.h"
@@ -52,7 +59,8 @@ struct FewP {
     float* row_w;                                            // [R]
     int32_t* active;                                         // groups with rows, rows used, then the groups
     int16_t* rowmap;                                         // [active][T] row of a token in the group, -1
-    int cb8, cb6, cb4, cb2; float per_grid;                  // few_w1: items of 8, 6, 4, 2 outputs of a group; 1 / grid
+    int split;                                               // few_w1: waves that share 16 weight rows
+    int cb8, cb6, cb4, cb2; float per_grid;                  // items of a group with 8, 6, 4, 2 outputs for every `split` waves; 1 / grid
     int blocks, cols;                                        // few_w2: blocks of `cols` (at most 16) columns
 };
 
@@ -394,24 +402,27 @@ MOE_DEV void few_turns(Slot (&ring)[RING], int steps, Step&& step) {
 // ------------------------------------------------------------------ few_w1
 // bytes of a token row in LDS: all units of all waves, and 64 so that rows start in other banks
 template <bool F8>
-__host__ __device__ inline int few_row_lds(int units) { return (units + kFewWaves - 1) / kFewWaves * kFewWaves * (F8 ? 256 : 128) + 64; }
+__host__ __device__ inline int few_row_lds(int units, int split) { return ((units + split - 1) / split * split * (F8 ? 256 : 128) + 1023) / 1024 * 1024 + 64; }
 
-// XL: token rows are read from LDS, all of them if ALL (staged by the caller), else
-// each group's in turn.
+// The items of `n_list` active groups (list: their places among the active ones;
+// NULL: all). XL: token rows are read from LDS, all of them if ALL (staged by the
+// caller), else each group's in turn.
 template <int EL, bool F8, int NT, bool XL, bool ALL>
-MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* part, uint8_t* swap, uint8_t* rows) {
+MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, const int* list, int n_list, float* part, uint8_t* swap, uint8_t* rows) {
     using Geo = FewGeom<F8, NT, XL>;
     constexpr int RING = Geo::Ring;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int q = lane >> 4, j = lane & 15;
-    // items of `ob` outputs of a group (8, or fewer where that fills the grid's
-    // last round better); a workgroup takes a contiguous run, so few groups
+    // an item is `subs` times `ob` outputs of a group, each by `split` waves: 8, or
+    // fewer where that fills the grid's last round better; a workgroup takes a
+    // contiguous run of items, so few groups
+    const int split = p.split, subs = kFewWaves / split, sub = w / split, wk = w - sub * split;
     int ob = 8, cb = __builtin_amdgcn_readfirstlane(p.cb8);
-    float least = ceilf((float)(n_act * cb) * p.per_grid) * 9.f;
+    float least = ceilf((float)(n_list * cb) * p.per_grid) * 9.f;
     auto consider = [&](int o, int c) __attribute__((always_inline)) {
         const int n = __builtin_amdgcn_readfirstlane(c);
-        const float cost = ceilf((float)(n_act * n) * p.per_grid) * (float)(o + 1);
+        const float cost = ceilf((float)(n_list * n) * p.per_grid) * (float)(o + 1);
         if (cost < least) { least = cost; ob = o; cb = n; }
     };
     consider(6, p.cb6);
@@ -419,14 +430,16 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
     consider(2, p.cb2);
     ob = __builtin_amdgcn_readfirstlane(ob);
     cb = __builtin_amdgcn_readfirstlane(cb);
-    const int n_items = n_act * cb, grid = gridDim.x, each = n_items / grid, more = n_items - each * grid;
+    const int wide = ob * subs;                              // outputs of an item
+    const int n_items = n_list * cb, grid = gridDim.x, each = n_items / grid, more = n_items - each * grid;
     const int first = (int)blockIdx.x * each + min((int)blockIdx.x, more), end = first + each + ((int)blockIdx.x < more ? 1 : 0);
     if (first >= end) return;
     const int wrow = p.H * (F8 ? 1 : 2);                     // bytes of a weight row
-    const int units = (p.H + Geo::UK - 1) / Geo::UK, upw = (units + kFewWaves - 1) / kFewWaves;
+    const int units = (p.H + Geo::UK - 1) / Geo::UK, upw = (units + split - 1) / split;
     const int nsb = (2 * p.I + 127) >> 7, ksb = (p.H + 127) >> 7;
     const FewGroups w_of(p.w1, p.w1s, (size_t)(2 * p.I) * (size_t)wrow, p.E_loc), s_of(p.s1, p.s1s, (size_t)(nsb * ksb) * 4, p.E_loc);
-    const int stride = few_row_lds<F8>(units);
+    const int stride = few_row_lds<F8>(units, split);
+    auto place = [&](int i) __attribute__((always_inline)) { return list ? __builtin_amdgcn_readfirstlane(list[i]) : i; };
     const rsrc_t rx = make_rsrc(p.x, p.x_bytes);
     uint8_t* const ex = swap + w * 2048;
 
@@ -435,7 +448,7 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
     auto open = [&]() __attribute__((always_inline)) {
         L.i = 0;
         L.live = L.left > 0;
-        const int ai = min(L.ai, n_act - 1), c0 = L.c * ob;
+        const int ai = place(min(L.ai, n_list - 1)), c0 = L.c * wide + sub * ob;
         const int g = __builtin_amdgcn_readfirstlane(tb.group[ai]);
         L.w = w_of.of(g);
         #pragma unroll
@@ -459,7 +472,7 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
     };
     auto load = [&](FewSlot<F8, NT, XL>& S) __attribute__((always_inline)) {
         const rsrc_t rw = make_rsrc(L.w, L.live ? (uint32_t)(2 * p.I) * (uint32_t)wrow : 0u);
-        const int u = L.i * kFewWaves + w;
+        const int u = L.i * split + wk;
         #pragma unroll
         for (int h = 0; h < 2; ++h) S.a[h] = few_load_w(rw, few_add(L.ro[h], few_koff_w<F8>(u, lane, p.H)));
         if constexpr (!XL) {
@@ -481,8 +494,8 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
         }
     };
     // the group's token rows into LDS; a wait for the requests and a barrier must follow
-    auto stage = [&](int ai) __attribute__((always_inline)) {
-        const int lo = tb.first[ai], n = tb.cnt[ai], chunks = stride / 1024;
+    auto stage = [&](int i) __attribute__((always_inline)) {
+        const int ai = place(i), lo = tb.first[ai], n = tb.cnt[ai], chunks = stride / 1024;
         for (int r = 0; r < n; ++r) {
             const int tok = __builtin_amdgcn_readfirstlane(tb.token[tb.member[lo + r]]);
             for (int c = w; c < chunks; c += kFewWaves) few_stage(rx, (uint32_t)tok * p.x_ld, 2 * p.H, c, rows + r * stride, lane);
@@ -506,9 +519,10 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
     const uint8_t* xrow[NT];
     int g, lo, n;
     auto rows_of = [&]() __attribute__((always_inline)) {    // (lanes past the group's rows read its last: not stored)
-        g = __builtin_amdgcn_readfirstlane(tb.group[ai]);
-        lo = __builtin_amdgcn_readfirstlane(tb.first[ai]);
-        n = __builtin_amdgcn_readfirstlane(tb.cnt[ai]);
+        const int a = place(ai);
+        g = __builtin_amdgcn_readfirstlane(tb.group[a]);
+        lo = __builtin_amdgcn_readfirstlane(tb.first[a]);
+        n = __builtin_amdgcn_readfirstlane(tb.cnt[a]);
         #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int r = min(16 * t + j, n - 1);
@@ -520,7 +534,7 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
     #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto step = [&](FewSlot<F8, NT, XL>& S) __attribute__((always_inline)) {
-        const int u = i * kFewWaves + w;
+        const int u = i * split + wk;
         float sc[2] = {1.f, 1.f};
         if constexpr (F8) {
             sc[0] = __uint_as_float(S.sc[0]);
@@ -549,14 +563,16 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, int n_act, float* p
             for (int v = 0; v < 4; ++v) mine[(w * NT + t) * 256 + v * 64 + lane] = acc[t][v];
         __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
         bare_barrier();
-        // thread (tile, output of a pair, lane of the result): gate v, up v + 2
-        const int e = threadIdx.x, t = e >> 7, v = (e >> 6) & 1, l = e & 63, r = 16 * t + (l & 15), o8 = 2 * (l >> 4) + v, c = ob * c8 + o8;
-        if (e < NT * 128 && o8 < ob && c < p.I && r < n) {
+        // thread (part of the item, tile, output of a pair, lane of the result): gate v, up v + 2
+        const int e = threadIdx.x, m = e / (NT * 128), t = (e >> 7) & (NT - 1), v = (e >> 6) & 1, l = e & 63;
+        const int r = 16 * t + (l & 15), o8 = 2 * (l >> 4) + v, c = wide * c8 + m * ob + o8;
+        if (m < subs && o8 < ob && c < p.I && r < n) {
+            const float* const src = mine + (m * split * NT + t) * 256 + v * 64 + l;
             float z = 0.f, y = 0.f;
-            #pragma unroll
-            for (int x = 0; x < kFewWaves; ++x) {
-                z += mine[(x * NT + t) * 256 + v * 64 + l];
-                y += mine[(x * NT + t) * 256 + (v + 2) * 64 + l];
+            #pragma unroll 4
+            for (int x = 0; x < split; ++x) {
+                z += src[x * (NT * 256)];
+                y += src[x * (NT * 256) + 128];
             }
             if (p.b1) {
                 z += p.b1[(size_t)g * 2 * p.I + c];
@@ -597,7 +613,7 @@ void few_w1_kernel(FewP p, int lds_rows) {
     uint8_t* const rows = swap + kFewWaves * 2048;           // [lds_rows]
     const FewTables tb = few_tables((int*)(rows + lds_rows), p.T, p.k, p.G, p.s);
     // the token rows, if all of them fit, are on their way while the tokens are routed
-    const int stride = few_row_lds<F8>((p.H + (F8 ? 127 : 63)) / (F8 ? 128 : 64));
+    const int stride = few_row_lds<F8>((p.H + (F8 ? 127 : 63)) / (F8 ? 128 : 64), p.split);
     const bool all = (int64_t)p.T * stride <= lds_rows;
     if (all) {
         const rsrc_t rx = make_rsrc(p.x, p.x_bytes);
@@ -621,17 +637,37 @@ void few_w1_kernel(FewP p, int lds_rows) {
             p.rowmap[i] = (int16_t)row;
         }
     }
-    // the longest group decides: one tile of 16 rows or two, rows in LDS where they fit
-    const bool fit = (int64_t)most * stride <= lds_rows;
-    if (TWO && most > 16) {
-        if (all) few_w1_body<EL, F8, NTM, true, true>(p, tb, n_act, part, swap, rows);
-        else if (fit) few_w1_body<EL, F8, NTM, true, false>(p, tb, n_act, part, swap, rows);
-        else few_w1_body<EL, F8, NTM, false, false>(p, tb, n_act, part, swap, rows);
-    } else {
-        if (all) few_w1_body<EL, F8, 1, true, true>(p, tb, n_act, part, swap, rows);
-        else if (fit) few_w1_body<EL, F8, 1, true, false>(p, tb, n_act, part, swap, rows);
-        else few_w1_body<EL, F8, 1, false, false>(p, tb, n_act, part, swap, rows);
+    // groups whose rows fit LDS, then the others (one tile of 16 rows, or two as the longest group has)
+    if (all) {
+        if (TWO && most > 16) few_w1_body<EL, F8, NTM, true, true>(p, tb, nullptr, n_act, part, swap, rows);
+        else few_w1_body<EL, F8, 1, true, true>(p, tb, nullptr, n_act, part, swap, rows);
+        return;
     }
+    const int cap = min(lds_rows / stride, 16);
+    if (most <= cap) {
+        few_w1_body<EL, F8, 1, true, false>(p, tb, nullptr, n_act, part, swap, rows);
+        return;
+    }
+    int* const list = tb.idx;                                // (the choices are not needed any more)
+    if (threadIdx.x < 64) {
+        const int lane = threadIdx.x;
+        int n = 0;
+        for (int big = 0; big < 2; ++big) {
+            for (int a0 = 0; a0 < n_act; a0 += 64) {
+                const bool in = a0 + lane < n_act && (tb.cnt[a0 + lane] > cap) == (big != 0);
+                const uint64_t m = __ballot(in);
+                if (in) list[n + __popcll(m & lanemask_lt(lane))] = a0 + lane;
+                n += __popcll(m);
+            }
+            if (big == 0 && lane == 0) tb.wave[0] = n;
+        }
+    }
+    __syncthreads();
+    const int small = __builtin_amdgcn_readfirstlane(tb.wave[0]);
+    few_w1_body<EL, F8, 1, true, false>(p, tb, list, small, part, swap, rows);
+    __syncthreads();                                         // (the sums' places are used again)
+    if (TWO && most > 16) few_w1_body<EL, F8, NTM, false, false>(p, tb, list + small, n_act - small, part, swap, rows);
+    else few_w1_body<EL, F8, 1, false, false>(p, tb, list + small, n_act - small, part, swap, rows);
 }
 
 // ------------------------------------------------------------------ few_w2
@@ -821,7 +857,13 @@ int launch_few(FewP& p, hipStream_t stream) {
                          (int64_t)few_table_ints(p.T, p.k, p.G, p.s) * 4;
     const int64_t fix2 = (int64_t)kFewWaves * NT * 1024 + kFewWaves * 2048 + (2 + most) * 4 + (most * p.T + 1) / 2 * 4;
     const int rows1 = (int)((kMmLds - fix1) / 16 * 16), rows2 = (int)((kMmLds - fix2) / 16 * 16);
-    p.cb8 = p.I / 8; p.cb6 = (p.I + 5) / 6; p.cb4 = p.I / 4; p.cb2 = p.I / 2;
+    // about four units of the reduction axis to a wave: a barrier and an epilogue
+    // for every unit cost more than they are worth (16 tokens on 51 experts of 2048
+    // x 1408 in E4M3, 16 units: 110 us with all 16 waves on a row, 103 with 4)
+    const int units = (p.H + (F8 ? 127 : 63)) / (F8 ? 128 : 64), subs = units >= 48 ? 1 : (units >= 24 ? 2 : 4);
+    p.split = kFewWaves / subs;
+    p.cb8 = (p.I + 8 * subs - 1) / (8 * subs); p.cb6 = (p.I + 6 * subs - 1) / (6 * subs);
+    p.cb4 = (p.I + 4 * subs - 1) / (4 * subs); p.cb2 = (p.I + 2 * subs - 1) / (2 * subs);
     p.per_grid = 1.0f / (float)grid1;
     k1<<<grid1, kFewThreads, (size_t)(fix1 + rows1), stream>>>(p, rows1);
     if ((e = (int)hipGetLastError())) return e;

@@ -274,3 +274,21 @@ def test_captured_and_on_two_streams():
     torch.cuda.synchronize()
     for pair in got:
         assert torch.equal(pair[0], want[0]) and torch.equal(pair[1], want[1])
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("T,E,k,H,I", [(32, 64, 2, 7168, 64), (12, 64, 2, 16384, 48), (20, 40, 1, 5120, 40), (3, 8, 2, 40000, 16)])
+def test_groups_that_fit_lds_beside_groups_that_do_not(eight, T, E, k, H, I):
+    """Long rows and a shared expert of all tokens: some groups' rows are staged, others read from memory."""
+    H, I = (H // 16 * 16, -(-I // 16) * 16) if eight else (H, I)
+    c = Case(T=T, E=E, k=k, e0=0, E_loc=E, H=H, I=I, eight=eight, shared=True, bias=True, residual=True, seed=T + eight)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("H", [64, 520, 1032, 2048, 2064, 4104])
+@pytest.mark.parametrize("eight", [False, True])
+def test_rows_split_among_waves(H, eight):
+    """Every number of waves that share a row, with units past the row's end."""
+    H = -(-H // 16) * 16 if eight else H
+    c = Case(T=6, E=24, k=3, e0=3, E_loc=17, H=H, I=304, eight=eight, renorm=True, residual=True, seed=H)
+    c.check(c.run())
