@@ -922,10 +922,17 @@ void grouped_mm_kernel(MmP p) {
                 if (lead) wait_for(std::integral_constant<int, (NST - 1) * (L1 + KEPT + L2)>{});
                 // (writes to LDS are done before the barrier)
                 if constexpr (mm_kind(MODE) == kWgrad8 && h == 0) __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-                bare_barrier();
+                // (an epilogue's item ends with this barrier apart, below)
+                if (EPI == kEpiNone || h == 0 || kt + 1 < c.nk) bare_barrier();
             });
             --stored;
         }
+        // The halves are half a turn apart: behind this barrier waves 4-7 still
+        // have their last products to form. They run their epilogue before the
+        // barrier that follows those, so both halves' epilogues run side by side
+        // (in turn, each held up the other half's products: the gradient of 24576
+        // x 1408 x 2048 PENDING us).
+        if (EPI != kEpiNone && lead) bare_barrier();
         if constexpr (EL == kElFp8) {
             #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -955,6 +962,7 @@ void grouped_mm_kernel(MmP p) {
                 store(c, same, no, no);
             }
         }
+        if (EPI != kEpiNone && !lead) bare_barrier();
     }
     if (lead) bare_barrier();
 }
