@@ -50,12 +50,25 @@ struct MmP {
     uint8_t* h;
     float* dw_part; float* dw;                               // partial row sums [16- or 64-column parts][R_max]
     int gated;
+    // the part of the output that a launch computes: `at` tiles of columns from
+    // col0; of a single group all rows (row_part 0), those of whole passes of
+    // row_tile rows (1) or the rest (2)
+    int col0, at, row_part, row_tile, dw_slot0;
 };
 
 // Rows [lo, hi) of group g, held inside [0, R_max) whatever the offsets say.
 MOE_DEV void group_rows(const MmP& p, int g, int& lo, int& hi) {
     lo = min(max(p.offsets[g], 0), p.R_max);
     hi = min(max(p.offsets[g + 1], lo), p.R_max);
+}
+// The rows of it that a launch of a product with an epilogue computes.
+template <bool EPI>
+MOE_DEV void part_rows(const MmP& p, int& lo, int& hi) {
+    if constexpr (EPI) {
+        const int rest = p.row_part ? (hi - lo) % p.row_tile : 0;
+        if (p.row_part == 1) hi -= rest;
+        if (p.row_part == 2) lo = hi - rest;
+    }
 }
 
 // The same of one group for the whole wave, by scalar loads: waiting for a
@@ -169,11 +182,13 @@ MOE_DEV MmItem mm_scalar(const MmItem& c) {
 // Rows are below 2^29 and a pass is 32 or more, so 64 groups' passes fit 32
 // bits; the items of all do wherever y is an array that exists, but groups that
 // overlap (offsets that do not ascend) can have more: then there are none.
+template <bool EPI = false>
 MOE_DEV void mm_passes(const MmP& p, int bt, int per, int lane, int* pass_off) {
     int64_t run = 0;
     for (int g0 = 0; g0 < p.G; g0 += 64) {
         int lo = 0, hi = 0;
         if (g0 + lane < p.G) group_rows(p, g0 + lane, lo, hi);
+        part_rows<EPI>(p, lo, hi);
         const int n = (hi - lo + bt - 1) / bt;
         const int inc = wave_incl_scan(n);
         if (g0 + lane < p.G) pass_off[g0 + lane] = (int)run + inc - n;
@@ -228,7 +243,7 @@ MOE_DEV int mm_nth(int round, const MmWhere& wh) {
 }
 
 // work item number `item`: tiles of AT values of the a axis (at of them), BT of the b axis
-template <int EL, int MODE, int BT, int AT = kATile>
+template <int EL, int MODE, int BT, int AT = kATile, bool EPI = false>
 MOE_DEV MmItem mm_decode(const MmP& p, const MmTables& tb, int at, int item) {
     constexpr int KT = EL == kElFp8 ? 128 : 64;
     MmItem c;
@@ -259,13 +274,14 @@ MOE_DEV MmItem mm_decode(const MmP& p, const MmTables& tb, int at, int item) {
         bt = __builtin_amdgcn_readfirstlane(tb.at[c.g + 1]) - first;
         l = item - first * at;
         group_rows_scalar(p, c.g, lo, hi);
+        part_rows<EPI>(p, lo, hi);
     }
     // bands of four b tiles, b fastest: the items that run together on one
     // XCD share operands in its L2
     const int band = l / (4 * at), h = min(4, bt - 4 * band), l2 = l - band * 4 * at;
     // (scalar registers: a descriptor built from them must not look divergent)
     const int ai = __builtin_amdgcn_readfirstlane(l2 / h);
-    c.a0 = ai * AT;
+    c.a0 = ai * AT + (EPI ? p.col0 : 0);
     c.b0 = (4 * __builtin_amdgcn_readfirstlane(band) + __builtin_amdgcn_readfirstlane(l2 - ai * h)) * BT;
     if constexpr (!is_wgrad(MODE)) {
         c.r0 = __builtin_amdgcn_readfirstlane(lo) + c.b0;

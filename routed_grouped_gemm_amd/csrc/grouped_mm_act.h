@@ -10,10 +10,67 @@
 namespace {
 
 template <int EL, int MODE, int EPI>
-int launch_epi(const MmP& p, int rows, hipStream_t stream) {
+int launch_part(MmP& p, int rows, int cols, hipStream_t stream) {
+    const int tile = rows > 64 ? a_tile(EPI) : rows_a(EPI);
+    p.at = (cols + tile - 1) / tile;
     if (rows > 128) return launch_mm<EL, MODE, 8, EPI>(p, mm_items(p, 256, a_tile(EPI)), stream);
     if (rows > 64) return launch_mm<EL, MODE, 4, EPI>(p, mm_items(p, 128, a_tile(EPI)), stream);
     return rows > 32 ? launch_rows<EL, MODE, 4, EPI>(p, stream) : launch_rows<EL, MODE, 2, EPI>(p, stream);
+}
+
+// How a product with an epilogue runs: mm_plan's kernel and split (weight rows:
+// gated 2 N), and for one group on the LDS-tiled kernel whether the last, mostly
+// empty tiles of rows or columns (up to 64 of either) go to the weight-streaming
+// kernel in launches of their own. A tile that is mostly empty takes as long as a
+// full one, so that pays where they make for another round of workgroups: 8191 x
+// 4104 x 4096 (8 columns past 16 tiles) 340 -> PENDING us, 4099 x 4096 x 2040 (3 rows past
+// 16 tiles) 141 -> PENDING. Times in rounds as mm_plan's; a tail's launch costs about 4
+// us. (Several groups: how full their last tiles are is not known here.)
+struct EpiPlan { int rows, parts; bool row_tail, col_tail; };
+inline EpiPlan epi_plan(int R_max, int G, int N, int K, bool gated) {
+    EpiPlan best{};
+    moe_mm_plan(false, R_max, G, gated ? 2 * N : N, K, &best.rows, &best.parts);
+    if (G > 1 || best.rows <= 64) return best;
+    const int64_t cus = device_cu_count(), nk = (K + 63) / 64, at = gated ? kATile / 2 : kATile, thin = gated ? kRowsA / 2 : kRowsA;
+    double least = 1e30;
+    for (int rows = 256; rows >= 128; rows /= 2)
+        for (int tails = 0; tails < 4; ++tails) {
+            const bool rt = tails & 1, ct = tails & 2;
+            const int r = R_max % rows, c = (int)(N % at);
+            if ((rt && (r == 0 || r > 64 || r == R_max)) || (ct && (c == 0 || c > 64 || c == N))) continue;
+            const int64_t items = ((R_max + rows - 1) / rows - rt) * ((N + at - 1) / at - ct);
+            double t = (double)((items + cus - 1) / cus) * ((double)nk * (rows == 256 ? 1.6 : 1.0) + 8.0);
+            if (rt) t += 4.0 + (double)((((N + thin - 1) / thin) + 2 * cus - 1) / (2 * cus)) * (double)nk * 0.5;
+            if (ct) t += 4.0 + (double)(((int64_t)((R_max + 63) / 64) * ((c + thin - 1) / thin) + 2 * cus - 1) / (2 * cus)) * (double)nk * 0.54;
+            if (t < least) { least = t; best = EpiPlan{rows, 1, rt, ct}; }
+        }
+    return best;
+}
+// columns of the main launch
+inline int epi_main_cols(const EpiPlan& plan, int N, bool gated) {
+    return plan.col_tail ? N - N % (gated ? kATile / 2 : kATile) : N;
+}
+
+// (three stages of 128 rows leave LDS for the tables of 2047 groups: mm_plan)
+template <int EL, int MODE, int EPI>
+int launch_epi(MmP& p, const EpiPlan& plan, hipStream_t stream) {
+    const int main = epi_main_cols(plan, p.N, EPI == kEpiGated);
+    p.row_tile = plan.rows;
+    p.row_part = plan.row_tail ? 1 : 0;
+    int e = launch_part<EL, MODE, EPI>(p, plan.rows, main, stream);
+    if (e) return e;
+    if (plan.col_tail) {
+        MmP q = p;
+        q.col0 = main;
+        q.dw_slot0 = 4 * p.at;
+        if ((e = launch_part<EL, MODE, EPI>(q, 64, p.N - main, stream))) return e;
+    }
+    if (plan.row_tail) {
+        MmP q = p;
+        q.row_part = 2;
+        if ((e = launch_part<EL, MODE, EPI>(q, 64, p.N, stream))) return e;
+    }
+    return 0;
 }
 
 // rows [lo, end) of all groups

@@ -1,8 +1,7 @@
 // Grouped 16-bit products with bias, activation, row weight and residual in
 // their epilogue (grouped_mm_epi.h): on the LDS-tiled kernel, on the
 // weight-streaming kernel for few rows per group, or split along K there and
-// joined by act_join_kernel. The choice is that of the plain product with as
-// many weight rows (gated: 2 N).
+// joined by act_join_kernel (epi_plan).
 //
 // The matrix instructions bound the large calls. Measured: gated 24576 x 2816 x
 // 2048 in 16 uneven groups, gathered, with bias, weights and kept
@@ -39,8 +38,8 @@ void act_join_kernel(MmP p) {
 }
 
 template <int EL, int MODE, int EPI>
-int launch_act(const MmP& p, int rows, hipStream_t stream) {
-    const int e = launch_epi<EL, MODE, EPI>(p, rows, stream);
+int launch_act(MmP& p, const EpiPlan& plan, hipStream_t stream) {
+    const int e = launch_epi<EL, MODE, EPI>(p, plan, stream);
     if (e || p.parts == 1) return e;
     const int64_t lanes = (int64_t)p.R_max * (p.N / (EPI == kEpiGated ? 2 : 4));
     const int grid = (int)std::min<int64_t>((lanes + 255) / 256, 4 * device_cu_count());
@@ -49,9 +48,9 @@ int launch_act(const MmP& p, int rows, hipStream_t stream) {
 }
 
 template <int EL>
-int launch_type(const MmActCall& c, const MmP& p, int rows, hipStream_t stream) {
-    if (c.gated) return launch_act<EL, kMmNK, kEpiGated>(p, rows, stream);
-    return c.kn ? launch_act<EL, kMmKN, kEpiAct>(p, rows, stream) : launch_act<EL, kMmNK, kEpiAct>(p, rows, stream);
+int launch_type(const MmActCall& c, MmP& p, const EpiPlan& plan, hipStream_t stream) {
+    if (c.gated) return launch_act<EL, kMmNK, kEpiGated>(p, plan, stream);
+    return c.kn ? launch_act<EL, kMmKN, kEpiAct>(p, plan, stream) : launch_act<EL, kMmNK, kEpiAct>(p, plan, stream);
 }
 
 }  // namespace
@@ -64,8 +63,7 @@ int moe_launch_mm_act(const MmActCall& c, hipStream_t stream) {
     p.res = (const uint8_t*)c.res; p.res_ld = (size_t)c.ld_res;
     p.pre = (uint8_t*)c.pre; p.pre_ld = (size_t)c.N * (c.gated ? 2 : 1);
     p.partial = (float*)c.ws;
-    int rows, parts;
-    moe_mm_plan(false, c.R_max, c.G, c.N * (c.gated ? 2 : 1), c.K, &rows, &parts);
-    p.parts = parts;
-    return c.dtype == MOE_T_F16 ? launch_type<kElF16>(c, p, rows, stream) : launch_type<kElBf16>(c, p, rows, stream);
+    const EpiPlan plan = epi_plan(c.R_max, c.G, c.N, c.K, c.gated);
+    p.parts = plan.parts;
+    return c.dtype == MOE_T_F16 ? launch_type<kElF16>(c, p, plan, stream) : launch_type<kElBf16>(c, p, plan, stream);
 }

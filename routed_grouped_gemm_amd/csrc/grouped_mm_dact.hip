@@ -27,29 +27,40 @@ void grad_join_kernel(MmP p) {
     }
 }
 
+// n: partial sums of a row; tail_n: of the rows past the whole passes of one group (0: none apart)
 __global__ __launch_bounds__(256)
-void grad_sum_kernel(MmP p, int n) {
+void grad_sum_kernel(MmP p, int n, int tail_n) {
     int lo, end;
     all_rows(p, lo, end);
     const int64_t row = lo + (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (row >= end) return;
+    if (tail_n && row >= end - (end - lo) % p.row_tile) n = tail_n;
     float sum = 0.f;
     #pragma unroll 8
     for (int i = 0; i < n; ++i) sum += p.dw_part[(size_t)i * p.R_max + row];
     p.dw[row] = sum;
 }
 
+// partial sums of a row: 4 a tile of columns of either kernel
+struct GradSums { int n, tail_n; };
+GradSums grad_sums(const EpiPlan& plan, int N) {
+    const int thin = 4 * ((N + kRowsA - 1) / kRowsA), main = epi_main_cols(plan, N, false);
+    if (plan.rows <= 64) return GradSums{thin, 0};
+    const int n = 4 * ((main + kATile - 1) / kATile) + 4 * ((N - main + kRowsA - 1) / kRowsA);
+    return GradSums{n, plan.row_tail ? thin : 0};
+}
+
 template <int EL, int MODE>
-int launch_dact(const MmP& p, int rows, hipStream_t stream) {
-    int e = launch_epi<EL, MODE, kEpiGrad>(p, rows, stream);
+int launch_dact(MmP& p, const EpiPlan& plan, hipStream_t stream) {
+    int e = launch_epi<EL, MODE, kEpiGrad>(p, plan, stream);
     if (e) return e;
     if (p.parts > 1) {
         grad_join_kernel<EL == kElF16><<<(int)std::min<int64_t>(((int64_t)p.R_max + 3) / 4, 8 * device_cu_count()), 256, 0, stream>>>(p);
         return (int)hipGetLastError();
     }
     if (!p.dw) return 0;
-    const int n = rows > 64 ? 4 * ((p.N + kATile - 1) / kATile) : 4 * ((p.N + kRowsA - 1) / kRowsA);
-    grad_sum_kernel<<<(unsigned)(((int64_t)p.R_max + 255) / 256), 256, 0, stream>>>(p, n);
+    const GradSums s = grad_sums(plan, p.N);
+    grad_sum_kernel<<<(unsigned)(((int64_t)p.R_max + 255) / 256), 256, 0, stream>>>(p, s.n, s.tail_n);
     return (int)hipGetLastError();
 }
 
@@ -57,11 +68,10 @@ int launch_dact(const MmP& p, int rows, hipStream_t stream) {
 
 size_t moe_mm_dact_bytes(int R_max, int G, int N, int K) {
     if (R_max <= 0) return 0;
-    int rows, parts;
-    moe_mm_plan(false, R_max, G, N, K, &rows, &parts);
-    if (parts > 1) return (size_t)parts * R_max * N * 4;
-    const int tile = rows > 64 ? kATile : kRowsA;
-    return (size_t)4 * ((N + tile - 1) / tile) * R_max * 4;
+    const EpiPlan plan = epi_plan(R_max, G, N, K, false);
+    if (plan.parts > 1) return (size_t)plan.parts * R_max * N * 4;
+    const GradSums s = grad_sums(plan, N);
+    return (size_t)std::max(s.n, s.tail_n) * R_max * 4;
 }
 
 int moe_launch_mm_dact(const MmActCall& c, hipStream_t stream) {
@@ -69,11 +79,10 @@ int moe_launch_mm_dact(const MmActCall& c, hipStream_t stream) {
     p.out = (uint8_t*)c.out;
     p.pre = (uint8_t*)c.pre; p.pre_ld = (size_t)c.ld_pre;
     p.h = (uint8_t*)c.h; p.dw = c.dw;
-    int rows, parts;
-    moe_mm_plan(false, c.R_max, c.G, c.N, c.K, &rows, &parts);
-    p.parts = parts;
-    if (parts > 1) p.partial = (float*)c.ws;
+    const EpiPlan plan = epi_plan(c.R_max, c.G, c.N, c.K, false);
+    p.parts = plan.parts;
+    if (plan.parts > 1) p.partial = (float*)c.ws;
     else if (c.dw) p.dw_part = (float*)c.ws;
-    if (c.dtype == MOE_T_F16) return c.kn ? launch_dact<kElF16, kMmKN>(p, rows, stream) : launch_dact<kElF16, kMmNK>(p, rows, stream);
-    return c.kn ? launch_dact<kElBf16, kMmKN>(p, rows, stream) : launch_dact<kElBf16, kMmNK>(p, rows, stream);
+    if (c.dtype == MOE_T_F16) return c.kn ? launch_dact<kElF16, kMmKN>(p, plan, stream) : launch_dact<kElF16, kMmNK>(p, plan, stream);
+    return c.kn ? launch_dact<kElBf16, kMmKN>(p, plan, stream) : launch_dact<kElBf16, kMmNK>(p, plan, stream);
 }

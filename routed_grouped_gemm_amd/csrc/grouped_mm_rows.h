@@ -54,7 +54,7 @@ template <int EL, int MODE, int BT, int EPI>
 MOE_DEV MmItem rows_item(const MmP& p, const MmTables& tb, const MmWhere& wh, int item, int& part, int& k0, int& k1) {
     const int tiles = wh.n_items / p.parts;
     part = __builtin_amdgcn_readfirstlane(item / tiles);
-    const MmItem c = mm_scalar(mm_decode<EL, MODE, BT, rows_a(EPI)>(p, tb, wh.at, item - part * tiles));
+    const MmItem c = mm_scalar(mm_decode<EL, MODE, BT, rows_a(EPI), EPI != kEpiNone>(p, tb, wh.at, item - part * tiles));
     k0 = __builtin_amdgcn_readfirstlane(c.nk * part / p.parts);
     k1 = __builtin_amdgcn_readfirstlane(c.nk * (part + 1) / p.parts);
     return c;
@@ -246,8 +246,8 @@ void grouped_mm_rows_kernel(MmP p) {
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int q = lane >> 4, j = lane & 15;
-    const int at = (p.N + rows_a(EPI) - 1) / rows_a(EPI);
-    if (w == 0) mm_passes(p, BT, at * p.parts, lane, tab);
+    const int at = EPI == kEpiNone ? (p.N + kRowsA - 1) / kRowsA : p.at;
+    if (w == 0) mm_passes<EPI != kEpiNone>(p, BT, at * p.parts, lane, tab);
     __syncthreads();
     const int n_items = __builtin_amdgcn_readfirstlane(tab[p.G]) * at * p.parts;
     const int grid = gridDim.x;
@@ -368,7 +368,7 @@ void grouped_mm_rows_kernel(MmP p) {
                 if (p.dw_part && p.parts == 1) {             // the sum over this wave's 16 columns
                     sum += __shfl_xor(sum, 16, 64);
                     sum += __shfl_xor(sum, 32, 64);
-                    if (lane < 16 && b < c.nrows) p.dw_part[(size_t)((c.a0 >> 4) + w) * p.R_max + row] = sum;
+                    if (lane < 16 && b < c.nrows) p.dw_part[(size_t)(p.dw_slot0 + ((c.a0 - p.col0) >> 4) + w) * p.R_max + row] = sum;
                 }
             }
         }

@@ -119,7 +119,7 @@ MOE_DEV void mm_look(const MmP& p, const MmTables& tb, const MmWhere& wh, MmReq<
     int round = R.round;
     bool live = false;
     for (int item; !live && (item = mm_nth<MODE>(round, wh)) < wh.n_items; ++round) {
-        R.n = mm_scalar(mm_decode<EL, MODE, 32 * NB, a_tile(EPI)>(p, tb, wh.at, item));
+        R.n = mm_scalar(mm_decode<EL, MODE, 32 * NB, a_tile(EPI), EPI != kEpiNone>(p, tb, wh.at, item));
         R.nat = item;
         live = R.n.nk > 0;
     }
@@ -614,14 +614,14 @@ void grouped_mm_kernel(MmP p) {
     const bool lead = w < 4;                                 // the half that multiplies first, half a step ahead
 
     const int na = is_wgrad(MODE) ? p.K : p.N;               // extent of the contiguous output axis
-    const int at = (na + a_tile(EPI) - 1) / a_tile(EPI);
+    const int at = EPI == kEpiNone ? (na + kATile - 1) / kATile : p.at;
     int n_items;
     if constexpr (is_wgrad(MODE)) {
         wgrad_tables(p, at * ((p.N + BT - 1) / BT), tab, order, tab + p.G + 1, (uint16_t*)(smem + NST * Geo::Stage));
         __syncthreads();
         n_items = __builtin_amdgcn_readfirstlane(tab[p.G]) * at * ((p.N + BT - 1) / BT);
     } else {
-        if (w == 0) mm_passes(p, BT, at, lane, tab);
+        if (w == 0) mm_passes<EPI != kEpiNone>(p, BT, at, lane, tab);
         __syncthreads();
         n_items = __builtin_amdgcn_readfirstlane(tab[p.G]) * at;
     }
@@ -897,7 +897,7 @@ void grouped_mm_kernel(MmP p) {
     if constexpr (EL == kElFp8) fwn = load_fw(mm_scalar(mm_decode<EL, MODE, 32 * NB>(p, tb, at, slot)), 0);
     for (int round = 0, item; (item = mm_nth<MODE>(round, wh)) < n_items; ++round) {
         // the item is the one being requested, unless items are very short
-        const MmItem c = R.live && R.at == item ? R.c : mm_scalar(mm_decode<EL, MODE, 32 * NB, a_tile(EPI)>(p, tb, at, item));
+        const MmItem c = R.live && R.at == item ? R.c : mm_scalar(mm_decode<EL, MODE, 32 * NB, a_tile(EPI), EPI != kEpiNone>(p, tb, at, item));
         if constexpr (EL == kElFp8) {   // the next item's scales are loaded an item ahead
             fwv = fwn;
             asm volatile("" : "+v"(fwv));

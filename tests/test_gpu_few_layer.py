@@ -59,7 +59,7 @@ class Case:
 
     def act64(self, z):
         if self.act == moe.MOE_ACT_GEGLU:
-            return z * torch.special.ndtr(z)
+            return z * 0.5 * torch.erfc(z * -0.5 ** 0.5)          # (ndtr loses the tail: 2% at -8)
         if self.act == moe.MOE_ACT_SRELU:
             return torch.relu(z) ** 2
         return z if self.act == moe.MOE_ACT_NONE else z * torch.sigmoid(self.beta * z)

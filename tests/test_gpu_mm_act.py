@@ -31,7 +31,7 @@ def test_shapes_reach_every_kernel():
 
 def a64(z, act, beta=1.0):
     if act == GELU:
-        return z * torch.special.ndtr(z)
+        return z * 0.5 * torch.erfc(z * -0.5 ** 0.5)          # (ndtr loses the tail: 2% at -8)
     if act == RELU2:
         return torch.relu(z).square()
     return z if act == NONE else z * torch.sigmoid(beta * z)
@@ -157,6 +157,28 @@ def test_forward_on_every_kernel(R, G, N, K, dtype, kind):
     act = [SWI, GELU, RELU2, NONE][(i + (kind == "kn")) % 4]
     forward(R, G, N, K, dtype, kind == "gated", act, kn=kind == "kn", T=(R // 2 + 1) * (i % 2), weighted=i % 3 != 1,
             bias=i % 4 != 2, residual=i % 2 == 0, seed=i)
+
+
+# One group whose last tiles are mostly empty: a few rows past 32 tiles, a few
+# columns past 8, both, and up to the 64 that still go apart; hi < R: fewer rows
+# in the group than the call allows for, so that its tail is another one
+TAILS = [(8195, 2048, 8195), (8192, 2056, 8192), (8195, 2056, 8195), (8256, 2112, 8256), (8195, 2056, 7900), (8195, 2056, 2),
+         (8191, 2040, 8191)]
+
+
+@pytest.mark.parametrize("R,N,hi", TAILS)
+@pytest.mark.parametrize("kind", ["gated", "nk", "kn"])
+def test_one_group_with_mostly_empty_last_tiles(R, N, hi, kind):
+    banner(f"act tails {kind} R={R} N={N} hi={hi}")
+    gated = kind == "gated"
+    forward(R, 1, N // 2 // 8 * 8 if gated else N, 136, torch.bfloat16, gated, SWI, kn=kind == "kn", weighted=True, seed=R + N, hi=hi)
+
+
+@pytest.mark.parametrize("R,N,hi", TAILS)
+@pytest.mark.parametrize("gated", [False, True])
+def test_gradient_of_one_group_with_mostly_empty_last_tiles(R, N, hi, gated):
+    banner(f"dact tails gated={gated} R={R} N={N} hi={hi}")
+    gradient(R, 1, N, 136, torch.bfloat16, gated, GELU, kn=gated, weighted=True, T=500, seed=R + N, hi=hi)
 
 
 @pytest.mark.parametrize("act,beta,limit", [(SWI, 1.0, 0.0), (SWI, 1.702, 0.75), (GELU, 1.0, 0.0), (GELU, 1.0, 1.5),
