@@ -23,8 +23,8 @@ int launch_part(MmP& p, int rows, int cols, hipStream_t stream) {
 // empty tiles of rows or columns (up to 64 of either) go to the weight-streaming
 // kernel in launches of their own. A tile that is mostly empty takes as long as a
 // full one, so that pays where they make for another round of workgroups: 8191 x
-// 4104 x 4096 (8 columns past 16 tiles) 340 -> PENDING us, 4099 x 4096 x 2040 (3 rows past
-// 16 tiles) 141 -> PENDING. Times in rounds as mm_plan's; a tail's launch costs about 4
+// 4104 x 4096 (8 columns past 16 tiles) 340 -> 314 us, 4099 x 4096 x 2040 (3 rows past
+// 16 tiles) 141 -> 126. Times in rounds as mm_plan's; a tail's launch costs about 4
 // us. (Several groups: how full their last tiles are is not known here.)
 struct EpiPlan { int rows, parts; bool row_tail, col_tail; };
 inline EpiPlan epi_plan(int R_max, int G, int N, int K, bool gated) {
@@ -63,12 +63,15 @@ int launch_epi(MmP& p, const EpiPlan& plan, hipStream_t stream) {
         MmP q = p;
         q.col0 = main;
         q.dw_slot0 = 4 * p.at;
-        if ((e = launch_part<EL, MODE, EPI>(q, 64, p.N - main, stream))) return e;
+        // 32 rows to a tile where 64 leave compute units without one (8 columns of 8191 x
+        // 4096: 51.5 -> 43.5 us)
+        const int64_t items = (int64_t)((p.R_max + 63) / 64) * ((p.N - main + rows_a(EPI) - 1) / rows_a(EPI));
+        if ((e = launch_part<EL, MODE, EPI>(q, items <= device_cu_count() ? 32 : 64, p.N - main, stream))) return e;
     }
     if (plan.row_tail) {
         MmP q = p;
-        q.row_part = 2;
-        if ((e = launch_part<EL, MODE, EPI>(q, 64, p.N, stream))) return e;
+        q.row_part = 2;      // (3 rows of 4096 x 2040, 32 against 64 to a tile: 27.3 -> 24.3 us)
+        if ((e = launch_part<EL, MODE, EPI>(q, p.R_max % plan.rows <= 32 ? 32 : 64, p.N, stream))) return e;
     }
     return 0;
 }

@@ -27,18 +27,26 @@ void grad_join_kernel(MmP p) {
     }
 }
 
-// n: partial sums of a row; tail_n: of the rows past the whole passes of one group (0: none apart)
+// n: partial sums of a row; tail_n: of the rows past the whole passes of one
+// group (0: none apart). 64 rows to a workgroup, a quarter of the sums to each
+// wave, the quarters joined in their order.
 __global__ __launch_bounds__(256)
 void grad_sum_kernel(MmP p, int n, int tail_n) {
+    __shared__ float part[3][64];
     int lo, end;
     all_rows(p, lo, end);
-    const int64_t row = lo + (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (row >= end) return;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t row = lo + (int64_t)blockIdx.x * 64 + lane;
+    const bool in = row < end;
     if (tail_n && row >= end - (end - lo) % p.row_tile) n = tail_n;
     float sum = 0.f;
-    #pragma unroll 8
-    for (int i = 0; i < n; ++i) sum += p.dw_part[(size_t)i * p.R_max + row];
-    p.dw[row] = sum;
+    if (in) {
+        #pragma unroll 8
+        for (int i = n * w / 4; i < n * (w + 1) / 4; ++i) sum += p.dw_part[(size_t)i * p.R_max + row];
+    }
+    if (w > 0) part[w - 1][lane] = sum;
+    __syncthreads();
+    if (w == 0 && in) p.dw[row] = ((sum + part[0][lane]) + part[1][lane]) + part[2][lane];
 }
 
 // partial sums of a row: 4 a tile of columns of either kernel
@@ -60,7 +68,7 @@ int launch_dact(MmP& p, const EpiPlan& plan, hipStream_t stream) {
     }
     if (!p.dw) return 0;
     const GradSums s = grad_sums(plan, p.N);
-    grad_sum_kernel<<<(unsigned)(((int64_t)p.R_max + 255) / 256), 256, 0, stream>>>(p, s.n, s.tail_n);
+    grad_sum_kernel<<<(unsigned)(((int64_t)p.R_max + 63) / 64), 256, 0, stream>>>(p, s.n, s.tail_n);
     return (int)hipGetLastError();
 }
 

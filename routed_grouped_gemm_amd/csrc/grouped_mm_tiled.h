@@ -931,7 +931,7 @@ void grouped_mm_kernel(MmP p) {
         // have their last products to form. They run their epilogue before the
         // barrier that follows those, so both halves' epilogues run side by side
         // (in turn, each held up the other half's products: the gradient of 24576
-        // x 1408 x 2048 PENDING us).
+        // x 1408 x 2048 276 -> 270 us).
         if (EPI != kEpiNone && lead) bare_barrier();
         if constexpr (EL == kElFp8) {
             #pragma unroll
