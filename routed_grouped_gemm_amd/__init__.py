@@ -444,7 +444,7 @@ _T_ANY = {**_T16, torch.float32: MOE_T_F32}
 
 def _mat(t: torch.Tensor, types, name: str, device=None) -> torch.Tensor:
     """A 2-D device tensor whose rows are dense (its row stride may be larger)."""
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise MoeError(f"{name} must be a device tensor")
     if device is not None and t.device != device:
         raise MoeError(f"{name} is on {t.device}, expected {device}")
@@ -457,11 +457,13 @@ def _mat(t: torch.Tensor, types, name: str, device=None) -> torch.Tensor:
 
 def _ld(t: torch.Tensor) -> int:
     """Leading dimension: the row stride (a single row's is not defined by its data)."""
-    if t.shape[0] > 1:
-        if t.stride(0) < t.shape[1]:
+    rows, cols = t.shape
+    if rows > 1:
+        ld = t.stride(0)
+        if ld < cols:
             raise MoeError("rows overlap")
-        return t.stride(0)
-    return t.shape[1]
+        return ld
+    return cols
 
 
 def _dense(t, shape, dtype, name: str, device) -> None:
@@ -767,11 +769,11 @@ def moe_grouped_mm_act(x, w, offsets, epi: Epilogue | None = None, gated: bool =
         raise MoeError(f"residual must be [{R}, {cols}], got {tuple(residual.shape)}")
     with _at(dev, stream):
         if out is None:
-            out = torch.empty((R, cols), dtype=x.dtype, device=dev)
+            out = x.new_empty((R, cols))
         elif _mat(out, (x.dtype,), "out", dev).shape != (R, cols):
             raise MoeError(f"out must be [{R}, {cols}], got {tuple(out.shape)}")
         if keep_pre and pre is None:
-            pre = torch.empty((R, N), dtype=x.dtype, device=dev)
+            pre = x.new_empty((R, N))
         _dense(pre, (R, N), x.dtype, "pre", dev)
         e = epi.desc
         desc = moe_epilogue(e.act, e.beta, e.limit, 0, e.bias, _p(pre))
@@ -808,9 +810,9 @@ def moe_grouped_mm_dact(dy, w, offsets, pre, epi: Epilogue | None = None, gated:
     if epi is None:
         epi = Epilogue(act=MOE_ACT_SWIGLU if gated else MOE_ACT_NONE)
     with _at(dev, stream):
-        out = dict(dpre=torch.empty((R, wide), dtype=dy.dtype, device=dev),
-                   h=torch.empty((R, N), dtype=dy.dtype, device=dev) if want_h else None,
-                   dw=torch.empty(R, dtype=torch.float32, device=dev) if want_dw else None)
+        out = dict(dpre=dy.new_empty((R, wide)),
+                   h=dy.new_empty((R, N)) if want_h else None,
+                   dw=dy.new_empty(R, dtype=torch.float32) if want_dw else None)
         nws = int(lib.moe_grouped_mm_dact_workspace_size(R, G, N, K))
         ws = _ws(nws, dev)
         flags = (MOE_MM_W_KN if w_kn else 0) | (MOE_MM_GATED if gated else 0)
@@ -853,36 +855,31 @@ def moe_layer_few(logits, x, w1, w2, k: int, e0: int = 0, w1_scales=None, w2_sca
         raise MoeError(f"w1 must be [E_loc, 2I, H], got {tuple(w1.shape)}")
     G, I, eight = w1.shape[0], w1.shape[1] // 2, w1_scales is not None
     _few_pair(w1, w2, w1_scales, w2_scales, G, H, I, x.dtype, eight, "", dev)
-    args = moe_few_args()
-    s = 0
+    s, sh = 0, (None, None, None, None)
     if shared is not None:
         a, sa, b, sb = shared
         _few_pair(a, b, sa, sb, 1, H, I, x.dtype, eight, "shared ", dev)
-        args.shared_w1, args.shared_w1_scales, args.shared_w2, args.shared_w2_scales = _p(a), _p(sa), _p(b), _p(sb)
-        s = 1
+        s, sh = 1, (_p(a), _p(b), _p(sa), _p(sb))
     if epi is not None:
         _dense(epi.bias, (G + s, 2 * I), torch.float32, "bias", dev)
-        args.epi = C.pointer(epi.desc)
     _dense(bias2, (G + s, H), torch.float32, "bias2", dev)
     if residual is not None:
         if _mat(residual, (x.dtype,), "residual", dev).shape != (T, H):
             raise MoeError(f"residual must be [{T}, {H}], got {tuple(residual.shape)}")
-        args.residual, args.ld_res = _p(residual), _ld(residual)
     with _at(dev, stream):
         if out is None:
-            out = torch.empty((T, H), dtype=x.dtype, device=dev)
+            out = x.new_empty((T, H))
         elif _mat(out, (x.dtype,), "out", dev).shape != (T, H):
             raise MoeError(f"out must be [{T}, {H}], got {tuple(out.shape)}")
         if ws is None:
-            ws = torch.empty(max(int(lib.moe_layer_few_workspace_size(T, k, G, H, I, s)), 1), dtype=torch.uint8, device=dev)
+            ws = x.new_empty(max(int(lib.moe_layer_few_workspace_size(T, k, G, H, I, s)), 1), dtype=torch.uint8)
         elif ws.dim() != 1:
             raise MoeError("ws must be 1-D")
         else:
             _dense(ws, ws.shape, torch.uint8, "ws", dev)
-        args.logits, args.T, args.E_tot, args.k, args.e0, args.E_loc = _p(logits), T, E, k, e0, G
-        args.dtype, args.x, args.ldx, args.H, args.I, args.flags = _T16[x.dtype], _p(x), _ld(x), H, I, flags
-        args.w1, args.w2, args.w1_scales, args.w2_scales = _p(w1), _p(w2), _p(w1_scales), _p(w2_scales)
-        args.bias2, args.out, args.ld_out = _p(bias2), _p(out), _ld(out)
+        args = moe_few_args(_p(logits), T, E, k, e0, G, _T16[x.dtype], _p(x), _ld(x), H, I, flags, _p(w1), _p(w2),
+                            _p(w1_scales), _p(w2_scales), *sh, C.pointer(epi.desc) if epi is not None else None,
+                            _p(bias2), _p(residual), _p(out), _ld(residual) if residual is not None else 0, _ld(out))
         _check(lib.moe_layer_few(C.byref(args), _p(ws), ws.shape[0], _raw_stream(dev)), "moe_layer_few")
     return out
 
@@ -908,7 +905,7 @@ def moe_grouped_bias_grad(dy, offsets, dy_src=None, row_w=None, out=None, accumu
         raise MoeError("accumulate needs out")
     with _at(dev, stream):
         if out is None:
-            out = torch.empty((G, N), dtype=torch.float32, device=dev)
+            out = dy.new_empty((G, N), dtype=torch.float32)
         _dense(out, (G, N), torch.float32, "out", dev)
         nws = int(lib.moe_grouped_bias_grad_workspace_size(R, G, N))
         ws = _ws(nws, dev)
@@ -941,7 +938,7 @@ def moe_route_backward(logits, topk_idx, dw, slot_row=None, prob_grad=None, z_co
     _dense(prob_grad, (E,), torch.float32, "prob_grad", dev)
     with _at(dev, stream):
         if out is None:
-            out = torch.empty((T, E), dtype=torch.float32, device=dev)
+            out = logits.new_empty((T, E))
         _dense(out, (T, E), torch.float32, "out", dev)
         _check(lib.moe_route_backward(_p(logits), T, E, k, flags, _p(topk_idx), _p(dw), dw.numel(), _p(slot_row),
                                       slot_row.shape[1] if slot_row is not None else 0, _p(prob_grad), z_coef, _p(out),
