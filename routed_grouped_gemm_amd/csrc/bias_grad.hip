@@ -7,7 +7,7 @@
 // joined in LDS. A group of one pass is done with that; the sums of longer
 // ones go to the workspace and a second launch adds them in the order of the
 // passes, so results are the same bits every time. `pass` follows from R_max
-// and N alone: about 2048 workgroups (8 on a compute unit, 16 KiB in flight
+// and N alone: about 1024 workgroups (4 on a compute unit, 32 KiB in flight
 // each), at least 32 rows of work for each.
 // Measured: 24576 rows of 2816 in 16 uneven groups 33 us (4.2 TB/s), 8191
 // gathered rows of 4104 in one group 19 us.
@@ -196,7 +196,7 @@ void bias_join_kernel(BiasP p) {
 
 int bias_pass(int R_max, int N) {
     const int64_t blocks = (N + kBgCols - 1) / kBgCols;
-    const int64_t rows = ((int64_t)R_max * blocks / 2048 + 15) / 16 * 16;
+    const int64_t rows = ((int64_t)R_max * blocks / 1024 + 15) / 16 * 16;
     return (int)std::min<int64_t>(std::max<int64_t>(rows, 32), 4096);
 }
 // passes that groups of several passes can have (each but a group's last is full)
