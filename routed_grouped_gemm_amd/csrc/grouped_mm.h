@@ -54,6 +54,7 @@ struct MmP {
     // col0; of a single group all rows (row_part 0), those of whole passes of
     // row_tile rows (1) or the rest (2)
     int col0, at, row_part, row_tile, dw_slot0;
+    size_t part_ld, part_rows;                               // its partial sums: values of a row, rows of a part
 };
 
 // Rows [lo, hi) of group g, held inside [0, R_max) whatever the offsets say.
@@ -71,7 +72,16 @@ MOE_DEV void part_rows(const MmP& p, int& lo, int& hi) {
     }
 }
 
-// The same of one group for the whole wave, by scalar loads: waiting for a
+// The row that is the first of a part's partial sums.
+MOE_DEV int first_part_row(const MmP& p) {
+    int lo = 0, hi;
+    if (p.row_part != 2) return 0;
+    group_rows(p, 0, lo, hi);
+    part_rows<true>(p, lo, hi);
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// The rows of one group for the whole wave, by scalar loads: waiting for a
 // vector load would drain the requests in flight at every item.
 MOE_DEV void group_rows_scalar(const MmP& p, int g, int& lo, int& hi) {
     typedef const __attribute__((address_space(4))) int32_t* const_i32;

@@ -21,12 +21,28 @@ int launch_part(MmP& p, int rows, int cols, hipStream_t stream) {
 // How a product with an epilogue runs: mm_plan's kernel and split (weight rows:
 // gated 2 N), and for one group on the LDS-tiled kernel whether the last, mostly
 // empty tiles of rows or columns (up to 64 of either) go to the weight-streaming
-// kernel in launches of their own. A tile that is mostly empty takes as long as a
-// full one, so that pays where they make for another round of workgroups: 8191 x
-// 4104 x 4096 (8 columns past 16 tiles) 340 -> 314 us, 4099 x 4096 x 2040 (3 rows past
-// 16 tiles) 141 -> 126. Times in rounds as mm_plan's; a tail's launch costs about 4
-// us. (Several groups: how full their last tiles are is not known here.)
-struct EpiPlan { int rows, parts; bool row_tail, col_tail; };
+// kernel in launches of their own, which may be split along K and joined. A tile
+// that is mostly empty takes as long as a full one, so that pays where they make
+// for another round of workgroups: 8191 x 4104 x 4096 (8 columns past 16 tiles)
+// 340 -> 314 us, 4099 x 4096 x 2040 (3 rows past 16 tiles) 141 -> 126, and split
+// 300 -> 288 and 111 -> 101. Times in rounds as mm_plan's; a tail's launch costs about 4 us. (Several
+// groups: how full their last tiles are is not known here.)
+struct EpiTail { bool on; int rows, parts; };                // rows to a tile, parts along K
+struct EpiPlan { int rows, parts; EpiTail row, col; };
+
+// a tail of R rows and n columns: 32 rows to a tile where 64 leave compute units
+// without one (8 columns of 8191 x 4096: 51.5 -> 43.5 us, 3 rows of 4096 x 2040:
+// 27.3 -> 24.3); as many parts as fill two workgroups on each, at least 8 K-tiles
+// to a part, where that saves more than the joining launch (about 8 K-tiles)
+inline EpiTail epi_tail(int64_t R, int64_t n, int64_t thin, int64_t nk, double& t) {
+    const int64_t cus = device_cu_count(), at = (n + thin - 1) / thin;
+    const int rows = (R + 63) / 64 * at <= cus ? 32 : 64;
+    const int64_t items = (R + rows - 1) / rows * at;
+    int64_t parts = std::min<int64_t>({2 * cus / std::max<int64_t>(items, 1), nk / 8, 8});
+    if (parts < 2 || nk - nk / parts < 12) parts = 1;
+    t += 4.0 + (double)((items * parts + 2 * cus - 1) / (2 * cus)) * (double)(nk / parts) * 0.5 + (parts > 1 ? 4.0 : 0.0);
+    return EpiTail{true, rows, (int)parts};
+}
 inline EpiPlan epi_plan(int R_max, int G, int N, int K, bool gated) {
     EpiPlan best{};
     moe_mm_plan(false, R_max, G, gated ? 2 * N : N, K, &best.rows, &best.parts);
@@ -40,40 +56,58 @@ inline EpiPlan epi_plan(int R_max, int G, int N, int K, bool gated) {
             if ((rt && (r == 0 || r > 64 || r == R_max)) || (ct && (c == 0 || c > 64 || c == N))) continue;
             const int64_t items = ((R_max + rows - 1) / rows - rt) * ((N + at - 1) / at - ct);
             double t = (double)((items + cus - 1) / cus) * ((double)nk * (rows == 256 ? 1.6 : 1.0) + 8.0);
-            if (rt) t += 4.0 + (double)((((N + thin - 1) / thin) + 2 * cus - 1) / (2 * cus)) * (double)nk * 0.5;
-            if (ct) t += 4.0 + (double)(((int64_t)((R_max + 63) / 64) * ((c + thin - 1) / thin) + 2 * cus - 1) / (2 * cus)) * (double)nk * 0.54;
-            if (t < least) { least = t; best = EpiPlan{rows, 1, rt, ct}; }
+            EpiPlan plan{rows, 1, {}, {}};
+            if (rt) plan.row = epi_tail(r, N, thin, nk, t);
+            if (ct) plan.col = epi_tail(rt ? R_max - r : R_max, c, thin, nk, t);
+            if (t < least) { least = t; best = plan; }
         }
     return best;
 }
 // columns of the main launch
 inline int epi_main_cols(const EpiPlan& plan, int N, bool gated) {
-    return plan.col_tail ? N - N % (gated ? kATile / 2 : kATile) : N;
+    return plan.col.on ? N - N % (gated ? kATile / 2 : kATile) : N;
+}
+// bytes of the partial sums. (A tail of rows is what lies past the whole tiles of
+// the group's rows, which the device knows: up to a tile's.)
+inline size_t epi_partial_bytes(const EpiPlan& plan, int R_max, int N, bool gated) {
+    const size_t wide = gated ? 2 : 1;
+    size_t n = plan.parts > 1 ? plan.parts * (size_t)R_max * N * wide : 0;
+    if (plan.col.on && plan.col.parts > 1) n = std::max(n, plan.col.parts * (size_t)R_max * (N - epi_main_cols(plan, N, gated)) * wide);
+    if (plan.row.on && plan.row.parts > 1) n = std::max(n, plan.row.parts * (size_t)plan.rows * N * wide);
+    return n * 4;
 }
 
-// (three stages of 128 rows leave LDS for the tables of 2047 groups: mm_plan)
-template <int EL, int MODE, int EPI>
-int launch_epi(MmP& p, const EpiPlan& plan, hipStream_t stream) {
+// join(p): the launch that joins a split one. (three stages of 128 rows leave
+// LDS for the tables of 2047 groups: mm_plan)
+template <int EL, int MODE, int EPI, typename Join>
+int launch_epi(MmP& p, const EpiPlan& plan, hipStream_t stream, Join&& join) {
+    const size_t wide = EPI == kEpiGated ? 2 : 1;
     const int main = epi_main_cols(plan, p.N, EPI == kEpiGated);
     p.row_tile = plan.rows;
-    p.row_part = plan.row_tail ? 1 : 0;
+    p.row_part = plan.row.on ? 1 : 0;
+    p.parts = plan.parts;
+    p.part_rows = (size_t)p.R_max;
+    p.part_ld = (size_t)p.N * wide;
     int e = launch_part<EL, MODE, EPI>(p, plan.rows, main, stream);
-    if (e) return e;
-    if (plan.col_tail) {
+    if (!e && p.parts > 1) e = join(p);
+    if (!e && plan.col.on) {
         MmP q = p;
         q.col0 = main;
         q.dw_slot0 = 4 * p.at;
-        // 32 rows to a tile where 64 leave compute units without one (8 columns of 8191 x
-        // 4096: 51.5 -> 43.5 us)
-        const int64_t items = (int64_t)((p.R_max + 63) / 64) * ((p.N - main + rows_a(EPI) - 1) / rows_a(EPI));
-        if ((e = launch_part<EL, MODE, EPI>(q, items <= device_cu_count() ? 32 : 64, p.N - main, stream))) return e;
+        q.parts = plan.col.parts;
+        q.part_ld = (size_t)(p.N - main) * wide;
+        e = launch_part<EL, MODE, EPI>(q, plan.col.rows, p.N - main, stream);
+        if (!e && q.parts > 1) e = join(q);
     }
-    if (plan.row_tail) {
+    if (!e && plan.row.on) {
         MmP q = p;
-        q.row_part = 2;      // (3 rows of 4096 x 2040, 32 against 64 to a tile: 27.3 -> 24.3 us)
-        if ((e = launch_part<EL, MODE, EPI>(q, p.R_max % plan.rows <= 32 ? 32 : 64, p.N, stream))) return e;
+        q.row_part = 2;
+        q.parts = plan.row.parts;
+        q.part_rows = (size_t)plan.rows;
+        e = launch_part<EL, MODE, EPI>(q, plan.row.rows, p.N, stream);
+        if (!e && q.parts > 1) e = join(q);
     }
-    return 0;
+    return e;
 }
 
 // rows [lo, end) of all groups
@@ -81,6 +115,12 @@ MOE_DEV void all_rows(const MmP& p, int& lo, int& end) {
     int hi, a;
     group_rows(p, 0, lo, hi);
     group_rows(p, p.G - 1, a, end);
+}
+// those that a launch computes, and the first row of its partial sums
+MOE_DEV void joined_rows(const MmP& p, int& lo, int& end, int& row0) {
+    all_rows(p, lo, end);
+    part_rows<true>(p, lo, end);
+    row0 = first_part_row(p);
 }
 
 // the sum of the parts of 4 values, in the order of the parts

@@ -11,20 +11,52 @@
 
 namespace {
 
-// one wave a row
+// The parts of a split product joined and its epilogue: 16 lanes a row of at most
+// 64 columns, else a workgroup a row. The row's sum is whole, or with dw_part one
+// of the row's.
+constexpr int kJoinThreads = 1024;
+
+template <int F16>
+MOE_DEV float grad_join_row(const MmP& p, int64_t row, int row0, int first, int step) {
+    const float* const src = p.partial + (size_t)(row - row0) * p.part_ld;
+    float sum = 0.f;
+    for (int a = p.col0 + first; a < p.N; a += step)
+        sum += rows_grad<F16>(p, (size_t)row, a, join_parts(src + (a - p.col0), p.part_rows * p.part_ld, p.parts));
+    return sum;
+}
+MOE_DEV void grad_join_sum(const MmP& p, int64_t row, float sum) {
+    if (p.dw_part) p.dw_part[(size_t)p.dw_slot0 * p.R_max + row] = sum;
+    else if (p.dw) p.dw[row] = sum;
+}
+
+template <int F16>
+__global__ __launch_bounds__(kJoinThreads)
+void grad_join_kernel(MmP p) {
+    __shared__ float part[kJoinThreads / 64];
+    int lo, end, row0;
+    joined_rows(p, lo, end, row0);
+    for (int64_t row = lo + (int64_t)blockIdx.x; row < end; row += gridDim.x) {
+        const float sum = wave_sum(grad_join_row<F16>(p, row, row0, (int)threadIdx.x * 4, kJoinThreads * 4));
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float all = 0.f;
+            #pragma unroll
+            for (int i = 0; i < kJoinThreads / 64; ++i) all += part[i];
+            grad_join_sum(p, row, all);
+        }
+        __syncthreads();
+    }
+}
 template <int F16>
 __global__ __launch_bounds__(256)
-void grad_join_kernel(MmP p) {
-    int lo, end;
-    all_rows(p, lo, end);
-    const int lane = threadIdx.x & 63;
-    for (int64_t row = lo + (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < end; row += (int64_t)gridDim.x * 4) {
-        float sum = 0.f;
-        for (int a = lane * 4; a < p.N; a += 256)
-            sum += rows_grad<F16>(p, (size_t)row, a, join_parts(p.partial + (size_t)row * p.N + a, (size_t)p.R_max * p.N, p.parts));
-        sum = wave_sum(sum);
-        if (p.dw && lane == 0) p.dw[row] = sum;
-    }
+void grad_join_narrow_kernel(MmP p) {
+    int lo, end, row0;
+    joined_rows(p, lo, end, row0);
+    const int li = threadIdx.x & 15;
+    const int64_t row = lo + (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const float sum = group_sum<16>(row < end ? grad_join_row<F16>(p, row, row0, li * 4, 64) : 0.f);
+    if (li == 0 && row < end) grad_join_sum(p, row, sum);
 }
 
 // n: partial sums of a row; tail_n: of the rows past the whole passes of one
@@ -49,24 +81,31 @@ void grad_sum_kernel(MmP p, int n, int tail_n) {
     if (w == 0 && in) p.dw[row] = ((sum + part[0][lane]) + part[1][lane]) + part[2][lane];
 }
 
-// partial sums of a row: 4 a tile of columns of either kernel
+// partial sums of a row: 4 a tile of columns of either kernel, one of a split launch
 struct GradSums { int n, tail_n; };
 GradSums grad_sums(const EpiPlan& plan, int N) {
-    const int thin = 4 * ((N + kRowsA - 1) / kRowsA), main = epi_main_cols(plan, N, false);
-    if (plan.rows <= 64) return GradSums{thin, 0};
-    const int n = 4 * ((main + kATile - 1) / kATile) + 4 * ((N - main + kRowsA - 1) / kRowsA);
-    return GradSums{n, plan.row_tail ? thin : 0};
+    const auto thin = [](int n) { return 4 * ((n + kRowsA - 1) / kRowsA); };
+    if (plan.rows <= 64) return GradSums{thin(N), 0};
+    const int main = epi_main_cols(plan, N, false), n = 4 * ((main + kATile - 1) / kATile);
+    return GradSums{n + (plan.col.on ? plan.col.parts > 1 ? 1 : thin(N - main) : 0),
+                    plan.row.on ? plan.row.parts > 1 ? 1 : thin(N) : 0};
+}
+// bytes of the rows' partial sums, before those of the products
+size_t dw_bytes(const EpiPlan& plan, int R_max, int N) {
+    if (plan.parts > 1) return 0;
+    const GradSums s = grad_sums(plan, N);
+    return ((size_t)std::max(s.n, s.tail_n) * R_max * 4 + 15) / 16 * 16;
 }
 
 template <int EL, int MODE>
 int launch_dact(MmP& p, const EpiPlan& plan, hipStream_t stream) {
-    int e = launch_epi<EL, MODE, kEpiGrad>(p, plan, stream);
-    if (e) return e;
-    if (p.parts > 1) {
-        grad_join_kernel<EL == kElF16><<<(int)std::min<int64_t>(((int64_t)p.R_max + 3) / 4, 8 * device_cu_count()), 256, 0, stream>>>(p);
+    const int e = launch_epi<EL, MODE, kEpiGrad>(p, plan, stream, [&](const MmP& q) {
+        const int64_t rows = q.row_part == 2 ? q.row_tile : q.R_max;
+        if (q.N - q.col0 <= 64) grad_join_narrow_kernel<EL == kElF16><<<(unsigned)((rows + 15) / 16), 256, 0, stream>>>(q);
+        else grad_join_kernel<EL == kElF16><<<(unsigned)std::min<int64_t>(rows, 4 * device_cu_count()), kJoinThreads, 0, stream>>>(q);
         return (int)hipGetLastError();
-    }
-    if (!p.dw) return 0;
+    });
+    if (e || !p.dw_part) return e;
     const GradSums s = grad_sums(plan, p.N);
     grad_sum_kernel<<<(unsigned)(((int64_t)p.R_max + 63) / 64), 256, 0, stream>>>(p, s.n, s.tail_n);
     return (int)hipGetLastError();
@@ -77,9 +116,7 @@ int launch_dact(MmP& p, const EpiPlan& plan, hipStream_t stream) {
 size_t moe_mm_dact_bytes(int R_max, int G, int N, int K) {
     if (R_max <= 0) return 0;
     const EpiPlan plan = epi_plan(R_max, G, N, K, false);
-    if (plan.parts > 1) return (size_t)plan.parts * R_max * N * 4;
-    const GradSums s = grad_sums(plan, N);
-    return (size_t)std::max(s.n, s.tail_n) * R_max * 4;
+    return dw_bytes(plan, R_max, N) + epi_partial_bytes(plan, R_max, N, false);
 }
 
 int moe_launch_mm_dact(const MmActCall& c, hipStream_t stream) {
@@ -88,9 +125,8 @@ int moe_launch_mm_dact(const MmActCall& c, hipStream_t stream) {
     p.pre = (uint8_t*)c.pre; p.pre_ld = (size_t)c.ld_pre;
     p.h = (uint8_t*)c.h; p.dw = c.dw;
     const EpiPlan plan = epi_plan(c.R_max, c.G, c.N, c.K, false);
-    p.parts = plan.parts;
-    if (plan.parts > 1) p.partial = (float*)c.ws;
-    else if (c.dw) p.dw_part = (float*)c.ws;
+    if (c.dw && plan.parts == 1) p.dw_part = (float*)c.ws;
+    p.partial = (float*)((uint8_t*)c.ws + dw_bytes(plan, c.R_max, c.N));
     if (c.dtype == MOE_T_F16) return c.kn ? launch_dact<kElF16, kMmKN>(p, plan, stream) : launch_dact<kElF16, kMmNK>(p, plan, stream);
     return c.kn ? launch_dact<kElBf16, kMmKN>(p, plan, stream) : launch_dact<kElBf16, kMmNK>(p, plan, stream);
 }

@@ -275,6 +275,7 @@ void grouped_mm_rows_kernel(MmP p) {
     #pragma unroll 1
     for (int i = 0; i < NST - 1; ++i) rows_request<EL, MODE, NB, EPI>(p, tb, wh, R, smem);
 
+    [[maybe_unused]] const int row0 = EPI != kEpiNone && p.parts > 1 ? first_part_row(p) : 0;
     int step = 0;
     for (int item = slot; item < n_items; item += grid) {
         int part, k0, k1;
@@ -353,7 +354,9 @@ void grouped_mm_rows_kernel(MmP p) {
             if (in) {
                 if (p.parts > 1) {
                     // (gated: in the order 2 gate, 2 up)
-                    if constexpr (EPI == kEpiGated) *(f32x4*)(p.partial + 2 * (((size_t)part * p.R_max + row) * p.N + a)) = acc[u];
+                    if constexpr (EPI != kEpiNone)
+                        *(f32x4*)(p.partial + (part * p.part_rows + (row - row0)) * p.part_ld +
+                                  (size_t)(a - p.col0) * (EPI == kEpiGated ? 2 : 1)) = acc[u];
                     else *(f32x4*)(p.partial + ((size_t)part * p.R_max + row) * p.N + a) = acc[u];
                 } else if constexpr (EPI == kEpiGrad) {
                     sum = rows_grad<EL == kElF16>(p, row, a, acc[u]);

@@ -181,6 +181,28 @@ def test_gradient_of_one_group_with_mostly_empty_last_tiles(R, N, hi, gated):
     gradient(R, 1, N, 136, torch.bfloat16, gated, GELU, kn=gated, weighted=True, T=500, seed=R + N, hi=hi)
 
 
+# The same where the launches of the tails are split along K: 3 rows past 16
+# tiles, 8 columns, both; fewer rows in the group (160 past the whole tiles, 2)
+SPLIT_TAILS = [(4099, 4096, 4099), (4095, 4104, 4095), (4099, 4104, 4099), (4099, 4104, 4000), (4099, 4104, 2)]
+
+
+@pytest.mark.parametrize("R,N,hi", SPLIT_TAILS)
+@pytest.mark.parametrize("kind", ["gated", "nk", "kn"])
+def test_split_tails(R, N, hi, kind):
+    banner(f"act split tails {kind} R={R} N={N} hi={hi}")
+    gated = kind == "gated"
+    assert moe.lib.moe_grouped_mm_act_workspace_size(R, 1, N, 2040) > 0         # (only what is split has one)
+    cols = (N // 2 + 7) // 8 * 8 if gated else N
+    forward(R, 1, cols, 2040, torch.float16, gated, GELU, kn=kind == "kn", weighted=True, residual=True, seed=R + N, hi=hi)
+
+
+@pytest.mark.parametrize("R,N,hi", SPLIT_TAILS)
+@pytest.mark.parametrize("gated", [False, True])
+def test_gradient_split_tails(R, N, hi, gated):
+    banner(f"dact split tails gated={gated} R={R} N={N} hi={hi}")
+    gradient(R, 1, N, 2040, torch.bfloat16, gated, SWI, kn=gated, weighted=True, T=500, seed=R + N, hi=hi)
+
+
 @pytest.mark.parametrize("act,beta,limit", [(SWI, 1.0, 0.0), (SWI, 1.702, 0.75), (GELU, 1.0, 0.0), (GELU, 1.0, 1.5),
                                             (RELU2, 1.0, 1.0), (NONE, 1.0, 0.5)])
 @pytest.mark.parametrize("gated", [False, True])
