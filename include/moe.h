@@ -21,6 +21,11 @@
  * scale per 128 (moe_quantize_block, moe_quantize_block_weights,
  * moe_grouped_mm_fp8), and the gated activation that keeps its input in 8 bits
  * for the backward pass (moe_glu_checkpoint, moe_glu_checkpoint_backward).
+ * Products with bias, activation, row weight and residual in their epilogue and
+ * their backward pass (moe_grouped_mm_act, moe_grouped_mm_dact), the gradients of
+ * biases and of the router (moe_grouped_bias_grad, moe_route_backward), and the
+ * whole layer for a few tokens on 16-bit or block-128 FP8 weights
+ * (moe_layer_few) take the same arrays.
  *
  * Conventions, for every entry point:
  *  - Tensor pointers are DEVICE pointers owned by the caller. Row-major,
@@ -610,7 +615,8 @@ int32_t moe_glu_checkpoint_backward(const uint8_t* q, const float* s, const void
  *
  * An infinite pre-activation follows the formulas in fp32 (Swish and GELU of
  * -inf are NaN). Workspaces at multiples of 16 bytes, one for each call in
- * flight; the same bits every time.
+ * flight: partial sums of at most 32 MiB, for moe_grouped_mm_dact and 16 bytes
+ * for each row and 64 columns. The same bits every time.
  */
 #define MOE_MM_GATED          (1u << 19)
 
@@ -657,7 +663,8 @@ int32_t moe_grouped_mm_dact(const void* dy, int32_t dy_rows, int32_t ld_dy, cons
  * NULL or f32 [G][H]. residual: NULL or [T, H] rows of ld_res; out itself may
  * be given. No other output may overlap an input.
  * H and I are multiples of 8 (16 for E4M3), at most 65536, 2 I H weights below
- * 4 GiB - 4 MiB; x rows and weights start at multiples of 16 bytes. T = 0
+ * 4 GiB - 4 MiB; x rows and weights start at multiples of 16 bytes, and so do
+ * logits where E_tot % 4 == 0. k + s <= 32, E_tot <= 2048. T = 0
  * enqueues nothing. ws: moe_layer_few_workspace_size bytes at a multiple of 16,
  * one for each call in flight.
  */

@@ -5,7 +5,8 @@ marshals arguments (device pointers, sizes, the current HIP stream) and calls
 the C ABI of the same name; all computation runs in the library's HIP kernels.
 PyTorch provides device memory and streams. No call records a gradient: the
 gradients of the products and of the activation are calls of their own
-(moe_grouped_mm with w_kn, moe_grouped_wgrad, moe_glu_checkpoint_backward), and
+(moe_grouped_mm with w_kn, moe_grouped_mm_dact, moe_grouped_wgrad,
+moe_grouped_bias_grad, moe_glu_checkpoint_backward, moe_route_backward), and
 outputs do not require one whatever the inputs do. Importing the package fails
 if the library has not been built (python routed_grouped_gemm_amd/build.py).
 """

@@ -24,9 +24,10 @@ int launch_part(MmP& p, int rows, int cols, hipStream_t stream) {
 // kernel in launches of their own, which may be split along K and joined. A tile
 // that is mostly empty takes as long as a full one, so that pays where they make
 // for another round of workgroups: 8191 x 4104 x 4096 (8 columns past 16 tiles)
-// 340 -> 314 us, 4099 x 4096 x 2040 (3 rows past 16 tiles) 141 -> 126, and split
-// 300 -> 288 and 111 -> 101. Times in rounds as mm_plan's; a tail's launch costs about 4 us. (Several
-// groups: how full their last tiles are is not known here.)
+// 340 -> 314 us, its gradient at 4099 x 4096 x 2040 (3 rows past 16 tiles) 141 ->
+// 126, and split 300 -> 288 and 111 -> 101. Times in rounds as mm_plan's; a tail's
+// launch costs about 4 us. (Several groups: how full their last tiles are is not
+// known here.)
 struct EpiTail { bool on; int rows, parts; };                // rows to a tile, parts along K
 struct EpiPlan { int rows, parts; EpiTail row, col; };
 

@@ -5,8 +5,11 @@
 // the weight-streaming kernel), added in their order by a second launch; a
 // product split along K has its epilogue in the launch that joins it.
 //
-// Measured: 24576 x 1408 x 2048 in 16 uneven groups, gathered, gated 265 us;
-// 4099 x 4096 x 2040 in FP16, squared ReLU 163 us.
+// Bound by HBM in its epilogues, which all workgroups reach together: a gated
+// tile's moves 640 KiB (pre, dpre and h), about 30 us a round at the rate of a
+// large copy, while the matrix instructions wait; by those between.
+// Measured: 24576 x 1408 x 2048 in 16 uneven groups, gathered, gated 262 us;
+// 4099 x 4096 x 2040 in FP16, squared ReLU 101 us.
 #include "grouped_mm_act.h"
 
 namespace {
