@@ -215,6 +215,19 @@ MOE_DEV int few_before(const int* wave, int w, int& all) {
     return run;
 }
 
+// The local group of routed assignment a, or -1. A token has one row in a group:
+// where its logits hold a NaN (so its weights are NaN) the router can name an
+// expert twice, and of those the first counts.
+MOE_DEV int few_group_of(const FewP& p, const FewTables& t, int a) {
+    const int e = t.idx[a] - p.e0;
+    if ((uint32_t)e >= (uint32_t)p.E_loc) return -1;
+    const float w = t.w[a];
+    if (w != w)
+        for (int i = a - a % p.k; i < a; ++i)
+            if (t.idx[i] == t.idx[a]) return -1;
+    return e;
+}
+
 // The grouping of up to 64 N assignments by one wave, without barriers (every
 // instruction of a workgroup's 16 waves costs 16 cycles of a SIMD: the whole
 // workgroup's way, below, takes 1.8 us): lane l of slot i has assignment 64 i + l; the
@@ -230,8 +243,7 @@ MOE_DEV void few_group_wave(const FewP& p, const FewTables& t, int lane) {
         tok[i] = a < Tk ? a / p.k : a - Tk;
         g[i] = -1;
         if (a < Tk) {
-            const int e = t.idx[a] - p.e0;
-            if ((uint32_t)e < (uint32_t)p.E_loc) g[i] = e;
+            g[i] = few_group_of(p, t, a);
         } else if (a < all) {
             g[i] = p.E_loc;
         }
@@ -320,8 +332,7 @@ MOE_DEV void few_route(const FewP& p, const FewTables& t) {
     if (a < Tk) {
         tok = a / p.k;
         wt = t.w[a];
-        const int e = t.idx[a] - p.e0;
-        g = (uint32_t)e < (uint32_t)p.E_loc ? e : -1;
+        g = few_group_of(p, t, a);
         if (g >= 0) {
             pos = atomicAdd(t.num + g, 1);
             atomicMin(t.of + g, a);

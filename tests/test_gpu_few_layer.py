@@ -203,6 +203,29 @@ def test_other_tokens_experts_stay_out():
         assert not bool(torch.isfinite(got[hit]).all(1).any())
 
 
+@pytest.mark.parametrize("T,k", [(16, 8), (32, 8), (12, 4)])
+@pytest.mark.parametrize("bits", [-1, 0x7FC00000, 0xFFC00000 - (1 << 32)])
+def test_nan_logits_stay_in_their_token(T, k, bits):
+    """Every kind of NaN in a token's logits, all of them or one: its row is NaN, the others are as without."""
+    c = Case(T=T, E=8, k=k, e0=0, E_loc=8, H=128, I=64, seed=T + k)
+    ref, tol = c.reference()
+    c.logits.view(torch.int32)[3] = bits
+    c.logits.view(torch.int32)[5, 2] = bits
+    got = c.run()
+    assert bool(got[[3, 5]].isnan().all())
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[[3, 5]] = False
+    assert bool(((got.double() - ref).abs() <= tol)[rest].all())
+
+
+def test_masked_logits():
+    """Experts masked by -inf: chosen last, with weight 0; fewer than k left to a token."""
+    c = Case(T=20, E=12, k=3, e0=2, E_loc=8, H=128, I=64, residual=True, renorm=True, seed=9)
+    c.logits[:, 1::2] = -float("inf")
+    c.logits[4, 1:] = -float("inf")
+    c.check(c.run())
+
+
 def test_every_e4m3_code_is_exact():
     """Weights of every code, x and h powers of two: sums of exact products."""
     codes = torch.arange(256, device="cuda", dtype=torch.uint8)
