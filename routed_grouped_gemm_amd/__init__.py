@@ -777,7 +777,7 @@ def moe_grouped_mm_act(x, w, offsets, epi: Epilogue | None = None, gated: bool =
             pre = x.new_empty((R, N))
         _dense(pre, (R, N), x.dtype, "pre", dev)
         e = epi.desc
-        desc = moe_epilogue(e.act, e.beta, e.limit, 0, e.bias, _p(pre))
+        desc = e if pre is None else moe_epilogue(e.act, e.beta, e.limit, 0, e.bias, _p(pre))
         nws = int(lib.moe_grouped_mm_act_workspace_size(R, G, N, K))
         ws = _ws(nws, dev)
         flags = (MOE_MM_W_KN if w_kn else 0) | (MOE_MM_GATED if gated else 0)
