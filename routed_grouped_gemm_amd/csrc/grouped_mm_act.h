@@ -47,9 +47,20 @@ inline EpiTail epi_tail(int64_t R, int64_t n, int64_t thin, int64_t nk, double& 
 inline EpiPlan epi_plan(int R_max, int G, int N, int K, bool gated) {
     EpiPlan best{};
     moe_mm_plan(false, R_max, G, gated ? 2 * N : N, K, &best.rows, &best.parts);
-    if (G > 1 || best.rows <= 64) return best;
+    if (best.rows <= 64) return best;
     const int64_t cus = device_cu_count(), nk = (K + 63) / 64, at = gated ? kATile / 2 : kATile, thin = gated ? kRowsA / 2 : kRowsA;
     double least = 1e30;
+    if (G > 1) {
+        // Tile height for groups that are not equal: half a tile more for each than
+        // its rows make (4096 rows in 16 uneven groups, gated 2816 x 2048: 107 us with
+        // 256 rows, 84 with 128). With 128 the tables of at most 2047 groups fit LDS.
+        for (int rows = 256; rows >= 128 && G <= 2047; rows /= 2) {
+            const int64_t items = ((int64_t)R_max / rows + (std::min(G, R_max) + 1) / 2) * ((N + at - 1) / at);
+            const double t = (double)((items + cus - 1) / cus) * ((double)nk * (rows == 256 ? 1.6 : 1.0) + 8.0);
+            if (t < least) { least = t; best.rows = rows; }
+        }
+        return best;
+    }
     for (int rows = 256; rows >= 128; rows /= 2)
         for (int tails = 0; tails < 4; ++tails) {
             const bool rt = tails & 1, ct = tails & 2;
