@@ -648,7 +648,8 @@ int32_t moe_grouped_mm_dact(const void* dy, int32_t dy_rows, int32_t ld_dy, cons
  * with the router's choice and weights w as moe_route (MOE_ROUTE_RENORM in
  * flags) on logits [T, E_tot], local experts [e0, e0 + E_loc), and a shared
  * expert (group E_loc, every token, weight 1) where shared_w1 and shared_w2 are
- * given. w_j h_j is rounded to dtype between the products; every sum is fp32, in
+ * given. w_j h_j is held in two parts of dtype between the products (16 bits of its
+ * value in BF16, 22 in FP16; past FP16's range it is infinite); every sum is fp32, in
  * a fixed order; one rounding to dtype at the end. A token without a local
  * expert gets its residual, or 0.
  *
@@ -664,8 +665,8 @@ int32_t moe_grouped_mm_dact(const void* dy, int32_t dy_rows, int32_t ld_dy, cons
  * be given. No other output may overlap an input.
  * H and I are multiples of 8 (16 for E4M3), at most 65536, 2 I H weights below
  * 4 GiB - 4 MiB; x rows and weights start at multiples of 16 bytes, and so do
- * logits where E_tot % 4 == 0. k + s <= 32, E_tot <= 2048. T = 0
- * enqueues nothing. ws: moe_layer_few_workspace_size bytes at a multiple of 16,
+ * logits where E_tot % 4 == 0. k + s <= 32, E_tot <= 2048, T (k + s) I below 2^26
+ * (h is 4 bytes a value of the workspace). T = 0 enqueues nothing. ws: moe_layer_few_workspace_size bytes at a multiple of 16,
  * one for each call in flight.
  */
 #define MOE_FEW_MAX_TOKENS 32

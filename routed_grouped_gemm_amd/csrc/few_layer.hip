@@ -11,7 +11,8 @@
 // a time; the waves split the reduction axis: unit i (128 bytes of each of the 16
 // rows) goes to wave i % 16 (few_w1: i % split, 16 / split runs of rows at once,
 // so that a wave has some units before each barrier). A wave keeps four units in
-// flight (128 KiB in a compute unit) and requests whole lines, 8 lanes a row: with
+// flight (128 KiB in a compute unit), or two or three where more than the weights
+// is in registers, and requests whole lines, 8 lanes a row: with
 // 4 lanes a row, the layout of the matrix instruction's operand, the same bytes
 // took a quarter longer. The operand's layout is made by passing a unit through 2
 // KiB of LDS a wave. The other operand, the token rows or h, is in LDS where it
@@ -21,18 +22,25 @@
 //
 // few_w1's 16 rows are 8 of the gate and the same 8 of the up projection, in
 // the order 2 gate, 2 up, so that a lane ends with both halves of its outputs.
-// few_w2's 16 columns of the 16x16 result are the tokens themselves: a unit's
-// sums are added for the tokens that chose its expert (a choice, not a product
-// with 0: another token's infinities stay out), so the sum over experts stays in
-// fp32 registers and nothing has to be combined afterwards.
+// Between the two, h is held in two parts of the operands' type, its value rounded and
+// the rest (16 bits of it in BF16, 22 in FP16): rounded once, it was most of the
+// outputs' error (2.3e-3 of them in the 2-norm in BF16, 1.6e-3 with two parts, which
+// is the outputs' own rounding). few_w2's 16 columns of the 16x16 result are both
+// parts of 8 rows of a group, or 16 rows with a product for each part (kCols8,
+// kCols16). A unit's sums are added for the tokens that chose its expert (a choice, not a
+// product with 0: another token's infinities stay out), so the sum over experts
+// stays in fp32 registers and nothing has to be combined afterwards.
 //
 // Measured (a plain read of memory: 6.9 TB/s): one token on 6 of 64 experts of
-// 2048 x 1408 in BF16 (104 MB) 28 us, of which the weights stream for 14 at 7
-// TB/s; the rest is the start of two kernels (routing 2, grouping 1, first
-// requests 3, the second's tables and first requests 3). 16 tokens on 12 of 32
-// local experts of 7168 x 2048 in E4M3 (528 MB) 95 us, on 16 in BF16 (1.4 GB) 214
-// us, 6.6 TB/s. 32 tokens on 21 of them in BF16 308 us, E4M3 206 us (h does not
-// fit LDS). 8 tokens on 8 experts of 4096 x 4096 128 us, 6.3 TB/s.
+// 2048 x 1408 in BF16 (104 MB) 30 us, of which the weights stream for 15 at 7
+// TB/s; the rest is the start of two kernels. 16 tokens on 11 of 32 local experts of
+// 7168 x 2048 in E4M3 (484 MB) 98 us, on 14 in BF16 (1.2 GB) 198 us, 6.2 TB/s.
+// 32 tokens on 20 of them in BF16 (1.8 GB) 279 us, on 15 in E4M3 (661 MB) 144 us,
+// 4.6 TB/s: few_w1 with two tiles of token rows and E4M3 weights has more in
+// flight than 128 registers hold. 8 tokens on 7 experts of 4096 x 4096 in BF16
+// 116 us, 6.1 TB/s. A shared expert costs more than its weights where its rows
+// are many: 32 tokens on 23 of those experts, one of them shared, 365 us in BF16,
+// 263 us on 22 in E4M3.
 #include <algorithm>
 
 #include "epilogue_act.h"
@@ -55,10 +63,10 @@ struct FewP {
     const uint16_t* res; size_t ld_res;
     uint16_t* out; size_t ld_out;
     // workspace
-    uint16_t* h;                                             // [R, I]
+    uint16_t* h;                                             // [R][2][I]: the two parts of a row
     float* row_w;                                            // [R]
     int32_t* active;                                         // groups with rows, rows used, then the groups
-    int16_t* rowmap;                                         // [active][T] row of a token in the group, -1
+    int16_t* map;                                            // few_w2's columns (few_map)
     int split;                                               // few_w1: waves that share 16 weight rows
     int cb8, cb6, cb4, cb2; float per_grid;                  // items of a group with 8, 6, 4, 2 outputs for every `split` waves; 1 / grid
     int blocks, cols;                                        // few_w2: blocks of `cols` (at most 16) columns
@@ -77,10 +85,47 @@ template <bool F8, int NT, bool XL>
 struct FewSlot {
     i32x4 a[2];
     i32x4 b[XL ? 1 : NT][XL ? 1 : FewGeom<F8, NT, XL>::NB];
-    uint32_t sc[2];                                          // scales of this lane's results (few_w1: gate, up)
-    int row[NT];                                             // few_w2: the token's row, -1,
-    int at[XL ? NT : 1];                                     // and the place of its first piece in LDS
+    uint32_t sc[2];                                          // scales of this lane's results: gate, up
 };
+// What the 16 columns of few_w2's products are. Eight rows of a group and both parts
+// of h: the first parts in columns 0 .. 7, the second in 8 .. 15, so that two parts
+// cost the requests, registers and instructions of one. Or, where a group has more
+// rows than 8, sixteen rows and a product for each part. The rows are those of the tokens in
+// their order (column t: token t) where so many columns hold all tokens, else the
+// group's, and the sums go from its columns to the tokens'.
+enum { kCols8 = 0, kCols16 = 1 };
+constexpr int few_cols_of(int form) { return form == kCols8 ? 8 : 16; }
+
+// A slot of few_w2 for NT tiles of 16 tokens, with LP parts of h in LDS and the
+// others requested with the weights.
+template <bool F8, int NT, int FORM, int LP>
+struct FewGeom2 {
+    static constexpr int NB = F8 ? 4 : 2;
+    static constexpr int UK = F8 ? 128 : 64;
+    static constexpr int Sets = LP == 2 ? 0 : (FORM == kCols8 ? 1 : 2 - LP);   // pieces of how many parts a lane requests
+    static constexpr int Regs = Sets * NB * 4;
+    static constexpr int Ring = Regs <= 8 ? 4 : (Regs <= 16 && !(F8 && NT == 2 && FORM == kCols16) ? 3 : 2);
+};
+template <bool F8, int NT, int FORM, int LP>
+struct FewSlot2 {
+    using Geo = FewGeom2<F8, NT, FORM, LP>;
+    i32x4 a[2];
+    i32x4 b[Geo::Sets ? Geo::Sets : 1][Geo::NB];
+    uint32_t sc;
+    int col;                                                 // the column of this lane's token, or -1; 16 bits for each of two tiles
+    int at;                                                  // place of the row's first piece in LDS
+};
+
+// h in two parts of the operands' type: the value rounded, and what that leaves
+// out, rounded (in FP16 times 2^11, or the part of a small value would be below
+// the type's range). 16 bits of it in BF16, 22 in FP16. A value past the type's
+// range is infinite, its second part 0.
+template <int F16>
+MOE_DEV void few_parts(float v, uint16_t& hi, uint16_t& lo) {
+    hi = (uint16_t)pack16(v, 0.f, F16);
+    const float r = lo16(hi, F16);
+    lo = (uint16_t)pack16(fabsf(r) < INFINITY ? (v - r) * (F16 ? 2048.f : 1.f) : 0.f, 0.f, F16);
+}
 
 // E4M3 codes (8 of them) as 16-bit values, exactly
 template <int EL>
@@ -118,8 +163,35 @@ MOE_DEV f32x4 few_unit(const i32x4 (&a)[2], Piece&& piece) {
     return d;
 }
 
+// The sum of the products of both parts. Where the first part's is not finite it
+// stands alone (an infinite weight times a second part of 0 is no number).
+template <int EL>
+MOE_DEV float few_both(float d, float e) {
+    const float s = EL == kElF16 ? fmaf(e, 1.f / 2048.f, d) : d + e;
+    return fabsf(d) < INFINITY ? s : d;
+}
+// The products of one unit with 16 rows and both parts of h, hi(i) and lo(i) their piece i.
+template <int EL, bool F8, typename Hi, typename Lo>
+MOE_DEV f32x4 few_unit2(const i32x4 (&a)[2], Hi&& hi, Lo&& lo) {
+    f32x4 d = {0.f, 0.f, 0.f, 0.f}, e = {0.f, 0.f, 0.f, 0.f};
+    #pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        #pragma unroll
+        for (int k = 0; k < (F8 ? 2 : 1); ++k) {
+            const i32x4 w = F8 ? few_decode<EL>(a[h][2 * k], a[h][2 * k + 1]) : a[h];
+            const int i = F8 ? 2 * h + k : h;
+            d = mfma16x16x32<EL>(w, hi(i), d);
+            e = mfma16x16x32<EL>(w, lo(i), e);
+        }
+    }
+    #pragma unroll
+    for (int v = 0; v < 4; ++v) d[v] = few_both<EL>(d[v], e[v]);
+    return d;
+}
+
 // An address that is the same in the whole wave, as the compiler is to know too
-// (a resource in vector registers is a loop over lanes at every request).
+// (a resource in vector registers is a loop over lanes at every request, which
+// few_w1's weights and scales still have where its token rows are not in LDS).
 MOE_DEV const uint8_t* few_uniform(uint64_t a) {
     return (const uint8_t*)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a) |
                             (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(a >> 32)) << 32);
@@ -203,6 +275,20 @@ MOE_DEV FewTables few_tables(int* lds, int T, int k, int G, int s) {
     t.wave = lds;
     return t;
 }
+// few_w2's columns: rows of the group in its map (the columns' rows, then the column
+// of each token, tokens t and t + 16 side by side), or -1. Tokens in their order: T
+// entries, the rows of the tokens.
+// A group of more than 16 rows is there twice, one after the other, so that its
+// weights come from a cache the second time.
+__host__ __device__ inline int few_map_width(int T) { return T > 16 ? 48 : (T > 8 ? 32 : T); }
+// most groups of few_w2
+__host__ __device__ inline int few_most(int T, int k, int G, int s) {
+    const int R = T * (k + s), most = G < R ? G : R;
+    return T > 16 ? most + R / 17 : most;
+}
+// the columns of a call, from the rows of its longest group
+MOE_DEV int few_form(int most) { return most <= 8 ? kCols8 : kCols16; }
+constexpr int kFewHead = 3;                                  // ints before the groups: their number, rows, form
 // sum of the waves' values before this wave's, and of all
 MOE_DEV int few_before(const int* wave, int w, int& all) {
     int run = 0;
@@ -594,7 +680,11 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, const int* list, in
             with_act(p.act, [&](auto act) { a = epi_act<decltype(act)::value>(z, p.beta); });
             const int row = tb.member[lo + r];
             const float o = a * epi_clamp(y, p.limit) * tb.row_w[row];
-            p.h[(size_t)row * p.I + c] = (uint16_t)pack16(o, 0.f, EL == kElF16);
+            uint16_t hi, lo;
+            few_parts<EL == kElF16>(o, hi, lo);
+            uint16_t* const d = p.h + (size_t)row * 2 * p.I + c;
+            d[0] = hi;
+            d[p.I] = lo;
         }
         #pragma unroll
         for (int x = 0; x < NT; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -612,6 +702,57 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, const int* list, in
         }
     };
     few_turns(ring, left * upw, step);
+}
+
+// What few_w2 reads of the routing, by one workgroup.
+MOE_DEV void few_map(const FewP& p, const FewTables& tb, int n_act, int R, int most) {
+    const int tid = threadIdx.x, lane = tid & 63, form = few_form(most);
+    for (int i = tid; i < R; i += kFewThreads) p.row_w[i] = tb.row_w[i];
+    if (tid == 0) { p.active[0] = n_act; p.active[1] = R; p.active[2] = form; }
+    if (p.T <= 8 || (p.T <= 16 && form == kCols16)) {        // the columns are the tokens (few_w2_body)
+        for (int i = tid; i < n_act; i += kFewThreads) p.active[kFewHead + i] = tb.group[i];
+        for (int i = tid; i < n_act * p.T; i += kFewThreads) {
+            const int a = i / p.T, t = i - a * p.T;
+            int row = -1;
+            for (int m = tb.first[a]; m < tb.first[a] + tb.cnt[a]; ++m) row = tb.token[tb.member[m]] == t ? tb.member[m] : row;
+            p.map[i] = (int16_t)row;
+        }
+        return;
+    }
+    int* const at = tb.num;                                  // [n_act] first place of a group among few_w2's
+    int* const sorted = tb.idx;                              // [R <= 2 T k] members, in each group in the order of the rows
+    if (tid < 64) {
+        int more = 0;
+        for (int a0 = 0; a0 < n_act; a0 += 64) {
+            const uint64_t big = __ballot(a0 + lane < n_act && tb.cnt[min(a0 + lane, n_act - 1)] > 16);
+            if (a0 + lane < n_act) at[a0 + lane] = a0 + lane + more + __popcll(big & lanemask_lt(lane));
+            more += __popcll(big);
+        }
+        if (lane == 0) p.active[0] = n_act + more;
+    }
+    for (int i = tid; i < n_act * 32; i += kFewThreads) {
+        const int a = i >> 5, m = i & 31, lo = tb.first[a], n = tb.cnt[a];
+        if (m >= n) continue;
+        const int row = tb.member[lo + m];
+        int rank = 0;
+        for (int x = 0; x < n; ++x) rank += tb.member[lo + x] < row ? 1 : 0;
+        sorted[lo + rank] = row;
+    }
+    __syncthreads();
+    const int width = few_map_width(p.T);
+    for (int i = tid; i < n_act * width; i += kFewThreads) {
+        const int a = i / width, e = i - a * width, lo = tb.first[a], n = tb.cnt[a];
+        const int t = p.T > 16 ? 16 * (e & 1) + ((e - 16) >> 1) : e - 16;
+        int mine = -1;                                       // of a token: its row's place in the group
+        if (e >= 16)
+            for (int x = 0; x < n; ++x) mine = tb.token[sorted[lo + x]] == t ? x : mine;
+        for (int h = 0; 16 * h < n; ++h) {
+            const int c = e < 16 ? (16 * h + e < n ? sorted[lo + 16 * h + e] : -1) : (mine >> 4 == h ? mine & 15 : -1);
+            p.map[(at[a] + h) * width + e] = (int16_t)c;
+            if (e == 0) p.active[kFewHead + at[a] + h] = tb.group[a];
+        }
+    }
+    __syncthreads();                                         // (the choices' place is used again)
 }
 
 template <int EL, bool F8, bool TWO>
@@ -636,18 +777,7 @@ void few_w1_kernel(FewP p, int lds_rows) {
     few_route(p, tb);
     const int n_act = __builtin_amdgcn_readfirstlane(tb.wave[3 * kFewWaves]), R = tb.wave[3 * kFewWaves + 1];
     const int most = __builtin_amdgcn_readfirstlane(tb.wave[3 * kFewWaves + 2]);
-    if (blockIdx.x == gridDim.x - 1) {                       // for few_w2
-        const int tid = threadIdx.x;
-        if (tid == 0) { p.active[0] = n_act; p.active[1] = R; }
-        for (int i = tid; i < n_act; i += kFewThreads) p.active[2 + i] = tb.group[i];
-        for (int i = tid; i < R; i += kFewThreads) p.row_w[i] = tb.row_w[i];
-        for (int i = tid; i < n_act * p.T; i += kFewThreads) {
-            const int a = i / p.T, t = i - a * p.T;
-            int row = -1;
-            for (int m = tb.first[a]; m < tb.first[a] + tb.cnt[a]; ++m) row = tb.token[tb.member[m]] == t ? tb.member[m] : row;
-            p.rowmap[i] = (int16_t)row;
-        }
-    }
+    if (blockIdx.x == gridDim.x - 1) few_map(p, tb, n_act, R, most);
     // groups whose rows fit LDS, then the others (one tile of 16 rows, or two as the longest group has)
     if (all) {
         if (TWO && most > 16) few_w1_body<EL, F8, NTM, true, true>(p, tb, nullptr, n_act, part, swap, rows);
@@ -682,9 +812,20 @@ void few_w1_kernel(FewP p, int lds_rows) {
 }
 
 // ------------------------------------------------------------------ few_w2
-template <int EL, bool F8, int NT, bool XL>
-MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, int n_act, int R, float* part, uint8_t* swap, uint8_t* rows) {
-    using Geo = FewGeom<F8, NT, XL>;
+// bytes in LDS of one part of a row of h, and of a row with n parts there (64 so that rows start in other banks)
+template <bool F8>
+MOE_DEV int few_h_part(int I) { return ((I + (F8 ? 127 : 63)) / (F8 ? 128 : 64) * (F8 ? 256 : 128) + 1023) / 1024 * 1024; }
+template <bool F8>
+MOE_DEV int few_h_row(int I, int n) { return n * few_h_part<F8>(I) + 64; }
+
+// The waves' sums take the place of their exchanged units.
+template <int EL, bool F8, int TC, int FORM, int LP>
+MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, int n_act, int R, uint8_t* swap, uint8_t* rows) {
+    constexpr int NT = TC == 32 ? 2 : 1;
+    using Geo = FewGeom2<F8, NT, FORM, LP>;
+    using Slot = FewSlot2<F8, NT, FORM, LP>;
+    constexpr bool PACK = FORM == kCols8, TOKENS = few_cols_of(FORM) >= TC;
+    const int width = TOKENS ? p.T : few_map_width(p.T);
     constexpr int RING = Geo::Ring;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -694,10 +835,11 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
     const int units = n_act * upg;
     const int nsb = (p.H + 127) >> 7, ksb = (p.I + 127) >> 7;
     const FewGroups w_of(p.w2, p.w2s, (size_t)p.H * (size_t)wrow, p.E_loc), s_of(p.s2, p.s2s, (size_t)(nsb * ksb) * 4, p.E_loc);
-    const int stride = (upg * (F8 ? 256 : 128) + 1023) / 1024 * 1024 + 64;
+    const int hpart = few_h_part<F8>(p.I), stride = few_h_row<F8>(p.I, LP);
     uint8_t* const ex = swap + w * 2048;
+    float* const part = (float*)swap;                        // [16 waves][2][4][64]
     const int upw = max(1, (units + kFewWaves - 1) / kFewWaves);      // rounds of units of a block of columns
-    const rsrc_t rh = make_rsrc(p.h, (uint32_t)((size_t)R * p.I * 2));
+    const rsrc_t rh = make_rsrc(p.h, (uint32_t)((size_t)R * p.I * 4));
 
     struct { int block, i, ai, ku, sb; bool live; uint32_t ro[2]; } L;
     auto open = [&]() __attribute__((always_inline)) {
@@ -714,27 +856,28 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
         L.ai = w / upg;
         L.ku = w - L.ai * upg;
     };
-    auto load = [&](FewSlot<F8, NT, XL>& S) __attribute__((always_inline)) {
+    auto load = [&](Slot& S) __attribute__((always_inline)) {
         const bool live = L.live && L.ai < n_act;
         const int g = live ? __builtin_amdgcn_readfirstlane(active[L.ai]) : 0;
         const rsrc_t rw = make_rsrc(w_of.of(g), live ? (uint32_t)p.H * (uint32_t)wrow : 0u);
         #pragma unroll
         for (int h = 0; h < 2; ++h) S.a[h] = few_load_w(rw, few_add(L.ro[h], few_koff_w<F8>(L.ku, lane, p.I)));
+        const int c = PACK ? j & 7 : j, m0 = PACK ? j >> 3 : 0;                // this lane's row's column, its part of h
+        const int row = live && (!TOKENS || c < p.T) ? map[L.ai * width + c] : -1;
         #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int row = live && 16 * t + j < p.T ? map[L.ai * p.T + 16 * t + j] : -1;
-            S.row[t] = row;
-            if constexpr (!XL) {
-                const uint32_t o = row >= 0 ? (uint32_t)row * (uint32_t)(p.I * 2) : kMmNoRow;
-                #pragma unroll
-                for (int i = 0; i < Geo::NB; ++i) S.b[t][i] = few_load(rh, few_add(o, few_koff_x<F8>(L.ku, i, q, p.I)));
-            } else {
-                S.at[t] = max(row, 0) * stride + few_kbyte_x<F8>(L.ku, 0, q);
-            }
+        for (int m = 0; m < Geo::Sets; ++m) {
+            const uint32_t o = row >= 0 ? (uint32_t)(2 * row + m0 + LP + m) * (uint32_t)(p.I * 2) : kMmNoRow;
+            #pragma unroll
+            for (int i = 0; i < Geo::NB; ++i) S.b[m][i] = few_load(rh, few_add(o, few_koff_x<F8>(L.ku, i, q, p.I)));
         }
+        if constexpr (LP > 0) S.at = max(row, 0) * stride + m0 * hpart + few_kbyte_x<F8>(L.ku, 0, q);
+        const int16_t* const cols = map + L.ai * width + 16;
+        if constexpr (TOKENS) S.col = row;                   // (its own column)
+        else if constexpr (NT == 1) S.col = live ? cols[j] : -1;
+        else S.col = live ? ((const int*)cols)[j] : -1;
         if constexpr (F8) {
             const rsrc_t rs = make_rsrc(s_of.of(g), live ? (uint32_t)(nsb * ksb) * 4u : 0u);
-            S.sc[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, (L.sb + L.ku) * 4, 0, 0);
+            S.sc = __builtin_amdgcn_raw_buffer_load_b32(rs, (L.sb + L.ku) * 4, 0, 0);
         }
         L.ku += kFewWaves;
         while (L.ku >= upg) { L.ku -= upg; ++L.ai; }
@@ -746,40 +889,59 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
         }
     };
 
-    if constexpr (XL) {
-        const int chunks = stride / 1024;
-        for (int c = w; c < R * chunks; c += kFewWaves) {
-            const int r = c / chunks;
-            few_stage(rh, (uint32_t)r * (uint32_t)(p.I * 2), 2 * p.I, c - r * chunks, rows + r * stride, lane);
+    if constexpr (LP > 0) {
+        const int chunks = hpart / 1024;
+        for (int c = w; c < R * LP * chunks; c += kFewWaves) {
+            const int rm = c / chunks, r = rm / LP, m = rm - r * LP;
+            few_stage(rh, (uint32_t)(2 * r + m) * (uint32_t)(p.I * 2), 2 * p.I, c - rm * chunks, rows + r * stride + m * hpart, lane);
         }
     }
     few_fence();
     L.block = blockIdx.x;
     open();
-    FewSlot<F8, NT, XL> ring[RING];
+    Slot ring[RING];
     static_for<RING>([&](auto s) __attribute__((always_inline)) { load(ring[decltype(s)::value]); });
-    if constexpr (XL) {
+    if constexpr (LP > 0) {                                  // (the rows were requested before the ring's units)
         few_fence();
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(RING * (F8 ? 3 : 2), 15));
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(RING * ((F8 ? 3 : 2) + Geo::Sets * Geo::NB), 15));
         bare_barrier();
     }
     f32x4 acc[NT];
     #pragma unroll
     for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     int block = blockIdx.x, i = 0;
-    auto step = [&](FewSlot<F8, NT, XL>& S) __attribute__((always_inline)) {
+    auto step = [&](Slot& S) __attribute__((always_inline)) {
         i32x4 a[2];
         few_swap(ex, lane, S.a, a);
+        // (the scale is used behind the slot's next requests, so it leaves the slot here:
+        // otherwise those go to other registers, and the copies back at the end of a
+        // turn wait for every request in flight)
+        uint32_t sc = 0;
+        if constexpr (F8) asm volatile("v_mov_b32 %0, %1" : "=v"(sc) : "v"(S.sc));
+        const int own = S.col;
+        auto piece = [&](auto m, int x) __attribute__((always_inline)) {
+            constexpr int M = decltype(m)::value;
+            if constexpr (M < LP) return *(const i32x4*)(rows + S.at + M * hpart + few_kbyte_x<F8>(0, x, 0));
+            else return S.b[M - LP][x];
+        };
+        auto first = [&](int x) __attribute__((always_inline)) { return piece(std::integral_constant<int, 0>{}, x); };
+        f32x4 d;
+        if constexpr (PACK) {
+            d = few_unit<EL, F8>(a, first);
+            #pragma unroll
+            for (int v = 0; v < 4; ++v)                      // the lane 8 columns on has the second part's
+                d[v] = few_both<EL>(d[v], __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(d[v]), 0x128, 0xF, 0xF, true)));
+        } else {
+            d = few_unit2<EL, F8>(a, first, [&](int x) __attribute__((always_inline)) { return piece(std::integral_constant<int, 1>{}, x); });
+        }
         #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const f32x4 d = few_unit<EL, F8>(a, [&](int x) __attribute__((always_inline)) {
-                if constexpr (XL) return *(const i32x4*)(rows + S.at[t] + few_kbyte_x<F8>(0, x, 0));
-                else return S.b[t][x];
-            });
-            const bool in = S.row[t] >= 0;
+            const int col = NT == 1 ? own : (t ? own >> 16 : (int)(int16_t)own);
+            const bool in = col >= 0;
             #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const float y = F8 ? fmaf(d[v], __uint_as_float(S.sc[0]), acc[t][v]) : acc[t][v] + d[v];
+                const float z = TOKENS ? d[v] : __shfl(d[v], (lane & 48) + (col & 15), 64);
+                const float y = F8 ? fmaf(z, __uint_as_float(sc), acc[t][v]) : acc[t][v] + z;
                 acc[t][v] = in ? y : acc[t][v];
             }
         }
@@ -789,7 +951,7 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
         #pragma unroll
         for (int t = 0; t < NT; ++t)
             #pragma unroll
-            for (int v = 0; v < 4; ++v) part[(w * NT + t) * 256 + v * 64 + lane] = acc[t][v];
+            for (int v = 0; v < 4; ++v) part[(2 * w + t) * 256 + v * 64 + lane] = acc[t][v];
         __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
         bare_barrier();
         // thread (token, column): the waves' sums in their order
@@ -797,11 +959,11 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
         if (e < NT * 256 && t < p.T && c < p.cols && n < p.H) {
             float o = 0.f;
             #pragma unroll
-            for (int x = 0; x < kFewWaves; ++x) o += part[(x * NT + (t >> 4)) * 256 + (c & 3) * 64 + (c >> 2) * 16 + (t & 15)];
+            for (int x = 0; x < kFewWaves; ++x) o += part[(2 * x + (t >> 4)) * 256 + (c & 3) * 64 + (c >> 2) * 16 + (t & 15)];
             if (p.b2) {
-                #pragma unroll 8
+                #pragma unroll 4
                 for (int a = 0; a < n_act; ++a) {
-                    const int row = map[a * p.T + t];
+                    const int c = TOKENS ? t : map[a * width + 16 + (NT == 2 ? 2 * (t & 15) + (t >> 4) : t)], row = c >= 0 ? map[a * width + c] : -1;
                     const float y = fmaf(p.row_w[max(row, 0)], p.b2[(size_t)active[a] * p.H + n], o);
                     o = row >= 0 ? y : o;
                 }
@@ -812,31 +974,40 @@ MOE_DEV void few_w2_body(const FewP& p, const int* active, const int16_t* map, i
         #pragma unroll
         for (int x = 0; x < NT; ++x) acc[x] = f32x4{0.f, 0.f, 0.f, 0.f};
         block += gridDim.x;
-        // the sums have been read before the next are written
+        // the sums have been read before the next units are exchanged
         __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
         bare_barrier();
     };
     few_turns(ring, (p.blocks - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * upw, step);
 }
 
-template <int EL, bool F8, int NT>
+// TC: 8, 16 or 32, at least the tokens
+template <int EL, bool F8, int TC>
 __global__ __launch_bounds__(kFewThreads, 4)
 void few_w2_kernel(FewP p, int lds_rows, int most) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    float* const part = (float*)smem;                        // [16 waves][NT][4][64]
-    uint8_t* const swap = smem + kFewWaves * NT * 1024;      // [16 waves][2 KiB]
+    uint8_t* const swap = smem;                              // [16 waves][2 KiB]
     uint8_t* const rows = swap + kFewWaves * 2048;           // [lds_rows]
-    int* const active = (int*)(rows + lds_rows);             // [2 + most], then the map
-    int16_t* const map = (int16_t*)(active + 2 + most);
+    int* const active = (int*)(rows + lds_rows);             // [kFewHead + most], then the map
+    int16_t* const map = (int16_t*)(active + kFewHead + most);
     // all of the tables at once, whatever they hold past the active groups
-    for (int i = threadIdx.x; i < most + 2; i += kFewThreads) active[i] = p.active[i];
-    for (int i = threadIdx.x; i < (most * p.T + 1) / 2; i += kFewThreads) ((int*)map)[i] = ((const int*)p.rowmap)[i];
+    for (int i = threadIdx.x; i < most + kFewHead; i += kFewThreads) active[i] = p.active[i];
+    for (int i = threadIdx.x; i < (most * few_map_width(p.T) + 1) / 2; i += kFewThreads) ((int*)map)[i] = ((const int*)p.map)[i];
     __syncthreads();
     const int n_act = __builtin_amdgcn_readfirstlane(active[0]), R = __builtin_amdgcn_readfirstlane(active[1]);
-    const int upg = (p.I + (F8 ? 127 : 63)) / (F8 ? 128 : 64);
-    const int64_t stride = (upg * (F8 ? 256 : 128) + 1023) / 1024 * 1024 + 64;
-    if (max(R, 1) * stride <= lds_rows) few_w2_body<EL, F8, NT, true>(p, active + 2, map, n_act, R, part, swap, rows);
-    else few_w2_body<EL, F8, NT, false>(p, active + 2, map, n_act, R, part, swap, rows);
+    const int64_t n = max(R, 1);
+    const bool both = n * few_h_row<F8>(p.I, 2) <= lds_rows;
+    const int* const groups = active + kFewHead;
+    if (TC == 8 || __builtin_amdgcn_readfirstlane(active[2]) == kCols8) {
+        if (both) few_w2_body<EL, F8, TC, kCols8, 2>(p, groups, map, n_act, R, swap, rows);
+        else few_w2_body<EL, F8, TC, kCols8, 0>(p, groups, map, n_act, R, swap, rows);
+        return;
+    }
+    if constexpr (TC > 8) {
+        if (both) few_w2_body<EL, F8, TC, kCols16, 2>(p, groups, map, n_act, R, swap, rows);
+        else if (n * few_h_row<F8>(p.I, 1) <= lds_rows) few_w2_body<EL, F8, TC, kCols16, 1>(p, groups, map, n_act, R, swap, rows);
+        else few_w2_body<EL, F8, TC, kCols16, 0>(p, groups, map, n_act, R, swap, rows);
+    }
 }
 
 template <typename K>
@@ -853,20 +1024,21 @@ int few_ready(K* k, bool (&ready)[64]) {
 }
 
 // LDS left for token rows: a compute unit's, less the sums and the tables
-template <int EL, bool F8, int NT>
+template <int EL, bool F8, int TC>
 int launch_few(FewP& p, hipStream_t stream) {
+    constexpr int NT = TC == 32 ? 2 : 1;
     static bool ready1[64] = {false}, ready2[64] = {false};
     auto* k1 = &few_w1_kernel<EL, F8, NT == 2>;
-    auto* k2 = &few_w2_kernel<EL, F8, NT>;
+    auto* k2 = &few_w2_kernel<EL, F8, TC>;
     int e = few_ready(k1, ready1);
     if (e || (e = few_ready(k2, ready2))) return e;
     const int64_t rows = (int64_t)p.T * (p.k + p.s), most = std::min<int64_t>(p.G, rows);
-    const int cus = device_cu_count();
+    const int cus = device_cu_count(), most2 = few_most(p.T, p.k, p.G, p.s);
     const int64_t items = most * (p.I / 8);
     const int grid1 = (int)std::min<int64_t>(items, cus), grid2 = std::min(p.blocks, cus);
     const int64_t fix1 = (int64_t)2 * kFewWaves * NT * 1024 + kFewWaves * 2048 +
                          (int64_t)few_table_ints(p.T, p.k, p.G, p.s) * 4;
-    const int64_t fix2 = (int64_t)kFewWaves * NT * 1024 + kFewWaves * 2048 + (2 + most) * 4 + (most * p.T + 1) / 2 * 4;
+    const int64_t fix2 = (int64_t)kFewWaves * 2048 + (kFewHead + most2) * 4 + (most2 * few_map_width(p.T) + 1) / 2 * 4;
     const int rows1 = (int)((kMmLds - fix1) / 16 * 16), rows2 = (int)((kMmLds - fix2) / 16 * 16);
     // about four units of the reduction axis to a wave: a barrier and an epilogue
     // for every unit cost more than they are worth (16 tokens on 51 experts of 2048
@@ -878,8 +1050,14 @@ int launch_few(FewP& p, hipStream_t stream) {
     p.per_grid = 1.0f / (float)grid1;
     k1<<<grid1, kFewThreads, (size_t)(fix1 + rows1), stream>>>(p, rows1);
     if ((e = (int)hipGetLastError())) return e;
-    k2<<<grid2, kFewThreads, (size_t)(fix2 + rows2), stream>>>(p, rows2, (int)most);
+    k2<<<grid2, kFewThreads, (size_t)(fix2 + rows2), stream>>>(p, rows2, most2);
     return (int)hipGetLastError();
+}
+
+template <int EL, bool F8>
+int launch_tokens(FewP& p, hipStream_t stream) {
+    if (p.T > 16) return launch_few<EL, F8, 32>(p, stream);
+    return p.T > 8 ? launch_few<EL, F8, 16>(p, stream) : launch_few<EL, F8, 8>(p, stream);
 }
 
 // Columns of few_w2's blocks: up to 16, fewer where that fills the last round of
@@ -897,14 +1075,14 @@ int few_cols(int H, bool eight) {
 
 size_t up16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-// byte offsets of the workspace's regions: h, row_w, active, rowmap, end
+// byte offsets of the workspace's regions: h, row_w, active, map, end
 void few_regions(int T, int k, int G, int s, int I, size_t (&at)[5]) {
-    const size_t R = (size_t)T * (k + s), most = std::min<size_t>(G, R);
+    const size_t R = (size_t)T * (k + s), most = few_most(T, k, G, s);
     at[0] = 0;
-    at[1] = at[0] + up16(R * I * 2);
+    at[1] = at[0] + up16(R * I * 4);
     at[2] = at[1] + up16(R * 4);
-    at[3] = at[2] + up16((most + 2) * 4);
-    at[4] = at[3] + up16(most * T * 2 + 2);
+    at[3] = at[2] + up16((most + kFewHead) * 4);
+    at[4] = at[3] + up16(most * few_map_width(T) * 2 + 2);
 }
 
 }  // namespace
@@ -935,12 +1113,8 @@ int moe_launch_few(const moe_few_args& a, void* ws, hipStream_t stream) {
     few_regions(p.T, p.k, p.G, p.s, p.I, at);
     uint8_t* b = (uint8_t*)ws;
     p.h = (uint16_t*)(b + at[0]); p.row_w = (float*)(b + at[1]); p.active = (int32_t*)(b + at[2]);
-    p.rowmap = (int16_t*)(b + at[3]);
-    const bool f8 = a.w1_scales != nullptr, two = a.T > 16;
-    if (a.dtype == MOE_T_F16) {
-        if (f8) return two ? launch_few<kElF16, true, 2>(p, stream) : launch_few<kElF16, true, 1>(p, stream);
-        return two ? launch_few<kElF16, false, 2>(p, stream) : launch_few<kElF16, false, 1>(p, stream);
-    }
-    if (f8) return two ? launch_few<kElBf16, true, 2>(p, stream) : launch_few<kElBf16, true, 1>(p, stream);
-    return two ? launch_few<kElBf16, false, 2>(p, stream) : launch_few<kElBf16, false, 1>(p, stream);
+    p.map = (int16_t*)(b + at[3]);
+    const bool f8 = a.w1_scales != nullptr;
+    if (a.dtype == MOE_T_F16) return f8 ? launch_tokens<kElF16, true>(p, stream) : launch_tokens<kElF16, false>(p, stream);
+    return f8 ? launch_tokens<kElBf16, true>(p, stream) : launch_tokens<kElBf16, false>(p, stream);
 }

@@ -20,14 +20,16 @@ int32_t check_few_sizes(int32_t T, int32_t k, int32_t E_loc, int32_t s) {
     return s < 0 || s > 1 || k > MOE_MAX_SLOTS - s ? MOE_ERR_SHAPE : MOE_OK;
 }
 
-// largest hidden and inner size of moe_layer_few
+// largest hidden and inner size of moe_layer_few, and bound on the values of h
 constexpr int32_t kFewMaxDim = 65536;
+constexpr int64_t kFewMaxH = 1ll << 26;
 
 }  // namespace
 
 MOE_EXPORT size_t moe_layer_few_workspace_size(int32_t T, int32_t k, int32_t E_loc, int32_t H, int32_t I,
                                                int32_t s) {
     if (check_few_sizes(T, k, E_loc, s) || H < 8 || H > kFewMaxDim || I < 8 || I > kFewMaxDim) return 0;
+    if ((int64_t)T * (k + s) * I >= kFewMaxH) return 0;
     return moe_few_bytes(T, k, E_loc + s, s, I);
 }
 
@@ -48,6 +50,7 @@ MOE_EXPORT int32_t moe_layer_few(const moe_few_args* a, void* ws, size_t ws_byte
     const int32_t mult = eight ? 16 : 8;
     if (a->H < mult || a->H % mult || a->H > kFewMaxDim || a->I < mult || a->I % mult || a->I > kFewMaxDim) return MOE_ERR_SHAPE;
     if ((int64_t)2 * a->I * a->H * (eight ? 1 : 2) >= kGatherBytes) return MOE_ERR_SHAPE;
+    if ((int64_t)a->T * (a->k + s) * a->I >= kFewMaxH) return MOE_ERR_SHAPE;
     if (a->ldx < a->H || a->ldx % 8 || a->ldx > kMaxLd || a->ld_out < a->H || (a->residual && a->ld_res < a->H)) return MOE_ERR_SHAPE;
     if (a->T == 0) return MOE_OK;
     if (!a->logits || !a->x || !a->w1 || !a->w2 || !a->out) return MOE_ERR_NULL;
