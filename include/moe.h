@@ -651,7 +651,9 @@ int32_t moe_grouped_mm_dact(const void* dy, int32_t dy_rows, int32_t ld_dy, cons
  * given. w_j h_j is held in two parts of dtype between the products (16 bits of its
  * value in BF16, 22 in FP16; past FP16's range it is infinite); every sum is fp32, in
  * a fixed order; one rounding to dtype at the end. A token without a local
- * expert gets its residual, or 0.
+ * expert gets its residual and the shared expert's term, or 0. A logit of -inf
+ * masks its expert (weight 0); a token of them only has no expert, as in
+ * moe_route_backward. NaN or +inf make the weights of the token NaN.
  *
  * dtype: MOE_T_BF16 or MOE_T_F16, of x, residual, out and 16-bit weights.
  * w1 [E_loc, 2I, H] (gate rows, then up rows), w2 [E_loc, H, I], shared_w1

@@ -389,6 +389,18 @@ MOE_DEV void few_group_wave(const FewP& p, const FewTables& t, int lane) {
     if (lane == 0) { t.wave[3 * kFewWaves] = n_act; t.wave[3 * kFewWaves + 1] = n_rows; t.wave[3 * kFewWaves + 2] = most; }
 }
 
+// A token whose logits are all -inf chooses nothing (its weights come out as NaN, like
+// those of a token with a NaN or +inf, which keeps them): by the wave that routed it.
+MOE_DEV void few_unrouted(const FewP& p, const FewTables& t, int tok, int lane) {
+    if (tok >= p.T) return;
+    const float w = t.w[tok * p.k];
+    if (__builtin_amdgcn_readfirstlane(w == w ? 1 : 0)) return;
+    bool other = false;
+    for (int e = lane; e < p.E; e += 64) other |= !(p.logits[(size_t)tok * p.E + e] == -INFINITY);
+    if (__ballot(other)) return;
+    if (lane < p.k) t.idx[tok * p.k + lane] = -1;
+}
+
 // Routes the T tokens and groups their local assignments, by the whole
 // workgroup; an assignment to a thread (T (k + s) <= 32 x 32).
 MOE_DEV void few_route(const FewP& p, const FewTables& t) {
@@ -402,6 +414,9 @@ MOE_DEV void few_route(const FewP& p, const FewTables& t) {
     else if (p.E <= 256) route_block<kFewWaves, 32, 8>(p.logits, p.T, p.E, p.k, r, t.idx, t.w, nullptr, nullptr);
     else if (p.E <= 512) route_block<kFewWaves, 64, 8>(p.logits, p.T, p.E, p.k, r, t.idx, t.w, nullptr, nullptr);
     else route_block<kFewWaves, 64, 32>(p.logits, p.T, p.E, p.k, r, t.idx, t.w, nullptr, nullptr);
+    // (route_block's tokens of a wave: two side by side up to 256 experts, else one and 16 on)
+    few_unrouted(p, t, p.E <= 256 ? 2 * w : w, lane);
+    few_unrouted(p, t, p.E <= 256 ? 2 * w + 1 : w + kFewWaves, lane);
     __syncthreads();
     // thread a: assignment a of the routed ones, then the shared expert's tokens
     const int Tk = p.T * p.k, all = Tk + p.s * p.T, a = tid;
