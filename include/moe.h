@@ -730,7 +730,7 @@ int32_t moe_grouped_bias_grad(const void* dy, int32_t dy_rows, int32_t ld_dy, co
  * moe_permute writes it: k + s) dw[slot_row[t * ld_slot + j]], 0 where that is
  * outside [0, dw_rows): the experts of other GPUs. The call is linear in dw,
  * prob_grad and z_coef, so the parts of several GPUs may be added. Indices
- * outside [0, E_tot) count as not chosen. A logit of -inf has p = 0 and no
+ * outside [0, E_tot) count as not chosen; the others need not be the largest. A logit of -inf has p = 0 and no
  * gradient, a row of them only likewise; NaN or +inf make the row's gradient
  * NaN (with MOE_ROUTE_RENORM and no other term, at least the chosen experts').
  * dlogits f32 [T, E_tot], fp32 throughout. 1 <= k <= min(E_tot, 32).

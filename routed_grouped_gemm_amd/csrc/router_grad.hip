@@ -76,10 +76,18 @@ void route_grad_kernel(RouteGradP p) {
     total = group_sum<LPT>(total);
     const float inv = total > 0.f ? 1.0f / total : (total == 0.f ? 0.f : total);
     const float lse = total == 0.f ? 0.f : m + logf(total);
-    float w_j = e_j >= 0 ? expf(l_j - m) * inv : 0.f;
+    float w_j;
     if (p.renorm) {
-        const float s = group_sum<LPT>(w_j);
-        w_j = s == 0.f ? 0.f : w_j / s;
+        // (relative to the largest of the chosen: choices need not hold the row's largest
+        // logit, and far below it their exponentials have few bits, or none)
+        float mc = group_max<LPT>(l_j);
+        if (mc == -INFINITY) mc = 0.f;
+        const float x = e_j >= 0 ? expf(l_j - mc) : 0.f, s = group_sum<LPT>(x);
+        w_j = s == 0.f ? 0.f : x / s;
+        // a NaN or +inf elsewhere in the row makes its weights NaN here too
+        if (!(total < INFINITY)) w_j = e_j >= 0 ? total - total : 0.f;
+    } else {
+        w_j = e_j >= 0 ? expf(l_j - m) * inv : 0.f;
     }
     const float mean = group_sum<LPT>(d_j * w_j);
     // what number j adds to its expert: scaled by p_e with the other terms, or by itself
