@@ -620,6 +620,16 @@ int32_t moe_glu_checkpoint_backward(const uint8_t* q, const float* s, const void
  */
 #define MOE_MM_GATED          (1u << 19)
 
+/*
+ * How a call of these sizes runs, as moe_grouped_mm_plan: rows of a tile and parts
+ * of the reduction axis; then the same of the launch for the last rows and of that
+ * for the last columns of a single group (0, 0: none). flags: MOE_MM_GATED of
+ * moe_grouped_mm_act (N = 2I) or 0. moe_grouped_mm_dact, gated or not, runs as the
+ * product of its N and K with flags 0.
+ */
+int32_t moe_grouped_mm_act_plan(int32_t R_max, int32_t G, int32_t N, int32_t K, uint32_t flags,
+                                int32_t plan[6]);
+
 size_t  moe_grouped_mm_act_workspace_size(int32_t R_max, int32_t G, int32_t N, int32_t K);
 int32_t moe_grouped_mm_act(const void* x, int32_t x_rows, int32_t ldx, const int32_t* row_src,
                            const void* w, int32_t dtype, const int32_t* offsets, int32_t R_max,

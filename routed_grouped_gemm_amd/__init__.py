@@ -787,6 +787,15 @@ def moe_grouped_mm_act(x, w, offsets, epi: Epilogue | None = None, gated: bool =
     return (out, pre) if keep_pre else out
 
 
+def moe_grouped_mm_act_plan(R_max: int, G: int, N: int, K: int, gated: bool = False) -> list[int]:
+    """How moe_grouped_mm_act runs for these sizes (N counts the weight rows): rows of a tile, parts
+    of the reduction axis, and the same of the launches for one group's last rows and last
+    columns (0: none). moe_grouped_mm_dact runs as the product of its N and K that is not gated."""
+    plan = (C.c_int32 * 6)()
+    _check(lib.moe_grouped_mm_act_plan(R_max, G, N, K, MOE_MM_GATED if gated else 0, plan), "moe_grouped_mm_act_plan")
+    return list(plan)
+
+
 def moe_grouped_mm_dact(dy, w, offsets, pre, epi: Epilogue | None = None, gated: bool = True, w_kn: bool = True, dy_src=None,
                         row_w=None, want_h: bool = True, want_dw: bool = True, stream=None):
     """The backward pass of moe_grouped_mm_act up to the pre-activation: dh = dy[r]

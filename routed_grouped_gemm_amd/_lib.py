@@ -105,6 +105,7 @@ SIGNATURES = {
     "moe_grouped_wgrad_plan": (I32, [I32, I32, I32, I32, C.POINTER(I32)]),
     "moe_glu_checkpoint": (I32, [P, I32, I32, I32, I32, P, P, EP, P, P, P, P]),
     "moe_glu_checkpoint_backward": (I32, [P, P, P, I32, I32, I32, I32, P, P, EP, P, P, P, P]),
+    "moe_grouped_mm_act_plan": (I32, [I32, I32, I32, I32, U32, C.POINTER(I32)]),
     "moe_grouped_mm_act_workspace_size": (SZ, [I32, I32, I32, I32]),
     "moe_grouped_mm_act": (I32, [P, I32, I32, P, P, I32, P, I32, I32, I32, I32, U32, EP, P, P, I32, P, I32, P, SZ, P]),
     "moe_grouped_mm_dact_workspace_size": (SZ, [I32, I32, I32, I32]),

@@ -54,6 +54,12 @@ int launch_type(const MmActCall& c, MmP& p, const EpiPlan& plan, hipStream_t str
 
 }  // namespace
 
+void moe_mm_act_plan(int R_max, int G, int N, int K, bool gated, int32_t* plan) {
+    const EpiPlan p = epi_plan(R_max, G, N, K, gated);
+    const int32_t v[6] = {p.rows, p.parts, p.row.rows, p.row.parts, p.col.rows, p.col.parts};
+    std::copy(v, v + 6, plan);
+}
+
 // (gated or not: the plans differ in their tails)
 size_t moe_mm_act_bytes(int R_max, int G, int weight_rows, int K) {
     if (R_max <= 0) return 0;

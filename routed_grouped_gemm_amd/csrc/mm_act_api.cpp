@@ -73,6 +73,16 @@ static int32_t check_act_dims(int32_t R_max, int32_t N, int32_t K, int32_t G, ui
     return N % 16 || (int64_t)N * K * 2 >= kGatherBytes ? MOE_ERR_SHAPE : MOE_OK;
 }
 
+MOE_EXPORT int32_t moe_grouped_mm_act_plan(int32_t R_max, int32_t G, int32_t N, int32_t K, uint32_t flags,
+                                           int32_t plan[6]) {
+    if (flags & ~MOE_MM_GATED) return MOE_ERR_UNSUPPORTED;
+    const int32_t st = check_act_dims(R_max, N, K, G, flags);
+    if (st) return st;
+    if (!plan) return MOE_ERR_NULL;
+    moe_mm_act_plan(R_max, G, (flags & MOE_MM_GATED) ? N / 2 : N, K, (flags & MOE_MM_GATED) != 0, plan);
+    return MOE_OK;
+}
+
 MOE_EXPORT size_t moe_grouped_mm_act_workspace_size(int32_t R_max, int32_t G, int32_t N, int32_t K) {
     if (check_dims(R_max, N, K, G, 8)) return 0;
     return moe_mm_act_bytes(R_max, G, N, K);

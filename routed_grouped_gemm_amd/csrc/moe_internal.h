@@ -203,6 +203,7 @@ struct MmActCall {
     void* h; float* dw;              // gradient
     void* ws;
 };
+void moe_mm_act_plan(int R_max, int G, int N, int K, bool gated, int32_t* plan);  // [6]
 size_t moe_mm_act_bytes(int R_max, int G, int weight_rows, int K);
 int moe_launch_mm_act(const MmActCall& c, hipStream_t stream);
 size_t moe_mm_dact_bytes(int R_max, int G, int N, int K);
