@@ -15,8 +15,9 @@ MOE_DEV float epi_inside(float v, float lim) { return !(lim > 0.f) || fabsf(v) <
 
 // Phi(z), the normal distribution, and e = exp(-z^2 / 2). For x = |z| / sqrt 2,
 // erfc(x) exp(x^2) is t times a polynomial in t = 1 / (1 + 0.45 x): degree 7,
-// fitted to the least largest relative error (4e-7; 7e-7 with fp32's roundings),
-// so Phi keeps its relative precision where it is small (1 + erf loses it: at z =
+// fitted to the least largest relative error (4e-7). With fp32's roundings, that of
+// the exponent growing with z^2, it is 7e-7 down to z = -2, 1e-6 to -4, 3e-6 to -8 and
+// 8e-6 to -13, so Phi keeps its relative precision where it is small (1 + erf loses it: at z =
 // -4 an error of 1e-3 of the value, past FP16's half step) at a few instructions
 // more than the exponential.
 MOE_DEV float epi_phi(float z, float& e) {
