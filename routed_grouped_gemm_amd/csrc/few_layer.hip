@@ -649,8 +649,9 @@ MOE_DEV void few_w1_body(const FewP& p, const FewTables& tb, const int* list, in
         const int u = i * split + wk;
         float sc[2] = {1.f, 1.f};
         if constexpr (F8) {
-            sc[0] = __uint_as_float(S.sc[0]);
-            sc[1] = __uint_as_float(S.sc[1]);
+            // (0 for a unit past the row's end, whose sums are 0: the last block's may be infinite)
+            sc[0] = u < units ? __uint_as_float(S.sc[0]) : 0.f;
+            sc[1] = u < units ? __uint_as_float(S.sc[1]) : 0.f;
         }
         i32x4 a[2];
         few_swap(ex, lane, S.a, a);
