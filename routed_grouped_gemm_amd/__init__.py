@@ -803,7 +803,8 @@ def moe_grouped_mm_dact(dy, w, offsets, pre, epi: Epilogue | None = None, gated:
     [G, N, K]) and the activation's gradient from pre [R, 2N] (gated) or [R, N].
     Returns a dict: dpre, shaped as pre; h [R, N], the activation's output
     with the row weight; dw f32 [R], the row weight's gradient (None where not
-    wanted)."""
+    wanted), without the term dy . b2 of a bias b2 that the second product adds behind
+    the row weight."""
     _mat(dy, _T16, "dy")
     dev, (T, K) = dy.device, dy.shape
     if w.dim() != 3 or w.shape[1 if w_kn else 2] != K:

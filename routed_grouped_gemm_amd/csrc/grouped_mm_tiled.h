@@ -883,7 +883,9 @@ void grouped_mm_kernel(MmP p) {
     // their reads. Requests not counted (row sources, stores) only make a wait
     // longer; once a stream has ended its requests still count. In the first
     // NST - 1 K-tiles after an item's stores the requests waited for are older
-    // than the stores, which then count as newer.
+    // than the stores, which then count as newer. (With an epilogue the compiler
+    // adds a wait for everything at the loop's head, as its row weights and bias seem
+    // to be pending on a path: these waits then take no effect.)
     constexpr int KEPT = mm_kind(MODE) == kWgrad8 ? 8 : 0;            // requests of the 8-bit rows in turn 1
     constexpr int L1 = mm_turn_requests(EL, MODE, NB, 1), L2 = mm_turn_requests(EL, MODE, NB, 0);
     constexpr int STORES = is_wgrad(MODE) ? 4 * NB : (EPI == kEpiGated ? NB : 2 * NB);   // (an epilogue's: at least)
